@@ -34,7 +34,9 @@
  *     workspace that does not hold what the call needs) set a sticky error
  *     word in ws; outputs are then unspecified.  Read it with
  *     topo_read_error after synchronising.  No kernel traps or asserts.
- *   - All results are integers and are bit-for-bit deterministic.
+ *   - The results of the planning calls are integers; all results, the
+ *     floating-point ones of the expert layer included, are bit-for-bit
+ *     deterministic.
  *   - Thread safety: calls on distinct workspaces are independent.
  */
 #ifndef TOPO_H
@@ -75,6 +77,10 @@ extern "C" {
 #define TOPO_DTYPE_F32 0    /* logits as float32 */
 #define TOPO_DTYPE_BF16 1   /* logits as bf16 bit patterns */
 #define TOPO_GATE_MAX_E 1024
+#define TOPO_SCORE_SOFTMAX 0  /* topo_route_opts.score */
+#define TOPO_SCORE_SIGMOID 1
+#define TOPO_ROUTE_MAX_GROUPS 32
+#define TOPO_BLOCK 128      /* values along the contraction that share one scale */
 #define TOPO_SHUFFLE_STATS 4
 #define TOPO_SHUFFLE_MAX_RANKS 256
 #define TOPO_PLACE_STATS 4
@@ -369,6 +375,151 @@ int topo_permute(const topo_cfg *cfg, int32_t n_layers, int32_t H, const uint16_
 int topo_combine(const topo_cfg *cfg, int32_t n_layers, int32_t H, const uint16_t *y,
                  const int32_t *sorted_pairs, const float *w, uint16_t *out, void *ws,
                  size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The expert layer: routing, the experts' products in 8 bits, and what lays
+ * their operands out.  The order of use is topo_route -> topo_hist ->
+ * topo_plan -> topo_reroute_layout -> topo_permute_quantize ->
+ * topo_expert_gemm -> topo_swiglu_quantize -> topo_expert_gemm ->
+ * topo_combine.  8-bit values are e4m3 (4 exponent bits, 3 mantissa bits, no
+ * infinities, largest 448), one byte each.
+ *
+ * Scales.  TOPO_BLOCK = 128 consecutive values along the contraction share a
+ * float32 scale; the last block of a row may be shorter.  The quantising calls
+ * use the smallest power of two s with amax <= 448 s (exponent at least -126;
+ * 1 for a block of zeros), amax over the block's finite values, and store
+ * q = e4m3(v / s), to nearest, ties to even: the scaling is exact, so each
+ * value is rounded once.  NaN and infinities are stored as NaN.  The products
+ * take any float32 scales.
+ *
+ * Device pointers to 8-bit and bf16 rows are 16-byte aligned, and row lengths
+ * are multiples of 16 values. */
+
+/* How scores become ids and weights (see topo_route). */
+typedef struct {
+    int32_t score;       /* TOPO_SCORE_SOFTMAX or TOPO_SCORE_SIGMOID */
+    int32_t n_group;     /* groups of E / n_group consecutive experts; 1 = none;
+                            E % n_group == 0, at most TOPO_ROUTE_MAX_GROUPS */
+    int32_t topk_group;  /* groups that stay, 1..n_group */
+    int32_t group_top;   /* values summed for a group's score: 1 or 2 */
+    int32_t renorm;      /* nonzero: weights of a token sum to scale */
+    float scale;         /* finite factor of the weights */
+} topo_route_opts;
+
+/* Routing to experts.  With x the logits as float32 and every operation
+ * rounded to float32:
+ *   s_e = exp(x_e - max) / sum exp(x - max), or 1 / (1 + exp(-x_e))
+ *   c_e = s_e + bias_e; x_e itself when bias is NULL and group_top is 1 (the
+ *         same order, without ties made by rounding); -inf where x_e is -inf
+ *   a group's score is the sum of its group_top largest c; the topk_group
+ *   groups of the largest scores stay (n_group = 1: every expert stays)
+ *   ids = the k largest c of the experts that stay, in descending order
+ *   weight_j = scale * s_j / (sum of the chosen s), or scale * s_j
+ * Equal values go to the lower group or expert; NaN ranks below every number.
+ * Where the sum is 0 (all chosen logits -inf, or all scores underflow) the
+ * weights are 0: a row whose mask leaves nothing has k ids and no weight.
+ * logits: device [n_layers][T][E], float32 or bf16 (logits_dtype).
+ * bias:   device float32 [E] or NULL (used to choose, not in the weights).
+ * ids:    device int32 [n_layers][T][k];  weights: device float32, the same.
+ * hist:   device int32 [n_layers][R][E] or NULL; when given, Omega and the
+ *         tile index of ids as topo_hist leaves them (ws then as topo_hist).
+ * ws:     at least the header (topo_workspace_bytes(NULL, 0,
+ *         TOPO_CALL_COOCCUR)); TOPO_CALL_GATE bytes with hist.
+ * Requires E <= TOPO_GATE_MAX_E and k <= topk_group * (E / n_group). */
+int topo_route(const topo_cfg *cfg, int32_t n_layers, const topo_route_opts *opts, const void *logits,
+               int32_t logits_dtype, const float *bias, int32_t *ids, float *weights, int32_t *hist,
+               void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Gradient of topo_route's weights in the logits, the choice held fixed:
+ *   grad_logits[t][e] = sum_j grad_weights[t][j] * d weight_j / d x_e,
+ * dense (0 for experts that no weight depends on).
+ * ids: topo_route's, distinct within a token.  grad_weights: device float32
+ * [n_layers][T][k].  grad_logits: device [n_layers][T][E] of the logits' type.
+ * ws: at least the header.  Device errors: TOPO_ERANGE (an id outside [0, E):
+ * skipped). */
+int topo_route_grad(const topo_cfg *cfg, int32_t n_layers, const topo_route_opts *opts, const void *logits,
+                    int32_t logits_dtype, const int32_t *ids, const float *grad_weights, void *grad_logits,
+                    void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* topo_permute into 8 bits: the rows of x quantised and copied to the layout
+ * positions of their pairs,
+ *   q[l][pos][:] = e4m3 of x[l][sorted_pairs[l][pos] / k][:].
+ * x: device bf16 [n_layers][T][H]; q: device e4m3 [n_layers][T*k][H]; scale:
+ * device float32 [n_layers][T*k][ceil(H / 128)]; H a positive multiple of 16;
+ * sorted_pairs, ws and device errors as topo_permute. */
+int topo_permute_quantize(const topo_cfg *cfg, int32_t n_layers, int32_t H, const uint16_t *x,
+                          const int32_t *sorted_pairs, uint8_t *q, float *scale, void *ws, size_t ws_bytes,
+                          cudaStream_t stream);
+
+/* Rows in 8 bits.  x: device bf16 [rows][C]; q: device e4m3 [rows][C]; scale:
+ * device float32 [rows][ceil(C / 128)]. */
+int topo_quantize_rows(int64_t rows, int32_t C, const uint16_t *x, uint8_t *q, float *scale, cudaStream_t stream);
+
+/* Experts' weights in 8 bits, one scale for each 128 x 128 block.
+ * w: device bf16 [n_w][N][K]; q: device e4m3 [n_w][N][K]; scale: device
+ * float32 [n_w][ceil(N / 128)][ceil(K / 128)].  qt [n_w][K][N] and scale_t
+ * [n_w][ceil(K / 128)][ceil(N / 128)], both or neither: the transposes, which
+ * topo_expert_gemm takes to give the gradient of its input. */
+int topo_quantize_weight(int32_t n_w, int32_t N, int32_t K, const uint16_t *w, uint8_t *q, float *scale,
+                         uint8_t *qt, float *scale_t, cudaStream_t stream);
+
+/* Rows in 8 bits down their columns, transposed: the operands of
+ * topo_expert_wgrad.  Each segment [seg_off[i], seg_off[i+1]) is cut into
+ * blocks of 128 rows from its first row, the last one padded with zeros; block
+ * b of all segments together takes columns 128 b .. 128 b + 127 of q.
+ * x: device bf16 [rows][C]; seg_off: device int32 [n_seg + 1]; q: device e4m3
+ * [C][cap]; scale: device float32 [cap / 128][C]; cap =
+ * topo_cols_capacity(n_seg, rows).  Columns past the last block are not
+ * written.  ws: at least the header.  Device errors: TOPO_ESTATE (an offset
+ * outside [0, rows] or out of order; the segment is taken as empty). */
+int64_t topo_cols_capacity(int32_t n_seg, int64_t rows);
+int topo_quantize_cols(int32_t n_seg, int64_t rows, int32_t C, const uint16_t *x, const int32_t *seg_off,
+                       int64_t cap, uint8_t *q, float *scale, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Gated activation a = silu(g) * u of rows h = [g | u], in 8 bits, and its
+ * gradient.  silu(g) = g / (1 + exp(-g)); a is formed in float32, every
+ * operation rounded.  h: device bf16 [rows][2 I]; q: device e4m3 [rows][I];
+ * scale: device float32 [rows][ceil(I / 128)]; dy: device bf16 [rows][I], the
+ * gradient of a; dh: device bf16 [rows][2 I]. */
+int topo_swiglu_quantize(int64_t rows, int32_t I, const uint16_t *h, uint8_t *q, float *scale,
+                         cudaStream_t stream);
+int topo_swiglu_grad(int64_t rows, int32_t I, const uint16_t *h, const uint16_t *dy, uint16_t *dh,
+                     cudaStream_t stream);
+
+/* The experts' products.  For the rows r of segment i, e = seg_w[i]:
+ *   out[r][n] = sum_b a_scale[r][b] * w_scale[e][n / 128][b] *
+ *               (sum over k in block b of a[r][k] * w[e][n][k])
+ * in float32, rounded once to bf16 (nearest, ties to even) or stored as float32.
+ * a: device e4m3 [rows][K]; a_scale: device float32 [rows][ceil(K / 128)];
+ * seg_off: device int32 [n_seg + 1] (the layout's, or a part of it: rows that
+ * no segment holds are not written); seg_w: device int32 [n_seg], or NULL for
+ * segment i's weights i (replicas of an expert name the same weights, or
+ * copies); w: device e4m3 [n_w][N][K]; w_scale: device float32
+ * [n_w][ceil(N / 128)][ceil(K / 128)]; out: device [rows][N] of out_dtype.
+ * The gradient of a is the same call with the rows' output gradient in 8 bits
+ * (topo_quantize_rows) and the transposed weights.
+ * ws: topo_expert_workspace_bytes bytes.  N and K positive multiples of 16,
+ * rows <= 2^31 - 1, n_w * N and n_w * K below 2^31.  Device errors:
+ * TOPO_ESTATE (an offset outside [0, rows] or out of order) and TOPO_ERANGE
+ * (seg_w outside [0, n_w)): the segment is skipped; TOPO_ETIMEOUT. */
+size_t topo_expert_workspace_bytes(int32_t n_seg, int64_t rows, int32_t N, int32_t K);
+int topo_expert_gemm(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, int32_t K, const uint8_t *a,
+                     const float *a_scale, const int32_t *seg_off, const int32_t *seg_w, const uint8_t *w,
+                     const float *w_scale, void *out, int32_t out_dtype, void *ws, size_t ws_bytes,
+                     cudaStream_t stream);
+
+/* Gradient of the weights of each segment (instance), float32:
+ *   dw[i][n][k] = sum over blocks b of segment i of dy_scale[b][n] * x_scale[b][k] *
+ *                 (sum over t in block b of dy[n][t] * x[k][t])
+ * and 0 for an empty segment.  dy [N][cap] and x [K][cap] with their scales
+ * are topo_quantize_cols' of the rows' output gradient and input, for the same
+ * seg_off, rows and cap.  dw: device float32 [n_seg][N][K]; instances of one
+ * expert are summed by the caller, as ranks sum theirs.  ws as
+ * topo_expert_gemm.  Device errors: TOPO_ESTATE (as topo_quantize_cols, or
+ * more blocks than cap holds; the segment is taken as empty), TOPO_ETIMEOUT. */
+int topo_expert_wgrad(int32_t n_seg, int64_t rows, int32_t N, int32_t K, int64_t cap, const uint8_t *dy,
+                      const float *dy_scale, const uint8_t *x, const float *x_scale, const int32_t *seg_off,
+                      float *dw, void *ws, size_t ws_bytes, cudaStream_t stream);
 
 /* topo_hist without a caller-supplied workspace.  No passage of the pages
  * has a counterpart: it computes exactly what topo_hist computes (Omega), for

@@ -30,6 +30,10 @@ TOPO_CALL_GATE = 9
 TOPO_DTYPE_F32 = 0
 TOPO_DTYPE_BF16 = 1
 TOPO_GATE_MAX_E = 1024
+TOPO_SCORE_SOFTMAX = 0
+TOPO_SCORE_SIGMOID = 1
+TOPO_ROUTE_MAX_GROUPS = 32
+TOPO_BLOCK = 128
 TOPO_SHUFFLE_STATS = 4
 TOPO_SHUFFLE_MAX_RANKS = 256
 TOPO_PLACE_STATS = 4
@@ -40,7 +44,10 @@ EXPORTS = ("topo_workspace_bytes", "topo_ws_reset", "topo_hist", "topo_cooccur",
            "topo_reroute", "topo_dispatch_layout", "topo_reroute_layout", "topo_read_error",
            "topo_strerror", "topo_hist_noalloc", "topo_permute", "topo_combine",
            "topo_dedup_layout", "topo_gate_hist", "topo_shuffle_workspace_bytes",
-           "topo_shuffle_targets", "topo_place_experts", "topo_cooccur_workspace_bytes")
+           "topo_shuffle_targets", "topo_place_experts", "topo_cooccur_workspace_bytes", "topo_route",
+           "topo_route_grad", "topo_permute_quantize", "topo_quantize_rows", "topo_quantize_weight",
+           "topo_cols_capacity", "topo_quantize_cols", "topo_swiglu_quantize", "topo_swiglu_grad",
+           "topo_expert_workspace_bytes", "topo_expert_gemm", "topo_expert_wgrad")
 TOPO_HIST_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -66,6 +73,12 @@ class TopoPlan(ctypes.Structure):
     _fields_ = [("slot_expert", ctypes.c_void_p), ("route_cnt", ctypes.c_void_p),
                 ("inst_load", ctypes.c_void_p), ("rank_load", ctypes.c_void_p),
                 ("stats", ctypes.c_void_p)]
+
+
+class TopoRouteOpts(ctypes.Structure):
+    """Mirror of topo_route_opts."""
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -102,12 +115,30 @@ def lib():
             L.topo_shuffle_targets.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
             L.topo_place_experts.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp]
             L.topo_combine.argtypes = [cfgp, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+            i64, optp = ctypes.c_int64, ctypes.POINTER(TopoRouteOpts)
+            L.topo_route.argtypes = [cfgp, i32, optp, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+            L.topo_route_grad.argtypes = [cfgp, i32, optp, vp, i32, vp, vp, vp, vp, sz, vp]
+            L.topo_permute_quantize.argtypes = [cfgp, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+            L.topo_quantize_rows.argtypes = [i64, i32, vp, vp, vp, vp]
+            L.topo_quantize_weight.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, vp]
+            L.topo_cols_capacity.argtypes = [i32, i64]
+            L.topo_cols_capacity.restype = i64
+            L.topo_quantize_cols.argtypes = [i32, i64, i32, vp, vp, i64, vp, vp, vp, sz, vp]
+            L.topo_swiglu_quantize.argtypes = [i64, i32, vp, vp, vp, vp]
+            L.topo_swiglu_grad.argtypes = [i64, i32, vp, vp, vp, vp]
+            L.topo_expert_workspace_bytes.argtypes = [i32, i64, i32, i32]
+            L.topo_expert_workspace_bytes.restype = sz
+            L.topo_expert_gemm.argtypes = [i32, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+            L.topo_expert_wgrad.argtypes = [i32, i64, i32, i32, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
             L.topo_read_error.argtypes = [vp]
             L.topo_strerror.argtypes = [ctypes.c_int]
             L.topo_strerror.restype = ctypes.c_char_p
             for f in ("topo_ws_reset", "topo_hist", "topo_cooccur", "topo_plan", "topo_reroute",
                       "topo_dispatch_layout", "topo_reroute_layout", "topo_read_error",
-                      "topo_hist_noalloc", "topo_permute", "topo_combine", "topo_dedup_layout", "topo_gate_hist", "topo_shuffle_targets", "topo_place_experts"):
+                      "topo_hist_noalloc", "topo_permute", "topo_combine", "topo_dedup_layout", "topo_gate_hist", "topo_shuffle_targets", "topo_place_experts",
+                      "topo_route", "topo_route_grad", "topo_permute_quantize", "topo_quantize_rows",
+                      "topo_quantize_weight", "topo_quantize_cols", "topo_swiglu_quantize", "topo_swiglu_grad",
+                      "topo_expert_gemm", "topo_expert_wgrad"):
                 getattr(L, f).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -266,6 +297,90 @@ def topo_combine(cfg: TopoCfg, n_layers: int, H: int, y, sorted_pairs, w, out, w
     return _chk("topo_combine", lib().topo_combine(ctypes.byref(cfg), n_layers, H, _p(y),
                                                    _p(sorted_pairs), _p(w), _p(out), _p(ws),
                                                    ws_bytes, _s(stream)))
+
+
+def make_route(score: int, n_group: int = 1, topk_group: int = 1, group_top: int = 1, renorm: bool = True,
+               scale: float = 1.0) -> TopoRouteOpts:
+    """topo_route_opts from plain values."""
+    return TopoRouteOpts(score, n_group, topk_group, group_top, int(bool(renorm)), scale)
+
+
+def topo_route(cfg: TopoCfg, n_layers: int, opts: TopoRouteOpts, logits, logits_dtype: int, bias, ids, weights, hist,
+               ws, ws_bytes: int, stream=None) -> int:
+    """Routing to experts: scores, groups, top-k ids and weights (and Omega when hist is given)."""
+    return _chk("topo_route", lib().topo_route(ctypes.byref(cfg), n_layers, ctypes.byref(opts), _p(logits),
+                                               logits_dtype, _p(bias), _p(ids), _p(weights), _p(hist), _p(ws),
+                                               ws_bytes, _s(stream)))
+
+
+def topo_route_grad(cfg: TopoCfg, n_layers: int, opts: TopoRouteOpts, logits, logits_dtype: int, ids, grad_weights,
+                    grad_logits, ws, ws_bytes: int, stream=None) -> int:
+    """Gradient of topo_route's weights in the logits."""
+    return _chk("topo_route_grad", lib().topo_route_grad(ctypes.byref(cfg), n_layers, ctypes.byref(opts), _p(logits),
+                                                         logits_dtype, _p(ids), _p(grad_weights), _p(grad_logits),
+                                                         _p(ws), ws_bytes, _s(stream)))
+
+
+def topo_permute_quantize(cfg: TopoCfg, n_layers: int, H: int, x, sorted_pairs, q, scale, ws, ws_bytes: int,
+                          stream=None) -> int:
+    """Dispatch pack in 8 bits: the rows of topo_permute as e4m3 with a scale per 128 values."""
+    return _chk("topo_permute_quantize",
+                lib().topo_permute_quantize(ctypes.byref(cfg), n_layers, H, _p(x), _p(sorted_pairs), _p(q),
+                                            _p(scale), _p(ws), ws_bytes, _s(stream)))
+
+
+def topo_quantize_rows(rows: int, C: int, x, q, scale, stream=None) -> int:
+    """bf16 rows as e4m3 with a scale per 128 values."""
+    return _chk("topo_quantize_rows", lib().topo_quantize_rows(rows, C, _p(x), _p(q), _p(scale), _s(stream)))
+
+
+def topo_quantize_weight(n_w: int, N: int, K: int, w, q, scale, qt=None, scale_t=None, stream=None) -> int:
+    """bf16 weights as e4m3 with a scale per 128 x 128 block, and their transpose when qt and scale_t are given."""
+    return _chk("topo_quantize_weight", lib().topo_quantize_weight(n_w, N, K, _p(w), _p(q), _p(scale), _p(qt),
+                                                                   _p(scale_t), _s(stream)))
+
+
+def topo_cols_capacity(n_seg: int, rows: int) -> int:
+    """Columns of topo_quantize_cols' output for rows in n_seg segments."""
+    return int(lib().topo_cols_capacity(n_seg, rows))
+
+
+def topo_quantize_cols(n_seg: int, rows: int, C: int, x, seg_off, cap: int, q, scale, ws, ws_bytes: int,
+                       stream=None) -> int:
+    """bf16 rows as e4m3 down their columns in 128-row blocks of each segment, transposed."""
+    return _chk("topo_quantize_cols", lib().topo_quantize_cols(n_seg, rows, C, _p(x), _p(seg_off), cap, _p(q),
+                                                               _p(scale), _p(ws), ws_bytes, _s(stream)))
+
+
+def topo_swiglu_quantize(rows: int, I: int, h, q, scale, stream=None) -> int:
+    """silu(g) * u of rows [g | u] as e4m3 with a scale per 128 values."""
+    return _chk("topo_swiglu_quantize", lib().topo_swiglu_quantize(rows, I, _p(h), _p(q), _p(scale), _s(stream)))
+
+
+def topo_swiglu_grad(rows: int, I: int, h, dy, dh, stream=None) -> int:
+    """Gradient of silu(g) * u in the rows [g | u]."""
+    return _chk("topo_swiglu_grad", lib().topo_swiglu_grad(rows, I, _p(h), _p(dy), _p(dh), _s(stream)))
+
+
+def topo_expert_workspace_bytes(n_seg: int, rows: int, N: int, K: int) -> int:
+    """Workspace bytes of topo_expert_gemm and topo_expert_wgrad."""
+    return int(lib().topo_expert_workspace_bytes(n_seg, rows, N, K))
+
+
+def topo_expert_gemm(n_seg: int, rows: int, n_w: int, N: int, K: int, a, a_scale, seg_off, seg_w, w, w_scale, out,
+                     out_dtype: int, ws, ws_bytes: int, stream=None) -> int:
+    """The experts' products: each segment's e4m3 rows times its weights' transpose."""
+    return _chk("topo_expert_gemm", lib().topo_expert_gemm(n_seg, rows, n_w, N, K, _p(a), _p(a_scale), _p(seg_off),
+                                                           _p(seg_w), _p(w), _p(w_scale), _p(out), out_dtype,
+                                                           _p(ws), ws_bytes, _s(stream)))
+
+
+def topo_expert_wgrad(n_seg: int, rows: int, N: int, K: int, cap: int, dy, dy_scale, x, x_scale, seg_off, dw, ws,
+                      ws_bytes: int, stream=None) -> int:
+    """Each segment's weight gradient from topo_quantize_cols' operands."""
+    return _chk("topo_expert_wgrad", lib().topo_expert_wgrad(n_seg, rows, N, K, cap, _p(dy), _p(dy_scale), _p(x),
+                                                             _p(x_scale), _p(seg_off), _p(dw), _p(ws), ws_bytes,
+                                                             _s(stream)))
 
 
 def topo_read_error(ws) -> int:

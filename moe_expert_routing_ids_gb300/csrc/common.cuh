@@ -322,9 +322,33 @@ size_t dedup_ws_bytes(const Geo &g, size_t *off_tile, size_t *off_src, size_t *o
 cudaError_t launch_dedup(const Geo &g, const int32_t *dst, int32_t *seg, int32_t *row_token,
                          uint64_t *row_slots, uint64_t *tok_dst, int64_t *send, int64_t *stats, void *ws,
                          cudaStream_t st);
+// Position of every pair (the inverse of sorted) into the pack workspace.
+cudaError_t launch_invert(const Geo &g, const int32_t *sorted, void *ws, cudaStream_t st);
 cudaError_t launch_permute(const Geo &g, int H, const uint16_t *x, const int32_t *sorted, uint16_t *y,
                            void *ws, cudaStream_t st);
 cudaError_t launch_combine(const Geo &g, int H, const uint16_t *y, const int32_t *sorted, const float *w,
                            uint16_t *out, void *ws, cudaStream_t st);
+// Routing to experts and its gradient (k_router.cu), over ntok token rows.
+cudaError_t launch_route(const topo_route_opts &o, int64_t ntok, int E, int k, const void *logits, bool bf16,
+                         const float *bias, int32_t *ids, float *weights, cudaStream_t st);
+cudaError_t launch_route_grad(const topo_route_opts &o, int64_t ntok, int E, int k, const void *logits, bool bf16,
+                              const int32_t *ids, const float *dw, void *dx, void *ws, cudaStream_t st);
+// 8-bit operands (k_quant.cu).
+cudaError_t launch_quantize_rows(int64_t rows, int C, const uint16_t *x, uint8_t *q, float *scale, bool swiglu,
+                                 cudaStream_t st);
+cudaError_t launch_permute_quantize(const Geo &g, int H, const uint16_t *x, const int32_t *sorted, uint8_t *q, float *scale,
+                                    void *ws, cudaStream_t st);
+cudaError_t launch_quantize_cols(int nseg, int64_t rows, int C, const uint16_t *x, const int32_t *seg_off, int64_t cap,
+                                 uint8_t *q, float *scale, void *ws, cudaStream_t st);
+cudaError_t launch_quantize_weight(int n_w, int N, int K, const uint16_t *w, uint8_t *q, float *scale, uint8_t *qt,
+                                   float *scale_t, cudaStream_t st);
+cudaError_t launch_swiglu_grad(int64_t rows, int I, const uint16_t *h, const uint16_t *dy, uint16_t *dh, cudaStream_t st);
+// The experts' products (k_experts.cu).
+cudaError_t launch_expert_gemm(int nseg, int64_t rows, int n_w, int N, int K, const uint8_t *a, const float *a_scale,
+                               const int32_t *seg_off, const int32_t *seg_w, const uint8_t *w, const float *w_scale,
+                               void *out, bool bf16, void *ws, cudaStream_t st);
+cudaError_t launch_expert_wgrad(int nseg, int64_t rows, int N, int K, int64_t cap, const uint8_t *dy, const float *dy_scale,
+                                const uint8_t *x, const float *x_scale, const int32_t *seg_off, float *dw, void *ws,
+                                cudaStream_t st);
 
 }  // namespace topo

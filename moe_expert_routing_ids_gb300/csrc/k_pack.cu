@@ -177,6 +177,8 @@ k_combine(const int4 *__restrict__ y, const int32_t *__restrict__ inv, const flo
     }
 }
 
+}  // namespace
+
 cudaError_t launch_invert(const Geo &g, const int32_t *sorted, void *ws, cudaStream_t st) {
     cudaError_t e;
     const int64_t total = (int64_t)g.L * g.npairs;
@@ -187,8 +189,6 @@ cudaError_t launch_invert(const Geo &g, const int32_t *sorted, void *ws, cudaStr
     k_invert<<<(unsigned)blocks, 256, 0, st>>>(sorted, inv, ws_at<WsHeader>(ws, 0), g.npairs, total);
     return cudaGetLastError();
 }
-
-}  // namespace
 
 cudaError_t launch_permute(const Geo &g, int H, const uint16_t *x, const int32_t *sorted, uint16_t *y,
                            void *ws, cudaStream_t st) {

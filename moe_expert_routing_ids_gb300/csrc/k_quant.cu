@@ -1,0 +1,408 @@
+// 8-bit operands of the experts' products: e4m3 values with one scale for each
+// block of 128 values along the contraction.
+//
+// A block's scale is the smallest power of two s with amax <= 448 s (exponent
+// at least -126; 1 for a block of zeros), amax over the block's finite values;
+// q = e4m3(v / s), to nearest, ties to even.  Scaling by a power of two is
+// exact, so a value is rounded once.  NaN and infinities become NaN.
+//
+//   k_quant_rows    rows as they are, dispatch rows (token row t to the k
+//                   layout positions of its pairs), or the gated activation
+//                   silu(g) * u of rows [g | u]
+//   k_quant_cols    128-row blocks of a segment down each column, transposed:
+//                   the operands of the weight gradient
+//   k_quant_weight  128 x 128 blocks of the experts' weights, and their
+//                   transpose (the operand of the input gradient)
+//   k_swiglu_grad   gradient of silu(g) * u
+//
+// All are bound by memory: a lane takes 16 consecutive values (32 bytes in, 16
+// bytes out), 8 lanes share a block.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+
+namespace topo {
+namespace {
+
+enum { kPlain = 0, kDispatch = 1, kSwiglu = 2 };
+
+// Scale of a block whose largest finite magnitude is amax, and its inverse.
+__device__ __forceinline__ float scale_of(float amax, float &inv) {
+    const uint32_t u = __float_as_uint(amax);
+    int n = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);   // 448 = 1.75 * 2^8
+    n = max(n, -126);
+    if (u == 0u) n = 0;
+    inv = __uint_as_float((uint32_t)(127 - n) << 23);
+    return __uint_as_float((uint32_t)(127 + n) << 23);
+}
+
+__device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
+
+// Two e4m3 values, lo in the low byte.
+__device__ __forceinline__ uint32_t cvt2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void unpack16(const uint4 &a, const uint4 &b, float (&v)[16]) {
+    const uint32_t q[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[2 * i] = __uint_as_float(q[i] << 16);
+        v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+    }
+}
+
+// Largest finite magnitude of 16 values; NaN and infinities are made NaN.
+__device__ __forceinline__ float amax16(float (&v)[16]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));      // fmaxf drops a NaN
+    if (!finite(m)) {
+        m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (finite(v[i])) m = fmaxf(m, fabsf(v[i]));
+            else v[i] = __int_as_float(0x7fffffff);
+        }
+    }
+    return m;
+}
+
+__device__ __forceinline__ uint4 quant16(const float (&v)[16], float inv) {
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        q[i] = cvt2(v[4 * i] * inv, v[4 * i + 1] * inv) | (cvt2(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16);
+    return make_uint4(q[0], q[1], q[2], q[3]);
+}
+
+struct QuantArgs {
+    const uint4 *x;          // bf16 rows, two uint4 per 16 values
+    const int32_t *inv;      // kDispatch: position of each pair
+    uint4 *q;                // e4m3 rows
+    float *scale;            // [rows][KB]
+    WsHeader *hdr;
+    int64_t rows;            // source rows over all layers
+    int64_t npairs;
+    int T, k;                // kDispatch: tokens per layer, copies of a row
+    int nv;                  // 16-value groups per (output) row
+    int KB;
+    int parts, per;          // a row is split over `parts` warps of `per` groups of 32 lanes
+};
+
+template <int SRC>
+__global__ void __launch_bounds__(256)
+k_quant_rows(QuantArgs g) {
+    const int64_t unit = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int64_t row = unit / g.parts;
+    if (row >= g.rows) return;                                   // whole warp
+    const int part = (int)(unit - row * g.parts);
+    const int lane = threadIdx.x & 31;
+    int pa = 0, pb = 0;
+    int64_t base = 0;
+    if (SRC == kDispatch) {
+        base = (row / g.T) * g.npairs;
+        const int32_t *iv = g.inv + row * g.k;
+        pa = lane < g.k ? __ldg(iv + lane) : 0;
+        pb = lane + 32 < g.k ? __ldg(iv + lane + 32) : 0;
+        if (!__all_sync(0xffffffffu, (uint64_t)pa < (uint64_t)g.npairs && (uint64_t)pb < (uint64_t)g.npairs)) {
+            if (lane == 0) set_error(g.hdr, TOPO_ESTATE);
+            return;
+        }
+    }
+    const int end = min(g.nv, (part + 1) * g.per * 32);
+    for (int c0 = part * g.per * 32; c0 < end; c0 += 32) {
+        const int c = c0 + lane;
+        const bool in = c < g.nv;
+        float v[16];
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        if (SRC == kSwiglu) {
+            const uint4 *src = g.x + row * (4 * (int64_t)g.nv);
+            float u[16];
+            unpack16(in ? __ldcs(src + 2 * c) : z, in ? __ldcs(src + 2 * c + 1) : z, v);
+            src += 2 * g.nv;
+            unpack16(in ? __ldcs(src + 2 * c) : z, in ? __ldcs(src + 2 * c + 1) : z, u);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(__fdiv_rn(v[i], __fadd_rn(1.f, expf(-v[i]))), u[i]);
+        } else {
+            const uint4 *src = g.x + row * (2 * (int64_t)g.nv);
+            unpack16(in ? __ldcs(src + 2 * c) : z, in ? __ldcs(src + 2 * c + 1) : z, v);
+        }
+        float m = amax16(v);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float iv;
+        const float s = scale_of(m, iv);
+        const uint4 q = quant16(v, iv);
+        if (SRC == kDispatch) {
+            for (int j = 0; j < g.k; ++j) {
+                const int a = __shfl_sync(0xffffffffu, pa, j & 31), b = __shfl_sync(0xffffffffu, pb, j & 31);
+                const int64_t r = base + (j < 32 ? a : b);
+                if (in) {
+                    g.q[r * g.nv + c] = q;
+                    if ((lane & 7) == 0) g.scale[r * g.KB + (c >> 3)] = s;
+                }
+            }
+        } else if (in) {
+            g.q[row * g.nv + c] = q;
+            if ((lane & 7) == 0) g.scale[row * g.KB + (c >> 3)] = s;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256)
+k_swiglu_grad(const uint4 *__restrict__ h, const uint4 *__restrict__ dy, uint4 *dh, int64_t n, int nv) {
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t row = i / nv;
+        const int64_t at = row * nv * 2 + (i - row * nv);
+        const uint4 a = __ldcs(h + at), b = __ldcs(h + at + nv), d = __ldcs(dy + i);
+        const uint32_t qa[4] = {a.x, a.y, a.z, a.w}, qb[4] = {b.x, b.y, b.z, b.w}, qd[4] = {d.x, d.y, d.z, d.w};
+        uint32_t rg[4], ru[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float og[2], ou[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float gg = __uint_as_float(e ? qa[j] & 0xffff0000u : qa[j] << 16);
+                const float u = __uint_as_float(e ? qb[j] & 0xffff0000u : qb[j] << 16);
+                const float y = __uint_as_float(e ? qd[j] & 0xffff0000u : qd[j] << 16);
+                const float s = __fdividef(1.f, 1.f + __expf(-gg));
+                og[e] = y * u * s * (1.f + gg * (1.f - s));
+                ou[e] = y * gg * s;
+            }
+            const __nv_bfloat162 x = __floats2bfloat162_rn(og[0], og[1]), z = __floats2bfloat162_rn(ou[0], ou[1]);
+            rg[j] = *reinterpret_cast<const uint32_t *>(&x);
+            ru[j] = *reinterpret_cast<const uint32_t *>(&z);
+        }
+        __stcs(dh + at, make_uint4(rg[0], rg[1], rg[2], rg[3]));
+        __stcs(dh + at + nv, make_uint4(ru[0], ru[1], ru[2], ru[3]));
+    }
+}
+
+// Block (row block, 128 columns): warp w holds rows 16 w .. 16 w + 15, lane l
+// columns 4 l .. 4 l + 3; 16 rows of a column are one 16-byte piece of the
+// transposed row.  The pieces pass through shared memory (chunk index XOR the
+// lane, so that 8 lanes hit 8 bank groups) to leave in whole 128-byte rows.
+__global__ void __launch_bounds__(256)
+k_quant_cols(const uint16_t *__restrict__ x, const int32_t *__restrict__ seg_off, uint8_t *q, float *scale, WsHeader *hdr,
+             int nseg, int64_t rows, int C, int64_t cap) {
+    __shared__ uint4 tile[128 * 8];
+    __shared__ float wmax[8][128];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b = blockIdx.x;
+    // the segment of padded block b
+    int seg = -1, first = 0, run = 0;
+    for (int i0 = 0; i0 < nseg && seg < 0; i0 += 32) {
+        const int i = i0 + lane;
+        int n = 0;
+        if (i < nseg) {
+            const int a = __ldg(seg_off + i), e = __ldg(seg_off + i + 1);
+            if (a < 0 || e < a || e > rows) set_error(hdr, TOPO_ESTATE);
+            else n = (e - a + 127) / 128;
+        }
+        int s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
+        }
+        const int lo = run + s - n;
+        const unsigned hit = __ballot_sync(0xffffffffu, b >= lo && b < lo + n);
+        if (hit) {
+            const int w = __ffs(hit) - 1;
+            seg = i0 + w;
+            first = __shfl_sync(0xffffffffu, lo, w);
+        }
+        run += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (seg < 0) return;                                          // past the last segment's blocks
+    const int r0 = __ldg(seg_off + seg) + (b - first) * 128;
+    const int nrow = min(128, __ldg(seg_off + seg + 1) - r0);
+    for (int c0 = blockIdx.y * 128; c0 < C; c0 += gridDim.y * 128) {
+        const int c = c0 + 4 * lane;
+        uint2 v[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int rr = 16 * warp + r;
+            v[r] = c < C && rr < nrow ? __ldcs(reinterpret_cast<const uint2 *>(x + (int64_t)(r0 + rr) * C + c)) : make_uint2(0, 0);
+        }
+        float m[4] = {0.f, 0.f, 0.f, 0.f};
+        float f[4][16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            f[0][r] = __uint_as_float(v[r].x << 16);
+            f[1][r] = __uint_as_float(v[r].x & 0xffff0000u);
+            f[2][r] = __uint_as_float(v[r].y << 16);
+            f[3][r] = __uint_as_float(v[r].y & 0xffff0000u);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            m[j] = amax16(f[j]);
+            wmax[warp][4 * lane + j] = m[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) a = fmaxf(a, wmax[w][4 * lane + j]);
+            float iv;
+            const float s = scale_of(a, iv);
+            tile[(4 * lane + j) * 8 + (warp ^ (lane & 7))] = quant16(f[j], iv);
+            if (warp == 0 && c + j < C) scale[(int64_t)b * C + c + j] = s;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = i * 256 + threadIdx.x, cc = e >> 3, ch = e & 7;
+            if (c0 + cc < C)
+                *reinterpret_cast<uint4 *>(q + (int64_t)(c0 + cc) * cap + (int64_t)b * 128 + 16 * ch) =
+                    tile[cc * 8 + (ch ^ ((cc >> 2) & 7))];
+        }
+        __syncthreads();
+    }
+}
+
+// One CTA per 128 x 128 block of a weight matrix [N][K].
+__global__ void __launch_bounds__(256)
+k_quant_weight(const uint16_t *__restrict__ w, uint8_t *q, float *scale, uint8_t *qt, float *scale_t, int N, int K) {
+    __shared__ float red[8];
+    __shared__ uint8_t tile[128][132];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int KB = (K + 127) / 128, NB = (N + 127) / 128;
+    const int kb = blockIdx.x, nb = blockIdx.y;
+    const int64_t base = (int64_t)blockIdx.z * N * K;
+    const int k = kb * 128 + 4 * lane;
+    uint2 v[16];
+    float m = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int n = nb * 128 + 16 * warp + r;
+        v[r] = n < N && k < K ? __ldcs(reinterpret_cast<const uint2 *>(w + base + (int64_t)n * K + k)) : make_uint2(0, 0);
+        const uint32_t p[4] = {v[r].x << 16, v[r].x & 0xffff0000u, v[r].y << 16, v[r].y & 0xffff0000u};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float f = __uint_as_float(p[j]);
+            if (finite(f)) m = fmaxf(m, fabsf(f));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, red[i]);
+    float iv;
+    const float s = scale_of(m, iv);
+    if (threadIdx.x == 0) {
+        scale[((int64_t)blockIdx.z * NB + nb) * KB + kb] = s;
+        if (scale_t) scale_t[((int64_t)blockIdx.z * KB + kb) * NB + nb] = s;
+    }
+    const float nan = __int_as_float(0x7fffffff);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int n = nb * 128 + 16 * warp + r;
+        float f[4] = {__uint_as_float(v[r].x << 16), __uint_as_float(v[r].x & 0xffff0000u),
+                      __uint_as_float(v[r].y << 16), __uint_as_float(v[r].y & 0xffff0000u)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (!finite(f[j])) f[j] = nan;
+        const uint32_t e = cvt2(f[0] * iv, f[1] * iv) | (cvt2(f[2] * iv, f[3] * iv) << 16);
+        if (n < N && k < K) *reinterpret_cast<uint32_t *>(q + base + (int64_t)n * K + k) = e;
+        *reinterpret_cast<uint32_t *>(&tile[16 * warp + r][4 * lane]) = e;
+    }
+    if (!qt) return;
+    __syncthreads();
+    const int n = nb * 128 + 4 * lane;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int kk = 16 * warp + r;
+        uint32_t e = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e |= (uint32_t)tile[4 * lane + j][kk] << (8 * j);
+        if (kb * 128 + kk < K && n < N) *reinterpret_cast<uint32_t *>(qt + base + (int64_t)(kb * 128 + kk) * N + n) = e;
+    }
+}
+
+template <int SRC>
+cudaError_t run_rows(QuantArgs a, cudaStream_t st) {
+    if (a.rows == 0) return cudaSuccess;
+    const int chunks = (a.nv + 31) / 32;
+    // few rows: a row's 512-value chunks go to warps of their own
+    a.per = a.rows * chunks <= 152 * 64 ? 1 : chunks;
+    a.parts = (chunks + a.per - 1) / a.per;
+    const int64_t units = a.rows * a.parts;
+    k_quant_rows<SRC><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(int64_t rows, int C, const uint16_t *x, uint8_t *q, float *scale, bool swiglu,
+                                 cudaStream_t st) {
+    QuantArgs a = {};
+    a.x = reinterpret_cast<const uint4 *>(x);
+    a.q = reinterpret_cast<uint4 *>(q);
+    a.scale = scale;
+    a.rows = rows;
+    a.nv = C / 16;
+    a.KB = (C + 127) / 128;
+    return swiglu ? run_rows<kSwiglu>(a, st) : run_rows<kPlain>(a, st);
+}
+
+cudaError_t launch_permute_quantize(const Geo &g, int H, const uint16_t *x, const int32_t *sorted, uint8_t *q, float *scale,
+                                    void *ws, cudaStream_t st) {
+    cudaError_t e;
+    if ((e = launch_invert(g, sorted, ws, st)) != cudaSuccess) return e;
+    QuantArgs a = {};
+    a.x = reinterpret_cast<const uint4 *>(x);
+    a.inv = ws_at<int32_t>(ws, g.off_pack_inv);
+    a.q = reinterpret_cast<uint4 *>(q);
+    a.scale = scale;
+    a.hdr = ws_at<WsHeader>(ws, 0);
+    a.rows = (int64_t)g.L * g.T;
+    a.npairs = g.npairs;
+    a.T = g.T;
+    a.k = g.k;
+    a.nv = H / 16;
+    a.KB = (H + 127) / 128;
+    return run_rows<kDispatch>(a, st);
+}
+
+cudaError_t launch_quantize_cols(int nseg, int64_t rows, int C, const uint16_t *x, const int32_t *seg_off, int64_t cap,
+                                 uint8_t *q, float *scale, void *ws, cudaStream_t st) {
+    const int64_t blocks = cap / 128;
+    const int cb = (C + 127) / 128;
+    const int split = (int)(blocks >= 152 * 8 ? (cb + 3) / 4 : cb);
+    k_quant_cols<<<dim3((unsigned)blocks, (unsigned)split), 256, 0, st>>>(x, seg_off, q, scale, ws_at<WsHeader>(ws, 0), nseg,
+                                                                         rows, C, cap);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_quantize_weight(int n_w, int N, int K, const uint16_t *w, uint8_t *q, float *scale, uint8_t *qt,
+                                   float *scale_t, cudaStream_t st) {
+    const unsigned KB = (unsigned)((K + 127) / 128), NB = (unsigned)((N + 127) / 128);
+    for (int z = 0; z < n_w; z += 65535) {
+        const int n = n_w - z < 65535 ? n_w - z : 65535;
+        const int64_t o = (int64_t)z * N * K, os = (int64_t)z * NB * KB;
+        k_quant_weight<<<dim3(KB, NB, (unsigned)n), 256, 0, st>>>(w + o, q + o, scale + os, qt ? qt + o : nullptr,
+                                                                  scale_t ? scale_t + os : nullptr, N, K);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_swiglu_grad(int64_t rows, int I, const uint16_t *h, const uint16_t *dy, uint16_t *dh, cudaStream_t st) {
+    const int nv = I / 8;
+    const int64_t n = rows * nv;
+    if (n == 0) return cudaSuccess;
+    const int64_t want = (n + 255) / 256;
+    k_swiglu_grad<<<(unsigned)(want < 152 * 32 ? want : 152 * 32), 256, 0, st>>>(
+        reinterpret_cast<const uint4 *>(h), reinterpret_cast<const uint4 *>(dy), reinterpret_cast<uint4 *>(dh), n, nv);
+    return cudaGetLastError();
+}
+
+}  // namespace topo

@@ -2,6 +2,7 @@
 #include <cuda_runtime.h>
 
 #include <climits>
+#include <cmath>
 #include <cstddef>
 #include <cstring>
 #include <map>
@@ -188,6 +189,34 @@ int pack_args(const topo_cfg *cfg, int32_t n_layers, int32_t H, const void *in, 
     if (!in || !sorted || !out) return TOPO_EINVAL;
     if (((uintptr_t)in | (uintptr_t)out) & 15) return TOPO_EINVAL;
     return TOPO_OK;
+}
+
+// Options of topo_route / topo_route_grad for this geometry.
+bool route_opts_ok(const topo_route_opts *o, const Geo &g) {
+    if (!o || (o->score != TOPO_SCORE_SOFTMAX && o->score != TOPO_SCORE_SIGMOID)) return false;
+    if (g.E > TOPO_GATE_MAX_E || o->n_group < 1 || o->n_group > TOPO_ROUTE_MAX_GROUPS || g.E % o->n_group) return false;
+    if (o->topk_group < 1 || o->topk_group > o->n_group) return false;
+    const int size = g.E / o->n_group;
+    if (o->group_top < 1 || o->group_top > 2 || o->group_top > size || g.k > o->topk_group * size) return false;
+    return std::isfinite(o->scale);
+}
+
+// A logits array of the given type and float32 / int32 arrays beside it.
+int logits_ok(int32_t dtype, const void *logits, const void *a, const void *b, const void *c) {
+    if (dtype != TOPO_DTYPE_F32 && dtype != TOPO_DTYPE_BF16) return TOPO_EINVAL;
+    if ((uintptr_t)logits % (dtype == TOPO_DTYPE_BF16 ? 2 : 4)) return TOPO_EINVAL;
+    if (((uintptr_t)a | (uintptr_t)b | (uintptr_t)c) % 4) return TOPO_EINVAL;
+    return TOPO_OK;
+}
+
+bool aligned16(const void *a, const void *b) { return (((uintptr_t)a | (uintptr_t)b) & 15) == 0; }
+
+bool rows_ok(int64_t rows, int32_t C) { return rows >= 0 && rows <= INT32_MAX && C >= 16 && C % 16 == 0 && C <= (1 << 24); }
+
+bool product_dims_ok(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, int32_t K) {
+    if (n_seg < 0 || rows < 0 || rows > INT32_MAX || n_w < 0 || N < 16 || K < 16 || N % 16 || K % 16) return false;
+    if (N > (1 << 24) || K > (1 << 24)) return false;
+    return (int64_t)n_w * N <= INT32_MAX && (int64_t)n_w * K <= INT32_MAX;
 }
 
 }  // namespace
@@ -379,6 +408,138 @@ int topo_combine(const topo_cfg *cfg, int32_t n_layers, int32_t H, const uint16_
     if (rc || n_layers == 0 || g.npairs == 0) return rc;
     if (!w) return TOPO_EINVAL;
     return cuda_rc(launch_combine(g, H, y, sorted_pairs, w, out, ws, stream));
+}
+
+int topo_route(const topo_cfg *cfg, int32_t n_layers, const topo_route_opts *opts, const void *logits,
+               int32_t logits_dtype, const float *bias, int32_t *ids, float *weights, int32_t *hist,
+               void *ws, size_t ws_bytes, cudaStream_t stream) {
+    Geo g;
+    int rc = make_geo(cfg, n_layers, &g);
+    if (rc) return rc;
+    if (!route_opts_ok(opts, g) || !ws) return TOPO_EINVAL;
+    if ((rc = logits_ok(logits_dtype, logits, bias, ids, weights)) != TOPO_OK) return rc;
+    const int64_t ntok = (int64_t)n_layers * g.T;
+    if (ntok > 0 && (!logits || !ids || !weights)) return TOPO_EINVAL;
+    if (ws_bytes < (hist ? g.total : sizeof(WsHeader))) return TOPO_ENOSPC;
+    if (n_layers == 0) return TOPO_OK;
+    cudaError_t e = launch_route(*opts, ntok, g.E, g.k, logits, logits_dtype == TOPO_DTYPE_BF16, bias, ids, weights, stream);
+    if (e == cudaSuccess && hist) {
+        bind_ws(g, ws);
+        e = launch_hist(g, ids, hist, ws, hist_fingerprint(g, ids), stream);
+    }
+    return cuda_rc(e);
+}
+
+int topo_route_grad(const topo_cfg *cfg, int32_t n_layers, const topo_route_opts *opts, const void *logits,
+                    int32_t logits_dtype, const int32_t *ids, const float *grad_weights, void *grad_logits,
+                    void *ws, size_t ws_bytes, cudaStream_t stream) {
+    Geo g;
+    int rc = make_geo(cfg, n_layers, &g);
+    if (rc) return rc;
+    if (!route_opts_ok(opts, g) || !ws) return TOPO_EINVAL;
+    if ((rc = logits_ok(logits_dtype, logits, grad_weights, ids, nullptr)) != TOPO_OK) return rc;
+    if ((rc = logits_ok(logits_dtype, grad_logits, nullptr, nullptr, nullptr)) != TOPO_OK) return rc;
+    const int64_t ntok = (int64_t)n_layers * g.T;
+    if (ntok > 0 && (!logits || !ids || !grad_weights || !grad_logits)) return TOPO_EINVAL;
+    if (ws_bytes < sizeof(WsHeader)) return TOPO_ENOSPC;
+    return cuda_rc(launch_route_grad(*opts, ntok, g.E, g.k, logits, logits_dtype == TOPO_DTYPE_BF16, ids, grad_weights,
+                                     grad_logits, ws, stream));
+}
+
+int topo_permute_quantize(const topo_cfg *cfg, int32_t n_layers, int32_t H, const uint16_t *x,
+                          const int32_t *sorted_pairs, uint8_t *q, float *scale, void *ws, size_t ws_bytes,
+                          cudaStream_t stream) {
+    Geo g;
+    if (H % 16) return TOPO_EINVAL;
+    const int rc = pack_args(cfg, n_layers, H, x, sorted_pairs, q, ws, ws_bytes, &g);
+    if (rc || n_layers == 0 || g.npairs == 0) return rc;
+    if (!scale || ((uintptr_t)scale & 3)) return TOPO_EINVAL;
+    return cuda_rc(launch_permute_quantize(g, H, x, sorted_pairs, q, scale, ws, stream));
+}
+
+int topo_quantize_rows(int64_t rows, int32_t C, const uint16_t *x, uint8_t *q, float *scale, cudaStream_t stream) {
+    if (!rows_ok(rows, C)) return TOPO_EINVAL;
+    if (rows == 0) return TOPO_OK;
+    if (!x || !q || !scale || !aligned16(x, q) || ((uintptr_t)scale & 3)) return TOPO_EINVAL;
+    return cuda_rc(launch_quantize_rows(rows, C, x, q, scale, false, stream));
+}
+
+int topo_swiglu_quantize(int64_t rows, int32_t I, const uint16_t *h, uint8_t *q, float *scale, cudaStream_t stream) {
+    if (!rows_ok(rows, I)) return TOPO_EINVAL;
+    if (rows == 0) return TOPO_OK;
+    if (!h || !q || !scale || !aligned16(h, q) || ((uintptr_t)scale & 3)) return TOPO_EINVAL;
+    return cuda_rc(launch_quantize_rows(rows, I, h, q, scale, true, stream));
+}
+
+int topo_swiglu_grad(int64_t rows, int32_t I, const uint16_t *h, const uint16_t *dy, uint16_t *dh,
+                     cudaStream_t stream) {
+    if (!rows_ok(rows, I)) return TOPO_EINVAL;
+    if (rows == 0) return TOPO_OK;
+    if (!h || !dy || !dh || !aligned16(h, dy) || !aligned16(dh, dh)) return TOPO_EINVAL;
+    return cuda_rc(launch_swiglu_grad(rows, I, h, dy, dh, stream));
+}
+
+int topo_quantize_weight(int32_t n_w, int32_t N, int32_t K, const uint16_t *w, uint8_t *q, float *scale,
+                         uint8_t *qt, float *scale_t, cudaStream_t stream) {
+    if (!product_dims_ok(n_w, 0, n_w, N, K)) return TOPO_EINVAL;
+    if (!qt != !scale_t) return TOPO_EINVAL;
+    if (n_w == 0) return TOPO_OK;
+    if (!w || !q || !scale || !aligned16(w, q) || !aligned16(qt, qt) || (((uintptr_t)scale | (uintptr_t)scale_t) & 3))
+        return TOPO_EINVAL;
+    return cuda_rc(launch_quantize_weight(n_w, N, K, w, q, scale, qt, scale_t, stream));
+}
+
+int64_t topo_cols_capacity(int32_t n_seg, int64_t rows) {
+    if (n_seg < 0 || rows < 0 || rows > INT32_MAX) return 0;
+    // ceil(l_i / 128) blocks for each segment that holds a row
+    const int64_t held = rows < n_seg ? rows : n_seg;
+    const int64_t blocks = (rows + 127 * held) / TOPO_BLOCK;
+    return (blocks < 1 ? 1 : blocks) * TOPO_BLOCK;
+}
+
+int topo_quantize_cols(int32_t n_seg, int64_t rows, int32_t C, const uint16_t *x, const int32_t *seg_off,
+                       int64_t cap, uint8_t *q, float *scale, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (n_seg < 0 || !rows_ok(rows, C) || !ws) return TOPO_EINVAL;
+    if (cap != topo_cols_capacity(n_seg, rows)) return TOPO_EINVAL;
+    if (ws_bytes < sizeof(WsHeader)) return TOPO_ENOSPC;
+    if (n_seg == 0 || rows == 0) return TOPO_OK;
+    if (!x || !seg_off || !q || !scale || !aligned16(x, q) || (((uintptr_t)scale | (uintptr_t)seg_off) & 3))
+        return TOPO_EINVAL;
+    return cuda_rc(launch_quantize_cols(n_seg, rows, C, x, seg_off, cap, q, scale, ws, stream));
+}
+
+size_t topo_expert_workspace_bytes(int32_t n_seg, int64_t rows, int32_t N, int32_t K) {
+    if (!product_dims_ok(n_seg, rows, 1, N, K)) return 0;
+    return sizeof(WsHeader);
+}
+
+int topo_expert_gemm(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, int32_t K, const uint8_t *a,
+                     const float *a_scale, const int32_t *seg_off, const int32_t *seg_w, const uint8_t *w,
+                     const float *w_scale, void *out, int32_t out_dtype, void *ws, size_t ws_bytes,
+                     cudaStream_t stream) {
+    if (!product_dims_ok(n_seg, rows, n_w, N, K) || !ws) return TOPO_EINVAL;
+    if (out_dtype != TOPO_DTYPE_F32 && out_dtype != TOPO_DTYPE_BF16) return TOPO_EINVAL;
+    if (!seg_w && n_seg > n_w) return TOPO_EINVAL;
+    if (ws_bytes < topo_expert_workspace_bytes(n_seg, rows, N, K)) return TOPO_ENOSPC;
+    if (n_seg == 0 || rows == 0) return TOPO_OK;
+    if (n_w == 0 || !a || !a_scale || !seg_off || !w || !w_scale || !out || !aligned16(a, w) || !aligned16(out, out) ||
+        (((uintptr_t)a_scale | (uintptr_t)w_scale | (uintptr_t)seg_off | (uintptr_t)seg_w) & 3))
+        return TOPO_EINVAL;
+    return cuda_rc(launch_expert_gemm(n_seg, rows, n_w, N, K, a, a_scale, seg_off, seg_w, w, w_scale, out,
+                                      out_dtype == TOPO_DTYPE_BF16, ws, stream));
+}
+
+int topo_expert_wgrad(int32_t n_seg, int64_t rows, int32_t N, int32_t K, int64_t cap, const uint8_t *dy,
+                      const float *dy_scale, const uint8_t *x, const float *x_scale, const int32_t *seg_off,
+                      float *dw, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (!product_dims_ok(n_seg, rows, 1, N, K) || !ws) return TOPO_EINVAL;
+    if (cap != topo_cols_capacity(n_seg, rows)) return TOPO_EINVAL;
+    if (ws_bytes < topo_expert_workspace_bytes(n_seg, rows, N, K)) return TOPO_ENOSPC;
+    if (n_seg == 0) return TOPO_OK;
+    if (!dy || !dy_scale || !x || !x_scale || !seg_off || !dw || !aligned16(dy, x) || !aligned16(dw, dw) ||
+        (((uintptr_t)dy_scale | (uintptr_t)x_scale | (uintptr_t)seg_off) & 3))
+        return TOPO_EINVAL;
+    return cuda_rc(launch_expert_wgrad(n_seg, rows, N, K, cap, dy, dy_scale, x, x_scale, seg_off, dw, ws, stream));
 }
 
 int topo_read_error(const void *ws) {
