@@ -41,7 +41,8 @@ constexpr int kKB = 128;                          // contraction values of a blo
 constexpr int kTileM = 128;
 constexpr int kTileN = 256;
 constexpr int kSumWarps = 8;                      // warps that scale, add and store
-constexpr int kThreads = (kSumWarps + 2) * 32;
+constexpr int kThreads = (kSumWarps + 4) * 32;    // two summing warpgroups, one of producer, issuer and two idle warps
+constexpr int kSumRegs = 224, kIoRegs = 56;       // 2 * 128 * 224 + 128 * 56 = 384 * 168, the launch's share
 constexpr int kTmemCols = 512;                    // two accumulators of 256 columns
 constexpr uint32_t kABytes = kTileM * kKB;
 constexpr int kMaxStages = 10;
@@ -135,6 +136,34 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// acc[c] += scale * D[row][c] for the first 32 * NC columns of this half: 32
+// columns are read while the 32 before them are added.  Columns past the
+// tile's hold whatever the accumulator held; they are never stored.
+template <int MODE, int NC>
+__device__ __forceinline__ void add_block(float2 (&acc)[64], uint32_t ta, float r, const float *cs) {
+    const float2 rr = make_float2(r, r);
+    uint32_t v[2][32];
+    tc::tmem_ld(ta, v[0]);
+    tc::tmem_wait(v[0]);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        if (c + 1 < NC) tc::tmem_ld(ta + 32 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 p = make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1]));
+            float2 &d = acc[16 * c + i];
+            if (MODE == kRowsM) {
+                tc::fma2(d, p, rr);
+            } else {
+                const float2 k2 = *reinterpret_cast<const float2 *>(cs + 32 * c + 2 * i);
+                if (MODE == kRowsN) tc::fma2(d, p, k2);
+                else tc::fma2(d, tc::mul2(p, k2), rr);
+            }
+        }
+        if (c + 1 < NC) tc::tmem_wait(v[(c + 1) & 1]);
+    }
+}
+
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 k_experts(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, GemmArgs g) {
@@ -224,6 +253,8 @@ k_experts(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
     const uint32_t tmem = tmem_slot;
     const int ntiles = tp[g.nseg];
 
+    if (warp >= kSumWarps) {
+        tc::regs_dec<kIoRegs>();
     if (warp == kSumWarps) {
         // ------------------------------------------------------------- producer
         if (lane == 0) {
@@ -294,7 +325,9 @@ k_experts(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
             if (!tc::mbar_wait(&drained, 0)) ok = false;
             if (!ok) atomicExch(&expired, 1);
         }
+    }
     } else {
+        tc::regs_inc<kSumRegs>();
         // --------------------------------------------------- scale, add and store
         const int half = warp >> 2;                      // columns 128 * half ..
         const int row = (warp & 3) * 32 + lane;          // row of the tile
@@ -321,42 +354,41 @@ k_experts(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
                 rs = row < q.mlim ? g.a_scale + (int64_t)q.kb0 * g.N + q.m0 + row : nullptr;
                 cl = c0 + row < q.nlim ? g.b_scale + (int64_t)q.kb0 * g.K + q.n0 + c0 + row : nullptr;
             }
+            // the next block's scales are on their way while this block is summed
+            float rn = 0.f, cn = 0.f, wn = 0.f;
+            auto fetch = [&](int kb) {
+                if (MODE == kRowsM) {
+                    rn = rs ? __ldg(rs + kb) : 0.f;
+                    wn = __ldg(wsc + kb);
+                } else if (MODE == kRowsN) {
+                    cn = cl ? __ldg(cl + kb) : 0.f;
+                    wn = __ldg(wsc + kb);
+                } else {
+                    rn = rs ? __ldg(rs + (int64_t)kb * g.N) : 0.f;
+                    cn = cl ? __ldg(cl + (int64_t)kb * g.K) : 0.f;
+                }
+            };
+            if (q.nkb > 0) fetch(0);
             for (int kb = 0; kb < q.nkb; ++kb, ++it) {
                 const int b = it & 1;
-                float r = 0.f;
-                if (MODE == kRowsM) {
-                    r = (rs ? __ldg(rs + kb) : 0.f) * __ldg(wsc + kb);
-                } else if (MODE == kRowsN) {
-                    cs[b][half][row] = (cl ? __ldg(cl + kb) : 0.f) * __ldg(wsc + kb);
-                } else {
-                    r = rs ? __ldg(rs + (int64_t)kb * g.N) : 0.f;
-                    cs[b][half][row] = cl ? __ldg(cl + (int64_t)kb * g.K) : 0.f;
+                const float r = MODE == kRowsM ? rn * wn : rn;
+                if (MODE != kRowsM) {
+                    cs[b][half][row] = MODE == kRowsN ? cn * wn : cn;
+                    tc::bar_sync(1 + half, 128);
                 }
-                if (MODE != kRowsM) tc::bar_sync(1 + half, 128);
+                if (kb + 1 < q.nkb) fetch(kb + 1);
                 if (ok && !tc::mbar_wait(&acc_full[b], (uint32_t)(it >> 1) & 1u)) ok = false;
                 ok = __all_sync(0xffffffffu, ok);
                 tc::fence_after();
                 if (ok) {
                     const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(b * kTileN + c0);
-                    const float2 rr = make_float2(r, r);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        if (16 * c < ncol) {
-                            uint32_t v[16];
-                            tc::tmem_ld16(ta + 16 * c, v);
-                            tc::tmem_wait(v);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float2 p = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                                if (MODE == kRowsM) {
-                                    tc::fma2(acc[8 * c + i], p, rr);
-                                } else {
-                                    const float2 k2 = *reinterpret_cast<const float2 *>(&cs[b][half][16 * c + 2 * i]);
-                                    if (MODE == kRowsN) tc::fma2(acc[8 * c + i], p, k2);
-                                    else tc::fma2(acc[8 * c + i], tc::mul2(p, k2), rr);
-                                }
-                            }
-                        }
+                    const float *k2 = cs[b][half];
+                    if (MODE == kRowsN) {
+                        if (ncol > 64) add_block<MODE, 4>(acc, ta, r, k2);
+                        else if (ncol > 32) add_block<MODE, 2>(acc, ta, r, k2);
+                        else if (ncol > 0) add_block<MODE, 1>(acc, ta, r, k2);
+                    } else if (ncol > 0) {
+                        add_block<MODE, 4>(acc, ta, r, k2);
                     }
                 }
                 tc::fence_before();
