@@ -41,7 +41,7 @@
 namespace topo {
 namespace {
 
-enum { kTokM = 0, kTokN = 1, kGrad = 2 };         // see above
+enum { kProduct = 0, kGrad = 1 };
 
 constexpr int kKB = 128;                          // contraction values of a block: one 128-byte swizzle row
 constexpr int kTileM = 128;                       // rows of a CTA
@@ -51,7 +51,7 @@ constexpr int kThreads = (kSumWarps + 4) * 32;    // two summing warpgroups, one
 // registers of a thread of the summing and of the other warpgroup; 2 * 128 times
 // the one and 128 times the other are the launch's 384 * 168
 template <int MODE>
-constexpr int kSumRegs = MODE == kTokM ? 224 : 216;
+constexpr int kSumRegs = MODE == kProduct ? 224 : 216;
 template <int MODE>
 constexpr int kIoRegs = (384 * 168 - 256 * kSumRegs<MODE>) / 128;
 constexpr int kTmemCols = 512;                    // two accumulators of 256 columns
@@ -94,7 +94,7 @@ struct Tile {
 
 template <int MODE, int CG>
 __device__ __forceinline__ int tiles_of(const GemmArgs &g, int len) {
-    const int m = MODE == kTokM ? len : g.N, n = MODE == kTokM ? g.N : MODE == kTokN ? len : g.K;
+    const int m = MODE == kProduct ? len : g.N, n = MODE == kProduct ? g.N : g.K;
     return ((m + CG * kTileM - 1) / (CG * kTileM)) * ((n + g.nt - 1) / g.nt);
 }
 
@@ -112,24 +112,14 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs &g, const int *tp, cons
     Tile r;
     r.seg = lo;
     const int loc = t - tp[lo], len = so[lo + 1] - so[lo];
-    const int me = MODE == kTokM ? len : g.N, ne = MODE == kTokM ? g.N : MODE == kTokN ? len : g.K;
-    int m, n;
-    if (MODE == kTokM) {
-        const int nm = (me + CG * kTileM - 1) / (CG * kTileM);
-        n = loc / nm;
-        m = loc - n * nm;
-    } else {
-        const int nn = (ne + g.nt - 1) / g.nt;
-        m = loc / nn;
-        n = loc - m * nn;
-    }
+    const int me = MODE == kProduct ? len : g.N, ne = MODE == kProduct ? g.N : g.K;
+    const int nm = (me + CG * kTileM - 1) / (CG * kTileM), n = loc / nm, m = loc - n * nm;
     r.w = MODE == kGrad ? 0 : g.seg_w ? __ldg(g.seg_w + lo) : g.seg0 + lo;
     r.m0 = m * CG * kTileM;
     r.mlim = min(CG * kTileM, me - r.m0);
     r.n0 = n * g.nt;
     r.nlim = min(g.nt, ne - r.n0);
-    if (MODE == kTokM) r.m0 += so[lo];
-    if (MODE == kTokN) r.n0 += so[lo];
+    if (MODE == kProduct) r.m0 += so[lo];
     r.ncols = (r.nlim + 16 * CG - 1) & ~(16 * CG - 1);
     r.kb0 = MODE == kGrad ? pad[lo] : 0;
     r.nkb = MODE == kGrad ? pad[lo + 1] - pad[lo] : g.KB;
@@ -145,12 +135,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float2 v) {
     return *reinterpret_cast<const uint32_t *>(&b);
 }
 
-// Sums of a thread.  kTokM: acc[i] holds columns 2 i and 2 i + 1 of row `lane`.
-// kTokN, kGrad: acc[(h * 16 + j) * 2 + r] holds columns 8 j + 2 (lane % 4) and the
+// Sums of a thread.  kProduct: acc[i] holds columns 2 i and 2 i + 1 of row `lane`.
+// kGrad: acc[(h * 16 + j) * 2 + r] holds columns 8 j + 2 (lane % 4) and the
 // next of row 16 h + 8 r + lane / 4.
 using Acc = float2[64];
 
-// kTokM: acc += s * block, 128 columns of this thread's row.  32 columns are
+// kProduct: acc += s * block, 128 columns of this thread's row.  32 columns are
 // read while the 32 before them are added.
 __device__ __forceinline__ void add_rows(Acc &acc, uint32_t ta, float s) {
     const float2 s2 = make_float2(s, s);
@@ -167,10 +157,10 @@ __device__ __forceinline__ void add_rows(Acc &acc, uint32_t ta, float s) {
     }
 }
 
-// kTokN, kGrad: acc += scales * block for NJ groups of 8 columns from group J0.
-// cs: the columns' scales in the order a lane takes them, 4 (two groups) per 16
-// bytes; rs: the rows' scales (gradient).
-template <int MODE, int J0, int NJ>
+// kGrad: acc += scales * block for NJ groups of 8 columns from group J0.  cs: the
+// columns' scales in the order a lane takes them, 4 (two groups) per 16 bytes;
+// rs: the rows' scales.
+template <int J0, int NJ>
 __device__ __forceinline__ void add_cols(Acc &acc, int h, const uint32_t (&v)[4 * NJ], const float *cs, const float (&rs)[4]) {
 #pragma unroll
     for (int jj = 0; jj < NJ; jj += 2) {
@@ -182,47 +172,28 @@ __device__ __forceinline__ void add_cols(Acc &acc, int h, const uint32_t (&v)[4 
             for (int r = 0; r < 2; ++r) {
                 const int i = 4 * (jj + u) + 2 * r;
                 const float2 p = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                float2 &d = acc[(h * 16 + J0 + jj + u) * 2 + r];
-                if (MODE == kGrad) tc::fma2(d, tc::mul2(p, k2), make_float2(rs[2 * h + r], rs[2 * h + r]));
-                else tc::fma2(d, p, k2);
+                tc::fma2(acc[(h * 16 + J0 + jj + u) * 2 + r], tc::mul2(p, k2), make_float2(rs[2 * h + r], rs[2 * h + r]));
             }
         }
     }
 }
 
-// 128 columns (64 at a time), 64 or 32: the next piece is read while the one
-// before it is added.  Columns past the tile's hold whatever the accumulator
-// held; they are never stored.
-template <int MODE>
-__device__ __forceinline__ void add_block(Acc &acc, uint32_t ta, int ncol, const float *cs, const float (&rs)[4]) {
+// kGrad: 128 columns, 16 rows x 64 columns read while the ones before are added.
+__device__ __forceinline__ void add_block(Acc &acc, uint32_t ta, const float *cs, const float (&rs)[4]) {
     constexpr uint32_t kRow16 = 16u << 16;
-    if (ncol > 32) {
-        uint32_t a[32], b[32];
-        tc::tmem_ld(ta, a);
-        tc::tmem_wait(a);
-        tc::tmem_ld(ta + kRow16, b);
-        add_cols<MODE, 0, 8>(acc, 0, a, cs, rs);
-        tc::tmem_wait(b);
-        if (ncol > 64) {
-            tc::tmem_ld(ta + 64, a);
-            add_cols<MODE, 0, 8>(acc, 1, b, cs, rs);
-            tc::tmem_wait(a);
-            tc::tmem_ld(ta + 64 + kRow16, b);
-            add_cols<MODE, 8, 8>(acc, 0, a, cs, rs);
-            tc::tmem_wait(b);
-            add_cols<MODE, 8, 8>(acc, 1, b, cs, rs);
-        } else {
-            add_cols<MODE, 0, 8>(acc, 1, b, cs, rs);
-        }
-    } else {
-        uint32_t a[16], b[16];
-        tc::tmem_ld(ta, a);
-        tc::tmem_ld(ta + kRow16, b);
-        tc::tmem_wait(a);
-        tc::tmem_wait(b);
-        add_cols<MODE, 0, 4>(acc, 0, a, cs, rs);
-        add_cols<MODE, 0, 4>(acc, 1, b, cs, rs);
-    }
+    uint32_t a[32], b[32];
+    tc::tmem_ld(ta, a);
+    tc::tmem_wait(a);
+    tc::tmem_ld(ta + kRow16, b);
+    add_cols<0, 8>(acc, 0, a, cs, rs);
+    tc::tmem_wait(b);
+    tc::tmem_ld(ta + 64, a);
+    add_cols<0, 8>(acc, 1, b, cs, rs);
+    tc::tmem_wait(a);
+    tc::tmem_ld(ta + 64 + kRow16, b);
+    add_cols<8, 8>(acc, 0, a, cs, rs);
+    tc::tmem_wait(b);
+    add_cols<8, 8>(acc, 1, b, cs, rs);
 }
 
 template <int MODE, int CG>
@@ -233,7 +204,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     __shared__ uint32_t tmem_slot;
     __shared__ int expired;
     __shared__ int so[kSegCap + 1], tp[kSegCap + 1], pad[MODE == kGrad ? kSegCap + 1 : 1];
-    __shared__ __align__(16) float cs[2][kScaleKB][kTileN];    // scales of the columns, see scale_at; kTokM: of the
+    __shared__ __align__(16) float cs[2][kScaleKB][kTileN];    // scales of the columns, see scale_at; kProduct: of the
                                                                // rows, times each half's weight scale
     __shared__ float rsc[MODE == kGrad ? 2 : 1][kScaleKB][kTileM];      // gradient: scales of the rows
     __shared__ __align__(128) unsigned char outs[MODE == kGrad ? 16 : kSumWarps * kStageOut];
@@ -331,9 +302,9 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             bool ok = true;
             for (int t = first; t < ntiles && ok; t += step) {
                 const Tile q = find_tile<MODE, CG>(g, tp, so, pad, t);
-                const int ym = (MODE == kTokN ? q.w * g.N : 0) + q.m0 + (int)rank * kTileM;
+                const int ym = q.m0 + (int)rank * kTileM;
                 const int nh = q.ncols / CG;                                // this CTA's columns
-                const int yn = (MODE == kTokM ? q.w * g.N : 0) + q.n0 + (int)rank * nh;
+                const int yn = (MODE == kProduct ? q.w * g.N : 0) + q.n0 + (int)rank * nh;
                 const int boxes = (nh + g.box - 1) / g.box;
                 const uint32_t bytes = CG * (kABytes + (uint32_t)(boxes * g.box) * kKB);
                 for (int kb = 0; kb < q.nkb; ++kb) {
@@ -416,13 +387,13 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 const int m1 = q.m0 + (int)rank * kTileM;
                 for (int kb = 0; kb < q.nkb; kb += kScaleKB, ++gi) {
                     const int slot = gi & 1, nk = min(kScaleKB, q.nkb - kb);
-                    constexpr int kCols = MODE == kTokM ? kTileM / 64 : kTileN / 64;
+                    constexpr int kCols = MODE == kProduct ? kTileM / 64 : kTileN / 64;
                     float v[kCols][kScaleKB], w[2][kScaleKB], r[2][kScaleKB];
                     if (MODE != kGrad) {
-                        // weight scales of this CTA's rows, or of the two halves of the columns
+                        // weight scales of the two halves of the columns
 #pragma unroll
-                        for (int h = 0; h < (MODE == kTokM ? 2 : 1); ++h) {
-                            const int nb = min((MODE == kTokM ? q.n0 : m1) / 128 + h, g.NB - 1);
+                        for (int h = 0; h < 2; ++h) {
+                            const int nb = min(q.n0 / 128 + h, g.NB - 1);
                             const float *wp = g.w_scale + ((int64_t)q.w * g.NB + nb) * g.KB + kb;
 #pragma unroll
                             for (int u = 0; u < kScaleKB; ++u) w[h][u] = u < nk ? __ldg(wp + u) : 0.f;
@@ -441,8 +412,8 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                                     if (u < nk) v[i][u] = __ldg(p + (int64_t)u * g.K);
                             }
                         } else {
-                            const bool in = MODE == kTokM ? (int)rank * kTileM + col < q.mlim : col < q.nlim;
-                            const float *p = g.x_scale + (int64_t)((MODE == kTokM ? m1 : q.n0) + col) * g.KB + kb;
+                            const bool in = (int)rank * kTileM + col < q.mlim;
+                            const float *p = g.x_scale + (int64_t)(m1 + col) * g.KB + kb;
                             if (in && g.vec_scale) {
                                 const float4 f = __ldg(reinterpret_cast<const float4 *>(p));
                                 v[i][0] = f.x;
@@ -473,11 +444,11 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
 #pragma unroll
                         for (int u = 0; u < kScaleKB; ++u) {
                             const int col = sl + 64 * i;
-                            if (MODE == kTokM) {
+                            if (MODE == kProduct) {
                                 cs[slot][u][col] = v[i][u] * w[0][u];
                                 cs[slot][u][128 + col] = v[i][u] * w[1][u];
                             } else {
-                                cs[slot][u][scale_at(col)] = MODE == kGrad ? v[i][u] : v[i][u] * w[0][u];
+                                cs[slot][u][scale_at(col)] = v[i][u];
                             }
                         }
                     if (MODE == kGrad) {
@@ -520,7 +491,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 const int b = it & 1, u = kb & (kScaleKB - 1), slot = gi & 1;
                 if (u == 0) tc::mbar_wait_or(&sc_full[slot], (uint32_t)(gi >> 1) & 1u, &expired);
                 float rs[4] = {1.f, 1.f, 1.f, 1.f};
-                if (MODE == kTokM) rs[0] = cs[slot][u][c0 + wq * 32 + lane];
+                if (MODE == kProduct) rs[0] = cs[slot][u][c0 + wq * 32 + lane];
                 if (MODE == kGrad) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) rs[i] = rsc[MODE == kGrad ? slot : 0][u][wq * 32 + 8 * i + r8];
@@ -530,8 +501,8 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 tc::fence_after();
                 const uint32_t ta = tmem + lanes + (uint32_t)(b * kTileN + c0);
                 if (ncol > 0) {
-                    if (MODE == kTokM) add_rows(acc, ta, rs[0]);
-                    else add_block<MODE>(acc, ta, ncol, &cs[slot][u][c0 + 4 * quad], rs);
+                    if (MODE == kProduct) add_rows(acc, ta, rs[0]);
+                    else add_block(acc, ta, &cs[slot][u][c0 + 4 * quad], rs);
                 }
                 tc::fence_before();
                 __syncwarp();
@@ -546,9 +517,8 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             // found again rather than kept in registers over the loop
             const Tile q = find_tile<MODE, CG>(g, tp, so, pad, t);
             const int m1 = (int)rank * kTileM + wq * 32;         // this warp's first row, from m0
-            if (MODE == kTokM) {
-                const bool out_bf16 = g.out_bf16;
-                if (out_bf16) {
+            if (MODE == kProduct) {
+                if (g.out_bf16) {
                     // 32 rows x 32 values at a time, turned through shared memory so that four
                     // lanes store 64 neighbouring bytes: 16-byte pieces, piece index XOR (row / 2)
                     unsigned char *w = outs + warp * kStageOut;
@@ -603,48 +573,6 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                             for (int j = 0; j < 16; ++j)
                                 if (c0 + 8 * j < q.nlim)
                                     *reinterpret_cast<float2 *>(o + (int64_t)(16 * h + 8 * r) * g.K + 8 * j) = acc[(h * 16 + j) * 2 + r];
-                        }
-            } else if (g.out_bf16) {
-                // 32 layout rows x 32 values at a time, turned through shared memory (as above)
-                unsigned char *w = outs + warp * kStageOut;
-                const int tok = lane & 7, piece = lane >> 3;
-                const uint32_t put = tc::smem_u32(w) + tok * 64 + ((piece ^ ((tok >> 1) & 3)) * 16);
-                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(g.out) + (int64_t)(q.n0 + c0 + r8) * g.N + q.m0 + m1 + 8 * quad;
-                const bool in = m1 + 8 * quad < q.mlim;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (32 * c < ncol) {
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int i = (4 * c + j) * 2;
-                            tc::store_trans4(put + j * 512, pack_bf16(acc[i]), pack_bf16(acc[i + 1]), pack_bf16(acc[32 + i]),
-                                             pack_bf16(acc[33 + i]));
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(w + (8 * i + r8) * 64 + ((quad ^ ((r8 >> 1) & 3)) * 16));
-                            const int n = 32 * c + 8 * i;
-                            if (in && c0 + n + r8 < q.nlim) *reinterpret_cast<uint4 *>(o + (int64_t)n * g.N) = v;
-                        }
-                    }
-                }
-            } else {
-                // eight lanes store 32 neighbouring bytes of a layout row
-                float *o = static_cast<float *>(g.out) + (int64_t)(q.n0 + c0 + 2 * quad) * g.N + q.m0 + m1 + r8;
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (c0 + 8 * j + 2 * quad + e < q.nlim) {
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int r = 0; r < 2; ++r)
-                                    if (m1 + 16 * h + 8 * r + r8 < q.mlim)
-                                        o[(int64_t)(8 * j + e) * g.N + 16 * h + 8 * r] =
-                                            e ? acc[(h * 16 + j) * 2 + r].y : acc[(h * 16 + j) * 2 + r].x;
                         }
             }
         }
@@ -737,17 +665,19 @@ cudaError_t launch_expert_gemm(int nseg, int64_t rows, int n_w, int N, int K, co
     g.NB = (N + 127) / 128;
     g.out_bf16 = bf16;
     g.vec_scale = g.KB % 4 == 0 && ((uintptr_t)a_scale & 15) == 0;
-    const int64_t avg = rows / nseg;
-    const bool tok_m = avg > 512, pair = avg > 64;
-    g.nt = pair ? 256 : avg > 16 ? 128 : 64;
-    g.box = tok_m ? kTileM : 16;
-    CUtensorMap mw, mx;
+    // A pair's tile of 256 rows wastes more of a short segment, and two CTAs move
+    // their weights with one TMA queue less; 64 experts of N = 2816, K = 4096, rows
+    // per expert, one CTA / a pair: 24: 146 / 179 us; 96: 171 / 185; 128: 191 / 201;
+    // 192: 239 / 218; 256: 299 / 254
+    const bool pair = rows / nseg > 144;
+    g.nt = kTileN;
+    g.box = kTileM;
+    CUtensorMap mx, mw;
     cudaError_t e;
+    if ((e = make_map(&mx, a, rows, K, kTileM)) != cudaSuccess) return e;
     if ((e = make_map(&mw, w, (int64_t)n_w * N, K, kTileM)) != cudaSuccess) return e;
-    if ((e = make_map(&mx, a, rows, K, g.box)) != cudaSuccess) return e;
-    if (tok_m) return run_experts<kTokM, 2>(g, nseg, seg_off, seg_w, mx, mw, st);
-    return pair ? run_experts<kTokN, 2>(g, nseg, seg_off, seg_w, mw, mx, st)
-                : run_experts<kTokN, 1>(g, nseg, seg_off, seg_w, mw, mx, st);
+    return pair ? run_experts<kProduct, 2>(g, nseg, seg_off, seg_w, mx, mw, st)
+                : run_experts<kProduct, 1>(g, nseg, seg_off, seg_w, mx, mw, st);
 }
 
 cudaError_t launch_expert_wgrad(int nseg, int64_t rows, int N, int K, int64_t cap, const uint8_t *dy, const float *dy_scale,
