@@ -11,11 +11,19 @@
 //   values go to the lower index, NaN ranks below every number
 //   weight_j = scale * s_j / sum s_j over the k chosen, or scale * s_j
 //
-// A group of G lanes per token, VPL scores to a lane.  The k-th largest of the
-// lanes' maxima bounds the k-th largest score from below, so the scores that
-// reach it are the only candidates, and a candidate's place is the number of
-// candidates above it; rows where that fails (few lanes, many ties, NaN) take
-// k rounds of an exact argmax.
+// A group of G lanes per token, VPL scores to a lane, each logit read once.
+// What decides the choice are the rounded c, but few of them matter, so the
+// sigmoid is first taken from the hardware's exp2 and reciprocal:
+//   - the k-th largest of the lanes' two largest values bounds the k-th largest
+//     value from below; what reaches it, less a margin for the approximation,
+//     is a candidate (a little more than k of them);
+//   - candidates are evaluated as defined and ranked by counting;
+//   - groups whose scores are closer than the margin, rows with NaN or
+//     infinities (where groups or the sigmoid are involved), many ties: the row
+//     is done again, every score as defined (exact_row).
+// The margin: exp2 of a rounded argument is off by |x| 2^-23 + 2^-22 relative,
+// times s (1 - s) <= 1/4 in s, below 2^-20 for every x; twice that and the
+// rounding of the sum with the bias stay below kMargin + |c| kMarginRel.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -23,10 +31,9 @@
 namespace topo {
 namespace {
 
-constexpr int kRouteThreads = 128;
-constexpr int kRouteCand = 64;              // candidates per token before the exact rounds take over
-constexpr int kMaxGroups = 32;
-
+constexpr int kRouteThreads = 256;
+constexpr int kRouteCand = 32;              // candidates per token before exact_row takes over
+constexpr float kMargin = 4e-6f, kMarginRel = 5e-7f;
 constexpr float kInf = __builtin_huge_valf();
 
 __device__ __forceinline__ bool above(float a, int ia, float b, int ib) {
@@ -46,24 +53,39 @@ __device__ __forceinline__ unsigned long long key_of(float v, int e) {
 
 __device__ __forceinline__ float sigmoid_rn(float x) { return __fdiv_rn(1.f, __fadd_rn(1.f, expf(-x))); }
 
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float sigmoid_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp2_approx(x * -1.4426950408889634f)));
+    return r;
+}
+
 template <bool BF>
 __device__ __forceinline__ float logit(const void *row, int e) {
     if (BF) return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short *>(row) + e) << 16);
     return __ldg(reinterpret_cast<const float *>(row) + e);
 }
 
-// Expert of slot u of lane gl: VEC consecutive experts per 16-byte load.
-template <int G, int VEC>
+// Expert of slot u of lane gl.  VEC = 1: lane-strided; else VEC consecutive
+// experts per 16-byte load, the loads strided over the lanes, or (BLK) all of a
+// lane's VPL experts consecutive, for groups that are whole lanes.
+template <int VPL, int G, int VEC, bool BLK>
 __device__ __forceinline__ int expert_of(int u, int gl) {
+    if (BLK) return gl * VPL + u;
     return VEC > 1 ? ((u / VEC) * G + gl) * VEC + (u % VEC) : u * G + gl;
 }
 
-template <int VPL, int G, bool BF, int VEC>
-__device__ __forceinline__ void load_row(const void *row, int E, int gl, float *x) {
+template <int VPL, int G, bool BF, int VEC, bool BLK>
+__device__ __forceinline__ void load_row(const void *row, int E, int gl, float (&x)[VPL]) {
     if (VEC > 1) {
 #pragma unroll
         for (int c = 0; c < VPL / VEC; ++c) {
-            const int ch = c * G + gl;
+            const int ch = BLK ? gl * (VPL / VEC) + c : c * G + gl;
             const bool in = ch * VEC < E;
             if (BF) {
                 const uint4 w = in ? __ldg(reinterpret_cast<const uint4 *>(row) + ch) : make_uint4(0, 0, 0, 0);
@@ -104,6 +126,34 @@ __device__ __forceinline__ float group_sum(unsigned mask, float v) {
     return v;
 }
 
+// (m1, m2), the two largest so far, with v.  A NaN is passed over.
+__device__ __forceinline__ void push2(float &m1, float &m2, float v) {
+    m2 = fmaxf(m2, fminf(m1, v));
+    m1 = fmaxf(m1, v);
+}
+
+// The k-th largest of the 2 G values (a >= b per lane): bitonic sort over
+// positions 2 gl + 0 .. 1, descending.
+template <int G>
+__device__ __forceinline__ float kth_largest(unsigned mask, int gl, float a, float b, int k) {
+#pragma unroll
+    for (int size = 2; size <= 2 * G; size <<= 1) {
+        const bool down = ((2 * gl) & size) == 0;              // this lane's run is descending
+#pragma unroll
+        for (int stride = size >> 1; stride > 1; stride >>= 1) {
+            const float oa = __shfl_xor_sync(mask, a, stride >> 1, G), ob = __shfl_xor_sync(mask, b, stride >> 1, G);
+            const bool keep_max = (((2 * gl) & stride) == 0) == down;
+            a = keep_max ? fmaxf(a, oa) : fminf(a, oa);
+            b = keep_max ? fmaxf(b, ob) : fminf(b, ob);
+        }
+        const float hi = fmaxf(a, b), lo = fminf(a, b);
+        a = down ? hi : lo;
+        b = down ? lo : hi;
+    }
+    const float ra = __shfl_sync(mask, a, (k - 1) >> 1, G), rb = __shfl_sync(mask, b, (k - 1) >> 1, G);
+    return (k - 1) & 1 ? rb : ra;
+}
+
 struct RouteArgs {
     const void *logits;
     const float *bias;
@@ -111,207 +161,306 @@ struct RouteArgs {
     float *weights;
     int64_t ntok;
     int E, k, score, n_group, topk_group, group_top, renorm;
+    int by_logit;       // c is the logit itself
+    int exact;          // every row by exact_row
     float scale;
+    FastDiv gdiv;       // by the experts of a group
 };
 
-template <int VPL, int G, bool BF, int VEC>
-__global__ void __launch_bounds__(kRouteThreads)
-k_route_experts(RouteArgs g) {
-    constexpr int kGroups = kRouteThreads / G;
-    __shared__ float stash_[kGroups][G * VPL];
-    __shared__ unsigned long long keys_[kGroups][kRouteCand];
-    __shared__ int sel_[kGroups][kMaxK];
-    __shared__ float gsc_[kGroups][kMaxGroups];
-    const int lane = threadIdx.x & 31, gl = lane & (G - 1), grp = threadIdx.x / G;
-    const unsigned gmask = G == 32 ? 0xffffffffu : (((1u << (G & 31)) - 1u) << (lane & ~(G - 1)));
-    float *stash = stash_[grp], *gsc = gsc_[grp];
-    unsigned long long *wk = keys_[grp];
-    int *sel = sel_[grp];
-    const int E = g.E, k = g.k;
-    const bool by_logit = !g.bias && g.group_top == 1;
-    unsigned in = 0;                                              // slots that hold an expert
-#pragma unroll
-    for (int u = 0; u < VPL; ++u) in |= (unsigned)(expert_of<G, VEC>(u, gl) < E) << u;
-    // bitonic directions of this lane, one bit per compare-exchange stage
-    unsigned kmax = 0;
-    {
-        int st = 0;
-#pragma unroll
-        for (int size = 2; size <= G; size <<= 1)
-#pragma unroll
-            for (int stride = size >> 1; stride > 0; stride >>= 1, ++st)
-                kmax |= (unsigned)(((gl & stride) == 0) == ((gl & size) == 0)) << st;
+// Shared memory of one token group.
+struct RouteScratch {
+    float *stash;       // [E rounded up] scores by expert
+    unsigned long long *keys;
+    float *cx;          // candidates' logits
+    int *ce;            // candidates' experts
+    int *sel;           // chosen experts and their logits
+    float *sx;
+    float *gsc;         // [n_group]
+};
+
+// Every score as defined, the groups, and k rounds of an argmax: chosen experts
+// to sel, logits to sx; *m and *total of a softmax over the row.
+template <int G, bool BF>
+__device__ __noinline__ void exact_row(const RouteArgs &g, const void *row, const RouteScratch &w, unsigned gmask, int gl,
+                                       float *row_max, float *row_sum) {
+    const int E = g.E, gs = E / g.n_group;
+    float m = 0.f, total = 0.f;
+    if (g.score == TOPO_SCORE_SOFTMAX) {
+        m = -kInf;
+        for (int e = gl; e < E; e += G) m = fmaxf(m, logit<BF>(row, e));
+        m = group_max<G>(gmask, m);
+        if (m == -kInf) m = 0.f;                                  // nothing to subtract in a row of -inf
+        for (int e = gl; e < E; e += G) total += expf(logit<BF>(row, e) - m);
+        total = group_sum<G>(gmask, total);
     }
-    for (int64_t tok = (int64_t)blockIdx.x * kGroups + grp; tok < g.ntok; tok += (int64_t)gridDim.x * kGroups) {
-        const void *row = static_cast<const char *>(g.logits) + (size_t)tok * E * (BF ? 2 : 4);
-        float x[VPL], c[VPL];
-        load_row<VPL, G, BF, VEC>(row, E, gl, x);
-        float m = 0.f, total = 0.f;                               // softmax: row maximum, sum of exp(x - m)
-        const bool whole = g.score == TOPO_SCORE_SOFTMAX && (!by_logit || !g.renorm);
-        if (whole) {
-            m = -kInf;
-            bool nan = false;
-#pragma unroll
-            for (int u = 0; u < VPL; ++u)
-                if ((in >> u) & 1u) {
-                    m = fmaxf(m, x[u]);
-                    nan |= x[u] != x[u];
-                }
-            m = group_max<G>(gmask, m);
-            if (m == -kInf) m = 0.f;                              // nothing to subtract in a row of -inf
-#pragma unroll
-            for (int u = 0; u < VPL; ++u)
-                if ((in >> u) & 1u) total += expf(x[u] - m);
-            total = group_sum<G>(gmask, total);
+    *row_max = m;
+    *row_sum = total;
+    for (int e = gl; e < E; e += G) {
+        const float x = logit<BF>(row, e);
+        float c = x;
+        if (!g.by_logit) {
+            float s;
+            if (g.score == TOPO_SCORE_SOFTMAX) s = total == 0.f ? 0.f : __fdiv_rn(expf(x - m), total);
+            else s = sigmoid_rn(x);
+            c = __fadd_rn(s, g.bias ? __ldg(g.bias + e) : 0.f);
+            if (x == -kInf) c = -kInf;
         }
-#pragma unroll
-        for (int u = 0; u < VPL; ++u) {
-            if (by_logit) {
-                c[u] = x[u];
-            } else {
-                float s;
-                if (g.score == TOPO_SCORE_SOFTMAX) s = total == 0.f ? 0.f : __fdiv_rn(expf(x[u] - m), total);
-                else s = sigmoid_rn(x[u]);
-                const int e = expert_of<G, VEC>(u, gl);
-                c[u] = __fadd_rn(s, g.bias && e < E ? __ldg(g.bias + e) : 0.f);
-                if (x[u] == -kInf) c[u] = -kInf;
-            }
-        }
-        unsigned valid = in;
-        if (g.n_group > 1) {
-            const int gs = E / g.n_group;
-#pragma unroll
-            for (int u = 0; u < VPL; ++u) stash[expert_of<G, VEC>(u, gl)] = c[u];
-            __syncwarp(gmask);
-            for (int q = gl; q < g.n_group; q += G) {
-                float a = stash[q * gs], b = -kInf;
-                bool hb = false;                                  // b holds a value
-                for (int i = 1; i < gs; ++i) {
-                    const float v = stash[q * gs + i];
-                    if (above(v, i, a, -1)) {
-                        b = a;
-                        a = v;
-                        hb = true;
-                    } else if (!hb || above(v, i, b, -1)) {
-                        b = v;
-                        hb = true;
-                    }
+        w.stash[e] = c;
+    }
+    __syncwarp(gmask);
+    unsigned keep = 0xffffffffu;
+    if (g.n_group > 1) {
+        for (int q = gl; q < g.n_group; q += G) {
+            float a = w.stash[q * gs], b = -kInf;
+            bool hb = false;                                      // b holds a value
+            for (int i = 1; i < gs; ++i) {
+                const float v = w.stash[q * gs + i];
+                if (above(v, i, a, -1)) {
+                    b = a;
+                    a = v;
+                    hb = true;
+                } else if (!hb || above(v, i, b, -1)) {
+                    b = v;
+                    hb = true;
                 }
-                gsc[q] = g.group_top == 2 ? __fadd_rn(a, b) : a;
             }
-            __syncwarp(gmask);
-            unsigned keep = 0;
-            for (int q = gl; q < g.n_group; q += G) {
-                int rank = 0;
-                for (int i = 0; i < g.n_group; ++i) rank += i != q && above(gsc[i], i, gsc[q], q);
-                keep |= (unsigned)(rank < g.topk_group) << q;
-            }
-#pragma unroll
-            for (int o = G / 2; o > 0; o >>= 1) keep |= __shfl_xor_sync(gmask, keep, o, G);
-#pragma unroll
-            for (int u = 0; u < VPL; ++u) {
-                const int e = expert_of<G, VEC>(u, gl);
-                if (e < E && !((keep >> (e / gs)) & 1u)) valid &= ~(1u << u);
-            }
-        }
-        // tau: the k-th largest lane maximum (bitonic sort, descending)
-        float tau = -kInf;
-        if (k <= G) {
-            float y = -kInf;
-#pragma unroll
-            for (int u = 0; u < VPL; ++u)
-                if ((valid >> u) & 1u) y = fmaxf(y, c[u]);
-            int st = 0;
-#pragma unroll
-            for (int size = 2; size <= G; size <<= 1)
-#pragma unroll
-                for (int stride = size >> 1; stride > 0; stride >>= 1, ++st) {
-                    const float o = __shfl_xor_sync(gmask, y, stride, G);
-                    y = ((kmax >> st) & 1u) ? fmaxf(y, o) : fminf(y, o);
-                }
-            tau = __shfl_sync(gmask, y, k - 1, G);
-        }
-        unsigned cm = 0;
-#pragma unroll
-        for (int u = 0; u < VPL; ++u) cm |= (unsigned)(((valid >> u) & 1u) && c[u] >= tau) << u;
-        const int cn = __popc(cm);
-        int incl = cn;
-#pragma unroll
-        for (int o = 1; o < G; o <<= 1) {
-            const int y = __shfl_up_sync(gmask, incl, o, G);
-            if (gl >= o) incl += y;
-        }
-        const int n = __shfl_sync(gmask, incl, G - 1, G);
-        if (k <= G && n >= k && n <= kRouteCand) {
-            int off = incl - cn;
-#pragma unroll
-            for (int u = 0; u < VPL; ++u)
-                if ((cm >> u) & 1u) wk[off++] = key_of(c[u], expert_of<G, VEC>(u, gl));
-            __syncwarp(gmask);
-            for (int q = gl; q < n; q += G) {
-                const unsigned long long key = wk[q];
-                int rank = 0;
-#pragma unroll 4
-                for (int j = 0; j < n; ++j) rank += wk[j] > key;
-                if (rank < k) sel[rank] = (int)~(uint32_t)key;
-            }
-        } else {
-            unsigned left = valid;
-            for (int j = 0; j < k; ++j) {
-                float bv = 0.f;
-                int bi = -1;
-#pragma unroll
-                for (int u = 0; u < VPL; ++u) {
-                    const int e = expert_of<G, VEC>(u, gl);
-                    if (((left >> u) & 1u) && (bi < 0 || above(c[u], e, bv, bi))) {
-                        bv = c[u];
-                        bi = e;
-                    }
-                }
-#pragma unroll
-                for (int o = G / 2; o > 0; o >>= 1) {
-                    const float ov = __shfl_xor_sync(gmask, bv, o, G);
-                    const int oi = __shfl_xor_sync(gmask, bi, o, G);
-                    if (oi >= 0 && (bi < 0 || above(ov, oi, bv, bi))) {
-                        bv = ov;
-                        bi = oi;
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < VPL; ++u)
-                    if (expert_of<G, VEC>(u, gl) == bi) left &= ~(1u << u);
-                if (gl == 0) sel[j] = bi;
-            }
+            w.gsc[q] = g.group_top == 2 ? __fadd_rn(a, b) : a;
         }
         __syncwarp(gmask);
+        keep = 0;
+        for (int q = gl; q < g.n_group; q += G) {
+            int rank = 0;
+            for (int i = 0; i < g.n_group; ++i) rank += i != q && above(w.gsc[i], i, w.gsc[q], q);
+            keep |= (unsigned)(rank < g.topk_group) << q;
+        }
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) keep |= __shfl_xor_sync(gmask, keep, o, G);
+    }
+    // taken experts are marked by a key of their own in ce's bits: lane-owned slots
+    unsigned taken[4] = {0u, 0u, 0u, 0u};                         // up to 128 slots per lane
+    for (int j = 0; j < g.k; ++j) {
+        float bv = 0.f;
+        int bi = -1;
+        for (int e = gl, u = 0; e < E; e += G, ++u) {
+            if ((taken[u >> 5] >> (u & 31)) & 1u) continue;
+            if (g.n_group > 1 && !((keep >> fast_quot((unsigned)e, g.gdiv)) & 1u)) continue;
+            const float v = w.stash[e];
+            if (bi < 0 || above(v, e, bv, bi)) {
+                bv = v;
+                bi = e;
+            }
+        }
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) {
+            const float ov = __shfl_xor_sync(gmask, bv, o, G);
+            const int oi = __shfl_xor_sync(gmask, bi, o, G);
+            if (oi >= 0 && (bi < 0 || above(ov, oi, bv, bi))) {
+                bv = ov;
+                bi = oi;
+            }
+        }
+        if (bi % G == gl) {
+            const int u = bi / G;
+            taken[u >> 5] |= 1u << (u & 31);
+            w.sel[j] = bi;
+            w.sx[j] = logit<BF>(row, bi);
+        }
+    }
+    __syncwarp(gmask);
+}
+
+template <int VPL, int G, bool BF, int VEC, bool BLK, bool SIG>
+__global__ void __launch_bounds__(kRouteThreads, VPL > 16 ? 2 : 3)
+k_route_experts(const __grid_constant__ RouteArgs g) {
+    constexpr int kGroups = kRouteThreads / G;
+    __shared__ unsigned long long keys_[kGroups][kRouteCand];
+    __shared__ float cx_[kGroups][kRouteCand];
+    __shared__ int ce_[kGroups][kRouteCand];
+    __shared__ int sel_[kGroups][kMaxK];
+    __shared__ float sx_[kGroups][kMaxK];
+    __shared__ float gsc_[kGroups][TOPO_ROUTE_MAX_GROUPS];
+    extern __shared__ __align__(16) float dyn[];
+    const int lane = threadIdx.x & 31, gl = lane & (G - 1), grp = threadIdx.x / G;
+    const unsigned gmask = G == 32 ? 0xffffffffu : (((1u << (G & 31)) - 1u) << (lane & ~(G - 1)));
+    const int E = g.E, k = g.k, Ep = (E + 3) & ~3;
+    float *sb = dyn;                                              // [Ep] bias
+    const RouteScratch w = {dyn + Ep + grp * Ep, keys_[grp], cx_[grp], ce_[grp], sel_[grp], sx_[grp], gsc_[grp]};
+    if (SIG) {
+        for (int e = threadIdx.x; e < Ep; e += kRouteThreads) sb[e] = g.bias && e < E ? __ldg(g.bias + e) : 0.f;
+        __syncthreads();
+    }
+    unsigned in = 0;                                              // slots that hold an expert
+#pragma unroll
+    for (int u = 0; u < VPL; ++u) in |= (unsigned)(expert_of<VPL, G, VEC, BLK>(u, gl) < E) << u;
+    const bool grouped = g.n_group > 1;
+    const int gs = E / g.n_group;
+    for (int64_t tok = (int64_t)blockIdx.x * kGroups + grp; tok < g.ntok; tok += (int64_t)gridDim.x * kGroups) {
+        const void *row = static_cast<const char *>(g.logits) + (size_t)tok * E * (BF ? 2 : 4);
+        float m = 0.f, total = 0.f;                               // softmax over the row
+        bool done = false;
+        if (!g.exact) {
+            float x[VPL], c[SIG ? VPL : 1];
+            load_row<VPL, G, BF, VEC, BLK>(row, E, gl, x);
+            float odd = 0.f;                                      // NaN with any NaN or infinity
+            float m1 = -kInf, m2 = -kInf;
+            if (SIG) {
+#pragma unroll
+                for (int u = 0; u < VPL; ++u) {
+                    const int e = expert_of<VPL, G, VEC, BLK>(u, gl);
+                    odd = fmaf(x[u], 0.f, odd);
+                    c[u] = sigmoid_approx(x[u]) + (e < E ? sb[e] : 0.f);
+                }
+            } else if (grouped) {
+#pragma unroll
+                for (int u = 0; u < VPL; ++u) odd = fmaf(x[u], 0.f, odd);
+            }
+            auto val = [&](int u) -> float & { return SIG ? c[SIG ? u : 0] : x[u]; };
+#pragma unroll
+            for (int u = 0; u < VPL; ++u)
+                if ((in >> u) & 1u) push2(m1, m2, val(u));
+            unsigned valid = in;
+            bool unsure = odd != 0.f;
+            if (grouped) {
+                float a = m1, b = m2;
+                if (BLK) {                                        // gs / VPL neighbouring lanes, a power of two
+                    for (int o = 1; o < gs / VPL; o <<= 1) {
+                        const float oa = __shfl_xor_sync(gmask, a, o, G), ob = __shfl_xor_sync(gmask, b, o, G);
+                        b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+                        a = fmaxf(a, oa);
+                    }
+                    if (gl % (gs / VPL) == 0) w.gsc[gl / (gs / VPL)] = g.group_top == 2 ? a + b : a;
+                } else {
+#pragma unroll
+                    for (int u = 0; u < VPL; ++u) {
+                        const int e = expert_of<VPL, G, VEC, BLK>(u, gl);
+                        if (e < E) w.stash[e] = val(u);
+                    }
+                    __syncwarp(gmask);
+                    // G / 2^ceil(log2 n_group) lanes to a group
+                    int lpg = G;
+                    while (lpg * g.n_group > G) lpg >>= 1;
+                    const int q = gl / lpg, sub = gl - q * lpg;
+                    a = b = -kInf;
+                    if (q < g.n_group)
+                        for (int i = sub; i < gs; i += lpg) push2(a, b, w.stash[q * gs + i]);
+                    for (int o = 1; o < lpg; o <<= 1) {
+                        const float oa = __shfl_xor_sync(gmask, a, o, G), ob = __shfl_xor_sync(gmask, b, o, G);
+                        b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+                        a = fmaxf(a, oa);
+                    }
+                    if (sub == 0 && q < g.n_group) w.gsc[q] = g.group_top == 2 ? a + b : a;
+                }
+                __syncwarp(gmask);
+                bool kept = false;
+                if (gl < g.n_group) {
+                    // groups surely above this one, and those that may be
+                    const float v = w.gsc[gl], d = SIG ? 2.f * (kMargin + fabsf(v) * kMarginRel) : 0.f;
+                    int sure = 0, may = 0;
+                    for (int i = 0; i < g.n_group; ++i) {
+                        const float o = w.gsc[i];
+                        sure += o > v + d;
+                        may += o >= v - d;
+                    }
+                    kept = may <= g.topk_group;                   // itself among them
+                    unsure |= !kept && sure < g.topk_group;
+                }
+                const unsigned keep = __ballot_sync(gmask, kept) >> (lane & ~(G - 1) & 31);
+                if (BLK) {
+                    if (!((keep >> (gl / (gs / VPL))) & 1u)) {
+                        valid = 0;
+                        m1 = m2 = -kInf;
+                    }
+                } else {
+                    m1 = m2 = -kInf;
+#pragma unroll
+                    for (int u = 0; u < VPL; ++u) {
+                        const int e = expert_of<VPL, G, VEC, BLK>(u, gl);
+                        if (!((keep >> (fast_quot((unsigned)e, g.gdiv) & 31)) & 1u)) valid &= ~(1u << u);
+                        if ((valid >> u) & 1u) push2(m1, m2, val(u));
+                    }
+                }
+            }
+            float thr = kth_largest<G>(gmask, gl, m1, m2, k);
+            if (SIG) thr -= kMargin + fabsf(thr) * kMarginRel;
+            unsigned cm = 0;
+#pragma unroll
+            for (int u = 0; u < VPL; ++u) cm |= (unsigned)(val(u) >= thr) << u;
+            cm &= valid;
+            const int cn = __popc(cm);
+            int incl = cn;
+#pragma unroll
+            for (int o = 1; o < G; o <<= 1) {
+                const int y = __shfl_up_sync(gmask, incl, o, G);
+                if (gl >= o) incl += y;
+            }
+            const int n = __shfl_sync(gmask, incl, G - 1, G);
+            done = n >= k && n <= kRouteCand && !__any_sync(gmask, unsure);
+            if (done) {
+                int off = incl - cn;
+#pragma unroll
+                for (int u = 0; u < VPL; ++u)
+                    if ((cm >> u) & 1u) {
+                        w.cx[off] = x[u];
+                        w.ce[off++] = expert_of<VPL, G, VEC, BLK>(u, gl);
+                    }
+                __syncwarp(gmask);
+                for (int q = gl; q < n; q += G) {
+                    const float v = w.cx[q];
+                    const int e = w.ce[q];
+                    w.keys[q] = key_of(SIG ? __fadd_rn(sigmoid_rn(v), sb[e]) : v, e);
+                }
+                __syncwarp(gmask);
+                for (int q = gl; q < n; q += G) {
+                    const unsigned long long key = w.keys[q];
+                    int rank = 0;
+                    for (int j = 0; j < n; ++j) rank += w.keys[j] > key;
+                    if (rank < k) {
+                        w.sel[rank] = w.ce[q];
+                        w.sx[rank] = w.cx[q];
+                    }
+                }
+                if (!SIG && g.score == TOPO_SCORE_SOFTMAX && !g.renorm) {
+                    m = group_max<G>(gmask, m1);
+                    if (grouped) {
+                        m = -kInf;
+#pragma unroll
+                        for (int u = 0; u < VPL; ++u)
+                            if ((in >> u) & 1u) m = fmaxf(m, x[u]);
+                        m = group_max<G>(gmask, m);
+                    }
+                    if (m == -kInf) m = 0.f;
+                    const float ml = m * 1.4426950408889634f;
+#pragma unroll
+                    for (int u = 0; u < VPL; ++u)
+                        if ((in >> u) & 1u) total += exp2_approx(fmaf(x[u], 1.4426950408889634f, -ml));
+                    total = group_sum<G>(gmask, total);
+                }
+                __syncwarp(gmask);
+            }
+        }
+        if (!done) exact_row<G, BF>(g, row, w, gmask, gl, &m, &total);
         // weights of the chosen, slot j on lane j (and j + G, ...)
-        float mc = m;
         const bool soft = g.score == TOPO_SCORE_SOFTMAX;
+        float mc = m;
         if (soft && g.renorm) {                                   // softmax over the chosen logits
             mc = -kInf;
-            for (int j = gl; j < k; j += G) mc = fmaxf(mc, logit<BF>(row, sel[j]));
+            for (int j = gl; j < k; j += G) mc = fmaxf(mc, w.sx[j]);
             mc = group_max<G>(gmask, mc);
             if (mc == -kInf) mc = 0.f;
         }
         float sum = 0.f;
         if (g.renorm) {
-            for (int j = gl; j < k; j += G) {
-                const float v = logit<BF>(row, sel[j]);
-                sum += soft ? expf(v - mc) : sigmoid_rn(v);
-            }
+            for (int j = gl; j < k; j += G) sum += soft ? expf(w.sx[j] - mc) : sigmoid_rn(w.sx[j]);
             sum = group_sum<G>(gmask, sum);
         }
         for (int j = gl; j < k; j += G) {
-            const int e = sel[j];
-            const float v = logit<BF>(row, e);
+            const float v = w.sx[j];
             float s = soft ? expf(v - mc) : sigmoid_rn(v);
             if (soft && !g.renorm) s = total == 0.f ? 0.f : __fdiv_rn(s, total);
-            float w = g.scale * s;
-            if (g.renorm) w = sum == 0.f ? 0.f : s * (g.scale / sum);
-            g.ids[tok * k + j] = e;
-            g.weights[tok * k + j] = w;
+            g.ids[tok * k + j] = w.sel[j];
+            g.weights[tok * k + j] = g.renorm ? (sum == 0.f ? 0.f : s * (g.scale / sum)) : g.scale * s;
         }
-        __syncwarp(gmask);                                        // sel, keys and stash are free again
+        __syncwarp(gmask);                                        // the scratch is free again
     }
 }
 
@@ -340,19 +489,20 @@ __device__ __forceinline__ void put(void *row, int e, float v) {
 
 // One warp per token: the row's dense gradient (0, or -p_e * sum for a softmax
 // whose weights are not renormalised), then the chosen experts' values over it.
-template <bool BF>
+// Bound by writing the rows; V: they are written 16 bytes at a time.
+template <bool BF, bool V>
 __global__ void __launch_bounds__(256)
 k_route_grad(RouteGradArgs g) {
     const int lane = threadIdx.x & 31;
     const int64_t nw = (int64_t)gridDim.x * (blockDim.x >> 5);
     const int E = g.E, k = g.k;
-    const bool soft = g.score == TOPO_SCORE_SOFTMAX;
+    const bool soft = g.score == TOPO_SCORE_SOFTMAX, dense = soft && !g.renorm;
     for (int64_t tok = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); tok < g.ntok; tok += nw) {
         const char *row = static_cast<const char *>(g.logits) + (size_t)tok * E * (BF ? 2 : 4);
         char *out = static_cast<char *>(g.dx) + (size_t)tok * E * (BF ? 2 : 4);
         // slots lane and lane + 32
         int id[2];
-        float gr[2], s[2], w[2];
+        float gr[2], x[2], s[2], w[2];
         bool bad = false;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -369,18 +519,24 @@ k_route_grad(RouteGradArgs g) {
             }
         }
         if (bad) set_error(g.hdr, TOPO_ERANGE);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[h] = id[h] >= 0 ? logit<BF>(row, id[h]) : -kInf;
+        if (!dense) {
+            if (V) {
+                const int nv = E * (BF ? 2 : 4) / 16;
+                for (int i = lane; i < nv; i += 32) reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int e = lane; e < E; e += 32) put<BF>(out, e, 0.f);
+            }
+        }
         float m = -kInf, total = 0.f;
         if (soft) {
-            if (g.renorm) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (id[h] >= 0) m = fmaxf(m, logit<BF>(row, id[h]));
-            } else {
+            if (g.renorm) m = fmaxf(x[0], x[1]);
+            else
                 for (int e = lane; e < E; e += 32) m = fmaxf(m, logit<BF>(row, e));
-            }
             m = group_max<32>(0xffffffffu, m);
             if (m == -kInf) m = 0.f;
-            if (!g.renorm) {
+            if (dense) {
                 for (int e = lane; e < E; e += 32) total += expf(logit<BF>(row, e) - m);
                 total = group_sum<32>(0xffffffffu, total);
             }
@@ -388,14 +544,10 @@ k_route_grad(RouteGradArgs g) {
         float sum = 0.f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            s[h] = 0.f;
-            if (id[h] >= 0) {
-                const float x = logit<BF>(row, id[h]);
-                s[h] = soft ? expf(x - m) : sigmoid_rn(x);
-            }
+            s[h] = id[h] < 0 ? 0.f : soft ? expf(x[h] - m) : sigmoid_rn(x[h]);
             sum += s[h];
         }
-        if (soft && !g.renorm) sum = total;
+        if (dense) sum = total;
         else if (g.renorm) sum = group_sum<32>(0xffffffffu, sum);
         else sum = 1.f;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -406,11 +558,9 @@ k_route_grad(RouteGradArgs g) {
             dot += gr[h] * w[h];
         }
         dot = soft || g.renorm ? group_sum<32>(0xffffffffu, dot) : 0.f;
-        if (soft && !g.renorm) {
+        if (dense) {
             const float f = -g.scale * dot * inv;
             for (int e = lane; e < E; e += 32) put<BF>(out, e, f == 0.f ? 0.f : f * expf(logit<BF>(row, e) - m));
-        } else {
-            for (int e = lane; e < E; e += 32) put<BF>(out, e, 0.f);
         }
         __syncwarp();
 #pragma unroll
@@ -420,39 +570,48 @@ k_route_grad(RouteGradArgs g) {
                 if (!soft) d *= 1.f - s[h];
                 put<BF>(out, id[h], d);
             }
-        __syncwarp();
     }
 }
 
-template <int VPL, int G, bool BF, int VEC>
+template <int VPL, int G, bool BF, int VEC, bool BLK>
 cudaError_t run_route(const RouteArgs &a, cudaStream_t st) {
     constexpr int kGroups = kRouteThreads / G;
+    const int Ep = (a.E + 3) & ~3;
+    const size_t smem = (size_t)(kGroups + 1) * Ep * 4;
+    const bool sig = !a.by_logit;
+    const void *fn = sig ? (const void *)k_route_experts<VPL, G, BF, VEC, BLK, true>
+                         : (const void *)k_route_experts<VPL, G, BF, VEC, BLK, false>;
+    cudaError_t e = ensure_smem(fn, smem);
+    if (e != cudaSuccess) return e;
     const int64_t want = (a.ntok + kGroups - 1) / kGroups;
-    const unsigned blocks = (unsigned)(want < 152 * 16 ? want : 152 * 16);
-    k_route_experts<VPL, G, BF, VEC><<<blocks, kRouteThreads, 0, st>>>(a);
+    const unsigned blocks = (unsigned)(want < 152 * 12 ? want : 152 * 12);
+    if (sig) k_route_experts<VPL, G, BF, VEC, BLK, true><<<blocks, kRouteThreads, smem, st>>>(a);
+    else k_route_experts<VPL, G, BF, VEC, BLK, false><<<blocks, kRouteThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 template <int VPL, int G, bool BF>
 cudaError_t route_vec(const RouteArgs &a, bool vec, cudaStream_t st) {
     constexpr int V = BF ? 8 : 4;
-    if (vec && VPL % V == 0) return run_route<VPL, G, BF, (VPL % V == 0 ? V : 1)>(a, st);
-    return run_route<VPL, G, BF, 1>(a, st);
+    constexpr int W = VPL % V == 0 ? V : 1;
+    const int gs = a.E / a.n_group, lanes = gs / VPL;
+    if (W > 1 && vec && a.n_group > 1 && a.E == G * VPL && gs % VPL == 0 && (lanes & (lanes - 1)) == 0)
+        return run_route<VPL, G, BF, W, (W > 1)>(a, st);
+    if (W > 1 && vec) return run_route<VPL, G, BF, W, false>(a, st);
+    return run_route<VPL, G, BF, 1, false>(a, st);
 }
 
+// 16 lanes per token up to 512 experts (two tokens of a warp share the sort,
+// scan and ranking), else 32.
 template <bool BF>
 cudaError_t route_vpl(const RouteArgs &a, bool vec, cudaStream_t st) {
-    if (a.E <= 512 && a.k <= 12) {
+    if (a.E <= 512) {
         const int vpl = (a.E + 15) / 16;
         if (vpl <= 4) return route_vec<4, 16, BF>(a, vec, st);
         if (vpl <= 8) return route_vec<8, 16, BF>(a, vec, st);
         if (vpl <= 16) return route_vec<16, 16, BF>(a, vec, st);
         return route_vec<32, 16, BF>(a, vec, st);
     }
-    const int vpl = (a.E + 31) / 32;
-    if (vpl <= 4) return route_vec<4, 32, BF>(a, vec, st);
-    if (vpl <= 8) return route_vec<8, 32, BF>(a, vec, st);
-    if (vpl <= 16) return route_vec<16, 32, BF>(a, vec, st);
     return route_vec<32, 32, BF>(a, vec, st);
 }
 
@@ -460,7 +619,25 @@ cudaError_t route_vpl(const RouteArgs &a, bool vec, cudaStream_t st) {
 
 cudaError_t launch_route(const topo_route_opts &o, int64_t ntok, int E, int k, const void *logits, bool bf16,
                          const float *bias, int32_t *ids, float *weights, cudaStream_t st) {
-    RouteArgs a = {logits, bias, ids, weights, ntok, E, k, o.score, o.n_group, o.topk_group, o.group_top, o.renorm, o.scale};
+    RouteArgs a = {};
+    a.logits = logits;
+    a.bias = bias;
+    a.ids = ids;
+    a.weights = weights;
+    a.ntok = ntok;
+    a.E = E;
+    a.k = k;
+    a.score = o.score;
+    a.n_group = o.n_group;
+    a.topk_group = o.topk_group;
+    a.group_top = o.group_top;
+    a.renorm = o.renorm;
+    a.scale = o.scale;
+    a.by_logit = !bias && o.group_top == 1;
+    // a softmax that the choice needs has no cheap bound; 16 lanes hold the
+    // candidates of at most 16 slots and the scores of at most 16 groups
+    a.exact = (o.score == TOPO_SCORE_SOFTMAX && !a.by_logit) || k > 16 || o.n_group > 16;
+    a.gdiv = make_fast_div((unsigned)(E / o.n_group));
     if (ntok == 0) return cudaSuccess;
     const bool vec = ((uintptr_t)logits & 15) == 0 && ((size_t)E * (bf16 ? 2 : 4)) % 16 == 0;
     return bf16 ? route_vpl<true>(a, vec, st) : route_vpl<false>(a, vec, st);
@@ -471,9 +648,12 @@ cudaError_t launch_route_grad(const topo_route_opts &o, int64_t ntok, int E, int
     RouteGradArgs a = {logits, ids, dw, dx, ws_at<WsHeader>(ws, 0), ntok, E, k, o.score, o.renorm, o.scale};
     if (ntok == 0) return cudaSuccess;
     const int64_t want = (ntok + 7) / 8;
-    const unsigned blocks = (unsigned)(want < 152 * 8 ? want : 152 * 8);
-    if (bf16) k_route_grad<true><<<blocks, 256, 0, st>>>(a);
-    else k_route_grad<false><<<blocks, 256, 0, st>>>(a);
+    const unsigned blocks = (unsigned)(want < 152 * 32 ? want : 152 * 32);
+    const bool v = ((uintptr_t)dx & 15) == 0 && ((size_t)E * (bf16 ? 2 : 4)) % 16 == 0;
+    if (bf16 && v) k_route_grad<true, true><<<blocks, 256, 0, st>>>(a);
+    else if (bf16) k_route_grad<true, false><<<blocks, 256, 0, st>>>(a);
+    else if (v) k_route_grad<false, true><<<blocks, 256, 0, st>>>(a);
+    else k_route_grad<false, false><<<blocks, 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 
