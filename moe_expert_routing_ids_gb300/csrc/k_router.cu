@@ -14,16 +14,18 @@
 // A group of G lanes per token, VPL scores to a lane, each logit read once.
 // What decides the choice are the rounded c, but few of them matter, so the
 // sigmoid is first taken from the hardware's exp2 and reciprocal:
-//   - the k-th largest of the lanes' two largest values bounds the k-th largest
-//     value from below; what reaches it, less a margin for the approximation,
-//     is a candidate (a little more than k of them);
+//   - the k-th largest of the lanes' maxima bounds the k-th largest value from
+//     below; what reaches it, less a margin for the approximation, is a
+//     candidate (10 to 15 of them for k = 8 or 10);
 //   - candidates are evaluated as defined and ranked by counting;
 //   - groups whose scores are closer than the margin, rows with NaN or
 //     infinities (where groups or the sigmoid are involved), many ties: the row
-//     is done again, every score as defined (exact_row).
+//     is done again, every score as defined (exact_token).
 // The margin: exp2 of a rounded argument is off by |x| 2^-23 + 2^-22 relative,
-// times s (1 - s) <= 1/4 in s, below 2^-20 for every x; twice that and the
-// rounding of the sum with the bias stay below kMargin + |c| kMarginRel.
+// times s (1 - s) in s (|x| s (1 - s) < 0.23), the sum and the reciprocal by
+// 2^-22 s: 3.3e-7 at most, and the score as defined, rounded four times, by
+// 2.5e-7; twice their sum and the roundings of the sums with the bias stay below
+// kMargin + |c| kMarginRel.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -32,8 +34,8 @@ namespace topo {
 namespace {
 
 constexpr int kRouteThreads = 256;
-constexpr int kRouteCand = 32;              // candidates per token before exact_row takes over
-constexpr float kMargin = 4e-6f, kMarginRel = 5e-7f;
+constexpr int kRouteCand = 64;              // candidates per token before exact_token takes over
+constexpr float kMargin = 2e-6f, kMarginRel = 5e-7f;
 constexpr float kInf = __builtin_huge_valf();
 
 __device__ __forceinline__ bool above(float a, int ia, float b, int ib) {
@@ -71,22 +73,20 @@ __device__ __forceinline__ float logit(const void *row, int e) {
     return __ldg(reinterpret_cast<const float *>(row) + e);
 }
 
-// Expert of slot u of lane gl.  VEC = 1: lane-strided; else VEC consecutive
-// experts per 16-byte load, the loads strided over the lanes, or (BLK) all of a
-// lane's VPL experts consecutive, for groups that are whole lanes.
-template <int VPL, int G, int VEC, bool BLK>
+// Expert of slot u of lane gl: VEC consecutive experts per 16-byte load, the
+// loads strided over the lanes; VEC = 1: lane-strided.
+template <int G, int VEC>
 __device__ __forceinline__ int expert_of(int u, int gl) {
-    if (BLK) return gl * VPL + u;
-    return VEC > 1 ? ((u / VEC) * G + gl) * VEC + (u % VEC) : u * G + gl;
+    return ((u / VEC) * G + gl) * VEC + (u % VEC);
 }
 
-template <int VPL, int G, bool BF, int VEC, bool BLK>
+template <int VPL, int G, bool BF, int VEC, bool FULL>
 __device__ __forceinline__ void load_row(const void *row, int E, int gl, float (&x)[VPL]) {
     if (VEC > 1) {
 #pragma unroll
         for (int c = 0; c < VPL / VEC; ++c) {
-            const int ch = BLK ? gl * (VPL / VEC) + c : c * G + gl;
-            const bool in = ch * VEC < E;
+            const int ch = c * G + gl;
+            const bool in = FULL || ch * VEC < E;
             if (BF) {
                 const uint4 w = in ? __ldg(reinterpret_cast<const uint4 *>(row) + ch) : make_uint4(0, 0, 0, 0);
                 const uint32_t q[4] = {w.x, w.y, w.z, w.w};
@@ -107,7 +107,7 @@ __device__ __forceinline__ void load_row(const void *row, int E, int gl, float (
 #pragma unroll
         for (int u = 0; u < VPL; ++u) {
             const int e = u * G + gl;
-            x[u] = e < E ? logit<BF>(row, e) : 0.f;
+            x[u] = FULL || e < E ? logit<BF>(row, e) : 0.f;
         }
     }
 }
@@ -132,26 +132,19 @@ __device__ __forceinline__ void push2(float &m1, float &m2, float v) {
     m1 = fmaxf(m1, v);
 }
 
-// The k-th largest of the 2 G values (a >= b per lane): bitonic sort over
-// positions 2 gl + 0 .. 1, descending.
+// The k-th largest of the lanes' values: bitonic sort, descending.  kmax: this
+// lane keeps the larger value, one bit per compare-exchange stage.
 template <int G>
-__device__ __forceinline__ float kth_largest(unsigned mask, int gl, float a, float b, int k) {
+__device__ __forceinline__ float kth_largest(unsigned mask, unsigned kmax, float y, int k) {
+    int st = 0;
 #pragma unroll
-    for (int size = 2; size <= 2 * G; size <<= 1) {
-        const bool down = ((2 * gl) & size) == 0;              // this lane's run is descending
+    for (int size = 2; size <= G; size <<= 1)
 #pragma unroll
-        for (int stride = size >> 1; stride > 1; stride >>= 1) {
-            const float oa = __shfl_xor_sync(mask, a, stride >> 1, G), ob = __shfl_xor_sync(mask, b, stride >> 1, G);
-            const bool keep_max = (((2 * gl) & stride) == 0) == down;
-            a = keep_max ? fmaxf(a, oa) : fminf(a, oa);
-            b = keep_max ? fmaxf(b, ob) : fminf(b, ob);
+        for (int stride = size >> 1; stride > 0; stride >>= 1, ++st) {
+            const float o = __shfl_xor_sync(mask, y, stride, G);
+            y = ((kmax >> st) & 1u) ? fmaxf(y, o) : fminf(y, o);
         }
-        const float hi = fmaxf(a, b), lo = fminf(a, b);
-        a = down ? hi : lo;
-        b = down ? lo : hi;
-    }
-    const float ra = __shfl_sync(mask, a, (k - 1) >> 1, G), rb = __shfl_sync(mask, b, (k - 1) >> 1, G);
-    return (k - 1) & 1 ? rb : ra;
+    return __shfl_sync(mask, y, k - 1, G);
 }
 
 struct RouteArgs {
@@ -162,7 +155,11 @@ struct RouteArgs {
     int64_t ntok;
     int E, k, score, n_group, topk_group, group_top, renorm;
     int by_logit;       // c is the logit itself
-    int exact;          // every row by exact_row
+    int exact;          // every row by exact_token
+    int whole;          // weights are not renormalised: the softmax's sum over the row is needed
+    int lpg_log;        // log2 of the lanes that find a group's score
+    int stash4;         // they can read four experts at a time
+    int chunk_group;    // a 16-byte load's experts are of one group
     float scale;
     FastDiv gdiv;       // by the experts of a group
 };
@@ -170,10 +167,9 @@ struct RouteArgs {
 // Shared memory of one token group.
 struct RouteScratch {
     float *stash;       // [E rounded up] scores by expert
-    unsigned long long *keys;
-    float *cx;          // candidates' logits
+    unsigned long long *keys;   // candidates
     int *ce;            // candidates' experts
-    int *sel;           // chosen experts and their logits
+    int *sel;           // chosen experts, and their logits (the fast rows of a sigmoid: scores)
     float *sx;
     float *gsc;         // [n_group]
 };
@@ -195,6 +191,7 @@ __device__ __noinline__ void exact_row(const RouteArgs &g, const void *row, cons
     }
     *row_max = m;
     *row_sum = total;
+#pragma unroll 4
     for (int e = gl; e < E; e += G) {
         const float x = logit<BF>(row, e);
         float c = x;
@@ -213,6 +210,7 @@ __device__ __noinline__ void exact_row(const RouteArgs &g, const void *row, cons
         for (int q = gl; q < g.n_group; q += G) {
             float a = w.stash[q * gs], b = -kInf;
             bool hb = false;                                      // b holds a value
+#pragma unroll 4
             for (int i = 1; i < gs; ++i) {
                 const float v = w.stash[q * gs + i];
                 if (above(v, i, a, -1)) {
@@ -236,20 +234,28 @@ __device__ __noinline__ void exact_row(const RouteArgs &g, const void *row, cons
 #pragma unroll
         for (int o = G / 2; o > 0; o >>= 1) keep |= __shfl_xor_sync(gmask, keep, o, G);
     }
-    // taken experts are marked by a key of their own in ce's bits: lane-owned slots
-    unsigned taken[4] = {0u, 0u, 0u, 0u};                         // up to 128 slots per lane
+    // k rounds of an argmax; a lane looks its experts over again only when its
+    // best one was taken
+    unsigned left = 0u;                                           // this lane's experts, at most 32
+    for (int e = gl, u = 0; e < E; e += G, ++u)
+        left |= (unsigned)(g.n_group == 1 || ((keep >> fast_quot((unsigned)e, g.gdiv)) & 1u)) << u;
+    float mv = 0.f;
+    int mi = -1;
+    bool look = true;
     for (int j = 0; j < g.k; ++j) {
-        float bv = 0.f;
-        int bi = -1;
-        for (int e = gl, u = 0; e < E; e += G, ++u) {
-            if ((taken[u >> 5] >> (u & 31)) & 1u) continue;
-            if (g.n_group > 1 && !((keep >> fast_quot((unsigned)e, g.gdiv)) & 1u)) continue;
-            const float v = w.stash[e];
-            if (bi < 0 || above(v, e, bv, bi)) {
-                bv = v;
-                bi = e;
+        if (look) {
+            mi = -1;
+#pragma unroll 4
+            for (int e = gl, u = 0; e < E; e += G, ++u) {
+                const float v = w.stash[e];
+                if (((left >> u) & 1u) && (mi < 0 || above(v, e, mv, mi))) {
+                    mv = v;
+                    mi = e;
+                }
             }
         }
+        float bv = mv;
+        int bi = mi;
 #pragma unroll
         for (int o = G / 2; o > 0; o >>= 1) {
             const float ov = __shfl_xor_sync(gmask, bv, o, G);
@@ -259,9 +265,9 @@ __device__ __noinline__ void exact_row(const RouteArgs &g, const void *row, cons
                 bi = oi;
             }
         }
-        if (bi % G == gl) {
-            const int u = bi / G;
-            taken[u >> 5] |= 1u << (u & 31);
+        look = bi == mi;
+        if (look) {
+            left &= ~(1u << (bi / G));
             w.sel[j] = bi;
             w.sx[j] = logit<BF>(row, bi);
         }
@@ -269,196 +275,277 @@ __device__ __noinline__ void exact_row(const RouteArgs &g, const void *row, cons
     __syncwarp(gmask);
 }
 
-template <int VPL, int G, bool BF, int VEC, bool BLK, bool SIG>
-__global__ void __launch_bounds__(kRouteThreads, VPL > 16 ? 2 : 3)
+// The chosen of one row, every score as defined: ids and weights.
+template <int G, bool BF>
+__device__ __noinline__ void exact_token(const RouteArgs &g, const void *row, const RouteScratch &w, unsigned gmask, int gl,
+                                         int64_t tok) {
+    float m, total;
+    exact_row<G, BF>(g, row, w, gmask, gl, &m, &total);
+    const bool soft = g.score == TOPO_SCORE_SOFTMAX;
+    float mc = m;
+    if (soft && g.renorm) {                                       // softmax over the chosen logits
+        mc = -kInf;
+        for (int j = gl; j < g.k; j += G) mc = fmaxf(mc, w.sx[j]);
+        mc = group_max<G>(gmask, mc);
+        if (mc == -kInf) mc = 0.f;
+    }
+    float sum = 0.f;
+    if (g.renorm) {
+        for (int j = gl; j < g.k; j += G) sum += soft ? expf(w.sx[j] - mc) : sigmoid_rn(w.sx[j]);
+        sum = group_sum<G>(gmask, sum);
+    }
+    for (int j = gl; j < g.k; j += G) {
+        const float v = w.sx[j];
+        float s = soft ? expf(v - mc) : sigmoid_rn(v);
+        if (soft && !g.renorm) s = total == 0.f ? 0.f : __fdiv_rn(s, total);
+        g.ids[tok * g.k + j] = w.sel[j];
+        g.weights[tok * g.k + j] = g.renorm ? (sum == 0.f ? 0.f : s * (g.scale / sum)) : g.scale * s;
+    }
+}
+
+// FULL: E == G * VPL, every slot of every lane holds an expert.  SIG: c is the
+// sigmoid plus the bias; else the logit (or every row is done by exact_token).
+template <int VPL, int G, bool BF, int VEC, bool FULL, bool SIG>
+__global__ void __launch_bounds__(kRouteThreads, VPL > 16 ? 3 : 4)
 k_route_experts(const __grid_constant__ RouteArgs g) {
     constexpr int kGroups = kRouteThreads / G;
-    __shared__ unsigned long long keys_[kGroups][kRouteCand];
-    __shared__ float cx_[kGroups][kRouteCand];
+    __shared__ __align__(16) unsigned long long keys_[kGroups][kRouteCand];
     __shared__ int ce_[kGroups][kRouteCand];
     __shared__ int sel_[kGroups][kMaxK];
     __shared__ float sx_[kGroups][kMaxK];
-    __shared__ float gsc_[kGroups][TOPO_ROUTE_MAX_GROUPS];
+    __shared__ __align__(16) float gsc_[kGroups][TOPO_ROUTE_MAX_GROUPS];
     extern __shared__ __align__(16) float dyn[];
     const int lane = threadIdx.x & 31, gl = lane & (G - 1), grp = threadIdx.x / G;
     const unsigned gmask = G == 32 ? 0xffffffffu : (((1u << (G & 31)) - 1u) << (lane & ~(G - 1)));
     const int E = g.E, k = g.k, Ep = (E + 3) & ~3;
     float *sb = dyn;                                              // [Ep] bias
-    const RouteScratch w = {dyn + Ep + grp * Ep, keys_[grp], cx_[grp], ce_[grp], sel_[grp], sx_[grp], gsc_[grp]};
+    const RouteScratch w = {dyn + Ep + grp * Ep, keys_[grp], ce_[grp], sel_[grp], sx_[grp], gsc_[grp]};
     if (SIG) {
         for (int e = threadIdx.x; e < Ep; e += kRouteThreads) sb[e] = g.bias && e < E ? __ldg(g.bias + e) : 0.f;
         __syncthreads();
     }
-    unsigned in = 0;                                              // slots that hold an expert
+    unsigned in = VPL >= 32 ? 0xffffffffu : (1u << (VPL & 31)) - 1u;    // slots that hold an expert
+    if (!FULL) {
+        in = 0;
 #pragma unroll
-    for (int u = 0; u < VPL; ++u) in |= (unsigned)(expert_of<VPL, G, VEC, BLK>(u, gl) < E) << u;
+        for (int u = 0; u < VPL; ++u) in |= (unsigned)(expert_of<G, VEC>(u, gl) < E) << u;
+    }
+    unsigned kmax = 0;
+    {
+        int st = 0;
+#pragma unroll
+        for (int size = 2; size <= G; size <<= 1)
+#pragma unroll
+            for (int stride = size >> 1; stride > 0; stride >>= 1, ++st)
+                kmax |= (unsigned)(((gl & stride) == 0) == ((gl & size) == 0)) << st;
+    }
     const bool grouped = g.n_group > 1;
     const int gs = E / g.n_group;
+    int chunk_of[VPL / VEC];                                      // groups of this lane's loads
+#pragma unroll
+    for (int c = 0; c < VPL / VEC; ++c) chunk_of[c] = (int)fast_quot((unsigned)((c * G + gl) * VEC), g.gdiv) & 31;
+    for (int q = gl; q < TOPO_ROUTE_MAX_GROUPS; q += G) w.gsc[q] = -kInf;   // past n_group: below every group
+    __syncwarp(gmask);
     for (int64_t tok = (int64_t)blockIdx.x * kGroups + grp; tok < g.ntok; tok += (int64_t)gridDim.x * kGroups) {
         const void *row = static_cast<const char *>(g.logits) + (size_t)tok * E * (BF ? 2 : 4);
-        float m = 0.f, total = 0.f;                               // softmax over the row
-        bool done = false;
-        if (!g.exact) {
-            float x[VPL], c[SIG ? VPL : 1];
-            load_row<VPL, G, BF, VEC, BLK>(row, E, gl, x);
-            float odd = 0.f;                                      // NaN with any NaN or infinity
-            float m1 = -kInf, m2 = -kInf;
-            if (SIG) {
+        if (g.exact) {
+            exact_token<G, BF>(g, row, w, gmask, gl, tok);
+            __syncwarp(gmask);
+            continue;
+        }
+        float c[VPL];
+        load_row<VPL, G, BF, VEC, FULL>(row, E, gl, c);
+        float odd = 0.f;                                          // NaN with any NaN or infinity
+        if (SIG || grouped) {
+#pragma unroll
+            for (int u = 0; u < VPL; ++u) odd = fmaf(c[u], 0.f, odd);
+        }
+        if (SIG) {
+#pragma unroll
+            for (int u = 0; u < VPL; u += (VEC >= 4 ? 4 : 1)) {
+                const int e = expert_of<G, VEC>(u, gl);
+                if (VEC >= 4) {
+                    const float4 b = FULL || e < E ? *reinterpret_cast<const float4 *>(sb + e) : make_float4(0, 0, 0, 0);
+                    c[u] = sigmoid_approx(c[u]) + b.x;
+                    c[u + (VEC >= 4 ? 1 : 0)] = sigmoid_approx(c[u + (VEC >= 4 ? 1 : 0)]) + b.y;
+                    c[u + (VEC >= 4 ? 2 : 0)] = sigmoid_approx(c[u + (VEC >= 4 ? 2 : 0)]) + b.z;
+                    c[u + (VEC >= 4 ? 3 : 0)] = sigmoid_approx(c[u + (VEC >= 4 ? 3 : 0)]) + b.w;
+                } else {
+                    c[u] = sigmoid_approx(c[u]) + (FULL || e < E ? sb[e] : 0.f);
+                }
+            }
+        }
+        unsigned valid = in;
+        bool unsure = odd != 0.f;
+        if (grouped) {
+#pragma unroll
+            for (int u = 0; u < VPL; u += (VEC >= 4 ? 4 : 1)) {
+                const int e = expert_of<G, VEC>(u, gl);
+                if (FULL || e < E) {
+                    if (VEC >= 4) *reinterpret_cast<float4 *>(w.stash + e) = make_float4(c[u], c[u + (VEC >= 4 ? 1 : 0)], c[u + (VEC >= 4 ? 2 : 0)], c[u + (VEC >= 4 ? 3 : 0)]);
+                    else w.stash[e] = c[u];
+                }
+            }
+            __syncwarp(gmask);
+            // lpg = G / 2^ceil(log2 n_group) lanes to a group; 16 bytes at a time where
+            // they fit, each group starting at another piece (its own banks)
+            const int q = gl >> g.lpg_log, sub = gl & ((1 << g.lpg_log) - 1);
+            float a = -kInf, b = -kInf;
+            if (q < g.n_group) {
+                const float *base = w.stash + q * gs;
+                if (g.stash4) {
+                    const int n4 = gs >> (2 + g.lpg_log);
+                    int i = q % n4;
+                    for (int r = 0; r < n4; ++r) {
+                        const float4 v = *reinterpret_cast<const float4 *>(base + 4 * (sub + (i << g.lpg_log)));
+                        push2(a, b, v.x);
+                        push2(a, b, v.y);
+                        push2(a, b, v.z);
+                        push2(a, b, v.w);
+                        if (++i == n4) i = 0;
+                    }
+                } else {
+                    for (int i = sub; i < gs; i += 1 << g.lpg_log) push2(a, b, base[i]);
+                }
+            }
+            for (int o = 1; o < 1 << g.lpg_log; o <<= 1) {
+                const float oa = __shfl_xor_sync(gmask, a, o, G), ob = __shfl_xor_sync(gmask, b, o, G);
+                b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+                a = fmaxf(a, oa);
+            }
+            if (sub == 0 && q < g.n_group) w.gsc[q] = g.group_top == 2 ? a + b : a;
+            __syncwarp(gmask);
+            bool kept = false;
+            if (gl < g.n_group) {
+                // groups surely above this one, and those that may be (itself among them)
+                const float v = w.gsc[gl], d = SIG ? 2.f * (kMargin + fabsf(v) * kMarginRel) : 0.f;
+                const float vh = v + d, vl = v - d;
+                int sure = 0, may = 0;
+                for (int i = 0; i < g.n_group; i += 4) {
+                    const float4 o = *reinterpret_cast<const float4 *>(w.gsc + i);
+                    sure += (o.x > vh) + (o.y > vh) + (o.z > vh) + (o.w > vh);
+                    may += (o.x >= vl) + (o.y >= vl) + (o.z >= vl) + (o.w >= vl);
+                }
+                kept = may <= g.topk_group;
+                unsure |= !kept && sure < g.topk_group;
+            }
+            const unsigned keep = __ballot_sync(gmask, kept) >> (lane & ~(G - 1) & 31);
+            if (VEC == 1 || g.chunk_group) {                      // a load's experts are of one group
+                unsigned out = 0;
+#pragma unroll
+                for (int c = 0; c < VPL / VEC; ++c)
+                    out |= ((~keep >> chunk_of[c]) & 1u) * (((1u << (VEC & 31)) - 1u) << (c * VEC));
+                valid &= ~out;
+            } else {
 #pragma unroll
                 for (int u = 0; u < VPL; ++u) {
-                    const int e = expert_of<VPL, G, VEC, BLK>(u, gl);
-                    odd = fmaf(x[u], 0.f, odd);
-                    c[u] = sigmoid_approx(x[u]) + (e < E ? sb[e] : 0.f);
+                    const int e = expert_of<G, VEC>(u, gl);
+                    if (!((keep >> (fast_quot((unsigned)e, g.gdiv) & 31)) & 1u)) valid &= ~(1u << u);
                 }
-            } else if (grouped) {
-#pragma unroll
-                for (int u = 0; u < VPL; ++u) odd = fmaf(x[u], 0.f, odd);
             }
-            auto val = [&](int u) -> float & { return SIG ? c[SIG ? u : 0] : x[u]; };
+        }
+        float top = -kInf;
+        if (FULL && !grouped) {
+#pragma unroll
+            for (int u = 0; u < VPL; ++u) top = fmaxf(top, c[u]);
+        } else {
 #pragma unroll
             for (int u = 0; u < VPL; ++u)
-                if ((in >> u) & 1u) push2(m1, m2, val(u));
-            unsigned valid = in;
-            bool unsure = odd != 0.f;
-            if (grouped) {
-                float a = m1, b = m2;
-                if (BLK) {                                        // gs / VPL neighbouring lanes, a power of two
-                    for (int o = 1; o < gs / VPL; o <<= 1) {
-                        const float oa = __shfl_xor_sync(gmask, a, o, G), ob = __shfl_xor_sync(gmask, b, o, G);
-                        b = fmaxf(fminf(a, oa), fmaxf(b, ob));
-                        a = fmaxf(a, oa);
-                    }
-                    if (gl % (gs / VPL) == 0) w.gsc[gl / (gs / VPL)] = g.group_top == 2 ? a + b : a;
-                } else {
+                if ((valid >> u) & 1u) top = fmaxf(top, c[u]);
+        }
+        float thr = kth_largest<G>(gmask, kmax, top, k);
+        if (SIG) thr -= kMargin + fabsf(thr) * kMarginRel;
+        unsigned cm = 0;
 #pragma unroll
-                    for (int u = 0; u < VPL; ++u) {
-                        const int e = expert_of<VPL, G, VEC, BLK>(u, gl);
-                        if (e < E) w.stash[e] = val(u);
-                    }
-                    __syncwarp(gmask);
-                    // G / 2^ceil(log2 n_group) lanes to a group
-                    int lpg = G;
-                    while (lpg * g.n_group > G) lpg >>= 1;
-                    const int q = gl / lpg, sub = gl - q * lpg;
-                    a = b = -kInf;
-                    if (q < g.n_group)
-                        for (int i = sub; i < gs; i += lpg) push2(a, b, w.stash[q * gs + i]);
-                    for (int o = 1; o < lpg; o <<= 1) {
-                        const float oa = __shfl_xor_sync(gmask, a, o, G), ob = __shfl_xor_sync(gmask, b, o, G);
-                        b = fmaxf(fminf(a, oa), fmaxf(b, ob));
-                        a = fmaxf(a, oa);
-                    }
-                    if (sub == 0 && q < g.n_group) w.gsc[q] = g.group_top == 2 ? a + b : a;
-                }
-                __syncwarp(gmask);
-                bool kept = false;
-                if (gl < g.n_group) {
-                    // groups surely above this one, and those that may be
-                    const float v = w.gsc[gl], d = SIG ? 2.f * (kMargin + fabsf(v) * kMarginRel) : 0.f;
-                    int sure = 0, may = 0;
-                    for (int i = 0; i < g.n_group; ++i) {
-                        const float o = w.gsc[i];
-                        sure += o > v + d;
-                        may += o >= v - d;
-                    }
-                    kept = may <= g.topk_group;                   // itself among them
-                    unsure |= !kept && sure < g.topk_group;
-                }
-                const unsigned keep = __ballot_sync(gmask, kept) >> (lane & ~(G - 1) & 31);
-                if (BLK) {
-                    if (!((keep >> (gl / (gs / VPL))) & 1u)) {
-                        valid = 0;
-                        m1 = m2 = -kInf;
-                    }
-                } else {
-                    m1 = m2 = -kInf;
+        for (int u = 0; u < VPL; ++u) cm |= c[u] >= thr ? 1u << u : 0u;
+        cm &= valid;
+        float total = 0.f, m = 0.f;                               // softmax over the row
+        if (!SIG && g.whole) {
+            m = -kInf;
 #pragma unroll
-                    for (int u = 0; u < VPL; ++u) {
-                        const int e = expert_of<VPL, G, VEC, BLK>(u, gl);
-                        if (!((keep >> (fast_quot((unsigned)e, g.gdiv) & 31)) & 1u)) valid &= ~(1u << u);
-                        if ((valid >> u) & 1u) push2(m1, m2, val(u));
-                    }
-                }
+            for (int u = 0; u < VPL; ++u)
+                if (FULL || ((in >> u) & 1u)) m = fmaxf(m, c[u]);
+            m = group_max<G>(gmask, m);
+            if (m == -kInf) m = 0.f;
+            const float ml = m * 1.4426950408889634f;
+#pragma unroll
+            for (int u = 0; u < VPL; ++u)
+                if (FULL || ((in >> u) & 1u)) total += exp2_approx(fmaf(c[u], 1.4426950408889634f, -ml));
+            total = group_sum<G>(gmask, total);
+        }
+        const int cn = __popc(cm);
+        int incl = cn;
+#pragma unroll
+        for (int o = 1; o < G; o <<= 1) {
+            const int y = __shfl_up_sync(gmask, incl, o, G);
+            if (gl >= o) incl += y;
+        }
+        const int n = __shfl_sync(gmask, incl, G - 1, G);
+        if (n < k || n > kRouteCand || __any_sync(gmask, unsure)) {
+            exact_token<G, BF>(g, row, w, gmask, gl, tok);
+            __syncwarp(gmask);
+            continue;
+        }
+        for (int off = incl - cn; cm; cm &= cm - 1) w.ce[off++] = expert_of<G, VEC>(__ffs(cm) - 1, gl);
+        __syncwarp(gmask);
+        // candidates q = gl, gl + G, ..: score as defined, key; mostly one pass
+        unsigned long long key = 0;
+        float sc = 0.f;
+        for (int q = gl; q < n; q += G) {
+            const int e = w.ce[q];
+            const float v = logit<BF>(row, e);
+            const float sv = SIG ? sigmoid_rn(v) : v;
+            const unsigned long long kv = key_of(SIG ? __fadd_rn(sv, sb[e]) : v, e);
+            w.keys[q] = kv;
+            if (q == gl) {
+                key = kv;
+                sc = sv;
             }
-            float thr = kth_largest<G>(gmask, gl, m1, m2, k);
-            if (SIG) thr -= kMargin + fabsf(thr) * kMarginRel;
-            unsigned cm = 0;
-#pragma unroll
-            for (int u = 0; u < VPL; ++u) cm |= (unsigned)(val(u) >= thr) << u;
-            cm &= valid;
-            const int cn = __popc(cm);
-            int incl = cn;
-#pragma unroll
-            for (int o = 1; o < G; o <<= 1) {
-                const int y = __shfl_up_sync(gmask, incl, o, G);
-                if (gl >= o) incl += y;
+        }
+        if (gl == 0 && (n & 1)) w.keys[n] = 0;                    // an odd count reads one more
+        __syncwarp(gmask);
+        for (int q = gl; q < n; q += G) {
+            if (q != gl) {
+                key = w.keys[q];
+                const float v = logit<BF>(row, (int)~(uint32_t)key);
+                sc = SIG ? sigmoid_rn(v) : v;
             }
-            const int n = __shfl_sync(gmask, incl, G - 1, G);
-            done = n >= k && n <= kRouteCand && !__any_sync(gmask, unsure);
-            if (done) {
-                int off = incl - cn;
-#pragma unroll
-                for (int u = 0; u < VPL; ++u)
-                    if ((cm >> u) & 1u) {
-                        w.cx[off] = x[u];
-                        w.ce[off++] = expert_of<VPL, G, VEC, BLK>(u, gl);
-                    }
-                __syncwarp(gmask);
-                for (int q = gl; q < n; q += G) {
-                    const float v = w.cx[q];
-                    const int e = w.ce[q];
-                    w.keys[q] = key_of(SIG ? __fadd_rn(sigmoid_rn(v), sb[e]) : v, e);
-                }
-                __syncwarp(gmask);
-                for (int q = gl; q < n; q += G) {
-                    const unsigned long long key = w.keys[q];
-                    int rank = 0;
-                    for (int j = 0; j < n; ++j) rank += w.keys[j] > key;
-                    if (rank < k) {
-                        w.sel[rank] = w.ce[q];
-                        w.sx[rank] = w.cx[q];
-                    }
-                }
-                if (!SIG && g.score == TOPO_SCORE_SOFTMAX && !g.renorm) {
-                    m = group_max<G>(gmask, m1);
-                    if (grouped) {
-                        m = -kInf;
-#pragma unroll
-                        for (int u = 0; u < VPL; ++u)
-                            if ((in >> u) & 1u) m = fmaxf(m, x[u]);
-                        m = group_max<G>(gmask, m);
-                    }
+            int rank = 0;
+            for (int j = 0; j < n; j += 2) {
+                const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(w.keys + j);
+                rank += (o.x > key) + (o.y > key);
+            }
+            if (rank < k) {
+                w.sel[rank] = (int)~(uint32_t)key;
+                w.sx[rank] = sc;
+            }
+        }
+        __syncwarp(gmask);
+        // weights: slot j on lane j (k <= 16 here)
+        const bool on = gl < k;
+        float s = on ? w.sx[gl] : -kInf;
+        if (!SIG) {
+            if (g.score == TOPO_SCORE_SOFTMAX) {
+                if (g.renorm) {                                   // softmax over the chosen logits, the largest first
+                    m = w.sx[0];
                     if (m == -kInf) m = 0.f;
-                    const float ml = m * 1.4426950408889634f;
-#pragma unroll
-                    for (int u = 0; u < VPL; ++u)
-                        if ((in >> u) & 1u) total += exp2_approx(fmaf(x[u], 1.4426950408889634f, -ml));
-                    total = group_sum<G>(gmask, total);
                 }
-                __syncwarp(gmask);
+                s = on ? expf(s - m) : 0.f;
+                if (!g.renorm) s = total == 0.f ? 0.f : s / total;
+            } else {
+                s = on ? sigmoid_rn(s) : 0.f;
             }
+        } else if (!on) {
+            s = 0.f;
         }
-        if (!done) exact_row<G, BF>(g, row, w, gmask, gl, &m, &total);
-        // weights of the chosen, slot j on lane j (and j + G, ...)
-        const bool soft = g.score == TOPO_SCORE_SOFTMAX;
-        float mc = m;
-        if (soft && g.renorm) {                                   // softmax over the chosen logits
-            mc = -kInf;
-            for (int j = gl; j < k; j += G) mc = fmaxf(mc, w.sx[j]);
-            mc = group_max<G>(gmask, mc);
-            if (mc == -kInf) mc = 0.f;
-        }
-        float sum = 0.f;
+        float f = g.scale;
         if (g.renorm) {
-            for (int j = gl; j < k; j += G) sum += soft ? expf(w.sx[j] - mc) : sigmoid_rn(w.sx[j]);
-            sum = group_sum<G>(gmask, sum);
+            const float sum = group_sum<G>(gmask, s);
+            f = sum == 0.f ? 0.f : f / sum;
         }
-        for (int j = gl; j < k; j += G) {
-            const float v = w.sx[j];
-            float s = soft ? expf(v - mc) : sigmoid_rn(v);
-            if (soft && !g.renorm) s = total == 0.f ? 0.f : __fdiv_rn(s, total);
-            g.ids[tok * k + j] = w.sel[j];
-            g.weights[tok * k + j] = g.renorm ? (sum == 0.f ? 0.f : s * (g.scale / sum)) : g.scale * s;
+        if (on) {
+            g.ids[tok * k + gl] = w.sel[gl];
+            g.weights[tok * k + gl] = s * f;
         }
         __syncwarp(gmask);                                        // the scratch is free again
     }
@@ -573,32 +660,39 @@ k_route_grad(RouteGradArgs g) {
     }
 }
 
-template <int VPL, int G, bool BF, int VEC, bool BLK>
+template <int VPL, int G, bool BF, int VEC, bool FULL, bool SIG>
 cudaError_t run_route(const RouteArgs &a, cudaStream_t st) {
     constexpr int kGroups = kRouteThreads / G;
-    const int Ep = (a.E + 3) & ~3;
-    const size_t smem = (size_t)(kGroups + 1) * Ep * 4;
-    const bool sig = !a.by_logit;
-    const void *fn = sig ? (const void *)k_route_experts<VPL, G, BF, VEC, BLK, true>
-                         : (const void *)k_route_experts<VPL, G, BF, VEC, BLK, false>;
-    cudaError_t e = ensure_smem(fn, smem);
+    const auto fn = k_route_experts<VPL, G, BF, VEC, FULL, SIG>;
+    const size_t smem = (size_t)(kGroups + 1) * ((a.E + 3) & ~3) * 4;
+    cudaError_t e = ensure_smem((const void *)fn, smem);
     if (e != cudaSuccess) return e;
     const int64_t want = (a.ntok + kGroups - 1) / kGroups;
-    const unsigned blocks = (unsigned)(want < 152 * 12 ? want : 152 * 12);
-    if (sig) k_route_experts<VPL, G, BF, VEC, BLK, true><<<blocks, kRouteThreads, smem, st>>>(a);
-    else k_route_experts<VPL, G, BF, VEC, BLK, false><<<blocks, kRouteThreads, smem, st>>>(a);
+    const int64_t most = 152 * (VPL > 16 ? 3 : 4);                // the CTAs that run together
+    fn<<<(unsigned)(want < most ? want : most), kRouteThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
+template <int VPL, int G, bool BF, int VEC, bool FULL>
+cudaError_t route_sig(const RouteArgs &a, cudaStream_t st) {
+    if (a.by_logit) return run_route<VPL, G, BF, VEC, FULL, false>(a, st);
+    return run_route<VPL, G, BF, VEC, FULL, true>(a, st);
+}
+
 template <int VPL, int G, bool BF>
-cudaError_t route_vec(const RouteArgs &a, bool vec, cudaStream_t st) {
+cudaError_t route_vec(RouteArgs a, bool vec, cudaStream_t st) {
     constexpr int V = BF ? 8 : 4;
     constexpr int W = VPL % V == 0 ? V : 1;
-    const int gs = a.E / a.n_group, lanes = gs / VPL;
-    if (W > 1 && vec && a.n_group > 1 && a.E == G * VPL && gs % VPL == 0 && (lanes & (lanes - 1)) == 0)
-        return run_route<VPL, G, BF, W, (W > 1)>(a, st);
-    if (W > 1 && vec) return run_route<VPL, G, BF, W, false>(a, st);
-    return run_route<VPL, G, BF, 1, false>(a, st);
+    const int gs = a.E / a.n_group;
+    a.lpg_log = 0;
+    while ((a.n_group << (a.lpg_log + 1)) <= G) ++a.lpg_log;
+    a.stash4 = gs % (4 << a.lpg_log) == 0;
+    a.chunk_group = gs % W == 0;
+    if (W > 1 && vec) {
+        if (a.E == G * VPL) return route_sig<VPL, G, BF, W, true>(a, st);
+        return route_sig<VPL, G, BF, W, false>(a, st);
+    }
+    return route_sig<VPL, G, BF, 1, false>(a, st);
 }
 
 // 16 lanes per token up to 512 experts (two tokens of a warp share the sort,
@@ -637,6 +731,7 @@ cudaError_t launch_route(const topo_route_opts &o, int64_t ntok, int E, int k, c
     // a softmax that the choice needs has no cheap bound; 16 lanes hold the
     // candidates of at most 16 slots and the scores of at most 16 groups
     a.exact = (o.score == TOPO_SCORE_SOFTMAX && !a.by_logit) || k > 16 || o.n_group > 16;
+    a.whole = o.score == TOPO_SCORE_SOFTMAX && !o.renorm;
     a.gdiv = make_fast_div((unsigned)(E / o.n_group));
     if (ntok == 0) return cudaSuccess;
     const bool vec = ((uintptr_t)logits & 15) == 0 && ((size_t)E * (bf16 ? 2 : 4)) % 16 == 0;
