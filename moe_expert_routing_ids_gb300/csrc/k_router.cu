@@ -18,9 +18,11 @@
 //     below; what reaches it, less a margin for the approximation, is a
 //     candidate (10 to 15 of them for k = 8 or 10);
 //   - candidates are evaluated as defined and ranked by counting;
-//   - groups whose scores are closer than the margin, rows with NaN or
-//     infinities (where groups or the sigmoid are involved), many ties: the row
-//     is done again, every score as defined (exact_token).
+//   - groups whose scores are closer than the margin: the row is done again with
+//     every score as defined;
+//   - rows with NaN or infinities (where groups or the sigmoid are involved),
+//     many ties: exact_token, which is not for speed (19 rows of 65536 sent
+//     there for their groups cost 24 us, its code being read from memory).
 // The margin: exp2 of a rounded argument is off by |x| 2^-23 + 2^-22 relative,
 // times s (1 - s) in s (|x| s (1 - s) < 0.23), the sum and the reciprocal by
 // 2^-22 s: 3.3e-7 at most, and the score as defined, rounded four times, by
@@ -354,111 +356,136 @@ k_route_experts(const __grid_constant__ RouteArgs g) {
             continue;
         }
         float c[VPL];
-        load_row<VPL, G, BF, VEC, FULL>(row, E, gl, c);
         float odd = 0.f;                                          // NaN with any NaN or infinity
-        if (SIG || grouped) {
+        unsigned cm;                                              // candidates among this lane's slots
+        bool precise = false, unsure;
+#pragma unroll 1
+        for (;;) {
+            load_row<VPL, G, BF, VEC, FULL>(row, E, gl, c);
+            if (SIG || grouped) {
 #pragma unroll
-            for (int u = 0; u < VPL; ++u) odd = fmaf(c[u], 0.f, odd);
-        }
-        if (SIG) {
-#pragma unroll
-            for (int u = 0; u < VPL; u += (VEC >= 4 ? 4 : 1)) {
-                const int e = expert_of<G, VEC>(u, gl);
-                if (VEC >= 4) {
-                    const float4 b = FULL || e < E ? *reinterpret_cast<const float4 *>(sb + e) : make_float4(0, 0, 0, 0);
-                    c[u] = sigmoid_approx(c[u]) + b.x;
-                    c[u + (VEC >= 4 ? 1 : 0)] = sigmoid_approx(c[u + (VEC >= 4 ? 1 : 0)]) + b.y;
-                    c[u + (VEC >= 4 ? 2 : 0)] = sigmoid_approx(c[u + (VEC >= 4 ? 2 : 0)]) + b.z;
-                    c[u + (VEC >= 4 ? 3 : 0)] = sigmoid_approx(c[u + (VEC >= 4 ? 3 : 0)]) + b.w;
-                } else {
-                    c[u] = sigmoid_approx(c[u]) + (FULL || e < E ? sb[e] : 0.f);
-                }
+                for (int u = 0; u < VPL; ++u) odd = fmaf(c[u], 0.f, odd);
             }
-        }
-        unsigned valid = in;
-        bool unsure = odd != 0.f;
-        if (grouped) {
-#pragma unroll
-            for (int u = 0; u < VPL; u += (VEC >= 4 ? 4 : 1)) {
-                const int e = expert_of<G, VEC>(u, gl);
-                if (FULL || e < E) {
-                    if (VEC >= 4) *reinterpret_cast<float4 *>(w.stash + e) = make_float4(c[u], c[u + (VEC >= 4 ? 1 : 0)], c[u + (VEC >= 4 ? 2 : 0)], c[u + (VEC >= 4 ? 3 : 0)]);
-                    else w.stash[e] = c[u];
-                }
-            }
-            __syncwarp(gmask);
-            // lpg = G / 2^ceil(log2 n_group) lanes to a group; 16 bytes at a time where
-            // they fit, each group starting at another piece (its own banks)
-            const int q = gl >> g.lpg_log, sub = gl & ((1 << g.lpg_log) - 1);
-            float a = -kInf, b = -kInf;
-            if (q < g.n_group) {
-                const float *base = w.stash + q * gs;
-                if (g.stash4) {
-                    const int n4 = gs >> (2 + g.lpg_log);
-                    int i = q % n4;
-                    for (int r = 0; r < n4; ++r) {
-                        const float4 v = *reinterpret_cast<const float4 *>(base + 4 * (sub + (i << g.lpg_log)));
-                        push2(a, b, v.x);
-                        push2(a, b, v.y);
-                        push2(a, b, v.z);
-                        push2(a, b, v.w);
-                        if (++i == n4) i = 0;
-                    }
-                } else {
-                    for (int i = sub; i < gs; i += 1 << g.lpg_log) push2(a, b, base[i]);
-                }
-            }
-            for (int o = 1; o < 1 << g.lpg_log; o <<= 1) {
-                const float oa = __shfl_xor_sync(gmask, a, o, G), ob = __shfl_xor_sync(gmask, b, o, G);
-                b = fmaxf(fminf(a, oa), fmaxf(b, ob));
-                a = fmaxf(a, oa);
-            }
-            if (sub == 0 && q < g.n_group) w.gsc[q] = g.group_top == 2 ? a + b : a;
-            __syncwarp(gmask);
-            bool kept = false;
-            if (gl < g.n_group) {
-                // groups surely above this one, and those that may be (itself among them)
-                const float v = w.gsc[gl], d = SIG ? 2.f * (kMargin + fabsf(v) * kMarginRel) : 0.f;
-                const float vh = v + d, vl = v - d;
-                int sure = 0, may = 0;
-                for (int i = 0; i < g.n_group; i += 4) {
-                    const float4 o = *reinterpret_cast<const float4 *>(w.gsc + i);
-                    sure += (o.x > vh) + (o.y > vh) + (o.z > vh) + (o.w > vh);
-                    may += (o.x >= vl) + (o.y >= vl) + (o.z >= vl) + (o.w >= vl);
-                }
-                kept = may <= g.topk_group;
-                unsure |= !kept && sure < g.topk_group;
-            }
-            const unsigned keep = __ballot_sync(gmask, kept) >> (lane & ~(G - 1) & 31);
-            if (VEC == 1 || g.chunk_group) {                      // a load's experts are of one group
-                unsigned out = 0;
-#pragma unroll
-                for (int c = 0; c < VPL / VEC; ++c)
-                    out |= ((~keep >> chunk_of[c]) & 1u) * (((1u << (VEC & 31)) - 1u) << (c * VEC));
-                valid &= ~out;
-            } else {
+            if (SIG && precise) {
+#pragma unroll 1
+                for (int e = gl; e < E; e += G) w.stash[e] = __fadd_rn(sigmoid_rn(logit<BF>(row, e)), sb[e]);
+                __syncwarp(gmask);
 #pragma unroll
                 for (int u = 0; u < VPL; ++u) {
                     const int e = expert_of<G, VEC>(u, gl);
-                    if (!((keep >> (fast_quot((unsigned)e, g.gdiv) & 31)) & 1u)) valid &= ~(1u << u);
+                    c[u] = FULL || e < E ? w.stash[e] : 0.f;
+                }
+                __syncwarp(gmask);
+            } else if (SIG) {
+#pragma unroll
+                for (int u = 0; u < VPL; u += (VEC >= 4 ? 4 : 1)) {
+                    const int e = expert_of<G, VEC>(u, gl);
+                    if (VEC >= 4) {
+                        const float4 b = FULL || e < E ? *reinterpret_cast<const float4 *>(sb + e) : make_float4(0, 0, 0, 0);
+                        c[u] = sigmoid_approx(c[u]) + b.x;
+                        c[u + (VEC >= 4 ? 1 : 0)] = sigmoid_approx(c[u + (VEC >= 4 ? 1 : 0)]) + b.y;
+                        c[u + (VEC >= 4 ? 2 : 0)] = sigmoid_approx(c[u + (VEC >= 4 ? 2 : 0)]) + b.z;
+                        c[u + (VEC >= 4 ? 3 : 0)] = sigmoid_approx(c[u + (VEC >= 4 ? 3 : 0)]) + b.w;
+                    } else {
+                        c[u] = sigmoid_approx(c[u]) + (FULL || e < E ? sb[e] : 0.f);
+                    }
                 }
             }
+            unsigned valid = in;
+            unsure = odd != 0.f;
+            if (grouped) {
+#pragma unroll
+                for (int u = 0; u < VPL; u += (VEC >= 4 ? 4 : 1)) {
+                    const int e = expert_of<G, VEC>(u, gl);
+                    if (FULL || e < E) {
+                        if (VEC >= 4) *reinterpret_cast<float4 *>(w.stash + e) = make_float4(c[u], c[u + (VEC >= 4 ? 1 : 0)], c[u + (VEC >= 4 ? 2 : 0)], c[u + (VEC >= 4 ? 3 : 0)]);
+                        else w.stash[e] = c[u];
+                    }
+                }
+                __syncwarp(gmask);
+                // lpg = G / 2^ceil(log2 n_group) lanes to a group; 16 bytes at a time where
+                // they fit, each group starting at another piece (its own banks)
+                const int q = gl >> g.lpg_log, sub = gl & ((1 << g.lpg_log) - 1);
+                float a = -kInf, b = -kInf;
+                if (q < g.n_group) {
+                    const float *base = w.stash + q * gs;
+                    if (g.stash4) {
+                        const int n4 = gs >> (2 + g.lpg_log);
+                        int i = q % n4;
+                        for (int r = 0; r < n4; ++r) {
+                            const float4 v = *reinterpret_cast<const float4 *>(base + 4 * (sub + (i << g.lpg_log)));
+                            push2(a, b, v.x);
+                            push2(a, b, v.y);
+                            push2(a, b, v.z);
+                            push2(a, b, v.w);
+                            if (++i == n4) i = 0;
+                        }
+                    } else {
+                        for (int i = sub; i < gs; i += 1 << g.lpg_log) push2(a, b, base[i]);
+                    }
+                }
+                for (int o = 1; o < 1 << g.lpg_log; o <<= 1) {
+                    const float oa = __shfl_xor_sync(gmask, a, o, G), ob = __shfl_xor_sync(gmask, b, o, G);
+                    b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+                    a = fmaxf(a, oa);
+                }
+                if (sub == 0 && q < g.n_group) w.gsc[q] = g.group_top == 2 ? a + b : a;
+                __syncwarp(gmask);
+                bool kept = false;
+                if (gl < g.n_group) {
+                    // groups surely above this one, and those that may be (itself among them)
+                    const float v = w.gsc[gl], d = SIG && !precise ? 2.f * (kMargin + fabsf(v) * kMarginRel) : 0.f;
+                    const float vh = v + d, vl = v - d;
+                    int sure = 0, may = 0;
+                    for (int i = 0; i < g.n_group; i += 4) {
+                        const float4 o = *reinterpret_cast<const float4 *>(w.gsc + i);
+                        sure += (o.x > vh) + (o.y > vh) + (o.z > vh) + (o.w > vh);
+                        may += (o.x >= vl) + (o.y >= vl) + (o.z >= vl) + (o.w >= vl);
+                    }
+                    if (precise) {                                    // equal scores by index
+#pragma unroll 1
+                        for (int i = 0; i < gl; ++i) sure += w.gsc[i] == v;
+                        kept = sure < g.topk_group;
+                    } else {
+                        kept = may <= g.topk_group;
+                        unsure |= !kept && sure < g.topk_group;
+                    }
+                }
+                const unsigned keep = __ballot_sync(gmask, kept) >> (lane & ~(G - 1) & 31);
+                if (VEC == 1 || g.chunk_group) {                      // a load's experts are of one group
+                    unsigned out = 0;
+#pragma unroll
+                    for (int c = 0; c < VPL / VEC; ++c)
+                        out |= ((~keep >> chunk_of[c]) & 1u) * (((1u << (VEC & 31)) - 1u) << (c * VEC));
+                    valid &= ~out;
+                } else {
+#pragma unroll
+                    for (int u = 0; u < VPL; ++u) {
+                        const int e = expert_of<G, VEC>(u, gl);
+                        if (!((keep >> (fast_quot((unsigned)e, g.gdiv) & 31)) & 1u)) valid &= ~(1u << u);
+                    }
+                }
+            }
+            float top = -kInf;
+            if (FULL && !grouped) {
+#pragma unroll
+                for (int u = 0; u < VPL; ++u) top = fmaxf(top, c[u]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < VPL; ++u)
+                    if ((valid >> u) & 1u) top = fmaxf(top, c[u]);
+            }
+            float thr = kth_largest<G>(gmask, kmax, top, k);
+            if (SIG && !precise) thr -= kMargin + fabsf(thr) * kMarginRel;
+            cm = 0;
+#pragma unroll
+            for (int u = 0; u < VPL; ++u) cm |= c[u] >= thr ? 1u << u : 0u;
+            cm &= valid;
+            unsure = __any_sync(gmask, unsure);
+            if (!unsure || precise || __any_sync(gmask, odd != 0.f)) break;
+            precise = true;
+            __syncwarp(gmask);
         }
-        float top = -kInf;
-        if (FULL && !grouped) {
-#pragma unroll
-            for (int u = 0; u < VPL; ++u) top = fmaxf(top, c[u]);
-        } else {
-#pragma unroll
-            for (int u = 0; u < VPL; ++u)
-                if ((valid >> u) & 1u) top = fmaxf(top, c[u]);
-        }
-        float thr = kth_largest<G>(gmask, kmax, top, k);
-        if (SIG) thr -= kMargin + fabsf(thr) * kMarginRel;
-        unsigned cm = 0;
-#pragma unroll
-        for (int u = 0; u < VPL; ++u) cm |= c[u] >= thr ? 1u << u : 0u;
-        cm &= valid;
         float total = 0.f, m = 0.f;                               // softmax over the row
         if (!SIG && g.whole) {
             m = -kInf;
@@ -481,7 +508,7 @@ k_route_experts(const __grid_constant__ RouteArgs g) {
             if (gl >= o) incl += y;
         }
         const int n = __shfl_sync(gmask, incl, G - 1, G);
-        if (n < k || n > kRouteCand || __any_sync(gmask, unsure)) {
+        if (n < k || n > kRouteCand || unsure) {
             exact_token<G, BF>(g, row, w, gmask, gl, tok);
             __syncwarp(gmask);
             continue;
