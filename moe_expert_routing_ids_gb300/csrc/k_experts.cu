@@ -48,17 +48,14 @@ constexpr int kTileM = 128;                       // rows of a CTA
 constexpr int kTileN = 256;
 constexpr int kSumWarps = 8;                      // warps that scale, add and store
 constexpr int kThreads = (kSumWarps + 4) * 32;    // two summing warpgroups, one of producer, issuer and two scale warps
-// registers of a thread of the summing and of the other warpgroup; 2 * 128 times
-// the one and 128 times the other are the launch's 384 * 168
-template <int MODE>
-constexpr int kSumRegs = MODE == kProduct ? 224 : 216;
-template <int MODE>
-constexpr int kIoRegs = (384 * 168 - 256 * kSumRegs<MODE>) / 128;
+constexpr int kSumRegs = 208, kIoRegs = 88;       // 2 * 128 * 208 + 128 * 88 = 384 * 168, the launch's share
 constexpr int kTmemCols = 512;                    // two accumulators of 256 columns
 constexpr uint32_t kABytes = kTileM * kKB;
 constexpr int kMaxStages = 9;
 constexpr int kScaleKB = 4;                       // blocks whose scales are brought together
-constexpr int kSegCap = 1024;                     // segments of one launch (the table in shared memory)
+constexpr int kFlush = 8;                         // gradient: blocks summed in tensor memory before the sum
+                                                  // moves to registers
+constexpr int kSegCap = 512;                      // segments of one launch (the table in shared memory)
 constexpr uint32_t kRingBytes = 192 * 1024;       // operand stages
 constexpr uint32_t kStageOut = 2048;              // bytes a warp stores through shared memory at a time
 constexpr int kSms = 152;
@@ -76,8 +73,6 @@ struct GemmArgs {
     int nseg, seg0, n_w;
     int N, K;                   // gradient: dw is [N][K]
     int KB, NB;                 // 128-blocks of K and N
-    int nt;                     // columns of a tile: up to 256
-    int box;                    // rows of one load of the columns' operand
     int stages;
     uint32_t stage_bytes;
     int out_bf16;
@@ -95,7 +90,7 @@ struct Tile {
 template <int MODE, int CG>
 __device__ __forceinline__ int tiles_of(const GemmArgs &g, int len) {
     const int m = MODE == kProduct ? len : g.N, n = MODE == kProduct ? g.N : g.K;
-    return ((m + CG * kTileM - 1) / (CG * kTileM)) * ((n + g.nt - 1) / g.nt);
+    return ((m + CG * kTileM - 1) / (CG * kTileM)) * ((n + kTileN - 1) / kTileN);
 }
 
 // Tile t: its segment by binary search over the exclusive prefix tp[0..nseg].
@@ -117,8 +112,8 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs &g, const int *tp, cons
     r.w = MODE == kGrad ? 0 : g.seg_w ? __ldg(g.seg_w + lo) : g.seg0 + lo;
     r.m0 = m * CG * kTileM;
     r.mlim = min(CG * kTileM, me - r.m0);
-    r.n0 = n * g.nt;
-    r.nlim = min(g.nt, ne - r.n0);
+    r.n0 = n * kTileN;
+    r.nlim = min(kTileN, ne - r.n0);
     if (MODE == kProduct) r.m0 += so[lo];
     r.ncols = (r.nlim + 16 * CG - 1) & ~(16 * CG - 1);
     r.kb0 = MODE == kGrad ? pad[lo] : 0;
@@ -126,74 +121,29 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs &g, const int *tp, cons
     return r;
 }
 
-// Place of column c's scale: a lane's columns 8 j + 2 (lane % 4) + 0 .. 1 of two
-// neighbouring groups j are 16 consecutive bytes.
-__device__ __forceinline__ int scale_at(int c) { return (c & ~15) + ((c >> 1) & 3) * 4 + ((c >> 3) & 1) * 2 + (c & 1); }
-
 __device__ __forceinline__ uint32_t pack_bf16(float2 v) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
     return *reinterpret_cast<const uint32_t *>(&b);
 }
 
-// Sums of a thread.  kProduct: acc[i] holds columns 2 i and 2 i + 1 of row `lane`.
-// kGrad: acc[(h * 16 + j) * 2 + r] holds columns 8 j + 2 (lane % 4) and the
-// next of row 16 h + 8 r + lane / 4.
+// Sums of a thread: acc[i] holds columns 2 i and 2 i + 1 of row `lane`.
 using Acc = float2[64];
 
-// kProduct: acc += s * block, 128 columns of this thread's row.  32 columns are
-// read while the 32 before them are added.
+// acc += s * accumulator, 128 columns of this thread's row.  16 columns are read
+// while the 16 before them are added.
 __device__ __forceinline__ void add_rows(Acc &acc, uint32_t ta, float s) {
     const float2 s2 = make_float2(s, s);
-    uint32_t v[2][32];
+    uint32_t v[2][16];
     tc::tmem_ld_rows(ta, v[0]);
     tc::tmem_wait(v[0]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if (c < 3) tc::tmem_ld_rows(ta + 32 * (c + 1), v[(c + 1) & 1]);
+    for (int c = 0; c < 8; ++c) {
+        if (c < 7) tc::tmem_ld_rows(ta + 16 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            tc::fma2(acc[16 * c + i], make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2);
-        if (c < 3) tc::tmem_wait(v[(c + 1) & 1]);
+        for (int i = 0; i < 8; ++i)
+            tc::fma2(acc[8 * c + i], make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2);
+        if (c < 7) tc::tmem_wait(v[(c + 1) & 1]);
     }
-}
-
-// kGrad: acc += scales * block for NJ groups of 8 columns from group J0.  cs: the
-// columns' scales in the order a lane takes them, 4 (two groups) per 16 bytes;
-// rs: the rows' scales.
-template <int J0, int NJ>
-__device__ __forceinline__ void add_cols(Acc &acc, int h, const uint32_t (&v)[4 * NJ], const float *cs, const float (&rs)[4]) {
-#pragma unroll
-    for (int jj = 0; jj < NJ; jj += 2) {
-        const float4 k4 = *reinterpret_cast<const float4 *>(cs + 8 * (J0 + jj));
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const float2 k2 = u ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int i = 4 * (jj + u) + 2 * r;
-                const float2 p = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                tc::fma2(acc[(h * 16 + J0 + jj + u) * 2 + r], tc::mul2(p, k2), make_float2(rs[2 * h + r], rs[2 * h + r]));
-            }
-        }
-    }
-}
-
-// kGrad: 128 columns, 16 rows x 64 columns read while the ones before are added.
-__device__ __forceinline__ void add_block(Acc &acc, uint32_t ta, const float *cs, const float (&rs)[4]) {
-    constexpr uint32_t kRow16 = 16u << 16;
-    uint32_t a[32], b[32];
-    tc::tmem_ld(ta, a);
-    tc::tmem_wait(a);
-    tc::tmem_ld(ta + kRow16, b);
-    add_cols<0, 8>(acc, 0, a, cs, rs);
-    tc::tmem_wait(b);
-    tc::tmem_ld(ta + 64, a);
-    add_cols<0, 8>(acc, 1, b, cs, rs);
-    tc::tmem_wait(a);
-    tc::tmem_ld(ta + 64 + kRow16, b);
-    add_cols<8, 8>(acc, 0, a, cs, rs);
-    tc::tmem_wait(b);
-    add_cols<8, 8>(acc, 1, b, cs, rs);
 }
 
 template <int MODE, int CG>
@@ -204,10 +154,8 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     __shared__ uint32_t tmem_slot;
     __shared__ int expired;
     __shared__ int so[kSegCap + 1], tp[kSegCap + 1], pad[MODE == kGrad ? kSegCap + 1 : 1];
-    __shared__ __align__(16) float cs[2][kScaleKB][kTileN];    // scales of the columns, see scale_at; kProduct: of the
-                                                               // rows, times each half's weight scale
-    __shared__ float rsc[MODE == kGrad ? 2 : 1][kScaleKB][kTileM];      // gradient: scales of the rows
-    __shared__ __align__(128) unsigned char outs[MODE == kGrad ? 16 : kSumWarps * kStageOut];
+    __shared__ float cs[MODE == kProduct ? 2 : 1][kScaleKB][kTileN];    // scales of the rows times each half's weight scale
+    __shared__ __align__(128) unsigned char outs[kSumWarps * kStageOut];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CG == 2 ? tc::cluster_rank() : 0;
     const int first = blockIdx.x / CG, step = gridDim.x / CG;
@@ -215,7 +163,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     if (warp == kSumWarps + 1) tc::tmem_alloc<CG>(&tmem_slot, kTmemCols);
     if (tid == 0) {
         for (int s = 0; s < g.stages; ++s) {
-            tc::mbar_init(&full[s], 1);
+            tc::mbar_init(&full[s], MODE == kGrad ? 3 : 1);      // gradient: and the two scale warps
             tc::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -232,6 +180,8 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
         tc::tma_prefetch(&map_m);
         tc::tma_prefetch(&map_n);
     }
+    pdl_trigger();
+    pdl_wait();                                    // everything read or written from here on
     // the segments' row offsets, then the exclusive prefix of their tile counts;
     // a segment outside the layout or without weights has no tiles and is reported
     for (int i = tid; i <= g.nseg; i += kThreads) so[i] = __ldg(g.seg_off + i);
@@ -292,7 +242,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     tc::fence_after();
 
     if (warp >= kSumWarps) {
-        tc::regs_dec<kIoRegs<MODE>>();
+        tc::regs_dec<kIoRegs>();
         const uint32_t tmem = tmem_slot;
         const int ntiles = tp[g.nseg];
         if (warp == kSumWarps) {
@@ -305,8 +255,8 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 const int ym = q.m0 + (int)rank * kTileM;
                 const int nh = q.ncols / CG;                                // this CTA's columns
                 const int yn = (MODE == kProduct ? q.w * g.N : 0) + q.n0 + (int)rank * nh;
-                const int boxes = (nh + g.box - 1) / g.box;
-                const uint32_t bytes = CG * (kABytes + (uint32_t)(boxes * g.box) * kKB);
+                const int boxes = (nh + kTileM - 1) / kTileM;               // 128 of them to a load
+                const uint32_t bytes = CG * (kABytes + (uint32_t)(boxes * kTileM) * kKB);
                 for (int kb = 0; kb < q.nkb; ++kb) {
                     if (fill > 0 && !tc::mbar_wait(&empty[s], (uint32_t)(fill - 1) & 1u)) {
                         ok = false;
@@ -320,7 +270,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                         if (rank == 0) tc::mbar_expect_tx(tc::smem_u32(&full[s]), bytes);
                         tc::tma_load<CG>(a, &map_m, x, ym, bar);
                         for (int c = 0; c < boxes; ++c)
-                            tc::tma_load<CG>(b + (uint32_t)(c * g.box) * kKB, &map_n, x, yn + c * g.box, bar);
+                            tc::tma_load<CG>(b + (uint32_t)(c * kTileM) * kKB, &map_n, x, yn + c * kTileM, bar);
                     }
                     __syncwarp();
                     if (++s == g.stages) {
@@ -344,14 +294,18 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             }
         } else if (warp == kSumWarps + 1 && rank == 0) {
             // ----------------------------------------------------------- issuer
-            int s = 0, fill = 0, it = 0;
+            int s = 0, fill = 0, it = 0;               // it: accumulators handed on
             bool ok = true;
             for (int t = first; t < ntiles && ok; t += step) {
                 const Tile q = find_tile<MODE, CG>(g, tp, so, pad, t);
-                const uint32_t idesc = tc::idesc_e4m3(CG * kTileM, q.ncols);
-                for (int kb = 0; kb < q.nkb; ++kb, ++it) {
-                    const int b = it & 1, round = it >> 1;
-                    if ((round > 0 && !tc::mbar_wait(&acc_empty[b], (uint32_t)(round - 1) & 1u)) ||
+                const uint32_t idesc = MODE == kGrad ? tc::idesc_scaled(kTileM, q.ncols) : tc::idesc_e4m3(CG * kTileM, q.ncols);
+                for (int kb = 0; kb < q.nkb; ++kb) {
+                    // the product hands a block on in turn in two accumulators, the gradient
+                    // kFlush blocks in one
+                    const int b = MODE == kGrad ? 0 : it & 1, round = MODE == kGrad ? it : it >> 1;
+                    const bool begin = MODE != kGrad || kb % kFlush == 0;
+                    const bool end = MODE != kGrad || kb % kFlush == kFlush - 1 || kb + 1 == q.nkb;
+                    if ((begin && round > 0 && !tc::mbar_wait(&acc_empty[b], (uint32_t)(round - 1) & 1u)) ||
                         !tc::mbar_wait(&full[s], (uint32_t)fill & 1u)) {
                         ok = false;
                         break;
@@ -360,13 +314,24 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     const uint32_t a = tc::smem_u32(ring) + (uint32_t)s * g.stage_bytes;
                     if (tc::elect()) {
                         const uint64_t dm = tc::smem_desc(a), dn = tc::smem_desc(a + kABytes);
+                        if (MODE == kGrad) {
+                            const uint32_t sf = a + kABytes + kTileN * kKB, ts = tmem + kTileN + (uint32_t)(kb & 1) * 16;
+                            tc::copy_scales(ts, sf);
+                            tc::copy_scales(ts + 4, sf + 512);
+                            tc::copy_scales(ts + 8, sf + 1024);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)            // 32 bytes on within the swizzled row
-                            tc::mma_e4m3<CG>(tmem + (uint32_t)(b * kTileN), dm + 2 * j, dn + 2 * j, idesc, j > 0);
+                            for (int j = 0; j < 4; ++j)
+                                tc::mma_scaled(tmem, dm + 2 * j, dn + 2 * j, idesc, ts, ts + 4, !begin || j > 0);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)        // 32 bytes on within the swizzled row
+                                tc::mma_e4m3<CG>(tmem + (uint32_t)(b * kTileN), dm + 2 * j, dn + 2 * j, idesc, j > 0);
+                        }
                         tc::mma_commit<CG>(tc::smem_u32(&empty[s]));
-                        tc::mma_commit<CG>(tc::smem_u32(&acc_full[b]));
+                        if (end) tc::mma_commit<CG>(tc::smem_u32(&acc_full[b]));
                     }
                     __syncwarp();
+                    it += end;
                     if (++s == g.stages) {
                         s = 0;
                         ++fill;
@@ -380,83 +345,87 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
         } else if (warp >= kSumWarps + 2) {
             // ----------------------------------------------------------- scales
             const int sl = tid - (kSumWarps + 2) * 32;           // 0 .. 63
-            int gi = 0;
+            int gi = 0, s = 0, fill = 0;
             bool ok = true;
             for (int t = first; t < ntiles && ok; t += step) {
                 const Tile q = find_tile<MODE, CG>(g, tp, so, pad, t);
                 const int m1 = q.m0 + (int)rank * kTileM;
-                for (int kb = 0; kb < q.nkb; kb += kScaleKB, ++gi) {
+                for (int kb = 0; kb < q.nkb && ok; kb += kScaleKB, ++gi) {
                     const int slot = gi & 1, nk = min(kScaleKB, q.nkb - kb);
-                    constexpr int kCols = MODE == kProduct ? kTileM / 64 : kTileN / 64;
-                    float v[kCols][kScaleKB], w[2][kScaleKB], r[2][kScaleKB];
-                    if (MODE != kGrad) {
-                        // weight scales of the two halves of the columns
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int nb = min(q.n0 / 128 + h, g.NB - 1);
-                            const float *wp = g.w_scale + ((int64_t)q.w * g.NB + nb) * g.KB + kb;
-#pragma unroll
-                            for (int u = 0; u < kScaleKB; ++u) w[h][u] = u < nk ? __ldg(wp + u) : 0.f;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i) {
-                        const int col = sl + 64 * i;
-#pragma unroll
-                        for (int u = 0; u < kScaleKB; ++u) v[i][u] = 0.f;
-                        if (MODE == kGrad) {
-                            const float *p = g.x_scale + (int64_t)(q.kb0 + kb) * g.K + q.n0 + col;
-                            if (col < q.nlim) {
-#pragma unroll
-                                for (int u = 0; u < kScaleKB; ++u)
-                                    if (u < nk) v[i][u] = __ldg(p + (int64_t)u * g.K);
-                            }
-                        } else {
-                            const bool in = (int)rank * kTileM + col < q.mlim;
-                            const float *p = g.x_scale + (int64_t)(m1 + col) * g.KB + kb;
-                            if (in && g.vec_scale) {
-                                const float4 f = __ldg(reinterpret_cast<const float4 *>(p));
-                                v[i][0] = f.x;
-                                v[i][1] = f.y;
-                                v[i][2] = f.z;
-                                v[i][3] = f.w;
-                            } else if (in) {
-#pragma unroll
-                                for (int u = 0; u < kScaleKB; ++u)
-                                    if (u < nk) v[i][u] = __ldg(p + u);
-                            }
-                        }
-                    }
                     if (MODE == kGrad) {
+                        // exponents of the scales, powers of two, into the stages: a row's byte
+                        // four times over, once for each step of 32
+                        uint32_t v[6][kScaleKB];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float *p = g.w_scale + (int64_t)(q.kb0 + kb) * g.N + m1 + sl + 64 * i;
+                        for (int i = 0; i < 6; ++i) {
+                            const int r = sl + 64 * (i & 1) + 128 * ((i >> 1) - 1);      // row, or column from i = 2 on
+                            const bool in = i < 2 ? sl + 64 * i < q.mlim : r < q.nlim;
+                            const float *p = i < 2 ? g.w_scale + (int64_t)(q.kb0 + kb) * g.N + m1 + sl + 64 * i
+                                                   : g.x_scale + (int64_t)(q.kb0 + kb) * g.K + q.n0 + r;
+                            const int64_t ld = i < 2 ? g.N : g.K;
 #pragma unroll
                             for (int u = 0; u < kScaleKB; ++u)
-                                r[i][u] = u < nk && m1 + sl + 64 * i < g.N ? __ldg(p + (int64_t)u * g.N) : 0.f;
+                                v[i][u] = in && u < nk ? __float_as_uint(__ldg(p + u * ld)) : 0x3f800000u;
+                        }
+#pragma unroll
+                        for (int u = 0; u < kScaleKB; ++u) {
+                            if (u < nk) {
+                                if (fill > 0) ok = ok && tc::mbar_wait(&empty[s], (uint32_t)(fill - 1) & 1u);
+                                ok = __all_sync(0xffffffffu, ok);
+                                if (!ok) break;
+                                const uint32_t at = (uint32_t)s * g.stage_bytes + kABytes + kTileN * kKB;
+#pragma unroll
+                                for (int i = 0; i < 6; ++i) {
+                                    const int r = sl + 64 * (i & 1);
+                                    *reinterpret_cast<uint32_t *>(ring + at + (i >> 1) * 512 + (r & 31) * 16 + (r >> 5) * 4) =
+                                        ((v[i][u] >> 23) & 0xffu) * 0x01010101u;
+                                }
+                                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                                __syncwarp();
+                                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&full[s]));
+                                if (++s == g.stages) {
+                                    s = 0;
+                                    ++fill;
+                                }
+                            }
+                        }
+                        continue;
+                    }
+                    float v[2][kScaleKB], w[2][kScaleKB];
+                    // weight scales of the two halves of the columns, scales of two rows
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int nb = min(q.n0 / 128 + h, g.NB - 1), row = sl + 64 * h;
+                        const float *wp = g.w_scale + ((int64_t)q.w * g.NB + nb) * g.KB + kb;
+                        const float *p = g.x_scale + (int64_t)(m1 + row) * g.KB + kb;
+                        const bool in = (int)rank * kTileM + row < q.mlim;
+#pragma unroll
+                        for (int u = 0; u < kScaleKB; ++u) {
+                            w[h][u] = u < nk ? __ldg(wp + u) : 0.f;
+                            v[h][u] = 0.f;
+                        }
+                        if (in && g.vec_scale) {
+                            const float4 f = __ldg(reinterpret_cast<const float4 *>(p));
+                            v[h][0] = f.x;
+                            v[h][1] = f.y;
+                            v[h][2] = f.z;
+                            v[h][3] = f.w;
+                        } else if (in) {
+#pragma unroll
+                            for (int u = 0; u < kScaleKB; ++u)
+                                if (u < nk) v[h][u] = __ldg(p + u);
                         }
                     }
                     if (gi >= 2) ok = tc::mbar_wait(&sc_empty[slot], (uint32_t)((gi >> 1) - 1) & 1u);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i)
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int u = 0; u < kScaleKB; ++u) {
-                            const int col = sl + 64 * i;
-                            if (MODE == kProduct) {
-                                cs[slot][u][col] = v[i][u] * w[0][u];
-                                cs[slot][u][128 + col] = v[i][u] * w[1][u];
-                            } else {
-                                cs[slot][u][scale_at(col)] = v[i][u];
-                            }
+                            cs[slot][u][sl + 64 * h] = v[h][u] * w[0][u];
+                            cs[slot][u][128 + sl + 64 * h] = v[h][u] * w[1][u];
                         }
-                    if (MODE == kGrad) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int u = 0; u < kScaleKB; ++u) rsc[slot][u][sl + 64 * i] = r[i][u];
-                    }
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sc_full[slot]));
                 }
@@ -464,7 +433,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             if (!ok && lane == 0) atomicExch(&expired, 1);
         }
     } else {
-        tc::regs_inc<kSumRegs<MODE>>();
+        tc::regs_inc<kSumRegs>();
         const uint32_t tmem = tmem_slot;
         const int ntiles = tp[g.nseg];
         // --------------------------------------------------- scale, add and store
@@ -487,93 +456,78 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             Acc acc;
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-            for (int kb = 0; kb < nkb; ++kb, ++it) {
-                const int b = it & 1, u = kb & (kScaleKB - 1), slot = gi & 1;
-                if (u == 0) tc::mbar_wait_or(&sc_full[slot], (uint32_t)(gi >> 1) & 1u, &expired);
-                float rs[4] = {1.f, 1.f, 1.f, 1.f};
-                if (MODE == kProduct) rs[0] = cs[slot][u][c0 + wq * 32 + lane];
-                if (MODE == kGrad) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) rs[i] = rsc[MODE == kGrad ? slot : 0][u][wq * 32 + 8 * i + r8];
+            constexpr int kStep = MODE == kGrad ? kFlush : 1;
+            for (int kb = 0; kb < nkb; kb += kStep, ++it) {
+                const int b = MODE == kGrad ? 0 : it & 1, round = MODE == kGrad ? it : it >> 1;
+                const int u = kb & (kScaleKB - 1), slot = gi & 1;
+                float scale = 1.f;
+                if (MODE == kProduct) {
+                    if (u == 0) tc::mbar_wait_or(&sc_full[slot], (uint32_t)(gi >> 1) & 1u, &expired);
+                    scale = cs[MODE == kProduct ? slot : 0][u][c0 + wq * 32 + lane];
                 }
-                tc::mbar_wait_or(&acc_full[b], (uint32_t)(it >> 1) & 1u, &expired);
+                tc::mbar_wait_or(&acc_full[b], (uint32_t)round & 1u, &expired);
                 __syncwarp();
                 tc::fence_after();
-                const uint32_t ta = tmem + lanes + (uint32_t)(b * kTileN + c0);
-                if (ncol > 0) {
-                    if (MODE == kProduct) add_rows(acc, ta, rs[0]);
-                    else add_block(acc, ta, &cs[slot][u][c0 + 4 * quad], rs);
-                }
+                if (ncol > 0) add_rows(acc, tmem + lanes + (uint32_t)(b * kTileN + c0), scale);
                 tc::fence_before();
                 __syncwarp();
+                const bool last = MODE == kProduct && (u == kScaleKB - 1 || kb + 1 == nkb);
                 if (lane == 0) {
                     if (CG == 2) tc::mbar_arrive_cluster(done + 8 * b);
                     else tc::mbar_arrive(done + 8 * b);
-                    if (u == kScaleKB - 1 || kb + 1 == nkb) tc::mbar_arrive(tc::smem_u32(&sc_empty[slot]));
+                    if (last) tc::mbar_arrive(tc::smem_u32(&sc_empty[slot]));
                 }
-                gi += u == kScaleKB - 1 || kb + 1 == nkb;
+                gi += last;
             }
             if (*(volatile int *)&expired) continue;
             // found again rather than kept in registers over the loop
             const Tile q = find_tile<MODE, CG>(g, tp, so, pad, t);
             const int m1 = (int)rank * kTileM + wq * 32;         // this warp's first row, from m0
-            if (MODE == kProduct) {
-                if (g.out_bf16) {
-                    // 32 rows x 32 values at a time, turned through shared memory so that four
-                    // lanes store 64 neighbouring bytes: 16-byte pieces, piece index XOR (row / 2)
-                    unsigned char *w = outs + warp * kStageOut;
-                    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(g.out) + (int64_t)(q.m0 + m1 + r8) * g.N + q.n0 + c0 + 8 * quad;
+            // 32 rows x 64 bytes at a time, turned through shared memory so that four lanes
+            // store 64 neighbouring bytes: 16-byte pieces, piece index XOR (row / 2)
+            unsigned char *w = outs + warp * kStageOut;
+            const int swz = (lane >> 1) & 3;
+            const int64_t ld = MODE == kGrad ? g.K : g.N;
+            const int64_t row0 = MODE == kGrad ? (int64_t)(g.seg0 + q.seg) * g.N + q.m0 : q.m0;
+            const int64_t at = (row0 + m1 + r8) * ld + q.n0 + c0;
+            if (MODE == kProduct && g.out_bf16) {
+                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(g.out) + at + 8 * quad;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (c0 + 32 * c < q.nlim) {
-                            __syncwarp();
+                for (int c = 0; c < 4; ++c) {
+                    if (c0 + 32 * c < q.nlim) {
+                        __syncwarp();
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                *reinterpret_cast<uint4 *>(w + lane * 64 + ((i ^ ((lane >> 1) & 3)) * 16)) =
-                                    make_uint4(pack_bf16(acc[16 * c + 4 * i]), pack_bf16(acc[16 * c + 4 * i + 1]),
-                                               pack_bf16(acc[16 * c + 4 * i + 2]), pack_bf16(acc[16 * c + 4 * i + 3]));
-                            __syncwarp();
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<uint4 *>(w + lane * 64 + (i ^ swz) * 16) =
+                                make_uint4(pack_bf16(acc[16 * c + 4 * i]), pack_bf16(acc[16 * c + 4 * i + 1]),
+                                           pack_bf16(acc[16 * c + 4 * i + 2]), pack_bf16(acc[16 * c + 4 * i + 3]));
+                        __syncwarp();
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint4 v = *reinterpret_cast<const uint4 *>(w + (8 * i + r8) * 64 + ((quad ^ ((r8 >> 1) & 3)) * 16));
-                                if (m1 + 8 * i + r8 < q.mlim && c0 + 32 * c + 8 * quad < q.nlim)
-                                    *reinterpret_cast<uint4 *>(o + (int64_t)(8 * i) * g.N + 32 * c) = v;
-                            }
-                        }
-                    }
-                } else {
-                    unsigned char *w = outs + warp * kStageOut;
-                    float *o = static_cast<float *>(g.out) + (int64_t)(q.m0 + m1 + r8) * g.N + q.n0 + c0 + 4 * quad;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        if (c0 + 16 * c < q.nlim) {
-                            __syncwarp();
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                *reinterpret_cast<float4 *>(w + lane * 64 + ((i ^ ((lane >> 1) & 3)) * 16)) =
-                                    make_float4(acc[8 * c + 2 * i].x, acc[8 * c + 2 * i].y, acc[8 * c + 2 * i + 1].x, acc[8 * c + 2 * i + 1].y);
-                            __syncwarp();
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float4 v = *reinterpret_cast<const float4 *>(w + (8 * i + r8) * 64 + ((quad ^ ((r8 >> 1) & 3)) * 16));
-                                if (m1 + 8 * i + r8 < q.mlim) *reinterpret_cast<float4 *>(o + (int64_t)(8 * i) * g.N + 16 * c) = v;
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(w + (8 * i + r8) * 64 + ((quad ^ ((r8 >> 1) & 3)) * 16));
+                            if (m1 + 8 * i + r8 < q.mlim && c0 + 32 * c + 8 * quad < q.nlim)
+                                *reinterpret_cast<uint4 *>(o + (int64_t)(8 * i) * ld + 32 * c) = v;
                         }
                     }
                 }
-            } else if (MODE == kGrad) {
-                // four lanes store 32 neighbouring bytes of a row
-                float *o = static_cast<float *>(g.out) + ((int64_t)(g.seg0 + q.seg) * g.N + q.m0 + m1 + r8) * g.K + q.n0 + c0 + 2 * quad;
+            } else {
+                float *o = static_cast<float *>(g.out) + at + 4 * quad;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int c = 0; c < 8; ++c) {
+                    if (c0 + 16 * c < q.nlim) {
+                        __syncwarp();
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        if (m1 + 16 * h + 8 * r + r8 < q.mlim) {
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<float4 *>(w + lane * 64 + (i ^ swz) * 16) =
+                                make_float4(acc[8 * c + 2 * i].x, acc[8 * c + 2 * i].y, acc[8 * c + 2 * i + 1].x, acc[8 * c + 2 * i + 1].y);
+                        __syncwarp();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (c0 + 8 * j < q.nlim)
-                                    *reinterpret_cast<float2 *>(o + (int64_t)(16 * h + 8 * r) * g.K + 8 * j) = acc[(h * 16 + j) * 2 + r];
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 v = *reinterpret_cast<const float4 *>(w + (8 * i + r8) * 64 + ((quad ^ ((r8 >> 1) & 3)) * 16));
+                            if (m1 + 8 * i + r8 < q.mlim) *reinterpret_cast<float4 *>(o + (int64_t)(8 * i) * ld + 16 * c) = v;
                         }
+                    }
+                }
             }
         }
     }
@@ -621,8 +575,9 @@ cudaError_t make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t col
 template <int MODE, int CG>
 cudaError_t run_experts(GemmArgs g, int nseg, const int32_t *seg_off, const int32_t *seg_w, const CUtensorMap &mm,
                         const CUtensorMap &mn, cudaStream_t st) {
-    g.stage_bytes = kABytes + (uint32_t)(g.nt / CG) * kKB;
+    g.stage_bytes = kABytes + (uint32_t)(kTileN / CG) * kKB;
     g.stages = std::min<int>(kMaxStages, (int)(kRingBytes / g.stage_bytes));
+    if (MODE == kGrad) g.stage_bytes += 2048;      // scales, the stages on 1024-byte boundaries
     const size_t smem = (size_t)g.stages * g.stage_bytes;
     cudaError_t e = ensure_smem((const void *)k_experts<MODE, CG>, smem);
     if (e != cudaSuccess) return e;
@@ -631,12 +586,14 @@ cudaError_t run_experts(GemmArgs g, int nseg, const int32_t *seg_off, const int3
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = CG;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     for (int s0 = 0; s0 < nseg; s0 += kSegCap) {
         g.nseg = std::min(kSegCap, nseg - s0);
         g.seg0 = s0;
@@ -670,8 +627,6 @@ cudaError_t launch_expert_gemm(int nseg, int64_t rows, int n_w, int N, int K, co
     // per expert, one CTA / a pair: 24: 146 / 179 us; 96: 171 / 185; 128: 191 / 201;
     // 192: 239 / 218; 256: 299 / 254
     const bool pair = rows / nseg > 144;
-    g.nt = kTileN;
-    g.box = kTileM;
     CUtensorMap mx, mw;
     cudaError_t e;
     if ((e = make_map(&mx, a, rows, K, kTileM)) != cudaSuccess) return e;
@@ -693,13 +648,11 @@ cudaError_t launch_expert_wgrad(int nseg, int64_t rows, int N, int K, int64_t ca
     g.cap = cap;
     g.N = N;
     g.K = K;
-    g.nt = kTileN;
-    g.box = kTileM;
     CUtensorMap my, mx;
     cudaError_t e;
     if ((e = make_map(&my, dy, N, cap, kTileM)) != cudaSuccess) return e;
-    if ((e = make_map(&mx, x, K, cap, g.box)) != cudaSuccess) return e;
-    return run_experts<kGrad, 2>(g, nseg, seg_off, nullptr, my, mx, st);
+    if ((e = make_map(&mx, x, K, cap, kTileM)) != cudaSuccess) return e;
+    return run_experts<kGrad, 1>(g, nseg, seg_off, nullptr, my, mx, st);
 }
 
 }  // namespace topo

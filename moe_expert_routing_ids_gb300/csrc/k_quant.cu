@@ -26,7 +26,7 @@
 namespace topo {
 namespace {
 
-enum { kPlain = 0, kDispatch = 1, kSwiglu = 2 };
+enum { kPlain = 0, kScatter = 1, kSwiglu = 2, kGather = 3 };
 
 // Scale of a block whose largest finite magnitude is amax, and its inverse.
 __device__ __forceinline__ float scale_of(float amax, float &inv) {
@@ -80,15 +80,17 @@ __device__ __forceinline__ uint4 quant16(const float (&v)[16], float inv) {
     return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
+constexpr int64_t kGatherBytes = 32 << 20;        // token rows that a dispatch reads k times
+
 struct QuantArgs {
     const uint4 *x;          // bf16 rows, two uint4 per 16 values
-    const int32_t *inv;      // kDispatch: position of each pair
+    const int32_t *inv;      // kScatter: position of each pair; kGather: pair of each position
     uint4 *q;                // e4m3 rows
     float *scale;            // [rows][KB]
     WsHeader *hdr;
-    int64_t rows;            // source rows over all layers
+    int64_t rows;            // rows over all layers (kGather: output rows)
     int64_t npairs;
-    int T, k;                // kDispatch: tokens per layer, copies of a row
+    int T, k;                // kScatter, kGather: tokens per layer, copies of a row
     int nv;                  // 16-value groups per (output) row
     int KB;
     int parts, per;          // a row is split over `parts` warps of `per` groups of 32 lanes
@@ -103,8 +105,19 @@ k_quant_rows(QuantArgs g) {
     const int part = (int)(unit - row * g.parts);
     const int lane = threadIdx.x & 31;
     int pa = 0, pb = 0;
-    int64_t base = 0;
-    if (SRC == kDispatch) {
+    int64_t base = 0, from = row;
+    pdl_trigger();
+    pdl_wait();
+    if (SRC == kGather) {
+        const int64_t l = row / g.npairs;
+        const int p = __ldg(g.inv + row);
+        if ((uint64_t)p >= (uint64_t)g.npairs) {
+            if (lane == 0) set_error(g.hdr, TOPO_ESTATE);
+            return;
+        }
+        from = l * g.T + p / g.k;
+    }
+    if (SRC == kScatter) {
         base = (row / g.T) * g.npairs;
         const int32_t *iv = g.inv + row * g.k;
         pa = lane < g.k ? __ldg(iv + lane) : 0;
@@ -129,8 +142,9 @@ k_quant_rows(QuantArgs g) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(__fdiv_rn(v[i], __fadd_rn(1.f, expf(-v[i]))), u[i]);
         } else {
-            const uint4 *src = g.x + row * (2 * (int64_t)g.nv);
-            unpack16(in ? __ldcs(src + 2 * c) : z, in ? __ldcs(src + 2 * c + 1) : z, v);
+            const uint4 *src = g.x + from * (2 * (int64_t)g.nv);
+            if (SRC == kGather) unpack16(in ? __ldg(src + 2 * c) : z, in ? __ldg(src + 2 * c + 1) : z, v);
+            else unpack16(in ? __ldcs(src + 2 * c) : z, in ? __ldcs(src + 2 * c + 1) : z, v);
         }
         float m = amax16(v);
 #pragma unroll
@@ -138,7 +152,7 @@ k_quant_rows(QuantArgs g) {
         float iv;
         const float s = scale_of(m, iv);
         const uint4 q = quant16(v, iv);
-        if (SRC == kDispatch) {
+        if (SRC == kScatter) {
             for (int j = 0; j < g.k; ++j) {
                 const int a = __shfl_sync(0xffffffffu, pa, j & 31), b = __shfl_sync(0xffffffffu, pb, j & 31);
                 const int64_t r = base + (j < 32 ? a : b);
@@ -156,6 +170,8 @@ k_quant_rows(QuantArgs g) {
 
 __global__ void __launch_bounds__(256)
 k_swiglu_grad(const uint4 *__restrict__ h, const uint4 *__restrict__ dy, uint4 *dh, int64_t n, int nv) {
+    pdl_trigger();
+    pdl_wait();
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t row = i / nv;
         const int64_t at = row * nv * 2 + (i - row * nv);
@@ -183,24 +199,50 @@ k_swiglu_grad(const uint4 *__restrict__ h, const uint4 *__restrict__ dy, uint4 *
     }
 }
 
-// Block (row block, 128 columns): warp w holds rows 16 w .. 16 w + 15, lane l
-// columns 4 l .. 4 l + 3; 16 rows of a column are one 16-byte piece of the
-// transposed row.  The pieces pass through shared memory (chunk index XOR the
-// lane, so that 8 lanes hit 8 bank groups) to leave in whole 128-byte rows.
-__global__ void __launch_bounds__(256)
+// Two bf16 magnitudes at a time.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
+// 16 rows of one column (bf16, in the low or high half of their words) as 16
+// e4m3 bytes.
+template <bool HI>
+__device__ __forceinline__ uint4 quant_col(const uint32_t (&v)[16], float inv, bool odd) {
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[j] = __uint_as_float(HI ? v[4 * i + j] & 0xffff0000u : v[4 * i + j] << 16);
+            if (odd && !finite(f[j])) f[j] = __int_as_float(0x7fffffff);
+            f[j] *= inv;
+        }
+        q[i] = cvt2(f[0], f[1]) | (cvt2(f[2], f[3]) << 16);
+    }
+    return make_uint4(q[0], q[1], q[2], q[3]);
+}
+
+// A CTA takes one row block and 128 columns at a time, the next ones' loads on
+// their way meanwhile: warp w holds rows 16 w .. 16 w + 15, lane l columns 4 l ..
+// 4 l + 3; 16 rows of a column are one 16-byte piece of the transposed row.  The
+// pieces pass through shared memory (piece index XOR the lane, so that 8 lanes
+// hit 8 bank groups) to leave in whole 128-byte rows.
+__global__ void __launch_bounds__(256, 2)
 k_quant_cols(const uint16_t *__restrict__ x, const int32_t *__restrict__ seg_off, uint8_t *q, float *scale, WsHeader *hdr,
              int nseg, int64_t rows, int C, int64_t cap) {
-    __shared__ uint4 tile[128 * 8];
-    __shared__ float wmax[8][128];
+    __shared__ uint4 tile[2][128 * 8];
+    __shared__ uint2 wmax[2][8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.x;
+    pdl_trigger();
+    pdl_wait();
     // the segment of padded block b
-    int seg = -1, first = 0, run = 0;
+    int seg = -1, r0 = 0, nrow = 0, run = 0;
     for (int i0 = 0; i0 < nseg && seg < 0; i0 += 32) {
         const int i = i0 + lane;
-        int n = 0;
+        int n = 0, a = 0, e = 0;
         if (i < nseg) {
-            const int a = __ldg(seg_off + i), e = __ldg(seg_off + i + 1);
+            a = __ldg(seg_off + i);
+            e = __ldg(seg_off + i + 1);
             if (a < 0 || e < a || e > rows) set_error(hdr, TOPO_ESTATE);
             else n = (e - a + 127) / 128;
         }
@@ -215,45 +257,70 @@ k_quant_cols(const uint16_t *__restrict__ x, const int32_t *__restrict__ seg_off
         if (hit) {
             const int w = __ffs(hit) - 1;
             seg = i0 + w;
-            first = __shfl_sync(0xffffffffu, lo, w);
+            r0 = __shfl_sync(0xffffffffu, a + (b - lo) * 128, w);
+            nrow = min(128, __shfl_sync(0xffffffffu, e, w) - r0);
         }
         run += __shfl_sync(0xffffffffu, s, 31);
     }
     if (seg < 0) return;                                          // past the last segment's blocks
-    const int r0 = __ldg(seg_off + seg) + (b - first) * 128;
-    const int nrow = min(128, __ldg(seg_off + seg + 1) - r0);
-    for (int c0 = blockIdx.y * 128; c0 < C; c0 += gridDim.y * 128) {
-        const int c = c0 + 4 * lane;
-        uint2 v[16];
+    const uint16_t *src = x + (int64_t)(r0 + 16 * warp) * C + 4 * lane;
+    uint2 nx[16];
+    auto load = [&](int c0) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            nx[r] = c0 + 4 * lane < C && 16 * warp + r < nrow
+                        ? __ldcs(reinterpret_cast<const uint2 *>(src + (int64_t)r * C + c0)) : make_uint2(0, 0);
+    };
+    int c0 = blockIdx.y * 128, s = 0;
+    if (c0 < C) load(c0);
+    for (; c0 < C; c0 += gridDim.y * 128, s ^= 1) {
+        uint32_t v0[16], v1[16];
+        uint2 m = make_uint2(0, 0);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int rr = 16 * warp + r;
-            v[r] = c < C && rr < nrow ? __ldcs(reinterpret_cast<const uint2 *>(x + (int64_t)(r0 + rr) * C + c)) : make_uint2(0, 0);
+            v0[r] = nx[r].x;
+            v1[r] = nx[r].y;
+            m.x = max2(m.x, v0[r] & 0x7fff7fffu);
+            m.y = max2(m.y, v1[r] & 0x7fff7fffu);
         }
-        float m[4] = {0.f, 0.f, 0.f, 0.f};
-        float f[4][16];
+        // some value of this warp's column is not finite: taken again without those
+        const bool odd = (m.x & 0x7fffu) >= 0x7f80u || (m.x >> 16) >= 0x7f80u || (m.y & 0x7fffu) >= 0x7f80u || (m.y >> 16) >= 0x7f80u;
+        if (odd) {
+            m = make_uint2(0, 0);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            f[0][r] = __uint_as_float(v[r].x << 16);
-            f[1][r] = __uint_as_float(v[r].x & 0xffff0000u);
-            f[2][r] = __uint_as_float(v[r].y << 16);
-            f[3][r] = __uint_as_float(v[r].y & 0xffff0000u);
+            for (int r = 0; r < 16; ++r) {
+                uint32_t a = v0[r] & 0x7fff7fffu, c = v1[r] & 0x7fff7fffu;
+                if ((a & 0x7fffu) >= 0x7f80u) a &= 0xffff0000u;
+                if ((a >> 16) >= 0x7f80u) a &= 0xffffu;
+                if ((c & 0x7fffu) >= 0x7f80u) c &= 0xffff0000u;
+                if ((c >> 16) >= 0x7f80u) c &= 0xffffu;
+                m.x = max2(m.x, a);
+                m.y = max2(m.y, c);
+            }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            m[j] = amax16(f[j]);
-            wmax[warp][4 * lane + j] = m[j];
-        }
+        if (c0 + (int)gridDim.y * 128 < C) load(c0 + gridDim.y * 128);
+        wmax[s][warp][lane] = m;
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float a = 0.f;
+        for (int w = 0; w < 8; ++w) {
+            const uint2 o = wmax[s][w][lane];
+            m.x = max2(m.x, o.x);
+            m.y = max2(m.y, o.y);
+        }
+        const int c = c0 + 4 * lane;
+        float iv[4], sc[4];
+        sc[0] = scale_of(__uint_as_float(m.x << 16), iv[0]);
+        sc[1] = scale_of(__uint_as_float(m.x & 0xffff0000u), iv[1]);
+        sc[2] = scale_of(__uint_as_float(m.y << 16), iv[2]);
+        sc[3] = scale_of(__uint_as_float(m.y & 0xffff0000u), iv[3]);
+        uint4 *t = tile[s] + 32 * lane + (warp ^ (lane & 7));
+        t[0] = quant_col<false>(v0, iv[0], odd);
+        t[8] = quant_col<true>(v0, iv[1], odd);
+        t[16] = quant_col<false>(v1, iv[2], odd);
+        t[24] = quant_col<true>(v1, iv[3], odd);
+        if (warp == 0 && c < C) {
 #pragma unroll
-            for (int w = 0; w < 8; ++w) a = fmaxf(a, wmax[w][4 * lane + j]);
-            float iv;
-            const float s = scale_of(a, iv);
-            tile[(4 * lane + j) * 8 + (warp ^ (lane & 7))] = quant16(f[j], iv);
-            if (warp == 0 && c + j < C) scale[(int64_t)b * C + c + j] = s;
+            for (int j = 0; j < 4; ++j) scale[(int64_t)b * C + c + j] = sc[j];
         }
         __syncthreads();
 #pragma unroll
@@ -261,9 +328,8 @@ k_quant_cols(const uint16_t *__restrict__ x, const int32_t *__restrict__ seg_off
             const int e = i * 256 + threadIdx.x, cc = e >> 3, ch = e & 7;
             if (c0 + cc < C)
                 *reinterpret_cast<uint4 *>(q + (int64_t)(c0 + cc) * cap + (int64_t)b * 128 + 16 * ch) =
-                    tile[cc * 8 + (ch ^ ((cc >> 2) & 7))];
+                    tile[s][cc * 8 + (ch ^ ((cc >> 2) & 7))];
         }
-        __syncthreads();
     }
 }
 
@@ -336,8 +402,7 @@ cudaError_t run_rows(QuantArgs a, cudaStream_t st) {
     a.per = a.rows * chunks <= 152 * 64 ? 1 : chunks;
     a.parts = (chunks + a.per - 1) / a.per;
     const int64_t units = a.rows * a.parts;
-    k_quant_rows<SRC><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(k_quant_rows<SRC>, dim3((unsigned)((units + 7) / 8)), dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -356,31 +421,40 @@ cudaError_t launch_quantize_rows(int64_t rows, int C, const uint16_t *x, uint8_t
 
 cudaError_t launch_permute_quantize(const Geo &g, int H, const uint16_t *x, const int32_t *sorted, uint8_t *q, float *scale,
                                     void *ws, cudaStream_t st) {
-    cudaError_t e;
-    if ((e = launch_invert(g, sorted, ws, st)) != cudaSuccess) return e;
     QuantArgs a = {};
     a.x = reinterpret_cast<const uint4 *>(x);
-    a.inv = ws_at<int32_t>(ws, g.off_pack_inv);
     a.q = reinterpret_cast<uint4 *>(q);
     a.scale = scale;
     a.hdr = ws_at<WsHeader>(ws, 0);
-    a.rows = (int64_t)g.L * g.T;
     a.npairs = g.npairs;
     a.T = g.T;
     a.k = g.k;
     a.nv = H / 16;
     a.KB = (H + 127) / 128;
-    return run_rows<kDispatch>(a, st);
+    // Position by position, one launch, while the token rows stay in L2 over their k
+    // reads; else token by token through the inverse permutation, each row read once.
+    if ((int64_t)g.L * g.T * H * 2 <= kGatherBytes) {
+        a.rows = (int64_t)g.L * g.npairs;
+        a.inv = sorted;
+        return run_rows<kGather>(a, st);
+    }
+    cudaError_t e;
+    if ((e = launch_invert(g, sorted, ws, st)) != cudaSuccess) return e;
+    a.rows = (int64_t)g.L * g.T;
+    a.inv = ws_at<int32_t>(ws, g.off_pack_inv);
+    return run_rows<kScatter>(a, st);
 }
 
 cudaError_t launch_quantize_cols(int nseg, int64_t rows, int C, const uint16_t *x, const int32_t *seg_off, int64_t cap,
                                  uint8_t *q, float *scale, void *ws, cudaStream_t st) {
     const int64_t blocks = cap / 128;
     const int cb = (C + 127) / 128;
-    const int split = (int)(blocks >= 152 * 8 ? (cb + 3) / 4 : cb);
-    k_quant_cols<<<dim3((unsigned)blocks, (unsigned)split), 256, 0, st>>>(x, seg_off, q, scale, ws_at<WsHeader>(ws, 0), nseg,
-                                                                         rows, C, cap);
-    return cudaGetLastError();
+    // two CTAs to an SM; finding the row block's segment costs two round trips to
+    // memory, so a CTA takes several column groups where there are enough CTAs
+    int64_t split = (152 * 8 + blocks - 1) / blocks;
+    if (split > cb) split = cb;
+    return launch_pdl(k_quant_cols, dim3((unsigned)blocks, (unsigned)split), dim3(256), 0, st, x, seg_off, q, scale,
+                      ws_at<WsHeader>(ws, 0), nseg, rows, C, cap);
 }
 
 cudaError_t launch_quantize_weight(int n_w, int N, int K, const uint16_t *w, uint8_t *q, float *scale, uint8_t *qt,
@@ -400,9 +474,8 @@ cudaError_t launch_swiglu_grad(int64_t rows, int I, const uint16_t *h, const uin
     const int64_t n = rows * nv;
     if (n == 0) return cudaSuccess;
     const int64_t want = (n + 255) / 256;
-    k_swiglu_grad<<<(unsigned)(want < 152 * 32 ? want : 152 * 32), 256, 0, st>>>(
-        reinterpret_cast<const uint4 *>(h), reinterpret_cast<const uint4 *>(dy), reinterpret_cast<uint4 *>(dh), n, nv);
-    return cudaGetLastError();
+    return launch_pdl(k_swiglu_grad, dim3((unsigned)(want < 152 * 32 ? want : 152 * 32)), dim3(256), 0, st,
+                      reinterpret_cast<const uint4 *>(h), reinterpret_cast<const uint4 *>(dy), reinterpret_cast<uint4 *>(dh), n, nv);
 }
 
 }  // namespace topo

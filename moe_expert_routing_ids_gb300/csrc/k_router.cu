@@ -321,6 +321,8 @@ k_route_experts(const __grid_constant__ RouteArgs g) {
     const unsigned gmask = G == 32 ? 0xffffffffu : (((1u << (G & 31)) - 1u) << (lane & ~(G - 1)));
     const int E = g.E, k = g.k, Ep = (E + 3) & ~3;
     float *sb = dyn;                                              // [Ep] bias
+    pdl_trigger();
+    pdl_wait();
     const RouteScratch w = {dyn + Ep + grp * Ep, keys_[grp], ce_[grp], sel_[grp], sx_[grp], gsc_[grp]};
     if (SIG) {
         for (int e = threadIdx.x; e < Ep; e += kRouteThreads) sb[e] = g.bias && e < E ? __ldg(g.bias + e) : 0.f;
@@ -611,6 +613,8 @@ k_route_grad(RouteGradArgs g) {
     const int64_t nw = (int64_t)gridDim.x * (blockDim.x >> 5);
     const int E = g.E, k = g.k;
     const bool soft = g.score == TOPO_SCORE_SOFTMAX, dense = soft && !g.renorm;
+    pdl_trigger();
+    pdl_wait();
     for (int64_t tok = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); tok < g.ntok; tok += nw) {
         const char *row = static_cast<const char *>(g.logits) + (size_t)tok * E * (BF ? 2 : 4);
         char *out = static_cast<char *>(g.dx) + (size_t)tok * E * (BF ? 2 : 4);
@@ -696,8 +700,7 @@ cudaError_t run_route(const RouteArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int64_t want = (a.ntok + kGroups - 1) / kGroups;
     const int64_t most = 152 * (VPL > 16 ? 3 : 4);                // the CTAs that run together
-    fn<<<(unsigned)(want < most ? want : most), kRouteThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(fn, dim3((unsigned)(want < most ? want : most)), dim3(kRouteThreads), smem, st, a);
 }
 
 template <int VPL, int G, bool BF, int VEC, bool FULL>
@@ -772,11 +775,9 @@ cudaError_t launch_route_grad(const topo_route_opts &o, int64_t ntok, int E, int
     const int64_t want = (ntok + 7) / 8;
     const unsigned blocks = (unsigned)(want < 152 * 32 ? want : 152 * 32);
     const bool v = ((uintptr_t)dx & 15) == 0 && ((size_t)E * (bf16 ? 2 : 4)) % 16 == 0;
-    if (bf16 && v) k_route_grad<true, true><<<blocks, 256, 0, st>>>(a);
-    else if (bf16) k_route_grad<true, false><<<blocks, 256, 0, st>>>(a);
-    else if (v) k_route_grad<false, true><<<blocks, 256, 0, st>>>(a);
-    else k_route_grad<false, false><<<blocks, 256, 0, st>>>(a);
-    return cudaGetLastError();
+    const auto fn = bf16 ? (v ? k_route_grad<true, true> : k_route_grad<true, false>)
+                         : (v ? k_route_grad<false, true> : k_route_grad<false, false>);
+    return launch_pdl(fn, dim3(blocks), dim3(256), 0, st, a);
 }
 
 }  // namespace topo
