@@ -48,7 +48,12 @@ constexpr int kTileM = 128;                       // rows of a CTA
 constexpr int kTileN = 256;
 constexpr int kSumWarps = 8;                      // warps that scale, add and store
 constexpr int kThreads = (kSumWarps + 4) * 32;    // two summing warpgroups, one of producer, issuer and two scale warps
-constexpr int kSumRegs = 208, kIoRegs = 88;       // 2 * 128 * 208 + 128 * 88 = 384 * 168, the launch's share
+// registers of a thread of the summing and of the other warpgroup; 2 * 128 times
+// the one and 128 times the other are the launch's share, 384 * 168
+template <int MODE>
+constexpr int kSumRegs = MODE == kProduct ? 224 : 208;
+template <int MODE>
+constexpr int kIoRegs = (384 * 168 - 256 * kSumRegs<MODE>) / 128;
 constexpr int kTmemCols = 512;                    // two accumulators of 256 columns
 constexpr uint32_t kABytes = kTileM * kKB;
 constexpr int kMaxStages = 9;
@@ -129,20 +134,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float2 v) {
 // Sums of a thread: acc[i] holds columns 2 i and 2 i + 1 of row `lane`.
 using Acc = float2[64];
 
-// acc += s * accumulator, 128 columns of this thread's row.  16 columns are read
-// while the 16 before them are added.
+// acc += s * accumulator, 128 columns of this thread's row.  NC columns are read
+// while the NC before them are added.
+template <int NC>
 __device__ __forceinline__ void add_rows(Acc &acc, uint32_t ta, float s) {
     const float2 s2 = make_float2(s, s);
-    uint32_t v[2][16];
+    uint32_t v[2][NC];
     tc::tmem_ld_rows(ta, v[0]);
     tc::tmem_wait(v[0]);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        if (c < 7) tc::tmem_ld_rows(ta + 16 * (c + 1), v[(c + 1) & 1]);
+    for (int c = 0; c < 128 / NC; ++c) {
+        const bool more = c + 1 < 128 / NC;
+        if (more) tc::tmem_ld_rows(ta + NC * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            tc::fma2(acc[8 * c + i], make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2);
-        if (c < 7) tc::tmem_wait(v[(c + 1) & 1]);
+        for (int i = 0; i < NC / 2; ++i)
+            tc::fma2(acc[NC / 2 * c + i], make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2);
+        if (more) tc::tmem_wait(v[(c + 1) & 1]);
     }
 }
 
@@ -242,7 +249,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     tc::fence_after();
 
     if (warp >= kSumWarps) {
-        tc::regs_dec<kIoRegs>();
+        tc::regs_dec<kIoRegs<MODE>>();
         const uint32_t tmem = tmem_slot;
         const int ntiles = tp[g.nseg];
         if (warp == kSumWarps) {
@@ -288,8 +295,8 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     if (n > 0 && !tc::mbar_wait(&full[i], (uint32_t)(n - 1) & 1u)) atomicExch(&expired, 1);
                 }
             } else if (!ok) {
-                const uint64_t t0 = tc::globaltimer_ns();
-                while (tc::globaltimer_ns() - t0 < 10000000ull) {
+                const uint32_t t0 = tc::clock_ns();
+                while (tc::clock_ns() - t0 < 10000000u) {
                 }
             }
         } else if (warp == kSumWarps + 1 && rank == 0) {
@@ -433,7 +440,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             if (!ok && lane == 0) atomicExch(&expired, 1);
         }
     } else {
-        tc::regs_inc<kSumRegs>();
+        tc::regs_inc<kSumRegs<MODE>>();
         const uint32_t tmem = tmem_slot;
         const int ntiles = tp[g.nseg];
         // --------------------------------------------------- scale, add and store
@@ -444,6 +451,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
         uint32_t done = tc::smem_u32(&acc_empty[0]);     // the even CTA's
         if (CG == 2) done = tc::in_cta(done, 0);
         int it = 0, gi = 0;
+        bool live = true;
         // an expired wait lets these warps run on without waiting (and without
         // storing), so that they reach the end with the rest of the CTA
         for (int t = first; t < ntiles; t += step) {
@@ -462,13 +470,13 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 const int u = kb & (kScaleKB - 1), slot = gi & 1;
                 float scale = 1.f;
                 if (MODE == kProduct) {
-                    if (u == 0) tc::mbar_wait_or(&sc_full[slot], (uint32_t)(gi >> 1) & 1u, &expired);
+                    if (live && u == 0) live = tc::mbar_wait_tries(&sc_full[slot], (uint32_t)(gi >> 1) & 1u);
                     scale = cs[MODE == kProduct ? slot : 0][u][c0 + wq * 32 + lane];
                 }
-                tc::mbar_wait_or(&acc_full[b], (uint32_t)round & 1u, &expired);
+                if (live) live = tc::mbar_wait_tries(&acc_full[b], (uint32_t)round & 1u);
                 __syncwarp();
                 tc::fence_after();
-                if (ncol > 0) add_rows(acc, tmem + lanes + (uint32_t)(b * kTileN + c0), scale);
+                if (ncol > 0) add_rows<MODE == kProduct ? 32 : 16>(acc, tmem + lanes + (uint32_t)(b * kTileN + c0), scale);
                 tc::fence_before();
                 __syncwarp();
                 const bool last = MODE == kProduct && (u == kScaleKB - 1 || kb + 1 == nkb);
@@ -479,7 +487,8 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 }
                 gi += last;
             }
-            if (*(volatile int *)&expired) continue;
+            live = __all_sync(0xffffffffu, live);
+            if (!live) continue;
             // found again rather than kept in registers over the loop
             const Tile q = find_tile<MODE, CG>(g, tp, so, pad, t);
             const int m1 = (int)rank * kTileM + wq * 32;         // this warp's first row, from m0
@@ -530,6 +539,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 }
             }
         }
+        if (!live) atomicExch(&expired, 1);
     }
     tc::fence_before();
     __syncthreads();

@@ -11,13 +11,15 @@
 namespace topo {
 namespace tc {
 
-constexpr uint64_t kWaitNs = 1000000000ull;   // longest mbarrier wait: 1 s of %globaltimer
+constexpr uint32_t kWaitNs = 1000000000u;     // longest mbarrier wait: 1 s of %globaltimer
+constexpr int kWaitTries = 1 << 22;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ uint64_t globaltimer_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+// Low word of the nanosecond clock; differences hold up to 4 s.
+__device__ __forceinline__ uint32_t clock_ns() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
     return t;
 }
 
@@ -39,10 +41,10 @@ __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
         " selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(1000)
         : "memory");
     return ok != 0;
 }
@@ -51,31 +53,22 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
     const uint32_t a = smem_u32(bar);
     if (mbar_try(a, parity)) return true;
-    const uint64_t start = globaltimer_ns();
-    for (;;) {
+    const uint32_t start = clock_ns();
 #pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try(a, parity)) return true;
-        if (globaltimer_ns() - start > kWaitNs) return false;
-    }
+    while (clock_ns() - start < kWaitNs)
+        if (mbar_try(a, parity)) return true;
+    return false;
 }
 
-// The same for a role that goes on regardless: an expired wait raises *expired,
-// and once that is raised no wait of the CTA lasts.
-__device__ __forceinline__ void mbar_wait_or(uint64_t *bar, uint32_t parity, volatile int *expired) {
+// The same, at most kWaitTries tries (a try suspends the thread for about a
+// microsecond at the longest): without the clock the summing loop keeps all of
+// its values in registers.
+__device__ __forceinline__ bool mbar_wait_tries(uint64_t *bar, uint32_t parity) {
     const uint32_t a = smem_u32(bar);
-    if (mbar_try(a, parity)) return;
-    const uint64_t start = globaltimer_ns();
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try(a, parity)) return;
-        if (*expired) return;
-        if (globaltimer_ns() - start > kWaitNs) {
-            *expired = 1;
-            return;
-        }
+    int left = kWaitTries;
+    while (!mbar_try(a, parity) && --left) {
     }
+    return left != 0;
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
@@ -228,8 +221,17 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 16 consecutive float32 columns of this warp's 32 tensor-memory lanes, lane l
-// holding row l; valid after tmem_wait().
+// 32 or 16 consecutive float32 columns of this warp's 32 tensor-memory lanes,
+// lane l holding row l; valid after tmem_wait(), the completion of this thread's
+// loads.  The values pass through that statement so that no use of them moves
+// above it.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+
 __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&v)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -237,8 +239,11 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&v)[16]) 
         : "r"(taddr));
 }
 
-// Completion of this thread's tensor-memory loads; the values pass through the
-// statement so that no use of them moves above it.
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
+}
+
 __device__ __forceinline__ void tmem_wait(uint32_t (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
