@@ -157,7 +157,7 @@ template <int MODE, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUtensorMap map_n, GemmArgs g) {
     extern __shared__ __align__(1024) unsigned char ring[];
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], sc_full[2], sc_empty[2], drained;
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], scaled[kMaxStages], acc_full[2], acc_empty[2], sc_full[2], sc_empty[2], drained;
     __shared__ uint32_t tmem_slot;
     __shared__ int expired;
     __shared__ int so[kSegCap + 1], tp[kSegCap + 1], pad[MODE == kGrad ? kSegCap + 1 : 1];
@@ -170,7 +170,8 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     if (warp == kSumWarps + 1) tc::tmem_alloc<CG>(&tmem_slot, kTmemCols);
     if (tid == 0) {
         for (int s = 0; s < g.stages; ++s) {
-            tc::mbar_init(&full[s], MODE == kGrad ? 3 : 1);      // gradient: and the two scale warps
+            tc::mbar_init(&full[s], 1);
+            tc::mbar_init(&scaled[s], 1);
             tc::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -263,7 +264,10 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 const int nh = q.ncols / CG;                                // this CTA's columns
                 const int yn = (MODE == kProduct ? q.w * g.N : 0) + q.n0 + (int)rank * nh;
                 const int boxes = (nh + kTileM - 1) / kTileM;               // 128 of them to a load
-                const uint32_t bytes = CG * (kABytes + (uint32_t)(boxes * kTileM) * kKB);
+                uint32_t bytes = CG * (kABytes + (uint32_t)(boxes * kTileM) * kKB);
+                // gradient: the scales of the tile's rows and columns, whole pieces of 16
+                const uint32_t ms = MODE == kGrad ? 4u * (uint32_t)q.mlim : 0u, ns = MODE == kGrad ? 4u * (uint32_t)q.nlim : 0u;
+                bytes += ms + ns;
                 for (int kb = 0; kb < q.nkb; ++kb) {
                     if (fill > 0 && !tc::mbar_wait(&empty[s], (uint32_t)(fill - 1) & 1u)) {
                         ok = false;
@@ -278,6 +282,11 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                         tc::tma_load<CG>(a, &map_m, x, ym, bar);
                         for (int c = 0; c < boxes; ++c)
                             tc::tma_load<CG>(b + (uint32_t)(c * kTileM) * kKB, &map_n, x, yn + c * kTileM, bar);
+                        if (MODE == kGrad) {
+                            const uint32_t sf = b + kTileN * kKB;
+                            tc::bulk_load(sf, g.w_scale + (int64_t)(q.kb0 + kb) * g.N + q.m0, ms, bar);
+                            tc::bulk_load(sf + 512, g.x_scale + (int64_t)(q.kb0 + kb) * g.K + q.n0, ns, bar);
+                        }
                     }
                     __syncwarp();
                     if (++s == g.stages) {
@@ -313,7 +322,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     const bool begin = MODE != kGrad || kb % kFlush == 0;
                     const bool end = MODE != kGrad || kb % kFlush == kFlush - 1 || kb + 1 == q.nkb;
                     if ((begin && round > 0 && !tc::mbar_wait(&acc_empty[b], (uint32_t)(round - 1) & 1u)) ||
-                        !tc::mbar_wait(&full[s], (uint32_t)fill & 1u)) {
+                        !tc::mbar_wait(MODE == kGrad ? &scaled[s] : &full[s], (uint32_t)fill & 1u)) {
                         ok = false;
                         break;
                     }
@@ -322,10 +331,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     if (tc::elect()) {
                         const uint64_t dm = tc::smem_desc(a), dn = tc::smem_desc(a + kABytes);
                         if (MODE == kGrad) {
-                            const uint32_t sf = a + kABytes + kTileN * kKB, ts = tmem + kTileN + (uint32_t)(kb & 1) * 16;
-                            tc::copy_scales(ts, sf);
-                            tc::copy_scales(ts + 4, sf + 512);
-                            tc::copy_scales(ts + 8, sf + 1024);
+                            const uint32_t ts = tmem + kTileN + 16u * (uint32_t)s;
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 tc::mma_scaled(tmem, dm + 2 * j, dn + 2 * j, idesc, ts, ts + 4, !begin || j > 0);
@@ -352,52 +358,48 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
         } else if (warp >= kSumWarps + 2) {
             // ----------------------------------------------------------- scales
             const int sl = tid - (kSumWarps + 2) * 32;           // 0 .. 63
-            int gi = 0, s = 0, fill = 0;
+            int gi = 0, s = 0, fill = 0, it = 0;
             bool ok = true;
             for (int t = first; t < ntiles && ok; t += step) {
                 const Tile q = find_tile<MODE, CG>(g, tp, so, pad, t);
                 const int m1 = q.m0 + (int)rank * kTileM;
-                for (int kb = 0; kb < q.nkb && ok; kb += kScaleKB, ++gi) {
-                    const int slot = gi & 1, nk = min(kScaleKB, q.nkb - kb);
-                    if (MODE == kGrad) {
-                        // exponents of the scales, powers of two, into the stages: a row's byte
-                        // four times over, once for each step of 32
-                        uint32_t v[6][kScaleKB];
+                if (MODE == kGrad) {
+                    // the warps take the stages in turn: the loaded scales, powers of two, become
+                    // their exponents, four times over (a step of 32 takes one), in the order
+                    // of tc::copy_scales, and go to the stage's own tensor-memory columns
+                    for (int kb = 0; kb < q.nkb; ++kb, ++it) {
+                        if ((it & 1) == (warp & 1)) {
+                            ok = tc::mbar_wait(&full[s], (uint32_t)fill & 1u);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            const uint32_t at = (uint32_t)s * g.stage_bytes + kABytes + kTileN * kKB;
+                            uint32_t *sf = reinterpret_cast<uint32_t *>(ring + at);
+                            uint32_t v[12];
 #pragma unroll
-                        for (int i = 0; i < 6; ++i) {
-                            const int r = sl + 64 * (i & 1) + 128 * ((i >> 1) - 1);      // row, or column from i = 2 on
-                            const bool in = i < 2 ? sl + 64 * i < q.mlim : r < q.nlim;
-                            const float *p = i < 2 ? g.w_scale + (int64_t)(q.kb0 + kb) * g.N + m1 + sl + 64 * i
-                                                   : g.x_scale + (int64_t)(q.kb0 + kb) * g.K + q.n0 + r;
-                            const int64_t ld = i < 2 ? g.N : g.K;
+                            for (int i = 0; i < 12; ++i) v[i] = ((sf[32 * i + lane] >> 23) & 0xffu) * 0x01010101u;
+                            __syncwarp();
 #pragma unroll
-                            for (int u = 0; u < kScaleKB; ++u)
-                                v[i][u] = in && u < nk ? __float_as_uint(__ldg(p + u * ld)) : 0x3f800000u;
-                        }
+                            for (int i = 0; i < 3; ++i)
+                                reinterpret_cast<uint4 *>(sf)[32 * i + lane] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                            if (tc::elect()) {
+                                const uint32_t ts = tmem + kTileN + 16u * (uint32_t)s, from = tc::smem_u32(ring) + at;
 #pragma unroll
-                        for (int u = 0; u < kScaleKB; ++u) {
-                            if (u < nk) {
-                                if (fill > 0) ok = ok && tc::mbar_wait(&empty[s], (uint32_t)(fill - 1) & 1u);
-                                ok = __all_sync(0xffffffffu, ok);
-                                if (!ok) break;
-                                const uint32_t at = (uint32_t)s * g.stage_bytes + kABytes + kTileN * kKB;
-#pragma unroll
-                                for (int i = 0; i < 6; ++i) {
-                                    const int r = sl + 64 * (i & 1);
-                                    *reinterpret_cast<uint32_t *>(ring + at + (i >> 1) * 512 + (r & 31) * 16 + (r >> 5) * 4) =
-                                        ((v[i][u] >> 23) & 0xffu) * 0x01010101u;
-                                }
-                                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                                __syncwarp();
-                                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&full[s]));
-                                if (++s == g.stages) {
-                                    s = 0;
-                                    ++fill;
-                                }
+                                for (int i = 0; i < 3; ++i) tc::copy_scales(ts + 4 * i, from + 512 * i);
+                                tc::mma_commit<CG>(tc::smem_u32(&scaled[s]));
                             }
+                            __syncwarp();
                         }
-                        continue;
+                        if (++s == g.stages) {
+                            s = 0;
+                            ++fill;
+                        }
                     }
+                    continue;
+                }
+                for (int kb = 0; kb < q.nkb; kb += kScaleKB, ++gi) {
+                    const int slot = gi & 1, nk = min(kScaleKB, q.nkb - kb);
                     float v[2][kScaleKB], w[2][kScaleKB];
                     // weight scales of the two halves of the columns, scales of two rows
 #pragma unroll

@@ -41,10 +41,10 @@ __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(1000)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
 }
@@ -60,9 +60,8 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
     return false;
 }
 
-// The same, at most kWaitTries tries (a try suspends the thread for about a
-// microsecond at the longest): without the clock the summing loop keeps all of
-// its values in registers.
+// The same, at most kWaitTries tries (a try may suspend the thread for a while):
+// without the clock the summing loop keeps all of its values in registers.
 __device__ __forceinline__ bool mbar_wait_tries(uint64_t *bar, uint32_t parity) {
     const uint32_t a = smem_u32(bar);
     int left = kWaitTries;
@@ -101,6 +100,13 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *m, int
             "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
                 "r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar)
             : "memory");
+}
+
+// bytes consecutive bytes; src, dst and bytes multiples of 16.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 // ------------------------------------------------------------------ CTA pair

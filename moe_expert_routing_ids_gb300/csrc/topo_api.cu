@@ -537,7 +537,7 @@ int topo_expert_wgrad(int32_t n_seg, int64_t rows, int32_t N, int32_t K, int64_t
     if (ws_bytes < topo_expert_workspace_bytes(n_seg, rows, N, K)) return TOPO_ENOSPC;
     if (n_seg == 0) return TOPO_OK;
     if (!dy || !dy_scale || !x || !x_scale || !seg_off || !dw || !aligned16(dy, x) || !aligned16(dw, dw) ||
-        (((uintptr_t)dy_scale | (uintptr_t)x_scale | (uintptr_t)seg_off) & 3))
+        !aligned16(dy_scale, x_scale) || ((uintptr_t)seg_off & 3))
         return TOPO_EINVAL;
     return cuda_rc(launch_expert_wgrad(n_seg, rows, N, K, cap, dy, dy_scale, x, x_scale, seg_off, dw, ws, stream));
 }
