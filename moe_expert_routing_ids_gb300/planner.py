@@ -12,8 +12,8 @@ import torch
 from . import (TOPO_CALL_CHAIN, TOPO_CALL_COOCCUR, TOPO_DTYPE_BF16, TOPO_DTYPE_F32, TOPO_LAYOUT_STATS,
                TOPO_STATS, make_cfg, make_plan, topo_cooccur, topo_cooccur_workspace_bytes,
                topo_dispatch_layout, topo_gate_hist,
-               topo_hist, topo_plan, topo_read_error, topo_reroute, topo_reroute_layout,
-               topo_workspace_bytes, topo_ws_reset)
+               topo_hist, topo_plan, topo_read_error, topo_reroute, topo_reroute_layout, topo_route,
+               topo_route_grad, topo_workspace_bytes, topo_ws_reset)
 
 
 @dataclasses.dataclass
@@ -96,6 +96,39 @@ class Planner:
             raise TypeError("logits must be float32 or bfloat16")
         topo_gate_hist(self.cfg, self.L, logits, dt, bias, ids, scores, self.buf.hist, self.ws,
                        self.ws_bytes, self._stream())
+
+    @staticmethod
+    def _dtype(logits: torch.Tensor) -> int:
+        if logits.dtype == torch.float32:
+            return TOPO_DTYPE_F32
+        if logits.dtype == torch.bfloat16:
+            return TOPO_DTYPE_BF16
+        raise TypeError("logits must be float32 or bfloat16")
+
+    def route(self, logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, opts,
+              bias: torch.Tensor | None = None):
+        """Routing to experts (opts: make_route(...)) of logits [L, T, E] into ids
+        (int32 [L, T, k]), weights (float32 [L, T, k]) and the histogram; leaves
+        the tile index so that make_plan / reroute_layout(ids) can follow."""
+        topo_route(self.cfg, self.L, opts, logits, self._dtype(logits), bias, ids, weights, self.buf.hist, self.ws,
+                   self.ws_bytes, self._stream())
+
+    def route_grad(self, logits: torch.Tensor, ids: torch.Tensor, grad_weights: torch.Tensor,
+                   grad_logits: torch.Tensor, opts):
+        """Gradient of route()'s weights in the logits (grad_logits: the logits' type)."""
+        topo_route_grad(self.cfg, self.L, opts, logits, self._dtype(logits), ids, grad_weights, grad_logits, self.ws,
+                        self.ws_bytes, self._stream())
+
+    def instance_experts(self) -> torch.Tensor:
+        """Expert of each instance of the plan, int32 [L, R * n_local], -1 for an
+        empty slot: each rank's mains in ascending order, then its replicas."""
+        R, E = self.cfg_dict["R"], self.cfg_dict["E"]
+        if self.main_rank is None:
+            mains = torch.arange(E, dtype=torch.int32, device=self.device)
+        else:
+            mains = torch.sort(self.main_rank, stable=True).indices.to(torch.int32)
+        mains = mains.reshape(1, R, E // R).expand(self.L, R, E // R)
+        return torch.cat([mains, self.buf.slot_expert], 2).reshape(self.L, -1)
 
     def make_plan(self, hist: torch.Tensor | None = None):
         h = self.buf.hist if hist is None else hist

@@ -1,0 +1,93 @@
+"""The expert layer's whole path on the planned layout, forward and backward,
+against plain float64 expressions of the same layer.
+
+Tolerances.  e4m3 rounds a value by at most 2^-4 of it, uniformly: 2^-4 /
+sqrt(3) = 0.036 root mean square at the worst exponent position, 0.026 over all.
+A product of two such operands sums independent errors: relative error in
+2-norm about 0.037.  The forward pass chains two (the activation's error and
+the second product's own): below 0.08; a gradient chains up to three more: below
+0.15.  The router's gradient starts from dot products of y, with the error of the
+forward pass."""
+import numpy as np
+import pytest
+
+import moe_expert_routing_ids_gb300 as topo
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def _rel(a, b):
+    return float((a.double().cpu() - b).norm() / b.norm())
+
+
+@pytest.mark.parametrize("T,E,k,R,slots,H,I,score,groups,mapped", [
+    (96, 8, 2, 4, 1, 128, 64, topo.TOPO_SCORE_SOFTMAX, 1, False),
+    (640, 16, 4, 4, 2, 272, 144, topo.TOPO_SCORE_SIGMOID, 4, True),
+    (1024, 4, 2, 2, 0, 256, 256, topo.TOPO_SCORE_SOFTMAX, 1, False)])
+def test_layer_forward_and_backward(T, E, k, R, slots, H, I, score, groups, mapped):
+    from moe_expert_routing_ids_gb300.experts import ExpertLayer
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    dev = torch.device("cuda:0")
+    gen = torch.Generator().manual_seed(T)
+    w_up = (torch.randn(E, 2 * I, H, generator=gen) / H ** 0.5).to(torch.bfloat16)
+    w_down = (torch.randn(E, H, I, generator=gen) / I ** 0.5).to(torch.bfloat16)
+    x = torch.randn(T, H, generator=gen).to(torch.bfloat16)
+    logits = torch.randn(T, E, generator=gen) + torch.linspace(1.5, 0, E)
+    dout = torch.randn(T, H, generator=gen).to(torch.bfloat16)
+    main = torch.randperm(E, generator=gen) % R if mapped else None
+    cfg = dict(T=T, E=E, k=k, R=R, ranks_per_node=2, n_slot=slots, tok_bytes=2 * H, expert_bytes=64,
+               c_intra=1, c_inter=4, max_refine_iters=0, main_rank=None if main is None else main.int().to(dev))
+    opts = topo.make_route(score, groups, max(1, groups // 2), 1 if groups == 1 else 2, True, 1.5)
+    bias = torch.zeros(E, device=dev) if groups > 1 else None
+    layer = ExpertLayer(cfg, w_up.to(dev), w_down.to(dev), opts, train=True)
+    xd, ld = x.to(dev), logits.to(dev)
+    out = layer.forward(xd, ld, bias)
+    assert layer.error() == 0
+    first = out.clone()
+    assert torch.equal(layer.forward(xd, ld, bias), first)
+    ids = layer.ids[0].cpu().long()
+    seg = layer.planner.buf.seg_off[0].cpu()
+    if slots:
+        assert (layer.seg_w >= 0).sum() > E                     # replicas are in use
+    assert int(seg[-1]) == T * k
+
+    xr, lr = x.double().requires_grad_(), logits.double().requires_grad_()
+    ur, dr = w_up.double().requires_grad_(), w_down.double().requires_grad_()
+    s = torch.softmax(lr, -1) if score == topo.TOPO_SCORE_SOFTMAX else torch.sigmoid(lr)
+    w = torch.gather(s, 1, ids)
+    w = w / w.sum(-1, keepdim=True) * 1.5
+    want = torch.zeros(T, H, dtype=torch.float64)
+    for e in range(E):
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        h = xr[t] @ ur[e].T
+        a = torch.nn.functional.silu(h[:, :I]) * h[:, I:]
+        want = want.index_add(0, t, (a @ dr[e].T) * w[t, j][:, None])
+    assert _rel(out, want.detach()) < 0.08
+    want.backward(dout.double())
+    dx, dl, du, dd = layer.backward(xd, ld, dout.to(dev))
+    assert layer.error() == 0
+    assert _rel(dx, xr.grad) < 0.15
+    assert _rel(du, ur.grad) < 0.15
+    assert _rel(dd, dr.grad) < 0.15
+    assert _rel(dl, lr.grad) < 0.15
+
+
+def test_layer_shapes_are_checked():
+    from moe_expert_routing_ids_gb300.experts import ExpertLayer
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    dev = torch.device("cuda:0")
+    cfg = dict(T=16, E=4, k=2, R=2, ranks_per_node=1, n_slot=0, tok_bytes=64, expert_bytes=64, c_intra=1, c_inter=1)
+    up = torch.zeros(4, 64, 32, dtype=torch.bfloat16, device=dev)
+    with pytest.raises(ValueError):
+        ExpertLayer(cfg, up, torch.zeros(4, 32, 16, dtype=torch.bfloat16, device=dev), topo.make_route(0))
+    layer = ExpertLayer(cfg, up, torch.zeros(4, 32, 32, dtype=torch.bfloat16, device=dev), topo.make_route(0))
+    x, lg = torch.zeros(16, 32, dtype=torch.bfloat16, device=dev), torch.zeros(16, 4, device=dev)
+    assert float(layer.forward(x, lg).float().abs().max()) == 0.0
+    with pytest.raises(RuntimeError):
+        layer.backward(x, lg, x)
+    with pytest.raises(TypeError):
+        layer.planner.route(lg.double(), layer.ids, layer.weights, layer.route)
+    assert np.array_equal(layer.planner.instance_experts().cpu().numpy(), [[0, 1, 2, 3]])
