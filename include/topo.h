@@ -498,7 +498,7 @@ int topo_swiglu_grad(int64_t rows, int32_t I, const uint16_t *h, const uint16_t 
  * [n_w][ceil(N / 128)][ceil(K / 128)]; out: device [rows][N] of out_dtype.
  * The gradient of a is the same call with the rows' output gradient in 8 bits
  * (topo_quantize_rows) and the transposed weights.
- * ws: topo_expert_workspace_bytes bytes.  N and K positive multiples of 16,
+ * ws: topo_expert_workspace_bytes bytes.  N and K multiples of 16 up to 2^22,
  * rows <= 2^31 - 1, n_w * N and n_w * K below 2^31.  Device errors:
  * TOPO_ESTATE (an offset outside [0, rows] or out of order) and TOPO_ERANGE
  * (seg_w outside [0, n_w)): the segment is skipped; TOPO_ETIMEOUT. */

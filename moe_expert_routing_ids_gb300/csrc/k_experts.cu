@@ -6,30 +6,40 @@
 //   gradient  dw[i][n][k] = sum_b sdy[b][n] * sx[b][k] * (sum over t in block b of dy[n][t] * x[k][t])
 //             b over the 128-row blocks of segment i, dy and x laid out column by column
 //
-// A block's inner sum runs on the tensor cores (tcgen05.mma kind::f8f6f4, four
-// steps of 32 into float32 tensor memory); scaling it and adding it to the
-// tile's float32 sums in registers is one packed multiply-add for two values
-// (two for the gradient, whose rows and columns both have scales).
-//
-// The tile's rows (M, 128 for each CTA) are weight rows n; its columns (N, up
-// to 256) are layout rows, or the gradient's k.  A tile takes as many layout
-// rows as its segment has, rounded up to 16 (32 for a CTA pair), so ragged
-// segments waste no more than that.  Segments start at any row: a tile's loads
-// may run past its segment's last row into the next one; those columns are
+// Tiles of 128 rows (layout rows; the gradient's n) x 256 columns (weight rows;
+// the gradient's k).  Persistent CTAs, one per SM, of 12 warps: one streams
+// operand tiles with TMA through a ring of shared-memory stages, one issues
+// tcgen05.mma (four steps of 32 a block) into tensor memory, two bring the
+// scales, and two warpgroups keep the tile's float32 sums in registers, a row x
+// 128 columns to a thread, and store them.  Segments start at any row: a tile's
+// loads may run past its segment's last row into the next one; those rows are
 // computed and not stored.
 //
-// Persistent CTAs, one per SM: one thread streams operand tiles with TMA
-// through a ring of shared-memory stages, one thread issues the products into
-// two alternating accumulators of 256 tensor-memory columns, and two
-// warpgroups scale and add the one that is complete, 32 rows x 128 columns to
-// a warp.  Two warps bring the scales of four blocks at a time to shared memory
-// ahead of them (a layout row's scales are consecutive, so a block's are one
-// line each: loaded by the summing warps a block ahead, they held them up for
-// the whole latency). With CG = 2 two neighbouring SMs work on one tile of 256 rows: each
-// holds its own 128 rows and half of the columns' operand, the tensor cores
-// read the other half from the neighbour, and a block of 128 x 256 costs a
-// CTA 32 KB of shared-memory traffic each way instead of 48 KB.  (One CTA
-// alone is held by that traffic: without any summing, 2.7 PFLOP/s.)
+// The product's scales are any float32, so every block leaves tensor memory: it
+// is scaled and added to the registers by one packed multiply-add for two
+// values, from two accumulators in turn, while the next block is multiplied.
+// The row's scale times the weights' is one value per thread and block; the
+// scale warps compute them four blocks ahead (a layout row's scales are
+// consecutive, so a block's are one line each: loaded by the summing warps
+// themselves a block ahead they held them up for the whole latency).
+// The gradient's scales are powers of two: the tensor cores apply them
+// (kind::mxf8f6f4, a scale for 32 values) and sum in tensor memory, which moves
+// to the registers every kFlush blocks, so that no float32 sum runs over more
+// than 2048 products.  The scale warps turn each stage's scales into exponents.
+//
+// What bounds it, on a GB300, per block of 128 x 256 x 128: the tensor core needs
+// 512 cycles; operands cross shared memory twice, 96 KB at 128 bytes a cycle,
+// 768 cycles; the sums' reads of tensor memory hold the tensor core up for
+// 256 more.  The product takes about 1000 cycles a block (690 with the reads
+// left out, 800 for the gradient).  Tried: pairs of CTAs (cta_group::2, 256 rows,
+// half the column traffic) take 880 cycles for twice the rows, but waste more of
+// ragged segments and start slower: equal at 2048 rows a segment, 40 percent
+// slower at 128; weights on the rows and layout rows on the columns (no waste on
+// ragged segments, a scale per column): slower at every length, 24 rows 163 us
+// against 133; reads of 16 lanes instead of 32: 160 cycles more.
+// Measured: 131072 rows, N = 4096, K = 7168 over 128 experts: 3.3 to 3.5 ms, 2.2
+// to 2.35 PFLOP/s; 1536 rows, 2816 x 4096, 64 experts: 120 us, 6.3 TB/s; gradient of
+// 98304 rows, 2816 x 4096, 64 experts: 1.21 ms, its 2.95 GB of output included.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -44,7 +54,7 @@ namespace {
 enum { kProduct = 0, kGrad = 1 };
 
 constexpr int kKB = 128;                          // contraction values of a block: one 128-byte swizzle row
-constexpr int kTileM = 128;                       // rows of a CTA
+constexpr int kTileM = 128;
 constexpr int kTileN = 256;
 constexpr int kSumWarps = 8;                      // warps that scale, add and store
 constexpr int kThreads = (kSumWarps + 4) * 32;    // two summing warpgroups, one of producer, issuer and two scale warps
@@ -54,14 +64,14 @@ template <int MODE>
 constexpr int kSumRegs = MODE == kProduct ? 224 : 208;
 template <int MODE>
 constexpr int kIoRegs = (384 * 168 - 256 * kSumRegs<MODE>) / 128;
-constexpr int kTmemCols = 512;                    // two accumulators of 256 columns
+constexpr int kTmemCols = 512;                    // two accumulators of 256 columns, or one and the scales
 constexpr uint32_t kABytes = kTileM * kKB;
-constexpr int kMaxStages = 9;
+constexpr int kStages = 4;                        // 48 KB of operands each
 constexpr int kScaleKB = 4;                       // blocks whose scales are brought together
-constexpr int kFlush = 8;                         // gradient: blocks summed in tensor memory before the sum
+constexpr int kFlush = 16;                        // gradient: blocks summed in tensor memory before the sum
                                                   // moves to registers
-constexpr int kSegCap = 512;                      // segments of one launch (the table in shared memory)
-constexpr uint32_t kRingBytes = 192 * 1024;       // operand stages
+template <int MODE>
+constexpr int kSegCap = MODE == kProduct ? 1024 : 512;   // segments of one launch (the table in shared memory)
 constexpr uint32_t kStageOut = 2048;              // bytes a warp stores through shared memory at a time
 constexpr int kSms = 152;
 
@@ -78,7 +88,6 @@ struct GemmArgs {
     int nseg, seg0, n_w;
     int N, K;                   // gradient: dw is [N][K]
     int KB, NB;                 // 128-blocks of K and N
-    int stages;
     uint32_t stage_bytes;
     int out_bf16;
     int vec_scale;              // product: a row's scales can be read four at a time
@@ -92,16 +101,16 @@ struct Tile {
     int kb0, nkb;      // blocks contracted
 };
 
-template <int MODE, int CG>
+template <int MODE>
 __device__ __forceinline__ int tiles_of(const GemmArgs &g, int len) {
     const int m = MODE == kProduct ? len : g.N, n = MODE == kProduct ? g.N : g.K;
-    return ((m + CG * kTileM - 1) / (CG * kTileM)) * ((n + kTileN - 1) / kTileN);
+    return ((m + kTileM - 1) / kTileM) * ((n + kTileN - 1) / kTileN);
 }
 
 // Tile t: its segment by binary search over the exclusive prefix tp[0..nseg].
 // Within a segment the layout-row tiles of one weight tile are neighbours, so
 // that CTAs running together share the weights through L2.
-template <int MODE, int CG>
+template <int MODE>
 __device__ __forceinline__ Tile find_tile(const GemmArgs &g, const int *tp, const int *so, const int *pad, int t) {
     int lo = 0, hi = g.nseg - 1;
     while (lo < hi) {
@@ -113,14 +122,14 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs &g, const int *tp, cons
     r.seg = lo;
     const int loc = t - tp[lo], len = so[lo + 1] - so[lo];
     const int me = MODE == kProduct ? len : g.N, ne = MODE == kProduct ? g.N : g.K;
-    const int nm = (me + CG * kTileM - 1) / (CG * kTileM), n = loc / nm, m = loc - n * nm;
+    const int nm = (me + kTileM - 1) / kTileM, n = loc / nm, m = loc - n * nm;
     r.w = MODE == kGrad ? 0 : g.seg_w ? __ldg(g.seg_w + lo) : g.seg0 + lo;
-    r.m0 = m * CG * kTileM;
-    r.mlim = min(CG * kTileM, me - r.m0);
+    r.m0 = m * kTileM;
+    r.mlim = min(kTileM, me - r.m0);
     r.n0 = n * kTileN;
     r.nlim = min(kTileN, ne - r.n0);
     if (MODE == kProduct) r.m0 += so[lo];
-    r.ncols = (r.nlim + 16 * CG - 1) & ~(16 * CG - 1);
+    r.ncols = (r.nlim + 15) & ~15;
     r.kb0 = MODE == kGrad ? pad[lo] : 0;
     r.nkb = MODE == kGrad ? pad[lo + 1] - pad[lo] : g.KB;
     return r;
@@ -153,30 +162,31 @@ __device__ __forceinline__ void add_rows(Acc &acc, uint32_t ta, float s) {
     }
 }
 
-template <int MODE, int CG>
+template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUtensorMap map_n, GemmArgs g) {
     extern __shared__ __align__(1024) unsigned char ring[];
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], scaled[kMaxStages], acc_full[2], acc_empty[2], sc_full[2], sc_empty[2], drained;
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], scaled[kStages], drained;
+    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], sc_full[2], sc_empty[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int expired;
-    __shared__ int so[kSegCap + 1], tp[kSegCap + 1], pad[MODE == kGrad ? kSegCap + 1 : 1];
-    __shared__ float cs[MODE == kProduct ? 2 : 1][kScaleKB][kTileN];    // scales of the rows times each half's weight scale
+    __shared__ int so[kSegCap<MODE> + 1], tp[kSegCap<MODE> + 1], pad[MODE == kGrad ? kSegCap<MODE> + 1 : 1];
+    // product: scales of the rows times the weight scale of each half of the columns
+    __shared__ float cs[MODE == kProduct ? 2 : 1][kScaleKB][MODE == kProduct ? kTileN : 1];
     __shared__ __align__(128) unsigned char outs[kSumWarps * kStageOut];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t rank = CG == 2 ? tc::cluster_rank() : 0;
-    const int first = blockIdx.x / CG, step = gridDim.x / CG;
+    const int first = blockIdx.x, step = gridDim.x;
 
-    if (warp == kSumWarps + 1) tc::tmem_alloc<CG>(&tmem_slot, kTmemCols);
+    if (warp == kSumWarps + 1) tc::tmem_alloc(&tmem_slot, kTmemCols);
     if (tid == 0) {
-        for (int s = 0; s < g.stages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&scaled[s], 1);
             tc::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&acc_full[b], 1);
-            tc::mbar_init(&acc_empty[b], CG * kSumWarps);
+            tc::mbar_init(&acc_empty[b], kSumWarps);
             tc::mbar_init(&sc_full[b], 2);
             tc::mbar_init(&sc_empty[b], kSumWarps);
         }
@@ -220,7 +230,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     }
                 }
                 if (MODE == kGrad && ok) pb = (b - a + kKB - 1) / kKB;
-                if (MODE == kGrad || ok) n = tiles_of<MODE, CG>(g, b - a);
+                if (MODE == kGrad || ok) n = tiles_of<MODE>(g, b - a);
             }
             int x = n, y = pb;
 #pragma unroll
@@ -246,7 +256,6 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     }
     tc::fence_before();
     __syncthreads();
-    if (CG == 2) tc::cluster_sync();               // the neighbour's barriers are initialised
     tc::fence_after();
 
     if (warp >= kSumWarps) {
@@ -255,16 +264,14 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
         const int ntiles = tp[g.nseg];
         if (warp == kSumWarps) {
             // --------------------------------------------------------- producer
-            // CG = 2: both CTAs' loads report to the even CTA's barrier
             int s = 0, fill = 0;                       // stage, and how often the ring went round
             bool ok = true;
             for (int t = first; t < ntiles && ok; t += step) {
-                const Tile q = find_tile<MODE, CG>(g, tp, so, pad, t);
-                const int ym = q.m0 + (int)rank * kTileM;
-                const int nh = q.ncols / CG;                                // this CTA's columns
-                const int yn = (MODE == kProduct ? q.w * g.N : 0) + q.n0 + (int)rank * nh;
-                const int boxes = (nh + kTileM - 1) / kTileM;               // 128 of them to a load
-                uint32_t bytes = CG * (kABytes + (uint32_t)(boxes * kTileM) * kKB);
+                const Tile q = find_tile<MODE>(g, tp, so, pad, t);
+                const int ym = q.m0;
+                const int yn = (MODE == kProduct ? q.w * g.N : 0) + q.n0;
+                const int boxes = (q.ncols + kTileM - 1) / kTileM;          // 128 columns to a load
+                uint32_t bytes = kABytes + (uint32_t)(boxes * kTileM) * kKB;
                 // gradient: the scales of the tile's rows and columns, whole pieces of 16
                 const uint32_t ms = MODE == kGrad ? 4u * (uint32_t)q.mlim : 0u, ns = MODE == kGrad ? 4u * (uint32_t)q.nlim : 0u;
                 bytes += ms + ns;
@@ -273,15 +280,14 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                         ok = false;
                         break;
                     }
-                    uint32_t bar = tc::smem_u32(&full[s]);
-                    if (CG == 2) bar = tc::in_cta(bar, 0);
+                    const uint32_t bar = tc::smem_u32(&full[s]);
                     const uint32_t a = tc::smem_u32(ring) + (uint32_t)s * g.stage_bytes, b = a + kABytes;
                     const int x = (q.kb0 + kb) * kKB;
                     if (tc::elect()) {
-                        if (rank == 0) tc::mbar_expect_tx(tc::smem_u32(&full[s]), bytes);
-                        tc::tma_load<CG>(a, &map_m, x, ym, bar);
+                        tc::mbar_expect_tx(bar, bytes);
+                        tc::tma_load(a, &map_m, x, ym, bar);
                         for (int c = 0; c < boxes; ++c)
-                            tc::tma_load<CG>(b + (uint32_t)(c * kTileM) * kKB, &map_n, x, yn + c * kTileM, bar);
+                            tc::tma_load(b + (uint32_t)(c * kTileM) * kKB, &map_n, x, yn + c * kTileM, bar);
                         if (MODE == kGrad) {
                             const uint32_t sf = b + kTileN * kKB;
                             tc::bulk_load(sf, g.w_scale + (int64_t)(q.kb0 + kb) * g.N + q.m0, ms, bar);
@@ -289,32 +295,25 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                         }
                     }
                     __syncwarp();
-                    if (++s == g.stages) {
+                    if (++s == kStages) {
                         s = 0;
                         ++fill;
                     }
                 }
             }
             if (!ok) atomicExch(&expired, 1);
-            // loads in flight land before the CTA ends: the barriers tell the even
-            // CTA for both; after an expired wait the other one allows them 10 ms
-            if (rank == 0) {
-                for (int i = 0; i < g.stages; ++i) {
-                    const int n = fill + (i < s ? 1 : 0);      // fills of stage i
-                    if (n > 0 && !tc::mbar_wait(&full[i], (uint32_t)(n - 1) & 1u)) atomicExch(&expired, 1);
-                }
-            } else if (!ok) {
-                const uint32_t t0 = tc::clock_ns();
-                while (tc::clock_ns() - t0 < 10000000u) {
-                }
+            // loads in flight land before the CTA ends
+            for (int i = 0; i < kStages; ++i) {
+                const int n = fill + (i < s ? 1 : 0);          // fills of stage i
+                if (n > 0 && !tc::mbar_wait(&full[i], (uint32_t)(n - 1) & 1u)) atomicExch(&expired, 1);
             }
-        } else if (warp == kSumWarps + 1 && rank == 0) {
+        } else if (warp == kSumWarps + 1) {
             // ----------------------------------------------------------- issuer
             int s = 0, fill = 0, it = 0;               // it: accumulators handed on
             bool ok = true;
             for (int t = first; t < ntiles && ok; t += step) {
-                const Tile q = find_tile<MODE, CG>(g, tp, so, pad, t);
-                const uint32_t idesc = MODE == kGrad ? tc::idesc_scaled(kTileM, q.ncols) : tc::idesc_e4m3(CG * kTileM, q.ncols);
+                const Tile q = find_tile<MODE>(g, tp, so, pad, t);
+                const uint32_t idesc = MODE == kGrad ? tc::idesc_scaled(kTileM, q.ncols) : tc::idesc_e4m3(kTileM, q.ncols);
                 for (int kb = 0; kb < q.nkb; ++kb) {
                     // the product hands a block on in turn in two accumulators, the gradient
                     // kFlush blocks in one
@@ -338,20 +337,20 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                         } else {
 #pragma unroll
                             for (int j = 0; j < 4; ++j)        // 32 bytes on within the swizzled row
-                                tc::mma_e4m3<CG>(tmem + (uint32_t)(b * kTileN), dm + 2 * j, dn + 2 * j, idesc, j > 0);
+                                tc::mma_e4m3(tmem + (uint32_t)(b * kTileN), dm + 2 * j, dn + 2 * j, idesc, j > 0);
                         }
-                        tc::mma_commit<CG>(tc::smem_u32(&empty[s]));
-                        if (end) tc::mma_commit<CG>(tc::smem_u32(&acc_full[b]));
+                        tc::mma_commit(tc::smem_u32(&empty[s]));
+                        if (end) tc::mma_commit(tc::smem_u32(&acc_full[b]));
                     }
                     __syncwarp();
                     it += end;
-                    if (++s == g.stages) {
+                    if (++s == kStages) {
                         s = 0;
                         ++fill;
                     }
                 }
             }
-            if (tc::elect()) tc::mma_commit<CG>(tc::smem_u32(&drained));
+            if (tc::elect()) tc::mma_commit(tc::smem_u32(&drained));
             __syncwarp();
             if (!tc::mbar_wait(&drained, 0)) ok = false;
             if (!ok) atomicExch(&expired, 1);
@@ -361,9 +360,9 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             int gi = 0, s = 0, fill = 0, it = 0;
             bool ok = true;
             for (int t = first; t < ntiles && ok; t += step) {
-                const Tile q = find_tile<MODE, CG>(g, tp, so, pad, t);
-                const int m1 = q.m0 + (int)rank * kTileM;
-                if (MODE == kGrad) {
+                const Tile q = find_tile<MODE>(g, tp, so, pad, t);
+                const int m1 = q.m0;
+                if constexpr (MODE == kGrad) {
                     // the warps take the stages in turn: the loaded scales, powers of two, become
                     // their exponents, four times over (a step of 32 takes one), in the order
                     // of tc::copy_scales, and go to the stage's own tensor-memory columns
@@ -387,17 +386,16 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                                 const uint32_t ts = tmem + kTileN + 16u * (uint32_t)s, from = tc::smem_u32(ring) + at;
 #pragma unroll
                                 for (int i = 0; i < 3; ++i) tc::copy_scales(ts + 4 * i, from + 512 * i);
-                                tc::mma_commit<CG>(tc::smem_u32(&scaled[s]));
+                                tc::mma_commit(tc::smem_u32(&scaled[s]));
                             }
                             __syncwarp();
                         }
-                        if (++s == g.stages) {
+                        if (++s == kStages) {
                             s = 0;
                             ++fill;
                         }
                     }
-                    continue;
-                }
+                } else
                 for (int kb = 0; kb < q.nkb; kb += kScaleKB, ++gi) {
                     const int slot = gi & 1, nk = min(kScaleKB, q.nkb - kb);
                     float v[2][kScaleKB], w[2][kScaleKB];
@@ -407,7 +405,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                         const int nb = min(q.n0 / 128 + h, g.NB - 1), row = sl + 64 * h;
                         const float *wp = g.w_scale + ((int64_t)q.w * g.NB + nb) * g.KB + kb;
                         const float *p = g.x_scale + (int64_t)(m1 + row) * g.KB + kb;
-                        const bool in = (int)rank * kTileM + row < q.mlim;
+                        const bool in = row < q.mlim;
 #pragma unroll
                         for (int u = 0; u < kScaleKB; ++u) {
                             w[h][u] = u < nk ? __ldg(wp + u) : 0.f;
@@ -450,8 +448,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
         const int c0 = half * 128;
         const int quad = lane & 3, r8 = lane >> 2;
         const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-        uint32_t done = tc::smem_u32(&acc_empty[0]);     // the even CTA's
-        if (CG == 2) done = tc::in_cta(done, 0);
+        const uint32_t done = tc::smem_u32(&acc_empty[0]);
         int it = 0, gi = 0;
         bool live = true;
         // an expired wait lets these warps run on without waiting (and without
@@ -459,9 +456,10 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
         for (int t = first; t < ntiles; t += step) {
             int nkb, ncol;
             {
-                const Tile q = find_tile<MODE, CG>(g, tp, so, pad, t);
+                const Tile q = find_tile<MODE>(g, tp, so, pad, t);
                 nkb = q.nkb;
-                ncol = max(0, min(128, q.ncols - c0));
+                // columns of this half; none for a warp whose rows all lie past the tile's
+                ncol = wq * 32 < q.mlim ? max(0, min(128, q.ncols - c0)) : 0;
             }
             Acc acc;
 #pragma unroll
@@ -473,7 +471,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 float scale = 1.f;
                 if (MODE == kProduct) {
                     if (live && u == 0) live = tc::mbar_wait_tries(&sc_full[slot], (uint32_t)(gi >> 1) & 1u);
-                    scale = cs[MODE == kProduct ? slot : 0][u][c0 + wq * 32 + lane];
+                    scale = cs[MODE == kProduct ? slot : 0][u][MODE == kProduct ? c0 + wq * 32 + lane : 0];
                 }
                 if (live) live = tc::mbar_wait_tries(&acc_full[b], (uint32_t)round & 1u);
                 __syncwarp();
@@ -483,8 +481,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 __syncwarp();
                 const bool last = MODE == kProduct && (u == kScaleKB - 1 || kb + 1 == nkb);
                 if (lane == 0) {
-                    if (CG == 2) tc::mbar_arrive_cluster(done + 8 * b);
-                    else tc::mbar_arrive(done + 8 * b);
+                    tc::mbar_arrive(done + 8 * b);
                     if (last) tc::mbar_arrive(tc::smem_u32(&sc_empty[slot]));
                 }
                 gi += last;
@@ -492,8 +489,8 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             live = __all_sync(0xffffffffu, live);
             if (!live) continue;
             // found again rather than kept in registers over the loop
-            const Tile q = find_tile<MODE, CG>(g, tp, so, pad, t);
-            const int m1 = (int)rank * kTileM + wq * 32;         // this warp's first row, from m0
+            const Tile q = find_tile<MODE>(g, tp, so, pad, t);
+            const int m1 = wq * 32;         // this warp's first row, from m0
             // 32 rows x 64 bytes at a time, turned through shared memory so that four lanes
             // store 64 neighbouring bytes: 16-byte pieces, piece index XOR (row / 2)
             unsigned char *w = outs + warp * kStageOut;
@@ -545,8 +542,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     }
     tc::fence_before();
     __syncthreads();
-    if (CG == 2) tc::cluster_sync();               // nothing of the neighbour's is in flight here any more
-    if (warp == kSumWarps + 1) tc::tmem_free<CG>(tmem_slot, kTmemCols);
+    if (warp == kSumWarps + 1) tc::tmem_free(tmem_slot, kTmemCols);
     if (tid == 0 && expired) set_error(g.hdr, TOPO_ETIMEOUT);
 }
 
@@ -583,35 +579,20 @@ cudaError_t make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t col
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Tiles of g.nt columns over CTA groups of CG, for the segments from seg0 on.
-template <int MODE, int CG>
+template <int MODE>
 cudaError_t run_experts(GemmArgs g, int nseg, const int32_t *seg_off, const int32_t *seg_w, const CUtensorMap &mm,
                         const CUtensorMap &mn, cudaStream_t st) {
-    g.stage_bytes = kABytes + (uint32_t)(kTileN / CG) * kKB;
-    g.stages = std::min<int>(kMaxStages, (int)(kRingBytes / g.stage_bytes));
-    if (MODE == kGrad) g.stage_bytes += 2048;      // scales, the stages on 1024-byte boundaries
-    const size_t smem = (size_t)g.stages * g.stage_bytes;
-    cudaError_t e = ensure_smem((const void *)k_experts<MODE, CG>, smem);
+    // the gradient's stages also hold their scales, and stay on 1024-byte boundaries
+    g.stage_bytes = kABytes + (uint32_t)kTileN * kKB + (MODE == kGrad ? 2048 : 0);
+    const size_t smem = (size_t)kStages * g.stage_bytes;
+    cudaError_t e = ensure_smem((const void *)k_experts<MODE>, smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kSms);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CG;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    for (int s0 = 0; s0 < nseg; s0 += kSegCap) {
-        g.nseg = std::min(kSegCap, nseg - s0);
+    for (int s0 = 0; s0 < nseg; s0 += kSegCap<MODE>) {
+        g.nseg = std::min(kSegCap<MODE>, nseg - s0);
         g.seg0 = s0;
         g.seg_off = seg_off + s0;
         g.seg_w = seg_w ? seg_w + s0 : nullptr;
-        if ((e = cudaLaunchKernelEx(&cfg, k_experts<MODE, CG>, mm, mn, g)) != cudaSuccess) return e;
+        if ((e = launch_pdl(k_experts<MODE>, dim3(kSms), dim3(kThreads), smem, st, mm, mn, g)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
@@ -634,17 +615,11 @@ cudaError_t launch_expert_gemm(int nseg, int64_t rows, int n_w, int N, int K, co
     g.NB = (N + 127) / 128;
     g.out_bf16 = bf16;
     g.vec_scale = g.KB % 4 == 0 && ((uintptr_t)a_scale & 15) == 0;
-    // A pair's tile of 256 rows wastes more of a short segment, and two CTAs move
-    // their weights with one TMA queue less; 64 experts of N = 2816, K = 4096, rows
-    // per expert, one CTA / a pair: 24: 146 / 179 us; 96: 171 / 185; 128: 191 / 201;
-    // 192: 239 / 218; 256: 299 / 254
-    const bool pair = rows / nseg > 144;
     CUtensorMap mx, mw;
     cudaError_t e;
     if ((e = make_map(&mx, a, rows, K, kTileM)) != cudaSuccess) return e;
     if ((e = make_map(&mw, w, (int64_t)n_w * N, K, kTileM)) != cudaSuccess) return e;
-    return pair ? run_experts<kProduct, 2>(g, nseg, seg_off, seg_w, mx, mw, st)
-                : run_experts<kProduct, 1>(g, nseg, seg_off, seg_w, mx, mw, st);
+    return run_experts<kProduct>(g, nseg, seg_off, seg_w, mx, mw, st);
 }
 
 cudaError_t launch_expert_wgrad(int nseg, int64_t rows, int N, int K, int64_t cap, const uint8_t *dy, const float *dy_scale,
@@ -664,7 +639,7 @@ cudaError_t launch_expert_wgrad(int nseg, int64_t rows, int N, int K, int64_t ca
     cudaError_t e;
     if ((e = make_map(&my, dy, N, cap, kTileM)) != cudaSuccess) return e;
     if ((e = make_map(&mx, x, K, cap, kTileM)) != cudaSuccess) return e;
-    return run_experts<kGrad, 1>(g, nseg, seg_off, nullptr, my, mx, st);
+    return run_experts<kGrad>(g, nseg, seg_off, nullptr, my, mx, st);
 }
 
 }  // namespace topo

@@ -202,23 +202,33 @@ k_swiglu_grad(const uint4 *__restrict__ h, const uint4 *__restrict__ dy, uint4 *
 // Two bf16 magnitudes at a time.
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
-// 16 rows of one column (bf16, in the low or high half of their words) as 16
-// e4m3 bytes.
+// 16 rows of one column (scaled bf16, in the low or high half of their words) as
+// 16 e4m3 bytes.
 template <bool HI>
-__device__ __forceinline__ uint4 quant_col(const uint32_t (&v)[16], float inv, bool odd) {
+__device__ __forceinline__ uint4 quant_col(const uint32_t (&v)[16]) {
     uint32_t q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float f[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[j] = __uint_as_float(HI ? v[4 * i + j] & 0xffff0000u : v[4 * i + j] << 16);
-            if (odd && !finite(f[j])) f[j] = __int_as_float(0x7fffffff);
-            f[j] *= inv;
-        }
+        for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(HI ? v[4 * i + j] & 0xffff0000u : v[4 * i + j] << 16);
         q[i] = cvt2(f[0], f[1]) | (cvt2(f[2], f[3]) << 16);
     }
     return make_uint4(q[0], q[1], q[2], q[3]);
+}
+
+// Values of a word that are not finite made NaN.
+__device__ __forceinline__ uint32_t nan2(uint32_t v) {
+    if ((v & 0x7fffu) >= 0x7f80u) v |= 0x7fffu;
+    if ((v >> 16 & 0x7fffu) >= 0x7f80u) v |= 0x7fff0000u;
+    return v;
+}
+
+// Two bf16 values times powers of two: exact, but for results that e4m3 rounds to
+// zero anyway.
+__device__ __forceinline__ uint32_t mul_bf2(uint32_t v, uint32_t by) {
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v), *reinterpret_cast<const __nv_bfloat162 *>(&by));
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // A CTA takes one row block and 128 columns at a time, the next ones' loads on
@@ -296,6 +306,8 @@ k_quant_cols(const uint16_t *__restrict__ x, const int32_t *__restrict__ seg_off
                 if ((c >> 16) >= 0x7f80u) c &= 0xffffu;
                 m.x = max2(m.x, a);
                 m.y = max2(m.y, c);
+                v0[r] = nan2(v0[r]);
+                v1[r] = nan2(v1[r]);
             }
         }
         if (c0 + (int)gridDim.y * 128 < C) load(c0 + gridDim.y * 128);
@@ -314,10 +326,17 @@ k_quant_cols(const uint16_t *__restrict__ x, const int32_t *__restrict__ seg_off
         sc[2] = scale_of(__uint_as_float(m.y << 16), iv[2]);
         sc[3] = scale_of(__uint_as_float(m.y & 0xffff0000u), iv[3]);
         uint4 *t = tile[s] + 32 * lane + (warp ^ (lane & 7));
-        t[0] = quant_col<false>(v0, iv[0], odd);
-        t[8] = quant_col<true>(v0, iv[1], odd);
-        t[16] = quant_col<false>(v1, iv[2], odd);
-        t[24] = quant_col<true>(v1, iv[3], odd);
+        const uint32_t b0 = (__float_as_uint(iv[0]) >> 16) | (__float_as_uint(iv[1]) & 0xffff0000u);
+        const uint32_t b1 = (__float_as_uint(iv[2]) >> 16) | (__float_as_uint(iv[3]) & 0xffff0000u);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            v0[r] = mul_bf2(v0[r], b0);
+            v1[r] = mul_bf2(v1[r], b1);
+        }
+        t[0] = quant_col<false>(v0);
+        t[8] = quant_col<true>(v0);
+        t[16] = quant_col<false>(v1);
+        t[24] = quant_col<true>(v1);
         if (warp == 0 && c < C) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) scale[(int64_t)b * C + c + j] = sc[j];

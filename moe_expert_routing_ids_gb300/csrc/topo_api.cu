@@ -215,7 +215,7 @@ bool rows_ok(int64_t rows, int32_t C) { return rows >= 0 && rows <= INT32_MAX &&
 
 bool product_dims_ok(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, int32_t K) {
     if (n_seg < 0 || rows < 0 || rows > INT32_MAX || n_w < 0 || N < 16 || K < 16 || N % 16 || K % 16) return false;
-    if (N > (1 << 24) || K > (1 << 24)) return false;
+    if (N > (1 << 22) || K > (1 << 22)) return false;
     return (int64_t)n_w * N <= INT32_MAX && (int64_t)n_w * K <= INT32_MAX;
 }
 
