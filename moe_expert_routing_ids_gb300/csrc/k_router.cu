@@ -20,8 +20,8 @@
 //   - candidates are evaluated as defined and ranked by counting;
 //   - groups whose scores are closer than the margin: the row is done again with
 //     every score as defined;
-//   - rows with NaN or infinities (where groups or the sigmoid are involved),
-//     many ties: exact_token, which is not for speed (19 rows of 65536 sent
+//   - rows with NaN or infinities (where groups or the sigmoid are involved; among
+//     the biases: every row), many ties: exact_token, which is not for speed (19 rows of 65536 sent
 //     there for their groups cost 24 us, its code being read from memory).
 // Measured, 1M x 512 softmax, k = 10: 570 us, 3.9 TB/s; 65536 x 256 sigmoid, 4 of 8
 // groups, k = 8: 44 us.  Bound by issue: 700 instructions for two rows of 512
@@ -328,9 +328,13 @@ k_route_experts(const __grid_constant__ RouteArgs g) {
     pdl_trigger();
     pdl_wait();
     const RouteScratch w = {dyn + Ep + grp * Ep, keys_[grp], ce_[grp], sel_[grp], sx_[grp], gsc_[grp]};
+    float bias_odd = 0.f;                                         // NaN with any NaN or infinity among the biases
     if (SIG) {
-        for (int e = threadIdx.x; e < Ep; e += kRouteThreads) sb[e] = g.bias && e < E ? __ldg(g.bias + e) : 0.f;
-        __syncthreads();
+        for (int e = threadIdx.x; e < Ep; e += kRouteThreads) {
+            sb[e] = g.bias && e < E ? __ldg(g.bias + e) : 0.f;
+            bias_odd = fmaf(sb[e], 0.f, bias_odd);
+        }
+        if (__syncthreads_or(bias_odd != 0.f)) bias_odd = kInf * 0.f;
     }
     unsigned in = VPL >= 32 ? 0xffffffffu : (1u << (VPL & 31)) - 1u;    // slots that hold an expert
     if (!FULL) {
@@ -362,7 +366,7 @@ k_route_experts(const __grid_constant__ RouteArgs g) {
             continue;
         }
         float c[VPL];
-        float odd = 0.f;                                          // NaN with any NaN or infinity
+        float odd = bias_odd;                                     // NaN with any NaN or infinity
         unsigned cm;                                              // candidates among this lane's slots
         bool precise = false, unsure;
 #pragma unroll 1

@@ -114,7 +114,7 @@ def test_quantize_rows(rows, C):
 
 @gpu
 @pytest.mark.parametrize("L,T,k,H", [(1, 1, 1, 16), (1, 5, 8, 7168), (2, 33, 3, 272), (1, 100, 40, 144),
-                                     (1, 3000, 6, 1408), (2, 4097, 2, 1024)])
+                                     (1, 3000, 6, 1408), (2, 4097, 2, 1024), (1, 2100, 40, 1024)])
 def test_permute_quantize(L, T, k, H):
     dev = _dev()
     rng = np.random.default_rng([L, T, k, H])
@@ -136,9 +136,10 @@ def test_permute_quantize(L, T, k, H):
 
 
 @gpu
-def test_permute_quantize_reports_pairs_outside_the_layer():
+@pytest.mark.parametrize("T,H", [(8, 32), (2100, 1024)])
+def test_permute_quantize_reports_pairs_outside_the_layer(T, H):
     dev = _dev()
-    T, k, H = 8, 2, 32
+    k = 2
     cfg = topo.make_cfg(T=T, E=4, k=k, R=1, ranks_per_node=1, n_slot=0)
     nb = topo.topo_workspace_bytes(cfg, 1, topo.TOPO_CALL_PACK)
     for bad in (-1, T * k):
@@ -146,7 +147,7 @@ def test_permute_quantize_reports_pairs_outside_the_layer():
         sp = torch.arange(T * k, dtype=torch.int32, device=dev)
         sp[3] = bad
         q = torch.zeros((T * k, H), dtype=torch.uint8, device=dev)
-        s = torch.zeros((T * k, 1), device=dev)
+        s = torch.zeros((T * k, _kb(H)), device=dev)
         topo.topo_permute_quantize(cfg, 1, H, torch.zeros((T, H), dtype=torch.bfloat16, device=dev), sp, q, s, ws, nb)
         torch.cuda.synchronize()
         assert topo.topo_read_error(ws) == topo.TOPO_ESTATE

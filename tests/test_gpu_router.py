@@ -51,7 +51,8 @@ def reference(x, k, score, bias=None, groups=1, kept=1, top=1, renorm=True, scal
     drop = np.zeros((T, E), bool)
     gs = None
     if groups > 1:
-        v = np.sort(c.reshape(T, groups, -1), -1)[:, :, ::-1][:, :, :top].sum(-1)
+        low = np.where(np.isnan(c), -np.inf, c)                # NaN ranks below every number
+        v = np.sort(low.reshape(T, groups, -1), -1)[:, :, ::-1][:, :, :top].sum(-1)
         keep = order(v)[:, :kept]
         drop = np.ones((T, groups), bool)
         np.put_along_axis(drop, keep, False, 1)
@@ -288,6 +289,45 @@ def test_nan_ranks_below_every_number(E):
     assert np.array_equal(ids, order(x)[:, :4])
     assert np.all(np.isfinite(w[0])) and np.all(np.isfinite(w[3:]))
     assert np.all(np.isnan(w[2]))
+
+
+@gpu
+@pytest.mark.parametrize("E,groups,kept", [(24, 1, 1), (256, 8, 4), (160, 8, 3)])
+def test_biases_that_mask_experts(E, groups, kept):
+    """A bias of -inf takes an expert out of the choice, NaN ranks it last."""
+    rng = np.random.default_rng(E)
+    x = rng.standard_normal((40, E)).astype(np.float32)
+    bias = (rng.standard_normal(E) * 0.05).astype(np.float32)
+    bias[rng.permutation(E)[: E // 3]] = -np.inf
+    for b in (bias, np.where(np.arange(E) == 5, np.nan, bias).astype(np.float32)):
+        args = (x, 4, SIG, b, groups, kept, 2 if groups > 1 else 1)
+        ids, w = run(*args)
+        rid, rw, c, gs, drop = reference(*args)
+        ok = clear_rows(np.nan_to_num(c, nan=-np.inf), None if gs is None else np.nan_to_num(gs, nan=-1e9), drop, 4, kept, 1e-5)
+        assert ok.mean() > 0.9
+        assert np.array_equal(ids[ok], rid[ok])
+        assert np.all(np.abs(w[ok] - rw[ok]) <= 64 * U * rw[ok])
+
+
+@gpu
+@pytest.mark.parametrize("gap", [0.0, 3e-8, 1e-6, 1e-5])
+def test_groups_that_are_nearly_equal(gap):
+    """Groups whose scores differ by less than a cheap evaluation could tell: the
+    choice is that of the scores as defined, every operation rounded to float32."""
+    E, G, kept, k, T = 64, 8, 3, 4, 64
+    rng = np.random.default_rng(8)
+    x = np.tile(rng.standard_normal((T, 1, E // G)), (1, G, 1)).reshape(T, E).astype(np.float32)
+    bias = np.repeat(rng.permutation(G) * gap, E // G).astype(np.float32)
+    x += (rng.standard_normal((T, E)) * gap).astype(np.float32)
+    ids, _ = run(x, k, SIG, bias, G, kept, 2)
+    dev = _dev()
+    xd = torch.as_tensor(x, device=dev)
+    c = 1.0 / (1.0 + torch.exp(-xd)) + torch.as_tensor(bias, device=dev)      # the definition in float32
+    top = torch.sort(c.reshape(T, G, -1), dim=-1, descending=True).values
+    keep = torch.sort(top[..., 0] + top[..., 1], dim=-1, descending=True, stable=True).indices[:, :kept]
+    on = torch.zeros(T, G, dtype=torch.bool, device=dev).scatter_(1, keep, True).repeat_interleave(E // G, 1)
+    want = torch.sort(c.masked_fill(~on, -torch.inf), dim=-1, descending=True, stable=True).indices[:, :k]
+    assert np.array_equal(ids, want.cpu().numpy())
 
 
 @gpu
