@@ -88,6 +88,8 @@ _lib = None
 def lib():
     """The loaded shared library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -147,9 +149,10 @@ def lib():
 def _p(x):
     if x is None:
         return None
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr() or None
-    return int(x) or None
+    except AttributeError:
+        return int(x) or None
 
 
 def _s(stream):

@@ -67,6 +67,10 @@ constexpr int kIoRegs = (384 * 168 - 256 * kSumRegs<MODE>) / 128;
 constexpr int kTmemCols = 512;                    // two accumulators of 256 columns, or one and the scales
 constexpr uint32_t kABytes = kTileM * kKB;
 constexpr int kStages = 4;                        // 48 KB of operands each
+// Rows up to which a tile loads only them, 16 at a time, not 128: 8 rows of 8
+// experts, 4096 x 7168: 62 -> 45 us; 6 of 64, 4096 x 1408: 13.4 -> 11.0; no
+// difference where every SM streams weights anyway (24 rows an expert).
+constexpr int kFew = 32;
 constexpr int kScaleKB = 4;                       // blocks whose scales are brought together
 constexpr int kFlush = 16;                        // gradient: blocks summed in tensor memory before the sum
                                                   // moves to registers
@@ -164,7 +168,8 @@ __device__ __forceinline__ void add_rows(Acc &acc, uint32_t ta, float s) {
 
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
-k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUtensorMap map_n, GemmArgs g) {
+k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUtensorMap map_few,
+          const __grid_constant__ CUtensorMap map_n, GemmArgs g) {
     extern __shared__ __align__(1024) unsigned char ring[];
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], scaled[kStages], drained;
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], sc_full[2], sc_empty[2];
@@ -271,7 +276,10 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 const int ym = q.m0;
                 const int yn = (MODE == kProduct ? q.w * g.N : 0) + q.n0;
                 const int boxes = (q.ncols + kTileM - 1) / kTileM;          // 128 columns to a load
-                uint32_t bytes = kABytes + (uint32_t)(boxes * kTileM) * kKB;
+                // few rows: only they are loaded, 16 at a time (what the other rows of the
+                // stage hold goes into sums that are not stored)
+                const int few = MODE == kProduct && q.mlim <= kFew ? (q.mlim + 15) / 16 : 0;
+                uint32_t bytes = (few ? (uint32_t)few * 16 * kKB : kABytes) + (uint32_t)(boxes * kTileM) * kKB;
                 // gradient: the scales of the tile's rows and columns, whole pieces of 16
                 const uint32_t ms = MODE == kGrad ? 4u * (uint32_t)q.mlim : 0u, ns = MODE == kGrad ? 4u * (uint32_t)q.nlim : 0u;
                 bytes += ms + ns;
@@ -285,7 +293,10 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     const int x = (q.kb0 + kb) * kKB;
                     if (tc::elect()) {
                         tc::mbar_expect_tx(bar, bytes);
-                        tc::tma_load(a, &map_m, x, ym, bar);
+                        if (few)
+                            for (int c = 0; c < few; ++c) tc::tma_load(a + (uint32_t)(c * 16) * kKB, &map_few, x, ym + 16 * c, bar);
+                        else
+                            tc::tma_load(a, &map_m, x, ym, bar);
                         for (int c = 0; c < boxes; ++c)
                             tc::tma_load(b + (uint32_t)(c * kTileM) * kKB, &map_n, x, yn + c * kTileM, bar);
                         if (MODE == kGrad) {
@@ -581,7 +592,7 @@ cudaError_t make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t col
 
 template <int MODE>
 cudaError_t run_experts(GemmArgs g, int nseg, const int32_t *seg_off, const int32_t *seg_w, const CUtensorMap &mm,
-                        const CUtensorMap &mn, cudaStream_t st) {
+                        const CUtensorMap &mf, const CUtensorMap &mn, cudaStream_t st) {
     // the gradient's stages also hold their scales, and stay on 1024-byte boundaries
     g.stage_bytes = kABytes + (uint32_t)kTileN * kKB + (MODE == kGrad ? 2048 : 0);
     const size_t smem = (size_t)kStages * g.stage_bytes;
@@ -592,7 +603,7 @@ cudaError_t run_experts(GemmArgs g, int nseg, const int32_t *seg_off, const int3
         g.seg0 = s0;
         g.seg_off = seg_off + s0;
         g.seg_w = seg_w ? seg_w + s0 : nullptr;
-        if ((e = launch_pdl(k_experts<MODE>, dim3(kSms), dim3(kThreads), smem, st, mm, mn, g)) != cudaSuccess) return e;
+        if ((e = launch_pdl(k_experts<MODE>, dim3(kSms), dim3(kThreads), smem, st, mm, mf, mn, g)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
@@ -615,11 +626,12 @@ cudaError_t launch_expert_gemm(int nseg, int64_t rows, int n_w, int N, int K, co
     g.NB = (N + 127) / 128;
     g.out_bf16 = bf16;
     g.vec_scale = g.KB % 4 == 0 && ((uintptr_t)a_scale & 15) == 0;
-    CUtensorMap mx, mw;
+    CUtensorMap mx, mf, mw;
     cudaError_t e;
     if ((e = make_map(&mx, a, rows, K, kTileM)) != cudaSuccess) return e;
+    if ((e = make_map(&mf, a, rows, K, 16)) != cudaSuccess) return e;
     if ((e = make_map(&mw, w, (int64_t)n_w * N, K, kTileM)) != cudaSuccess) return e;
-    return run_experts<kProduct>(g, nseg, seg_off, seg_w, mx, mw, st);
+    return run_experts<kProduct>(g, nseg, seg_off, seg_w, mx, mf, mw, st);
 }
 
 cudaError_t launch_expert_wgrad(int nseg, int64_t rows, int N, int K, int64_t cap, const uint8_t *dy, const float *dy_scale,
@@ -639,7 +651,7 @@ cudaError_t launch_expert_wgrad(int nseg, int64_t rows, int N, int K, int64_t ca
     cudaError_t e;
     if ((e = make_map(&my, dy, N, cap, kTileM)) != cudaSuccess) return e;
     if ((e = make_map(&mx, x, K, cap, kTileM)) != cudaSuccess) return e;
-    return run_experts<kGrad>(g, nseg, seg_off, nullptr, my, mx, st);
+    return run_experts<kGrad>(g, nseg, seg_off, nullptr, my, my, mx, st);
 }
 
 }  // namespace topo
