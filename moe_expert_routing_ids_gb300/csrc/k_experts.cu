@@ -39,7 +39,12 @@
 // against 133; reads of 16 lanes instead of 32: 160 cycles more.
 // Measured: 131072 rows, N = 4096, K = 7168 over 128 experts: 3.3 to 3.5 ms, 2.2
 // to 2.35 PFLOP/s; 1536 rows, 2816 x 4096, 64 experts: 120 us, 6.3 TB/s; gradient of
-// 98304 rows, 2816 x 4096, 64 experts: 1.21 ms, its 2.95 GB of output included.
+// 98304 rows, 2816 x 4096, 64 experts: 1.14 to 1.15 ms, its 2.95 GB of output included
+// (0.94 ms without the stores; 1.19 ms when the warps read the turned rows back and
+// stored them, against one TMA store of 32 rows x 64 bytes; 16 rows x 128 bytes the
+// same).  Tiles of 256 x 192, which the two accumulators fill, kept in tensor memory and
+// taken while the next tile is multiplied: 1.20 ms, since each product of 128 rows reads
+// its columns again (1088 cycles of shared memory for one and a half times the work).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -178,7 +183,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     __shared__ int so[kSegCap<MODE> + 1], tp[kSegCap<MODE> + 1], pad[MODE == kGrad ? kSegCap<MODE> + 1 : 1];
     // product: scales of the rows times the weight scale of each half of the columns
     __shared__ float cs[MODE == kProduct ? 2 : 1][kScaleKB][MODE == kProduct ? kTileN : 1];
-    __shared__ __align__(128) unsigned char outs[kSumWarps * kStageOut];
+    __shared__ __align__(1024) unsigned char outs[kSumWarps * kStageOut];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int first = blockIdx.x, step = gridDim.x;
 
@@ -506,10 +511,26 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             // store 64 neighbouring bytes: 16-byte pieces, piece index XOR (row / 2)
             unsigned char *w = outs + warp * kStageOut;
             const int swz = (lane >> 1) & 3;
-            const int64_t ld = MODE == kGrad ? g.K : g.N;
-            const int64_t row0 = MODE == kGrad ? (int64_t)(g.seg0 + q.seg) * g.N + q.m0 : q.m0;
-            const int64_t at = (row0 + m1 + r8) * ld + q.n0 + c0;
-            if (MODE == kProduct && g.out_bf16) {
+            const int64_t ld = g.N, at = (int64_t)(q.m0 + m1 + r8) * ld + q.n0 + c0;
+            if constexpr (MODE == kGrad) {
+                // the same 64-byte rows, XOR included, as one TMA store; rows and columns
+                // past the segment's end are left out
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    if (c0 + 16 * c < q.nlim && m1 < q.mlim) {
+                        if (tc::elect()) tc::bulk_wait_read();      // the piece before has left shared memory
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<float4 *>(w + lane * 64 + (i ^ swz) * 16) =
+                                make_float4(acc[8 * c + 2 * i].x, acc[8 * c + 2 * i].y, acc[8 * c + 2 * i + 1].x, acc[8 * c + 2 * i + 1].y);
+                        tc::fence_async();
+                        __syncwarp();
+                        if (tc::elect()) tc::tma_store(&map_few, q.n0 + c0 + 16 * c, q.m0 + m1, g.seg0 + q.seg, tc::smem_u32(w));
+                        __syncwarp();
+                    }
+                }
+            } else if (g.out_bf16) {
                 __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(g.out) + at + 8 * quad;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -549,6 +570,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 }
             }
         }
+        if (MODE == kGrad && tc::elect()) tc::bulk_wait();
         if (!live) atomicExch(&expired, 1);
     }
     tc::fence_before();
@@ -587,6 +609,19 @@ cudaError_t make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t col
     const CUresult r = f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dim, stride, box, es,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Map of out[nseg][N][K] in float32, stored in boxes of 32 rows x 16 columns from
+// 64-byte rows in the 64-byte swizzle.
+cudaError_t make_out_map(CUtensorMap *m, float *out, int nseg, int N, int K) {
+    const EncodeFn f = encode_fn();
+    if (!f) return cudaErrorNotSupported;
+    const cuuint64_t dim[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)nseg};
+    const cuuint64_t stride[2] = {(cuuint64_t)K * 4, (cuuint64_t)N * K * 4};
+    const cuuint32_t box[3] = {16, 32, 1}, es[3] = {1, 1, 1};
+    const CUresult r = f(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, out, dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -647,11 +682,12 @@ cudaError_t launch_expert_wgrad(int nseg, int64_t rows, int N, int K, int64_t ca
     g.cap = cap;
     g.N = N;
     g.K = K;
-    CUtensorMap my, mx;
+    CUtensorMap my, mx, mo;
     cudaError_t e;
     if ((e = make_map(&my, dy, N, cap, kTileM)) != cudaSuccess) return e;
     if ((e = make_map(&mx, x, K, cap, kTileM)) != cudaSuccess) return e;
-    return run_experts<kGrad>(g, nseg, seg_off, nullptr, my, my, mx, st);
+    if ((e = make_out_map(&mo, dw, nseg, N, K)) != cudaSuccess) return e;
+    return run_experts<kGrad>(g, nseg, seg_off, nullptr, my, mo, mx, st);
 }
 
 }  // namespace topo

@@ -101,6 +101,20 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
+// This thread's writes to shared memory, before the TMA reads them.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// A box from shared memory to a map of three dimensions, as a group of this thread's.
+__device__ __forceinline__ void tma_store(const CUtensorMap *m, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n"
+                 "cp.async.bulk.commit_group;" ::"l"(m), "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+
+// This thread's stores have read shared memory; have written.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // ------------------------------------------------------------------- tcgen05
 // Instruction descriptor of kind::f8f6f4: D float32 (bits 4-5 = 1), A and B
 // e4m3 (bits 7-9 and 10-12 = 0), both K-major (bits 15, 16 = 0), N >> 3 at
