@@ -72,6 +72,7 @@ constexpr int kIoRegs = (384 * 168 - 256 * kSumRegs<MODE>) / 128;
 constexpr int kTmemCols = 512;                    // two accumulators of 256 columns, or one and the scales
 constexpr uint32_t kABytes = kTileM * kKB;
 constexpr int kStages = 4;                        // 48 KB of operands each
+static_assert(kStages % 2 == 0, "the two scale warps take the stages in turn, and each keeps its own: the barriers' parity repeats");
 // Rows up to which a tile loads only them, 16 at a time, not 128: 8 rows of 8
 // experts, 4096 x 7168: 62 -> 45 us; 6 of 64, 4096 x 1408: 13.4 -> 11.0; no
 // difference where every SM streams weights anyway (24 rows an expert).
@@ -396,7 +397,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
 #pragma unroll
                             for (int i = 0; i < 3; ++i)
                                 reinterpret_cast<uint4 *>(sf)[32 * i + lane] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            tc::fence_async();
                             __syncwarp();
                             if (tc::elect()) {
                                 const uint32_t ts = tmem + kTileN + 16u * (uint32_t)s, from = tc::smem_u32(ring) + at;
