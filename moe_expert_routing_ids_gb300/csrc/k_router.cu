@@ -32,6 +32,10 @@
 // 2^-22 s: 3.3e-7 at most, and the score as defined, rounded four times, by
 // 2.5e-7; twice their sum and the roundings of the sums with the bias stay below
 // kMargin + |c| kMarginRel.
+// The row's sum of weights that are not renormalised takes that exp2 of x - max as
+// well: a term is off by 2^-22 + |x - max| 2^-22 of itself, at most 2^-22 of the sum's
+// largest term in each, where expf would cost 5 instructions more a logit.  The
+// chosen experts' own exp is expf.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -504,10 +508,10 @@ k_route_experts(const __grid_constant__ RouteArgs g) {
                 if (FULL || ((in >> u) & 1u)) m = fmaxf(m, c[u]);
             m = group_max<G>(gmask, m);
             if (m == -kInf) m = 0.f;
-            const float ml = m * 1.4426950408889634f;
+            // the difference first: a rounded m log2(e) would not cancel, nor hold for every m
 #pragma unroll
             for (int u = 0; u < VPL; ++u)
-                if (FULL || ((in >> u) & 1u)) total += exp2_approx(fmaf(c[u], 1.4426950408889634f, -ml));
+                if (FULL || ((in >> u) & 1u)) total += exp2_approx((c[u] - m) * 1.4426950408889634f);
             total = group_sum<G>(gmask, total);
         }
         const int cn = __popc(cm);

@@ -410,3 +410,35 @@ def test_arguments_are_checked_on_the_host():
     with pytest.raises(topo.TopoError) as ex:
         topo.topo_route_grad(c, 1, topo.make_route(SOFT), a, topo.TOPO_DTYPE_F32, a, a, a + 2, a, 256)
     assert ex.value.code == topo.TOPO_EINVAL
+
+
+@gpu
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("E", [8, 64, 256, 500])
+def test_softmax_weights_of_rows_far_from_zero(E, bf16):
+    """Weights that are not renormalised are shares of the whole row: logits far
+    from zero, rows masked to -1e9 or the type's lowest value in whole or in part,
+    rows near the type's largest.  The logits of a row that count lie within 16 of
+    its largest, whose differences are exact to 16 roundings: the 64 above hold."""
+    rng = np.random.default_rng([E, bf16])
+    k, scale = 4, 2.5
+    low = float(torch.finfo(torch.bfloat16 if bf16 else torch.float32).min)
+    x = rng.standard_normal((14, E)).astype(np.float32)
+    for i, v in enumerate((100.0, -100.0, 1e4, -1e4, 1e6)):
+        x[i] += v
+    for i, v in enumerate((-1e9, low, -low, 2.5e38, -1e4, 0.0)):
+        x[5 + i] = v
+    x[11, : E // 2] = -1e9
+    x[12, : E // 2] = low
+    x[13] = -np.inf
+    x[13, 3] = 300.0
+    if bf16:
+        x = torch.as_tensor(x).to(torch.bfloat16).float().numpy()
+    ids, w = run(x, k, SOFT, renorm=False, scale=scale, bf16=bf16)
+    rid, rw, *_ = reference(x, k, SOFT, renorm=False, scale=scale)
+    assert np.array_equal(ids, rid)
+    assert np.all(np.abs(w - rw) <= 64 * U * rw)
+    g = rng.standard_normal(ids.shape).astype(np.float32)
+    dx = grad(x, ids, g, SOFT, False, scale, bf16)
+    want, size = grad_reference(x, ids, g, SOFT, False, scale)
+    assert np.all(np.abs(dx - want) <= (2.0 ** -8 if bf16 else 0.0) * np.abs(want) + 128 * U * size + 1e-30)
