@@ -18,7 +18,7 @@ from . import (TOPO_BLOCK, TOPO_CALL_PACK, TOPO_DTYPE_BF16, TopoRouteOpts, topo_
                topo_expert_gemm, topo_expert_wgrad, topo_expert_workspace_bytes, topo_permute_quantize,
                topo_quantize_cols, topo_quantize_rows, topo_quantize_weight, topo_read_error, topo_swiglu_grad,
                topo_swiglu_quantize, topo_workspace_bytes, topo_ws_reset)
-from .planner import Planner
+from .planner import Planner, ordered
 
 
 def blocks(n: int) -> int:
@@ -33,20 +33,29 @@ class ExpertWeights:
         E, self.N, self.K = w.shape
         self.E = E
         dev, u8, f32 = w.device, torch.uint8, torch.float32
-        self.q = torch.empty((E, self.N, self.K), dtype=u8, device=dev)
-        self.scale = torch.empty((E, blocks(self.N), blocks(self.K)), dtype=f32, device=dev)
-        self.qt = torch.empty((E, self.K, self.N), dtype=u8, device=dev) if train else None
-        self.scale_t = torch.empty((E, blocks(self.K), blocks(self.N)), dtype=f32, device=dev) if train else None
-        topo_quantize_weight(E, self.N, self.K, w, self.q, self.scale, self.qt, self.scale_t,
-                             stream if stream is not None else torch.cuda.current_stream(dev))
+        with ordered(stream, dev, w):
+            self.q = torch.empty((E, self.N, self.K), dtype=u8, device=dev)
+            self.scale = torch.empty((E, blocks(self.N), blocks(self.K)), dtype=f32, device=dev)
+            self.qt = torch.empty((E, self.K, self.N), dtype=u8, device=dev) if train else None
+            self.scale_t = torch.empty((E, blocks(self.K), blocks(self.N)), dtype=f32, device=dev) if train else None
+            topo_quantize_weight(E, self.N, self.K, w, self.q, self.scale, self.qt, self.scale_t,
+                                 torch.cuda.current_stream(dev))
 
 
 class ExpertLayer:
     """cfg: as for Planner (one layer per call); w_up: bf16 [E, 2 I, H], gate
-    rows then up rows; w_down: bf16 [E, H, I]; route: topo_route_opts."""
+    rows then up rows; w_down: bf16 [E, H, I]; route: topo_route_opts.
+
+    stream: every step of every call runs on it (None: torch's current stream).
+    The calls take their place in the caller's current stream all the same: what
+    it holds so far comes before them, what it gets next comes after."""
 
     def __init__(self, cfg: dict, w_up: torch.Tensor, w_down: torch.Tensor, route: TopoRouteOpts, train: bool = False,
                  stream=None):
+        with ordered(stream, w_up.device, w_up, w_down):
+            self._build(cfg, w_up, w_down, route, train, stream)
+
+    def _build(self, cfg, w_up, w_down, route, train, stream):
         self.planner = P = Planner(cfg, 1, w_up.device, stream)
         self.T, self.E, self.k, self.R = cfg["T"], cfg["E"], cfg["k"], cfg["R"]
         self.H, self.I = w_down.shape[1], w_down.shape[2]
@@ -83,6 +92,12 @@ class ExpertLayer:
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor, bias: torch.Tensor | None = None) -> torch.Tensor:
         """x: bf16 [T, H]; logits: float32 or bf16 [T, E]; returns bf16 [T, H]."""
+        with ordered(self.planner.stream, self.out.device, x, logits, bias) as outs:
+            self._forward(x, logits, bias)
+            outs.append(self.out)
+        return self.out
+
+    def _forward(self, x, logits, bias):
         P, s = self.planner, self.planner._stream()
         P.route(logits, self.ids, self.weights, self.route, bias)
         P.make_plan()
@@ -95,7 +110,6 @@ class ExpertLayer:
         self._product(self.aq, self.as_, self.H, self.I, self.down.q, self.down.scale, self.y)
         topo_combine(P.cfg, 1, self.H, self.y, P.buf.sorted_pairs, self.weights, self.out, self.pack_ws,
                      self.pack_bytes, s)
-        return self.out
 
     def _rows8(self, x):
         q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
@@ -123,10 +137,14 @@ class ExpertLayer:
 
     def backward(self, x: torch.Tensor, logits: torch.Tensor, dout: torch.Tensor):
         """Gradients of the last forward(x, logits) for dout (bf16 [T, H]): x
-        (bf16), logits (their type), w_up and w_down (float32, by expert).  Runs
-        on the current stream."""
+        (bf16), logits (their type), w_up and w_down (float32, by expert)."""
         if not self.train:
             raise RuntimeError("ExpertLayer was built without train=True")
+        with ordered(self.planner.stream, self.out.device, x, logits, dout) as outs:
+            outs += self._backward(x, logits, dout)
+        return tuple(outs)
+
+    def _backward(self, x, logits, dout):
         P, s = self.planner, self.planner._stream()
         pair = P.buf.sorted_pairs[0].long()
         token = pair // self.k

@@ -5,6 +5,7 @@ a call into libtopoep through the same-named binding functions.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 
 import torch
@@ -14,6 +15,39 @@ from . import (TOPO_CALL_CHAIN, TOPO_CALL_COOCCUR, TOPO_DTYPE_BF16, TOPO_DTYPE_F
                topo_dispatch_layout, topo_gate_hist,
                topo_hist, topo_plan, topo_read_error, topo_reroute, topo_reroute_layout, topo_route,
                topo_route_grad, topo_workspace_bytes, topo_ws_reset)
+
+
+def torch_stream(stream, device) -> torch.cuda.Stream:
+    """stream (a stream, a raw handle, or None: the current one) as torch's own operations take it."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(getattr(stream, "cuda_stream", stream))
+    return torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+
+
+@contextlib.contextmanager
+def ordered(stream, device, *inputs):
+    """Runs torch's own operations on stream as well, behind what the caller's
+    current stream holds so far and ahead of what it gets next.  inputs: the
+    caller's tensors (or None) that are read there; tensors put into the list
+    that this gives are the caller's to use."""
+    s, caller, outs = torch_stream(stream, device), torch.cuda.current_stream(device), []
+    if s.cuda_stream == caller.cuda_stream:
+        yield outs
+        return
+    s.wait_stream(caller)
+    for t in inputs:
+        if t is not None:
+            t.record_stream(s)
+    try:
+        with torch.cuda.stream(s):
+            yield outs
+    finally:
+        caller.wait_stream(s)
+        for t in outs:
+            t.record_stream(caller)
 
 
 @dataclasses.dataclass
@@ -123,12 +157,15 @@ class Planner:
         """Expert of each instance of the plan, int32 [L, R * n_local], -1 for an
         empty slot: each rank's mains in ascending order, then its replicas."""
         R, E = self.cfg_dict["R"], self.cfg_dict["E"]
-        if self.main_rank is None:
-            mains = torch.arange(E, dtype=torch.int32, device=self.device)
-        else:
-            mains = torch.sort(self.main_rank, stable=True).indices.to(torch.int32)
-        mains = mains.reshape(1, R, E // R).expand(self.L, R, E // R)
-        return torch.cat([mains, self.buf.slot_expert], 2).reshape(self.L, -1)
+        with ordered(self.stream, self.device) as outs:
+            if self.main_rank is None:
+                mains = torch.arange(E, dtype=torch.int32, device=self.device)
+            else:
+                mains = torch.sort(self.main_rank, stable=True).indices.to(torch.int32)
+            mains = mains.reshape(1, R, E // R).expand(self.L, R, E // R)
+            out = torch.cat([mains, self.buf.slot_expert], 2).reshape(self.L, -1)
+            outs.append(out)
+        return out
 
     def make_plan(self, hist: torch.Tensor | None = None):
         h = self.buf.hist if hist is None else hist

@@ -91,3 +91,46 @@ def test_layer_shapes_are_checked():
     with pytest.raises(TypeError):
         layer.planner.route(lg.double(), layer.ids, layer.weights, layer.route)
     assert np.array_equal(layer.planner.instance_experts().cpu().numpy(), [[0, 1, 2, 3]])
+
+
+def _layer(T, E, k, R, slots, H, I, opts, seed=0, stream=None, hot=0.0):
+    """A training layer and inputs x, logits (expert 0 ahead by hot), dout."""
+    from moe_expert_routing_ids_gb300.experts import ExpertLayer
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    dev = torch.device("cuda:0")
+    gen = torch.Generator().manual_seed(seed)
+    up = (torch.randn(E, 2 * I, H, generator=gen) / H ** 0.5).to(torch.bfloat16).to(dev)
+    down = (torch.randn(E, H, I, generator=gen) / I ** 0.5).to(torch.bfloat16).to(dev)
+    x = torch.randn(T, H, generator=gen).to(torch.bfloat16).to(dev)
+    logits = torch.randn(T, E, generator=gen)
+    logits[:, 0] += hot
+    dout = torch.randn(T, H, generator=gen).to(torch.bfloat16).to(dev)
+    cfg = dict(T=T, E=E, k=k, R=R, ranks_per_node=2, n_slot=slots, tok_bytes=2 * H, expert_bytes=64,
+               c_intra=1, c_inter=4, max_refine_iters=0)
+    return ExpertLayer(cfg, up, down, opts, train=True, stream=stream), x, logits.to(dev), dout
+
+
+def test_layer_on_a_stream_of_its_own():
+    """Built with a stream, the layer gives what it gives on the current one,
+    whichever of the two is busy and however late the inputs come."""
+    args = (640, 8, 2, 2, 1, 256, 128, topo.make_route(topo.TOPO_SCORE_SOFTMAX))
+    plain, x, logits, dout = _layer(*args, hot=4.0)
+    want = [plain.forward(x, logits).clone(), *plain.backward(x, logits, dout)]
+    assert int((plain.seg_w >= 0).sum()) > 8                    # replicas are in use
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        torch.cuda._sleep(10_000_000)
+        layer, *_ = _layer(*args, hot=4.0, stream=stream)
+        for _ in range(3):
+            late = [torch.full_like(v, float("nan")) for v in (x, logits, dout)]
+            torch.cuda._sleep(10_000_000)
+            for v, t in zip(late, (x, logits, dout)):
+                v.copy_(t)
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(10_000_000)
+            got = [layer.forward(*late[:2]).clone(), *layer.backward(*late)]
+            late = [v.zero_() for v in late]                    # the caller's next step on its tensors
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert layer.error() == 0
+        assert torch.equal(layer.planner.instance_experts(), plain.planner.instance_experts())
