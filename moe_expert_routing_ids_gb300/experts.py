@@ -18,7 +18,7 @@ from . import (TOPO_BLOCK, TOPO_CALL_PACK, TOPO_DTYPE_BF16, TopoRouteOpts, topo_
                topo_expert_gemm, topo_expert_wgrad, topo_expert_workspace_bytes, topo_permute_quantize,
                topo_quantize_cols, topo_quantize_rows, topo_quantize_weight, topo_read_error, topo_swiglu_grad,
                topo_swiglu_quantize, topo_workspace_bytes, topo_ws_reset)
-from .planner import Planner, ordered
+from .planner import Planner, need, ordered
 
 
 def blocks(n: int) -> int:
@@ -30,8 +30,11 @@ class ExpertWeights:
     their transposes (the operand of the input gradient) when train is set."""
 
     def __init__(self, w: torch.Tensor, train: bool = False, stream=None):
+        if not isinstance(w, torch.Tensor) or w.dim() != 3 or not w.is_cuda:
+            raise ValueError("weights are a tensor [E, N, K] on a GPU")
         E, self.N, self.K = w.shape
         self.E = E
+        need("weights", w, (torch.bfloat16,), E * self.N, self.K, w.device)
         dev, u8, f32 = w.device, torch.uint8, torch.float32
         with ordered(stream, dev, w):
             self.q = torch.empty((E, self.N, self.K), dtype=u8, device=dev)
@@ -52,6 +55,14 @@ class ExpertLayer:
 
     def __init__(self, cfg: dict, w_up: torch.Tensor, w_down: torch.Tensor, route: TopoRouteOpts, train: bool = False,
                  stream=None):
+        for name, w in (("w_up", w_up), ("w_down", w_down)):
+            if not isinstance(w, torch.Tensor) or w.dim() != 3 or not w.is_cuda:
+                raise ValueError(f"{name} must be a tensor of three dimensions on a GPU")
+        E, H, I = cfg["E"], w_down.shape[1], w_down.shape[2]
+        if tuple(w_up.shape) != (E, 2 * I, H) or w_down.shape[0] != E:
+            raise ValueError("w_up is [E, 2 I, H] and w_down [E, H, I]")
+        need("w_up", w_up, (torch.bfloat16,), E * 2 * I, H, w_up.device)
+        need("w_down", w_down, (torch.bfloat16,), E * H, I, w_up.device)
         with ordered(stream, w_up.device, w_up, w_down):
             self._build(cfg, w_up, w_down, route, train, stream)
 
@@ -59,8 +70,6 @@ class ExpertLayer:
         self.planner = P = Planner(cfg, 1, w_up.device, stream)
         self.T, self.E, self.k, self.R = cfg["T"], cfg["E"], cfg["k"], cfg["R"]
         self.H, self.I = w_down.shape[1], w_down.shape[2]
-        if w_up.shape != (self.E, 2 * self.I, self.H) or w_down.shape[0] != self.E:
-            raise ValueError("w_up is [E, 2 I, H] and w_down [E, H, I]")
         self.route, self.train = route, train
         self.up = ExpertWeights(w_up, train, stream)
         self.down = ExpertWeights(w_down, train, stream)
@@ -91,7 +100,9 @@ class ExpertLayer:
                          w_scale, out, TOPO_DTYPE_BF16, self.ws, self.ws_bytes, self.planner._stream())
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor, bias: torch.Tensor | None = None) -> torch.Tensor:
-        """x: bf16 [T, H]; logits: float32 or bf16 [T, E]; returns bf16 [T, H]."""
+        """x: bf16 [T, H]; logits: float32 or bf16 [T, E]; bias: float32 [E] or
+        None; returns bf16 [T, H]."""
+        need("x", x, (torch.bfloat16,), self.T, self.H, self.out.device)
         with ordered(self.planner.stream, self.out.device, x, logits, bias) as outs:
             self._forward(x, logits, bias)
             outs.append(self.out)
@@ -136,10 +147,16 @@ class ExpertLayer:
         return out.index_add_(0, self.seg_w.reshape(-1)[held].long(), dw[held])
 
     def backward(self, x: torch.Tensor, logits: torch.Tensor, dout: torch.Tensor):
-        """Gradients of the last forward(x, logits) for dout (bf16 [T, H]): x
-        (bf16), logits (their type), w_up and w_down (float32, by expert)."""
+        """Gradients of the last forward(x, logits) for dout ([T, H], bf16 or any
+        floating type, any strides): x (bf16), logits (their type), w_up and
+        w_down (float32, by expert)."""
         if not self.train:
             raise RuntimeError("ExpertLayer was built without train=True")
+        need("x", x, (torch.bfloat16,), self.T, self.H, self.out.device)
+        if not isinstance(dout, torch.Tensor) or not dout.is_floating_point():
+            raise TypeError("dout must be a tensor of floating point")
+        if dout.numel() != self.T * self.H or dout.shape[-1] != self.H or dout.device != x.device:
+            raise ValueError(f"dout must hold {self.T} x {self.H} values on {x.device}, is {list(dout.shape)}")
         with ordered(self.planner.stream, self.out.device, x, logits, dout) as outs:
             outs += self._backward(x, logits, dout)
         return tuple(outs)
@@ -149,7 +166,7 @@ class ExpertLayer:
         pair = P.buf.sorted_pairs[0].long()
         token = pair // self.k
         # combine: out[t] = sum_j w[t, j] y[pos(t, j)]
-        d = dout[token].float()
+        d = dout.reshape(self.T, self.H)[token].float()
         dw = torch.empty(self.rows, dtype=torch.float32, device=x.device)
         dw[pair] = (self.y.float() * d).sum(-1)
         dy = (d * self.weights.reshape(-1)[pair][:, None]).to(torch.bfloat16)
@@ -169,7 +186,7 @@ class ExpertLayer:
         dx = torch.empty_like(x)
         topo_combine(P.cfg, 1, self.H, dxr, P.buf.sorted_pairs, torch.ones_like(self.weights), dx, self.pack_ws,
                      self.pack_bytes, s)
-        dw_up = self._weight_grad(dh, x[token])
+        dw_up = self._weight_grad(dh, x.view(self.T, self.H)[token])
         return dx, dlogits, dw_up, dw_down
 
     def error(self) -> int:

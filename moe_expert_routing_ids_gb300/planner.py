@@ -27,6 +27,19 @@ def torch_stream(stream, device) -> torch.cuda.Stream:
     return torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
 
 
+def need(name: str, t, dtypes, rows: int, last: int, device):
+    """Raises unless t holds rows x last values of one of the types, rows by rows
+    without gaps, on the device: a call reads its memory as just that."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a tensor of {' or '.join(str(d)[6:] for d in dtypes)}")
+    if t.numel() != rows * last or (t.dim() > 1 and t.shape[-1] != last):
+        raise ValueError(f"{name} must hold {rows} x {last} values, is {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device.type != device.type or device.index not in (None, t.device.index):
+        raise ValueError(f"{name} must be on {device}")
+
+
 @contextlib.contextmanager
 def ordered(stream, device, *inputs):
     """Runs torch's own operations on stream as well, behind what the caller's
@@ -131,26 +144,40 @@ class Planner:
         topo_gate_hist(self.cfg, self.L, logits, dt, bias, ids, scores, self.buf.hist, self.ws,
                        self.ws_bytes, self._stream())
 
-    @staticmethod
-    def _dtype(logits: torch.Tensor) -> int:
-        if logits.dtype == torch.float32:
-            return TOPO_DTYPE_F32
-        if logits.dtype == torch.bfloat16:
-            return TOPO_DTYPE_BF16
-        raise TypeError("logits must be float32 or bfloat16")
+    def _logits(self, logits: torch.Tensor) -> int:
+        """The type of router logits [L, T, E] ([T, E] for one layer)."""
+        if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("logits must be float32 or bfloat16")
+        self._need("logits", logits, logits.dtype, self.cfg_dict["E"])
+        return TOPO_DTYPE_F32 if logits.dtype == torch.float32 else TOPO_DTYPE_BF16
+
+    def _need(self, name: str, t, dtype, last: int):
+        """A tensor of all layers' tokens, [L, T, last]."""
+        need(name, t, (dtype,), self.L * self.cfg_dict["T"], last, self.device)
 
     def route(self, logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, opts,
               bias: torch.Tensor | None = None):
         """Routing to experts (opts: make_route(...)) of logits [L, T, E] into ids
         (int32 [L, T, k]), weights (float32 [L, T, k]) and the histogram; leaves
-        the tile index so that make_plan / reroute_layout(ids) can follow."""
-        topo_route(self.cfg, self.L, opts, logits, self._dtype(logits), bias, ids, weights, self.buf.hist, self.ws,
+        the tile index so that make_plan / reroute_layout(ids) can follow.
+        bias: float32 [E]."""
+        dt, k = self._logits(logits), self.cfg_dict["k"]
+        self._need("ids", ids, torch.int32, k)
+        self._need("weights", weights, torch.float32, k)
+        if bias is not None:
+            need("bias", bias, (torch.float32,), 1, self.cfg_dict["E"], self.device)
+        topo_route(self.cfg, self.L, opts, logits, dt, bias, ids, weights, self.buf.hist, self.ws,
                    self.ws_bytes, self._stream())
 
     def route_grad(self, logits: torch.Tensor, ids: torch.Tensor, grad_weights: torch.Tensor,
                    grad_logits: torch.Tensor, opts):
-        """Gradient of route()'s weights in the logits (grad_logits: the logits' type)."""
-        topo_route_grad(self.cfg, self.L, opts, logits, self._dtype(logits), ids, grad_weights, grad_logits, self.ws,
+        """Gradient of route()'s weights in the logits (grad_weights: float32
+        [L, T, k]; grad_logits: as the logits)."""
+        dt, k = self._logits(logits), self.cfg_dict["k"]
+        self._need("ids", ids, torch.int32, k)
+        self._need("grad_weights", grad_weights, torch.float32, k)
+        self._need("grad_logits", grad_logits, logits.dtype, self.cfg_dict["E"])
+        topo_route_grad(self.cfg, self.L, opts, logits, dt, ids, grad_weights, grad_logits, self.ws,
                         self.ws_bytes, self._stream())
 
     def instance_experts(self) -> torch.Tensor:

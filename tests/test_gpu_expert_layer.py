@@ -134,3 +134,57 @@ def test_layer_on_a_stream_of_its_own():
             assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert layer.error() == 0
         assert torch.equal(layer.planner.instance_experts(), plain.planner.instance_experts())
+
+
+def test_layer_arguments_are_checked():
+    """Types, sizes, layouts and devices that a call would misread are refused;
+    other strides and types of dout, which torch reads, are not."""
+    from moe_expert_routing_ids_gb300.experts import ExpertLayer, ExpertWeights
+    T, E, k, H, I = 64, 8, 2, 128, 64
+    route = topo.make_route(topo.TOPO_SCORE_SIGMOID)
+    layer, x, logits, dout = _layer(T, E, k, 4, 1, H, I, route)
+    dev = x.device
+    bias = torch.zeros(E, device=dev)
+    want = layer.forward(x, logits, bias).clone()
+    grads = layer.backward(x, logits, dout)
+    assert torch.equal(layer.forward(x[None], logits[None], bias), want)
+
+    def refused(kind, f, *args):
+        with pytest.raises(kind):
+            f(*args)
+
+    short = torch.zeros(T - 1, H, dtype=torch.bfloat16, device=dev)
+    for bad, kind in ((x.float(), TypeError), (None, TypeError), (x.half(), TypeError), (short, ValueError),
+                      (x.t().contiguous().t(), ValueError), (x.t().contiguous(), ValueError), (x.cpu(), ValueError),
+                      (torch.zeros(T, 2 * H, dtype=torch.bfloat16, device=dev)[:, :H], ValueError)):
+        refused(kind, layer.forward, bad, logits)
+        refused(kind, layer.backward, bad, logits, dout)
+    for bad, kind in ((logits.double(), TypeError), (logits[:-1], ValueError), (logits[:, :4], ValueError),
+                      (logits.t().contiguous().t(), ValueError), (logits.cpu(), ValueError)):
+        refused(kind, layer.forward, x, bad)
+        refused(kind, layer.backward, x, bad, dout)
+    for bad, kind in ((bias.double(), TypeError), (bias[:4], ValueError), (bias.cpu(), ValueError)):
+        refused(kind, layer.forward, x, logits, bad)
+    for bad, kind in ((short, ValueError), (dout.long(), TypeError), (None, TypeError), (dout.cpu(), ValueError)):
+        refused(kind, layer.backward, x, logits, bad)
+    layer.forward(x, logits, bias)
+    for same in (dout.float(), dout.t().contiguous().t(), dout[None]):
+        assert all(torch.equal(a, b) for a, b in zip(layer.backward(x, logits, same), grads))
+
+    P, ids, w = layer.planner, layer.ids, layer.weights
+    for i, w_ in ((ids.long(), w), (ids, w.double()), (ids[:, 1:], w), (ids, w[:, 1:])):
+        refused((TypeError, ValueError), P.route, logits, i, w_, route)
+    refused(ValueError, P.route_grad, logits, ids, w[:, 1:], torch.empty_like(logits), route)
+    refused(TypeError, P.route_grad, logits, ids, w, torch.empty_like(logits, dtype=torch.bfloat16), route)
+
+    up = torch.zeros(E, 2 * I, H, dtype=torch.bfloat16, device=dev)
+    down = torch.zeros(E, H, I, dtype=torch.bfloat16, device=dev)
+    cfg = dict(T=T, E=E, k=k, R=4, ranks_per_node=2, n_slot=1, tok_bytes=64, expert_bytes=64, c_intra=1, c_inter=1)
+    for u, d, kind in ((up.float(), down, TypeError), (up, down.float(), TypeError), (up.cpu(), down, ValueError),
+                       (up, down.cpu(), ValueError), (up.transpose(1, 2).contiguous().transpose(1, 2), down, ValueError),
+                       (up[:4], down[:4], ValueError), (up[0], down, ValueError)):
+        refused(kind, ExpertLayer, cfg, u, d, route)
+    refused(TypeError, ExpertWeights, up.float())
+    refused(ValueError, ExpertWeights, up[0])
+    refused(ValueError, ExpertWeights, up.cpu())
+    assert layer.error() == 0
