@@ -142,9 +142,16 @@ class ExpertLayer:
         N, K = dy.shape[1], x.shape[1]
         dw = torch.empty((self.n_seg, N, K), dtype=torch.float32, device=dev)
         topo_expert_wgrad(self.n_seg, self.rows, N, K, cap, *ops, P.buf.seg_off, dw, self.ws, self.ws_bytes, s)
-        out = torch.zeros((self.E, N, K), dtype=torch.float32, device=dev)
-        held = self.seg_w.reshape(-1) >= 0
-        return out.index_add_(0, self.seg_w.reshape(-1)[held].long(), dw[held])
+        # an expert's instances one after the other, its main one first, then its
+        # replicas by rank: the same bits each time (float32 atomics would not give that)
+        seg = self.seg_w.view(self.R, -1)
+        inst = torch.arange(self.n_seg, device=dev).view(self.R, -1)
+        m = self.E // self.R
+        out = dw[inst[:, :m].reshape(-1)[torch.argsort(seg[:, :m].reshape(-1))]]
+        for i, e in zip(inst[:, m:].reshape(-1).tolist(), seg[:, m:].reshape(-1).tolist()):
+            if e >= 0:
+                out[e] += dw[i]
+        return out
 
     def backward(self, x: torch.Tensor, logits: torch.Tensor, dout: torch.Tensor):
         """Gradients of the last forward(x, logits) for dout ([T, H], bf16 or any

@@ -188,3 +188,43 @@ def test_layer_arguments_are_checked():
     refused(ValueError, ExpertWeights, up[0])
     refused(ValueError, ExpertWeights, up.cpu())
     assert layer.error() == 0
+
+
+def test_backward_repeats_bit_for_bit():
+    """Four instances of one expert: their weight gradients are added in one order."""
+    layer, x, logits, dout = _layer(2048, 8, 2, 8, 1, 256, 128, topo.make_route(topo.TOPO_SCORE_SOFTMAX), hot=6.0)
+    layer.forward(x, logits)
+    assert int((layer.seg_w == 0).sum()) >= 4
+    first = [g.clone() for g in layer.backward(x, logits, dout)]
+    for _ in range(8):
+        for a, b in zip(layer.backward(x, logits, dout), first):
+            assert torch.equal(a, b)
+    assert layer.error() == 0
+
+
+def test_weight_gradients_of_instances_are_added_in_order(monkeypatch):
+    """An expert's gradient is its main instance's plus its replicas', by rank."""
+    from moe_expert_routing_ids_gb300 import experts
+    layer, x, logits, dout = _layer(2048, 8, 2, 8, 2, 256, 128, topo.make_route(topo.TOPO_SCORE_SOFTMAX), hot=6.0)
+    layer.forward(x, logits)
+    seen, call = [], experts.topo_expert_wgrad
+
+    def watched(*args):
+        call(*args)
+        seen.append(args[10].clone())
+
+    monkeypatch.setattr(experts, "topo_expert_wgrad", watched)
+    *_, up, down = layer.backward(x, logits, dout)
+    seg = layer.seg_w.reshape(8, -1).cpu()
+    nm = 1                                                      # mains of a rank
+    assert int((seg == 0).sum()) >= 4
+    for inst, got in zip(seen, (down, up)):
+        inst = inst.reshape(8, seg.shape[1], *inst.shape[1:])
+        for e in range(8):
+            want = inst[e, 0]
+            for r in range(8):
+                for j in range(nm, seg.shape[1]):
+                    if seg[r, j] == e:
+                        want = want + inst[r, j]
+            assert torch.equal(got[e], want)
+    assert layer.error() == 0
