@@ -700,7 +700,7 @@ k_route_grad(RouteGradArgs g) {
         for (int h = 0; h < 2; ++h)
             if (id[h] >= 0) {
                 float d = g.scale * w[h] * (gr[h] - dot);
-                if (!soft) d *= 1.f - s[h];
+                if (!soft) d *= sigmoid_rn(-x[h]);                // 1 - s: from the rounded s it would be 0 from 17.4 on
                 put<BF>(out, id[h], d);
             }
     }

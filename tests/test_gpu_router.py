@@ -442,3 +442,24 @@ def test_softmax_weights_of_rows_far_from_zero(E, bf16):
     dx = grad(x, ids, g, SOFT, False, scale, bf16)
     want, size = grad_reference(x, ids, g, SOFT, False, scale)
     assert np.all(np.abs(dx - want) <= (2.0 ** -8 if bf16 else 0.0) * np.abs(want) + 128 * U * size + 1e-30)
+
+
+@gpu
+@pytest.mark.parametrize("renorm", [True, False])
+def test_sigmoid_gradient_of_large_logits(renorm):
+    """The derivative s (1 - s) is 1 - s near 1: it is held to its own size, to
+    which exp and three roundings of each of the two factors count, not to s's."""
+    rng = np.random.default_rng(11)
+    T, E, k, scale = 40, 24, 5, 2.5
+    x = rng.uniform(5, 30, (T, E)).astype(np.float32)
+    x[20:] = rng.uniform(-30, 30, (20, E))
+    ids, _ = run(x, k, SIG, renorm=renorm, scale=scale)
+    g = rng.standard_normal((T, k)).astype(np.float32)
+    dx = grad(x, ids, g, SIG, renorm, scale)
+    p = np.take_along_axis(scores(x, SIG), ids, 1)
+    q = np.take_along_axis(scores(-x, SIG), ids, 1)      # 1 - p
+    S = p.sum(-1, keepdims=True) if renorm else np.ones((T, 1))
+    dot = (g * p).sum(-1, keepdims=True) / S if renorm else 0.0
+    size = (np.abs(g) * p).sum(-1, keepdims=True) / S if renorm else 0.0
+    got = np.take_along_axis(dx, ids, 1)
+    assert np.all(np.abs(got - scale * (g - dot) * p * q / S) <= 128 * U * scale * (np.abs(g) + size) * p * q / S + 1e-30)
