@@ -309,7 +309,8 @@ __device__ __noinline__ void exact_token(const RouteArgs &g, const void *row, co
         float s = soft ? expf(v - mc) : sigmoid_rn(v);
         if (soft && !g.renorm) s = total == 0.f ? 0.f : __fdiv_rn(s, total);
         g.ids[tok * g.k + j] = w.sel[j];
-        g.weights[tok * g.k + j] = g.renorm ? (sum == 0.f ? 0.f : s * (g.scale / sum)) : g.scale * s;
+        if (g.renorm) s = sum == 0.f ? 0.f : s / sum;             // scale / sum may overflow
+        g.weights[tok * g.k + j] = g.scale * s;
     }
 }
 
@@ -579,14 +580,13 @@ k_route_experts(const __grid_constant__ RouteArgs g) {
         } else if (!on) {
             s = 0.f;
         }
-        float f = g.scale;
         if (g.renorm) {
             const float sum = group_sum<G>(gmask, s);
-            f = sum == 0.f ? 0.f : f / sum;
+            s = sum == 0.f ? 0.f : s / sum;                       // scale / sum may overflow
         }
         if (on) {
             g.ids[tok * k + gl] = w.sel[gl];
-            g.weights[tok * k + gl] = s * f;
+            g.weights[tok * k + gl] = g.scale * s;
         }
         __syncwarp(gmask);                                        // the scratch is free again
     }
@@ -683,16 +683,15 @@ k_route_grad(RouteGradArgs g) {
         if (dense) sum = total;
         else if (g.renorm) sum = group_sum<32>(0xffffffffu, sum);
         else sum = 1.f;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         float dot = 0.f;                                          // sum of g_j w_j / scale
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            w[h] = soft || g.renorm ? s[h] * inv : s[h];
+            w[h] = sum == 0.f ? 0.f : s[h] / sum;                 // a sum of small scores has no finite inverse
             dot += gr[h] * w[h];
         }
         dot = soft || g.renorm ? group_sum<32>(0xffffffffu, dot) : 0.f;
         if (dense) {
-            const float f = -g.scale * dot * inv;
+            const float f = sum == 0.f ? 0.f : -g.scale * dot / sum;
             for (int e = lane; e < E; e += 32) put<BF>(out, e, f == 0.f ? 0.f : f * expf(logit<BF>(row, e) - m));
         }
         __syncwarp();

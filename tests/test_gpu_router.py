@@ -463,3 +463,28 @@ def test_sigmoid_gradient_of_large_logits(renorm):
     size = (np.abs(g) * p).sum(-1, keepdims=True) / S if renorm else 0.0
     got = np.take_along_axis(dx, ids, 1)
     assert np.all(np.abs(got - scale * (g - dot) * p * q / S) <= 128 * U * scale * (np.abs(g) + size) * p * q / S + 1e-30)
+
+
+@gpu
+@pytest.mark.parametrize("k,scale", [(1, 2.5), (4, 2.5), (4, 1.0), (20, 16.0)])
+def test_sigmoid_weights_of_scores_near_underflow(k, scale):
+    """Renormalised weights are finite and sum to scale while any chosen score is
+    above 0; a score is 0 in float32 below a logit of -88.72, and from -86 down
+    it has 21 bits or more: half a unit of the last is 2^-22 = 4 * 2^-24."""
+    E, T = 64, 30
+    rng = np.random.default_rng(k)
+    x = rng.uniform(-88.7, -86, (T, E)).astype(np.float32)
+    x[10:] = -95.0
+    x[10:20, 7] = np.linspace(-88.7, -86, 10)
+    x[10:20, 40] = -88.7
+    ids, w = run(x, k, SIG, renorm=True, scale=scale)
+    assert np.array_equal(ids, reference(x, k, SIG)[0])
+    p = np.where(np.take_along_axis(x, ids, 1) < -88.72, 0.0, np.take_along_axis(scores(x, SIG), ids, 1))
+    S = p.sum(-1, keepdims=True)
+    want = np.where(S == 0, 0.0, scale * p / np.where(S == 0, 1.0, S))
+    assert np.all(np.abs(w - want) <= 64 * U * want)
+    g = rng.standard_normal((T, k)).astype(np.float32)
+    got = np.take_along_axis(grad(x, ids, g, SIG, True, scale), ids, 1)
+    r = want / scale
+    dot, size = (g * r).sum(-1, keepdims=True), (np.abs(g) * r).sum(-1, keepdims=True)
+    assert np.all(np.abs(got - scale * r * (g - dot)) <= 128 * U * scale * r * (np.abs(g) + size) + 1e-30)
