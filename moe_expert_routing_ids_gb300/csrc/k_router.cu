@@ -20,8 +20,8 @@
 //   - candidates are evaluated as defined and ranked by counting;
 //   - groups whose scores are closer than the margin: the row is done again with
 //     every score as defined;
-//   - rows with NaN or infinities (where groups or the sigmoid are involved; among
-//     the biases: every row), many ties: exact_token, which is not for speed (19 rows of 65536 sent
+//   - rows with NaN or infinities (where groups or the sigmoid are involved; a bias
+//     that is neither finite nor below 3e30: every row), many ties: exact_token, which is not for speed (19 rows of 65536 sent
 //     there for their groups cost 24 us, its code being read from memory).
 // Measured, 1M x 512 softmax, k = 10: 570 us, 3.9 TB/s; 65536 x 256 sigmoid, 4 of 8
 // groups, k = 8: 44 us.  Bound by issue: 700 instructions for two rows of 512
@@ -31,7 +31,11 @@
 // times s (1 - s) in s (|x| s (1 - s) < 0.23), the sum and the reciprocal by
 // 2^-22 s: 3.3e-7 at most, and the score as defined, rounded four times, by
 // 2.5e-7; twice their sum and the roundings of the sums with the bias stay below
-// kMargin + |c| kMarginRel.
+// kMargin + |c| kMarginRel.  A group's score a + b is off by what its two values are
+// (1.2e-6 and an ulp of each: 1.2e-7 (|a| + |b|), which may cancel in a + b) and the
+// sums' own roundings: below kMargin + (|a| + |b|) kMarginRel to either side, so each
+// group has bounds of its own, and two groups whose bounds overlap may be in either
+// order.
 // The row's sum of weights that are not renormalised takes that exp2 of x - max as
 // well: a term is off by 2^-22 + |x - max| 2^-22 of itself, at most 2^-22 of the sum's
 // largest term in each, where expf would cost 5 instructions more a logit.  The
@@ -187,7 +191,7 @@ struct RouteScratch {
     int *ce;            // candidates' experts
     int *sel;           // chosen experts, and their logits (the fast rows of a sigmoid: scores)
     float *sx;
-    float *gsc;         // [n_group]
+    float *gsc;         // [n_group] groups' scores; the fast rows of a sigmoid: lower bounds
 };
 
 // Every score as defined, the groups, and k rounds of an argmax: chosen experts
@@ -331,7 +335,8 @@ k_route_experts(const __grid_constant__ RouteArgs g) {
     __shared__ int ce_[kGroups][kRouteCand];
     __shared__ int sel_[kGroups][kMaxK];
     __shared__ float sx_[kGroups][kMaxK];
-    __shared__ __align__(16) float gsc_[kGroups][TOPO_ROUTE_MAX_GROUPS];
+    constexpr int kHi = SIG ? TOPO_ROUTE_MAX_GROUPS : 0;          // upper bounds of the groups' scores, behind the lower ones
+    __shared__ __align__(16) float gsc_[kGroups][TOPO_ROUTE_MAX_GROUPS + kHi];
     extern __shared__ __align__(16) float dyn[];
     const int lane = threadIdx.x & 31, gl = lane & (G - 1), grp = threadIdx.x / G;
     const unsigned gmask = G == 32 ? 0xffffffffu : (((1u << (G & 31)) - 1u) << (lane & ~(G - 1)));
@@ -340,11 +345,11 @@ k_route_experts(const __grid_constant__ RouteArgs g) {
     pdl_trigger();
     pdl_wait();
     const RouteScratch w = {dyn + Ep + grp * Ep, keys_[grp], ce_[grp], sel_[grp], sx_[grp], gsc_[grp]};
-    float bias_odd = 0.f;                                         // NaN with any NaN or infinity among the biases
+    float bias_odd = 0.f;                                         // NaN with a bias whose sums may not be finite
     if (SIG) {
         for (int e = threadIdx.x; e < Ep; e += kRouteThreads) {
             sb[e] = g.bias && e < E ? __ldg(g.bias + e) : 0.f;
-            bias_odd = fmaf(sb[e], 0.f, bias_odd);
+            bias_odd = fmaf(sb[e] * 1e8f, 0.f, bias_odd);
         }
         if (__syncthreads_or(bias_odd != 0.f)) bias_odd = kInf * 0.f;
     }
@@ -368,7 +373,7 @@ k_route_experts(const __grid_constant__ RouteArgs g) {
     int chunk_of[VPL / VEC];                                      // groups of this lane's loads
 #pragma unroll
     for (int c = 0; c < VPL / VEC; ++c) chunk_of[c] = (int)fast_quot((unsigned)((c * G + gl) * VEC), g.gdiv) & 31;
-    for (int q = gl; q < TOPO_ROUTE_MAX_GROUPS; q += G) w.gsc[q] = -kInf;   // past n_group: below every group
+    for (int q = gl; q < TOPO_ROUTE_MAX_GROUPS; q += G) w.gsc[q] = w.gsc[kHi + q] = -kInf;   // past n_group: below every group
     __syncwarp(gmask);
     for (int64_t tok = (int64_t)blockIdx.x * kGroups + grp; tok < g.ntok; tok += (int64_t)gridDim.x * kGroups) {
         const void *row = static_cast<const char *>(g.logits) + (size_t)tok * E * (BF ? 2 : 4);
@@ -451,29 +456,36 @@ k_route_experts(const __grid_constant__ RouteArgs g) {
                     b = fmaxf(fminf(a, oa), fmaxf(b, ob));
                     a = fmaxf(a, oa);
                 }
-                if (sub == 0 && q < g.n_group) w.gsc[q] = g.group_top == 2 ? a + b : a;
+                if (sub == 0 && q < g.n_group) {
+                    const float v = g.group_top == 2 ? a + b : a;
+                    if (SIG) {
+                        const float size = g.group_top == 2 ? fabsf(a) + fabsf(b) : fabsf(a);
+                        const float d = precise ? 0.f : kMargin + size * kMarginRel;
+                        w.gsc[q] = v - d;
+                        w.gsc[kHi + q] = v + d;
+                    } else {
+                        w.gsc[q] = v;
+                    }
+                }
                 __syncwarp(gmask);
                 bool kept = false;
                 if (gl < g.n_group) {
-                    // groups surely above this one, and those that may be (itself among them)
-                    const float v = w.gsc[gl], d = SIG && !precise ? 2.f * (kMargin + fabsf(v) * kMarginRel) : 0.f;
-                    const float vh = v + d, vl = v - d;
-                    int sure = 0, may = 0;
-                    for (int i = 0; i < g.n_group; i += 4) {
-                        const float4 o = *reinterpret_cast<const float4 *>(w.gsc + i);
-                        sure += (o.x > vh) + (o.y > vh) + (o.z > vh) + (o.w > vh);
-                        may += (o.x >= vl) + (o.y >= vl) + (o.z >= vl) + (o.w >= vl);
-                    }
+                    // groups that may be above this one, itself among them
+                    const float v = w.gsc[gl];
+                    int may = 0;
                     if (precise) {                                    // equal scores by index
 #pragma unroll 1
-                        for (int i = 0; i < gl; ++i) sure += w.gsc[i] == v;
-                        kept = sure < g.topk_group;
+                        for (int i = 0; i < g.n_group; ++i) may += i == gl || above(w.gsc[i], i, v, gl);
                     } else {
-                        kept = may <= g.topk_group;
-                        unsure |= !kept && sure < g.topk_group;
+                        for (int i = 0; i < g.n_group; i += 4) {
+                            const float4 o = *reinterpret_cast<const float4 *>(w.gsc + kHi + i);
+                            may += (o.x >= v) + (o.y >= v) + (o.z >= v) + (o.w >= v);
+                        }
                     }
+                    kept = may <= g.topk_group;
                 }
                 const unsigned keep = __ballot_sync(gmask, kept) >> (lane & ~(G - 1) & 31);
+                unsure |= __popc(keep) != g.topk_group;               // fewer are sure to stay
                 if (VEC == 1 || g.chunk_group) {                      // a load's experts are of one group
                     unsigned out = 0;
 #pragma unroll

@@ -488,3 +488,48 @@ def test_sigmoid_weights_of_scores_near_underflow(k, scale):
     r = want / scale
     dot, size = (g * r).sum(-1, keepdims=True), (np.abs(g) * r).sum(-1, keepdims=True)
     assert np.all(np.abs(got - scale * r * (g - dot)) <= 128 * U * scale * r * (np.abs(g) + size) + 1e-30)
+
+
+def group_choice(x, bias, G, kept, k):
+    """The ids of the definition in float32, every operation rounded."""
+    xd = torch.as_tensor(x, device=_dev())
+    c = 1.0 / (1.0 + torch.exp(-xd)) + torch.as_tensor(bias, device=xd.device)
+    T, E = x.shape
+    top = torch.sort(c.reshape(T, G, -1), dim=-1, descending=True).values
+    keep = torch.sort(top[..., 0] + top[..., 1], dim=-1, descending=True, stable=True).indices[:, :kept]
+    on = torch.zeros(T, G, dtype=torch.bool, device=xd.device).scatter_(1, keep, True).repeat_interleave(E // G, 1)
+    return torch.sort(c.masked_fill(~on, -torch.inf), dim=-1, descending=True, stable=True).indices[:, :k].cpu().numpy()
+
+
+@gpu
+@pytest.mark.parametrize("which", ["all", "one"])
+@pytest.mark.parametrize("size", [32.0, 64.0, 500.0, 1e6])
+def test_group_scores_whose_biases_cancel(size, which):
+    """The two largest values of a group near +size and -size: their sum is
+    small, its rounding is not.  Groups alike up to a few such roundings."""
+    E, G, kept, k, T = 64, 8, 3, 4, 4096
+    rng = np.random.default_rng([int(size), which == "one"])
+    x = np.tile(rng.standard_normal((T, 1, E // G)), (1, G, 1)).reshape(T, E)
+    x = (x + rng.standard_normal((T, E)) * size * 2.0 ** -22).astype(np.float32)
+    bias = np.full((G, E // G), -size, np.float32)
+    bias[:, 0] = size
+    if which == "one":                                   # the others reach the same sums without cancelling
+        bias[1:] = np.array([0.0, 0.0] + [-4.0] * (E // G - 2), np.float32)
+        x = x.reshape(T, G, -1)
+        x[:, :, 1:] = np.minimum(x[:, :, 1:], x[:, :, 1:2])
+        x = x.reshape(T, E)
+    bias = bias.reshape(-1)
+    ids, _ = run(x, k, SIG, bias, G, kept, 2)
+    assert np.array_equal(ids, group_choice(x, bias, G, kept, k))
+
+
+@gpu
+def test_group_scores_that_overflow():
+    """Sums of two biases past the largest float32 are equal: the lower group stays."""
+    E, G, k, T = 64, 8, 4, 33
+    x = np.random.default_rng(3).standard_normal((T, E)).astype(np.float32)
+    bias = np.zeros(E, np.float32)
+    bias[[17, 18, 41, 42]] = 3e38
+    ids, _ = run(x, k, SIG, bias, G, 1, 2)
+    assert np.array_equal(ids, group_choice(x, bias, G, 1, k))
+    assert np.all(ids // 8 == 2)
