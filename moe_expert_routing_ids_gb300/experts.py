@@ -73,7 +73,8 @@ class ExpertLayer:
         self.route, self.train = route, train
         self.up = ExpertWeights(w_up, train, stream)
         self.down = ExpertWeights(w_down, train, stream)
-        dev, rows = w_up.device, self.T * self.k
+        self.device = dev = w_up.device
+        rows = self.T * self.k
         self.rows, self.n_seg = rows, self.R * P.n_local
         u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
 
@@ -86,7 +87,6 @@ class ExpertLayer:
         self.h = buf(rows, 2 * self.I, dtype=bf16)
         self.aq, self.as_ = buf(rows, self.I, dtype=u8), buf(rows, blocks(self.I), dtype=f32)
         self.y = buf(rows, self.H, dtype=bf16)
-        self.out = buf(self.T, self.H, dtype=bf16)
         self.pack_bytes = topo_workspace_bytes(P.cfg, 1, TOPO_CALL_PACK)
         self.pack_ws = buf(self.pack_bytes, dtype=u8)
         self.ws_bytes = topo_expert_workspace_bytes(self.n_seg, rows, 2 * self.I, self.H)
@@ -102,11 +102,10 @@ class ExpertLayer:
     def forward(self, x: torch.Tensor, logits: torch.Tensor, bias: torch.Tensor | None = None) -> torch.Tensor:
         """x: bf16 [T, H]; logits: float32 or bf16 [T, E]; bias: float32 [E] or
         None; returns bf16 [T, H]."""
-        need("x", x, (torch.bfloat16,), self.T, self.H, self.out.device)
-        with ordered(self.planner.stream, self.out.device, x, logits, bias) as outs:
-            self._forward(x, logits, bias)
-            outs.append(self.out)
-        return self.out
+        need("x", x, (torch.bfloat16,), self.T, self.H, self.device)
+        with ordered(self.planner.stream, self.device, x, logits, bias) as outs:
+            outs.append(self._forward(x, logits, bias))
+        return outs[0]
 
     def _forward(self, x, logits, bias):
         P, s = self.planner, self.planner._stream()
@@ -119,8 +118,9 @@ class ExpertLayer:
         self._product(self.xq, self.xs, 2 * self.I, self.H, self.up.q, self.up.scale, self.h)
         topo_swiglu_quantize(self.rows, self.I, self.h, self.aq, self.as_, s)
         self._product(self.aq, self.as_, self.H, self.I, self.down.q, self.down.scale, self.y)
-        topo_combine(P.cfg, 1, self.H, self.y, P.buf.sorted_pairs, self.weights, self.out, self.pack_ws,
-                     self.pack_bytes, s)
+        out = torch.empty((self.T, self.H), dtype=torch.bfloat16, device=self.device)
+        topo_combine(P.cfg, 1, self.H, self.y, P.buf.sorted_pairs, self.weights, out, self.pack_ws, self.pack_bytes, s)
+        return out
 
     def _rows8(self, x):
         q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
@@ -159,12 +159,12 @@ class ExpertLayer:
         w_down (float32, by expert)."""
         if not self.train:
             raise RuntimeError("ExpertLayer was built without train=True")
-        need("x", x, (torch.bfloat16,), self.T, self.H, self.out.device)
+        need("x", x, (torch.bfloat16,), self.T, self.H, self.device)
         if not isinstance(dout, torch.Tensor) or not dout.is_floating_point():
             raise TypeError("dout must be a tensor of floating point")
         if dout.numel() != self.T * self.H or dout.shape[-1] != self.H or dout.device != x.device:
             raise ValueError(f"dout must hold {self.T} x {self.H} values on {x.device}, is {list(dout.shape)}")
-        with ordered(self.planner.stream, self.out.device, x, logits, dout) as outs:
+        with ordered(self.planner.stream, self.device, x, logits, dout) as outs:
             outs += self._backward(x, logits, dout)
         return tuple(outs)
 

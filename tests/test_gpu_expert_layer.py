@@ -228,3 +228,11 @@ def test_weight_gradients_of_instances_are_added_in_order(monkeypatch):
                         want = want + inst[r, j]
             assert torch.equal(got[e], want)
     assert layer.error() == 0
+
+
+def test_an_output_outlives_the_next_call():
+    layer, x, logits, _ = _layer(64, 8, 2, 4, 1, 128, 64, topo.make_route(topo.TOPO_SCORE_SOFTMAX))
+    a = layer.forward(x, logits)
+    kept = a.clone()
+    b = layer.forward(-x, logits)
+    assert torch.equal(a, kept) and not torch.equal(a, b)
