@@ -34,15 +34,20 @@ class ExpertWeights:
             raise ValueError("weights are a tensor [E, N, K] on a GPU")
         E, self.N, self.K = w.shape
         self.E = E
-        need("weights", w, (torch.bfloat16,), E * self.N, self.K, w.device)
         dev, u8, f32 = w.device, torch.uint8, torch.float32
         with ordered(stream, dev, w):
             self.q = torch.empty((E, self.N, self.K), dtype=u8, device=dev)
             self.scale = torch.empty((E, blocks(self.N), blocks(self.K)), dtype=f32, device=dev)
             self.qt = torch.empty((E, self.K, self.N), dtype=u8, device=dev) if train else None
             self.scale_t = torch.empty((E, blocks(self.K), blocks(self.N)), dtype=f32, device=dev) if train else None
-            topo_quantize_weight(E, self.N, self.K, w, self.q, self.scale, self.qt, self.scale_t,
-                                 torch.cuda.current_stream(dev))
+            self.load(w)
+
+    def load(self, w: torch.Tensor, stream=None):
+        """Takes the values of w (bf16 [E, N, K]) in place of those held."""
+        need("weights", w, (torch.bfloat16,), self.E * self.N, self.K, self.q.device)
+        with ordered(stream, self.q.device, w):
+            topo_quantize_weight(self.E, self.N, self.K, w, self.q, self.scale, self.qt, self.scale_t,
+                                 torch.cuda.current_stream(self.q.device))
 
 
 class ExpertLayer:
@@ -58,23 +63,32 @@ class ExpertLayer:
         for name, w in (("w_up", w_up), ("w_down", w_down)):
             if not isinstance(w, torch.Tensor) or w.dim() != 3 or not w.is_cuda:
                 raise ValueError(f"{name} must be a tensor of three dimensions on a GPU")
-        E, H, I = cfg["E"], w_down.shape[1], w_down.shape[2]
-        if tuple(w_up.shape) != (E, 2 * I, H) or w_down.shape[0] != E:
-            raise ValueError("w_up is [E, 2 I, H] and w_down [E, H, I]")
-        need("w_up", w_up, (torch.bfloat16,), E * 2 * I, H, w_up.device)
-        need("w_down", w_down, (torch.bfloat16,), E * H, I, w_up.device)
+        self.E, self.H, self.I, self.device = cfg["E"], w_down.shape[1], w_down.shape[2], w_up.device
+        self._need_weights(w_up, w_down)
         with ordered(stream, w_up.device, w_up, w_down):
             self._build(cfg, w_up, w_down, route, train, stream)
 
+    def _need_weights(self, w_up, w_down):
+        E, H, I = self.E, self.H, self.I
+        if tuple(w_up.shape) != (E, 2 * I, H) or tuple(w_down.shape) != (E, H, I):
+            raise ValueError("w_up is [E, 2 I, H] and w_down [E, H, I]")
+        need("w_up", w_up, (torch.bfloat16,), E * 2 * I, H, self.device)
+        need("w_down", w_down, (torch.bfloat16,), E * H, I, self.device)
+
+    def set_weights(self, w_up: torch.Tensor, w_down: torch.Tensor):
+        """New values of the weights, as after an optimiser's step; the layer keeps
+        them in 8 bits only.  A backward() belongs to the weights of its forward()."""
+        self._need_weights(w_up, w_down)
+        self.up.load(w_up, self.planner.stream)
+        self.down.load(w_down, self.planner.stream)
+
     def _build(self, cfg, w_up, w_down, route, train, stream):
         self.planner = P = Planner(cfg, 1, w_up.device, stream)
-        self.T, self.E, self.k, self.R = cfg["T"], cfg["E"], cfg["k"], cfg["R"]
-        self.H, self.I = w_down.shape[1], w_down.shape[2]
+        self.T, self.k, self.R = cfg["T"], cfg["k"], cfg["R"]
         self.route, self.train = route, train
         self.up = ExpertWeights(w_up, train, stream)
         self.down = ExpertWeights(w_down, train, stream)
-        self.device = dev = w_up.device
-        rows = self.T * self.k
+        dev, rows = self.device, self.T * self.k
         self.rows, self.n_seg = rows, self.R * P.n_local
         u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
 

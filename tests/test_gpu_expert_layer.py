@@ -236,3 +236,26 @@ def test_an_output_outlives_the_next_call():
     kept = a.clone()
     b = layer.forward(-x, logits)
     assert torch.equal(a, kept) and not torch.equal(a, b)
+
+
+@pytest.mark.parametrize("own", [False, True])
+def test_new_weights(own):
+    """set_weights gives what a layer built from those weights gives."""
+    args = (96, 8, 2, 4, 1, 128, 64, topo.make_route(topo.TOPO_SCORE_SIGMOID))
+    stream = torch.cuda.Stream() if own and torch.cuda.is_available() else None
+    layer, x, logits, dout = _layer(*args, stream=stream)
+    other = _layer(*args, seed=1)[0]
+    gen = torch.Generator().manual_seed(1)                      # the weights of seed 1
+    up = (torch.randn(8, 128, 128, generator=gen) / 128 ** 0.5).to(torch.bfloat16).to(x.device)
+    down = (torch.randn(8, 128, 64, generator=gen) / 64 ** 0.5).to(torch.bfloat16).to(x.device)
+    before = layer.forward(x, logits)
+    layer.set_weights(up, down)
+    got = [layer.forward(x, logits), *layer.backward(x, logits, dout)]
+    want = [other.forward(x, logits), *other.backward(x, logits, dout)]
+    assert not torch.equal(before, got[0])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for u, d, kind in ((up.float(), down, TypeError), (up[:4], down[:4], ValueError), (up, down.transpose(1, 2), ValueError),
+                       (up.cpu(), down, ValueError)):
+        with pytest.raises(kind):
+            layer.set_weights(u, d)
+    assert layer.error() == 0
