@@ -141,7 +141,8 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs &g, const int *tp, cons
     if (MODE == kProduct) r.m0 += so[lo];
     r.ncols = (r.nlim + 15) & ~15;
     r.kb0 = MODE == kGrad ? pad[lo] : 0;
-    r.nkb = MODE == kGrad ? pad[lo + 1] - pad[lo] : g.KB;
+    // a segment whose blocks the operands do not hold is empty
+    r.nkb = MODE != kGrad ? g.KB : pad[lo + 1] <= (int)(g.cap / kKB) ? pad[lo + 1] - pad[lo] : 0;
     return r;
 }
 
@@ -256,8 +257,8 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 tp[i] = run + x - n;
                 if (MODE == kGrad) {
                     if (prun + y > cap) set_error(g.hdr, TOPO_ESTATE);   // more blocks than the operands hold
-                    pad[i] = min(prun + y - pb, cap);
-                    if (i == g.nseg - 1) pad[g.nseg] = min(prun + y, cap);
+                    pad[i] = prun + y - pb;
+                    if (i == g.nseg - 1) pad[g.nseg] = prun + y;
                 }
             }
             run += __shfl_sync(0xffffffffu, x, 31);

@@ -542,3 +542,38 @@ def test_arguments_are_checked_on_the_host():
     refused(E, topo.topo_permute_quantize, c, 1, 32, a, a, a, None, a, nb)
     refused(E, topo.topo_permute_quantize, c, 1, 32, a + 8, a, a, a, a, nb)
     refused(S, topo.topo_permute_quantize, c, 1, 32, a, a, a, a, a, nb - 1)
+
+
+@gpu
+def test_weight_gradients_of_offsets_out_of_order():
+    """Offsets that go back: that segment is empty, and so is every segment whose
+    blocks the operands do not hold; the ones before them are whole."""
+    dev = _dev()
+    rng = np.random.default_rng(4)
+    so, rows, N, K = np.array([0, 300, 0, 300], np.int32), 300, 144, 272
+    n = len(so) - 1
+    cap = topo.topo_cols_capacity(n, rows)
+    assert cap == 5 * B                                        # 3 blocks of the first segment, 2 of the third's 3
+    sod = torch.as_tensor(so, device=dev)
+    ws = torch.zeros(256, dtype=torch.uint8, device=dev)
+    ops = []
+    for C in (N, K):
+        q, s = torch.full((C, cap), 0x7F, dtype=torch.uint8, device=dev), torch.full((cap // B, C), float("nan"), device=dev)
+        topo.topo_quantize_cols(n, rows, C, bf16(rng.standard_normal((rows, C))).to(dev), sod, cap, q, s, ws, 256)
+        ops += [q, s]
+    torch.cuda.synchronize()
+    assert topo.topo_read_error(ws) == topo.TOPO_ESTATE
+    ws.zero_()
+    dw = torch.full((n, N, K), float("nan"), device=dev)
+    topo.topo_expert_wgrad(n, rows, N, K, cap, *ops, sod, dw, ws, 256)
+    torch.cuda.synchronize()
+    assert topo.topo_read_error(ws) == topo.TOPO_ESTATE
+    q = [o.cpu().numpy().astype(np.float64) if o.dtype == torch.float32 else E4M3[o.cpu().numpy()] for o in ops]
+    want, size = np.zeros((N, K)), np.zeros((N, K))
+    for b in range(3):
+        c = slice(b * B, (b + 1) * B)
+        A, X = q[0][:, c] * q[1][b][:, None], q[2][:, c] * q[3][b][:, None]
+        want += A @ X.T
+        size += np.abs(A) @ np.abs(X).T
+    assert np.all(np.abs(dw[0].cpu().numpy() - want) <= (4 * 3 + 4 * 3 + 2) * 2.0 ** -23 * size)
+    assert torch.all(dw[1:] == 0)
