@@ -84,6 +84,7 @@ template <int MODE>
 constexpr int kSegCap = MODE == kProduct ? 1024 : 512;   // segments of one launch (the table in shared memory)
 constexpr uint32_t kStageOut = 2048;              // bytes a warp stores through shared memory at a time
 constexpr int kSms = 152;
+constexpr int kMostTiles = 1 << 30;               // of one launch; segments in order have fewer than 2^26
 
 struct GemmArgs {
     const int32_t *seg_off;     // [nseg + 1]
@@ -213,7 +214,9 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     pdl_trigger();
     pdl_wait();                                    // everything read or written from here on
     // the segments' row offsets, then the exclusive prefix of their tile counts;
-    // a segment outside the layout or without weights has no tiles and is reported
+    // a segment outside the layout or without weights has no tiles and is reported.
+    // Offsets out of order can make the good segments overlap, any number of times:
+    // the sums stop at kMostTiles, and at one block more than the operands hold
     for (int i = tid; i <= g.nseg; i += kThreads) so[i] = __ldg(g.seg_off + i);
     __syncthreads();
     if (warp == 0) {
@@ -222,10 +225,10 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
         if (MODE == kGrad) {                                // blocks of the segments of earlier launches
             for (int i = lane; i < g.seg0; i += 32) {
                 const int a = __ldg(g.seg_all + i), b = __ldg(g.seg_all + i + 1);
-                if (a >= 0 && b >= a && b <= lim) prun += (b - a + kKB - 1) / kKB;
+                if (a >= 0 && b >= a && b <= lim) prun = min(prun + (b - a + kKB - 1) / kKB, cap + 1);
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) prun += __shfl_xor_sync(0xffffffffu, prun, o);
+            for (int o = 16; o > 0; o >>= 1) prun = min(prun + __shfl_xor_sync(0xffffffffu, prun, o), cap + 1);
         }
         for (int i0 = 0; i0 < g.nseg; i0 += 32) {
             const int i = i0 + lane;
@@ -242,6 +245,10 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     }
                 }
                 if (MODE == kGrad && ok) pb = (b - a + kKB - 1) / kKB;
+                if (MODE == kProduct && ok && b > a && run > kMostTiles) {
+                    set_error(g.hdr, TOPO_ESTATE);
+                    ok = false;
+                }
                 if (MODE == kGrad || ok) n = tiles_of<MODE>(g, b - a);
             }
             int x = n, y = pb;
@@ -262,7 +269,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 }
             }
             run += __shfl_sync(0xffffffffu, x, 31);
-            prun += __shfl_sync(0xffffffffu, y, 31);
+            prun = min(prun + __shfl_sync(0xffffffffu, y, 31), cap + 1);
         }
         if (lane == 0) tp[g.nseg] = run;
     }

@@ -577,3 +577,23 @@ def test_weight_gradients_of_offsets_out_of_order():
         size += np.abs(A) @ np.abs(X).T
     assert np.all(np.abs(dw[0].cpu().numpy() - want) <= (4 * 3 + 4 * 3 + 2) * 2.0 ** -23 * size)
     assert torch.all(dw[1:] == 0)
+
+
+@gpu
+def test_weight_gradients_of_offsets_that_go_back_many_times():
+    """The same 2^24 rows 2^14 times over: 2^31 blocks, of which the operands hold
+    the first segment's 2^17.  Ones make its sum exact."""
+    dev = _dev()
+    rows, n, C = 1 << 24, 1 << 15, 16
+    so = torch.zeros(n + 1, dtype=torch.int32, device=dev)
+    so[1::2] = rows
+    cap = topo.topo_cols_capacity(n, rows)
+    ws = torch.zeros(256, dtype=torch.uint8, device=dev)
+    x = torch.ones((rows, C), dtype=torch.bfloat16, device=dev)
+    q, s = torch.empty((C, cap), dtype=torch.uint8, device=dev), torch.empty((cap // B, C), device=dev)
+    topo.topo_quantize_cols(n, rows, C, x, so, cap, q, s, ws, 256)
+    dw = torch.full((n, C, C), float("nan"), device=dev)
+    topo.topo_expert_wgrad(n, rows, C, C, cap, q, s, q, s, so, dw, ws, 256)
+    torch.cuda.synchronize()
+    assert topo.topo_read_error(ws) == topo.TOPO_ESTATE
+    assert torch.all(dw[0] == rows) and torch.all(dw[1:] == 0)
