@@ -513,9 +513,10 @@ int topo_expert_gemm(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, int32_
  *                 (sum over t in block b of dy[n][t] * x[k][t])
  * and 0 for an empty segment.  dy [N][cap] and x [K][cap] with their scales
  * are topo_quantize_cols' of the rows' output gradient and input, for the same
- * seg_off, rows and cap (the scales 16-byte aligned and powers of two: of any
- * other positive value the power of two below it is taken).  dw: device float32 [n_seg][N][K]; instances of one
- * expert are summed by the caller, as ranks sum theirs.  ws as
+ * seg_off, rows and cap (cap at most 2^31; the scales 16-byte aligned and
+ * powers of two: of any other positive value the power of two below it is
+ * taken).  dw: device float32 [n_seg][N][K]; instances of one expert are summed
+ * by the caller, as ranks sum theirs.  ws as
  * topo_expert_gemm.  Device errors: TOPO_ESTATE (as topo_quantize_cols, or
  * more blocks than cap holds; the segment is taken as empty), TOPO_ETIMEOUT. */
 int topo_expert_wgrad(int32_t n_seg, int64_t rows, int32_t N, int32_t K, int64_t cap, const uint8_t *dy,

@@ -533,7 +533,7 @@ int topo_expert_wgrad(int32_t n_seg, int64_t rows, int32_t N, int32_t K, int64_t
                       const float *dy_scale, const uint8_t *x, const float *x_scale, const int32_t *seg_off,
                       float *dw, void *ws, size_t ws_bytes, cudaStream_t stream) {
     if (!product_dims_ok(n_seg, rows, 1, N, K) || !ws) return TOPO_EINVAL;
-    if (cap != topo_cols_capacity(n_seg, rows)) return TOPO_EINVAL;
+    if (cap != topo_cols_capacity(n_seg, rows) || cap > (int64_t)1 << 31) return TOPO_EINVAL;   // 32-bit coordinates
     if (ws_bytes < topo_expert_workspace_bytes(n_seg, rows, N, K)) return TOPO_ENOSPC;
     if (n_seg == 0) return TOPO_OK;
     if (!dy || !dy_scale || !x || !x_scale || !seg_off || !dw || !aligned16(dy, x) || !aligned16(dw, dw) ||

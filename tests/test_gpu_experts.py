@@ -597,3 +597,17 @@ def test_weight_gradients_of_offsets_that_go_back_many_times():
     torch.cuda.synchronize()
     assert topo.topo_read_error(ws) == topo.TOPO_ESTATE
     assert torch.all(dw[0] == rows) and torch.all(dw[1:] == 0)
+
+
+def test_columns_past_32_bit_coordinates_are_refused():
+    try:
+        topo.lib()
+    except RuntimeError:
+        pytest.skip("library not built")
+    a, rows = 1 << 20, (1 << 31) - 1                            # never dereferenced
+    for n in (2, 500):
+        cap = topo.topo_cols_capacity(n, rows)
+        assert cap > 1 << 31
+        with pytest.raises(topo.TopoError) as ex:
+            topo.topo_expert_wgrad(n, rows, 16, 16, cap, a, a, a, a, a, a, a, 256)
+        assert ex.value.code == topo.TOPO_EINVAL
