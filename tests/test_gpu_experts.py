@@ -611,3 +611,26 @@ def test_columns_past_32_bit_coordinates_are_refused():
         with pytest.raises(topo.TopoError) as ex:
             topo.topo_expert_wgrad(n, rows, 16, 16, cap, a, a, a, a, a, a, a, 256)
         assert ex.value.code == topo.TOPO_EINVAL
+
+
+@gpu
+@pytest.mark.parametrize("lens,N,K", [([2049, 0, 3], 16, 272), ([4096, 130], 144, 16), ([7, 5000, 0, 2176], 272, 144)])
+def test_weight_gradients_of_long_segments(lens, N, K):
+    """More than 2048 rows: the sum leaves tensor memory more than once."""
+    wgrad(lens, N, K)
+
+
+@gpu
+def test_weight_gradients_of_many_tiles():
+    """Several tiles to a CTA, of different depths, with ragged edges: 2 segments
+    x 9 x 17 tiles, the last of 16 rows and of 16 columns."""
+    wgrad([300, 2200], 1040, 4112)
+
+
+@gpu
+@pytest.mark.parametrize("out", [F32, BF])
+def test_products_of_many_tiles(out):
+    """Several tiles to a CTA, 11 blocks each, few rows and many, ragged columns."""
+    lens = [(37 * i) % 150 if i % 5 else 0 for i in range(36)]
+    lens[7] = 300
+    product(lens, 3, 2064, 1408, out, seg_w=[i % 3 for i in range(36)])
