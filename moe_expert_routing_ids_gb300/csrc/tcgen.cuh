@@ -12,7 +12,7 @@ namespace topo {
 namespace tc {
 
 constexpr uint32_t kWaitNs = 1000000000u;     // longest mbarrier wait: 1 s of %globaltimer
-constexpr int kWaitTries = 1 << 22;
+constexpr int kWaitTries = 1 << 18;           // about 1 s as well: a try in vain takes 4 us (measured)
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -60,8 +60,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
     return false;
 }
 
-// The same, at most kWaitTries tries (a try may suspend the thread for a while):
-// without the clock the summing loop keeps all of its values in registers.
+// The same, at most kWaitTries tries, each of which suspends the thread until the
+// phase completes or 4 us are over: without the clock the summing loop keeps all of
+// its values in registers.
 __device__ __forceinline__ bool mbar_wait_tries(uint64_t *bar, uint32_t parity) {
     const uint32_t a = smem_u32(bar);
     int left = kWaitTries;
