@@ -108,6 +108,8 @@ def _layer(T, E, k, R, slots, H, I, opts, seed=0, stream=None, hot=0.0):
     dout = torch.randn(T, H, generator=gen).to(torch.bfloat16).to(dev)
     cfg = dict(T=T, E=E, k=k, R=R, ranks_per_node=2, n_slot=slots, tok_bytes=2 * H, expert_bytes=64,
                c_intra=1, c_inter=4, max_refine_iters=0)
+    if T % R:                                                   # ranks of unequal token counts
+        cfg["rank_offsets"] = np.linspace(0, T, R + 1).astype(np.int64)
     return ExpertLayer(cfg, up, down, opts, train=True, stream=stream), x, logits.to(dev), dout
 
 
@@ -258,4 +260,47 @@ def test_new_weights(own):
                        (up.cpu(), down, ValueError)):
         with pytest.raises(kind):
             layer.set_weights(u, d)
+    assert layer.error() == 0
+
+
+@pytest.mark.parametrize("T,E,k,R,score,groups,renorm,bf16", [
+    (384, 16, 4, 4, topo.TOPO_SCORE_SOFTMAX, 4, True, False), (384, 16, 4, 4, topo.TOPO_SCORE_SOFTMAX, 4, False, True),
+    (200, 8, 3, 2, topo.TOPO_SCORE_SIGMOID, 1, False, True), (1, 8, 2, 4, topo.TOPO_SCORE_SIGMOID, 1, True, False)])
+def test_layer_with_other_routers(T, E, k, R, score, groups, renorm, bf16):
+    """Softmax with groups, weights that are shares of the whole row, logits in
+    bf16, one token; the gradient of bf16 logits is rounded to 2^-9 of itself."""
+    H, I, scale = 256, 128, 2.0
+    top = 2 if groups > 1 else 1
+    layer, x, logits, dout = _layer(T, E, k, R, 1, H, I, topo.make_route(score, groups, max(1, groups // 2), top, renorm, scale),
+                                    hot=1.0)
+    if bf16:
+        logits = logits.to(torch.bfloat16)
+    out = layer.forward(x, logits)
+    dx, dl, du, dd = layer.backward(x, logits, dout)
+    assert layer.error() == 0 and dl.dtype == logits.dtype
+    gen = torch.Generator().manual_seed(0)                      # the weights again
+    ur = (torch.randn(E, 2 * I, H, generator=gen) / H ** 0.5).to(torch.bfloat16).double().requires_grad_()
+    dr = (torch.randn(E, H, I, generator=gen) / I ** 0.5).to(torch.bfloat16).double().requires_grad_()
+    xr, lr = x.double().cpu().requires_grad_(), logits.double().cpu().requires_grad_()
+    ids = layer.ids[0].cpu().long()
+    s = torch.softmax(lr, -1) if score == topo.TOPO_SCORE_SOFTMAX else torch.sigmoid(lr)
+    w = torch.gather(s, 1, ids)
+    w = (w / w.sum(-1, keepdim=True) if renorm else w) * scale
+    want = torch.zeros(T, H, dtype=torch.float64)
+    for e in range(E):
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        h = xr[t] @ ur[e].T
+        want = want.index_add(0, t, (torch.nn.functional.silu(h[:, :I]) * h[:, I:] @ dr[e].T) * w[t, j][:, None])
+    assert _rel(out, want.detach()) < 0.08
+    want.backward(dout.double().cpu())
+    for got, ref in ((dx, xr.grad), (dl, lr.grad), (du, ur.grad), (dd, dr.grad)):
+        assert _rel(got, ref) < 0.15
+
+
+def test_layer_without_tokens():
+    layer, x, logits, dout = _layer(0, 8, 2, 4, 1, 128, 64, topo.make_route(topo.TOPO_SCORE_SOFTMAX))
+    assert layer.forward(x, logits).shape == (0, 128)
+    dx, dl, du, dd = layer.backward(x, logits, dout)
+    assert dx.shape == (0, 128) and dl.shape == (0, 8)
+    assert torch.all(du == 0) and torch.all(dd == 0) and du.shape == (8, 128, 128) and dd.shape == (8, 128, 64)
     assert layer.error() == 0
