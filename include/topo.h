@@ -415,6 +415,8 @@ typedef struct {
  *   groups of the largest scores stay (n_group = 1: every expert stays)
  *   ids = the k largest c of the experts that stay, in descending order
  *   weight_j = scale * s_j / (sum of the chosen s), or scale * s_j
+ * (the choice is exactly that of these; the sums' order and the last bits of a
+ * weight, within 2^-18 of it, are not fixed by them)
  * Equal values go to the lower group or expert; NaN ranks below every number.
  * Where the sum is 0 (all chosen logits -inf, or all scores underflow) the
  * weights are 0: a row whose mask leaves nothing has k ids and no weight.

@@ -37,8 +37,8 @@
 // slower at 128; weights on the rows and layout rows on the columns (no waste on
 // ragged segments, a scale per column): slower at every length, 24 rows 163 us
 // against 133; reads of 16 lanes instead of 32: 160 cycles more.
-// Measured: 131072 rows, N = 4096, K = 7168 over 128 experts: 3.3 to 3.5 ms, 2.2
-// to 2.35 PFLOP/s; 1536 rows, 2816 x 4096, 64 experts: 120 us, 6.3 TB/s; gradient of
+// Measured: 131072 rows, N = 4096, K = 7168 over 128 experts: 3.4 ms for a first call,
+// 3.6 to 3.8 ms call after call (against the power limit), 2.05 to 2.25 PFLOP/s; 1536 rows, 2816 x 4096, 64 experts: 120 us, 6.3 TB/s; gradient of
 // 98304 rows, 2816 x 4096, 64 experts: 1.14 to 1.15 ms, its 2.95 GB of output included
 // (0.94 ms without the stores; 1.19 ms when the warps read the turned rows back and
 // stored them, against one TMA store of 32 rows x 64 bytes; 16 rows x 128 bytes the

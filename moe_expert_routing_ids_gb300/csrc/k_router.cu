@@ -23,10 +23,12 @@
 //   - rows with NaN or infinities (where groups or the sigmoid are involved; a bias
 //     that is neither finite nor below 3e30: every row), many ties: exact_token, which is not for speed (19 rows of 65536 sent
 //     there for their groups cost 24 us, its code being read from memory).
-// Measured, 1M x 512 softmax, k = 10: 570 us, 3.9 TB/s; 65536 x 256 sigmoid, 4 of 8
-// groups, k = 8: 44 us.  Bound by issue: 700 instructions for two rows of 512
-// (what the memory's rate allows), 890 for two of 256 in groups, 60 to 70
-// percent of the issue slots used at 24 to 32 warps an SM.
+// Measured, 1M x 512 softmax, k = 10: 554 us, 4.0 TB/s (weights that are not
+// renormalised: 636); 65536 x 256 sigmoid, 4 of 8 groups, k = 8: 44 us, and 56 to 60
+// where one of the rows has more than 64 candidates and goes to exact_token (5 draws of
+// 40); softmax with a bias, every row by exact_token: 65536 x 256, k = 8: 248 us.
+// Bound by the instructions' latency at 24 to 32 warps an SM, 60 to 70 percent of the
+// issue slots used: 700 instructions for two rows of 512, 890 for two of 256 in groups.
 // The margin: exp2 of a rounded argument is off by |x| 2^-23 + 2^-22 relative,
 // times s (1 - s) in s (|x| s (1 - s) < 0.23), the sum and the reciprocal by
 // 2^-22 s: 3.3e-7 at most, and the score as defined, rounded four times, by
@@ -38,8 +40,7 @@
 // order.
 // The row's sum of weights that are not renormalised takes that exp2 of x - max as
 // well: a term is off by 2^-22 + |x - max| 2^-22 of itself, at most 2^-22 of the sum's
-// largest term in each, where expf would cost 5 instructions more a logit.  The
-// chosen experts' own exp is expf.
+// largest term each (max of (1 + d) exp(-d) is 1).  The chosen experts' own exp is expf.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -636,10 +637,11 @@ __device__ __forceinline__ void put(void *row, int e, float v) {
 
 // One warp per token: the row's dense gradient (0, or -p_e * sum for a softmax
 // whose weights are not renormalised), then the chosen experts' values over it.
-// Bound by memory: 1M tokens x 512 in 480 us, 2.1 GB written and 10 sectors of 64
-// bytes read for each token's chosen logits, 6 TB/s (V: the rows are written 16
+// Bound by memory: 1M tokens x 512 in 500 us, 2.1 GB written and 10 sectors of 64
+// bytes read for each token's chosen logits, 5.8 TB/s (V: the rows are written 16
 // bytes at a time, else 579 us; ids and logits of later tokens loaded ahead
-// changed nothing).
+// changed nothing).  Dense rows (a softmax that is not renormalised) are read three
+// times and written a value at a time: 1050 us.
 template <bool BF, bool V>
 __global__ void __launch_bounds__(256)
 k_route_grad(RouteGradArgs g) {

@@ -198,6 +198,8 @@ class ExpertLayer:
         self._product(*self._rows8(dy), self.I, self.H, self.down.qt, self.down.scale_t, da)
         dh = torch.empty_like(self.h)
         topo_swiglu_grad(self.rows, self.I, self.h, da, dh, s)
+        # the rows of the product as the forward pass had them, rounded to e4m3; laid out
+        # for the weight gradient they are rounded a second time, down their columns
         act = (self.aq.view(torch.float8_e4m3fn).float()
                * self.as_.repeat_interleave(TOPO_BLOCK, 1)[:, :self.I]).to(torch.bfloat16)
         dw_down = self._weight_grad(dy, act)
