@@ -21,8 +21,9 @@
 //   - groups whose scores are closer than the margin: the row is done again with
 //     every score as defined;
 //   - rows with NaN or infinities (where groups or the sigmoid are involved; a bias
-//     that is neither finite nor below 3e30: every row), many ties: exact_token, which is not for speed (19 rows of 65536 sent
-//     there for their groups cost 24 us, its code being read from memory).
+//     of 3e30 and more, or NaN: every row), many ties: exact_token, which is not for
+//     speed (19 rows of 65536 sent there for their groups cost 24 us, its code being
+//     read from memory).
 // Measured, 1M x 512 softmax, k = 10: 554 us, 4.0 TB/s (weights that are not
 // renormalised: 636); 65536 x 256 sigmoid, 4 of 8 groups, k = 8: 44 us, and 56 to 60
 // where one of the rows has more than 64 candidates and goes to exact_token (5 draws of
