@@ -81,6 +81,10 @@ extern "C" {
 #define TOPO_SCORE_SIGMOID 1
 #define TOPO_ROUTE_MAX_GROUPS 32
 #define TOPO_BLOCK 128      /* values along the contraction that share one scale */
+#define TOPO_FMT_EIGHT 0    /* weights: e4m3 with a float32 scale per 128 x 128 block */
+#define TOPO_FMT_MX 1       /* 4 bits, a power of two per 32 values */
+#define TOPO_FMT_NV 2       /* 4 bits, an e4m3 scale per 16 values, a power of two per row */
+#define TOPO_FEW_MAX_TOKENS 32
 #define TOPO_SHUFFLE_STATS 4
 #define TOPO_SHUFFLE_MAX_RANKS 256
 #define TOPO_PLACE_STATS 4
@@ -524,6 +528,91 @@ int topo_expert_gemm(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, int32_
 int topo_expert_wgrad(int32_t n_seg, int64_t rows, int32_t N, int32_t K, int64_t cap, const uint8_t *dy,
                       const float *dy_scale, const uint8_t *x, const float *x_scale, const int32_t *seg_off,
                       float *dw, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Microscaled 4 bits.
+ *
+ * Values are e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; the code of
+ * a value is sign, two exponent bits, one mantissa bit), two to a byte, the
+ * earlier one in the low half: a row of C values is C / 2 bytes.  A row's
+ * scales are topo_micro_pitch(C, fmt) bytes, one for each block, the bytes
+ * past the last block's as scales of 1.
+ *   TOPO_FMT_MX  blocks of 32; byte b is the scale 2^(b - 127), 255 a NaN.
+ *                The quantising calls use the smallest power of two s with
+ *                amax <= 6 s (exponent at least -126; 1 for a block of zeros).
+ *   TOPO_FMT_NV  blocks of 16; a byte is the scale in e4m3, times the row's
+ *                float32 row_scale.  The quantising calls use for the row the
+ *                smallest power of two g with amax <= 6 * 448 g, amax over the
+ *                row's finite values (exponent at least -126; 1 for a row of
+ *                zeros), and for a block the smallest e4m3 value s with
+ *                amax <= 6 s g (1 for a block of zeros).
+ * A value is stored as e2m1(v / scale), to nearest, ties to even; none is
+ * clipped.  A block with a NaN or an infinity gets the scale NaN, and so do all
+ * its values.  row_scale (float32 [rows]) is NULL for TOPO_FMT_MX.
+ *
+ * C is a positive multiple of 32; packed rows and bf16 rows are 16-byte
+ * aligned, scales 16-byte aligned, row scales 4-byte aligned (16-byte those of
+ * weights). */
+int64_t topo_micro_pitch(int32_t C, int32_t fmt);      /* 0 for an invalid C or fmt */
+
+/* Rows (or, with rows = n_w * N, experts' weights [n_w][N][C]) in 4 bits.
+ * x: device bf16 [rows][C]. */
+int topo_quantize_rows_micro(int64_t rows, int32_t C, int32_t fmt, const uint16_t *x, uint8_t *q, uint8_t *scale,
+                             float *row_scale, cudaStream_t stream);
+
+/* topo_permute_quantize into 4 bits.  q: device [n_layers][T*k][H / 2]; scale:
+ * [n_layers][T*k][pitch]; row_scale: [n_layers][T*k]. */
+int topo_permute_quantize_micro(const topo_cfg *cfg, int32_t n_layers, int32_t H, int32_t fmt, const uint16_t *x,
+                                const int32_t *sorted_pairs, uint8_t *q, uint8_t *scale, float *row_scale, void *ws,
+                                size_t ws_bytes, cudaStream_t stream);
+
+/* The gated activation of topo_swiglu_quantize into 4 bits.  h: device bf16
+ * [rows][2 I]. */
+int topo_swiglu_quantize_micro(int64_t rows, int32_t I, int32_t fmt, const uint16_t *h, uint8_t *q, uint8_t *scale,
+                               float *row_scale, cudaStream_t stream);
+
+/* The values of rows in 4 bits, rounded to bf16 (exactly, where bf16's range
+ * holds them).  out: device bf16 [rows][C]. */
+int topo_dequantize_micro(int64_t rows, int32_t C, int32_t fmt, const uint8_t *q, const uint8_t *scale,
+                          const float *row_scale, uint16_t *out, cudaStream_t stream);
+
+/* topo_expert_gemm of rows and weights in 4 bits, both of format fmt:
+ *   out[r][n] = sum over k of a[r][k] * w[e][n][k], the values that the codes
+ *               and scales stand for,
+ * in float32 (the row scales multiply the sum), rounded once to bf16 or stored
+ * as float32.  a: device [rows][K / 2]; w: device [n_w][N][K / 2]; w_row: device
+ * float32 [n_w][N].  Segments, out, ws, limits and device errors as
+ * topo_expert_gemm; N a multiple of 16, K of 32; bytes past the last block of a
+ * row's scales hold no NaN (0xff; 0x7f, 0xff). */
+int topo_expert_gemm_micro(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, int32_t K, int32_t fmt, const uint8_t *a,
+                           const uint8_t *a_scale, const float *a_row, const int32_t *seg_off, const int32_t *seg_w,
+                           const uint8_t *w, const uint8_t *w_scale, const float *w_row, void *out, int32_t out_dtype,
+                           void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* The experts applied to a few tokens, without a plan or a layout:
+ *   out[t] = sum over j of weights[t][j] * (W_down[e] a), e = ids[t][j],
+ *   a = silu(g) * u,  [g | u] = W_up[e] x[t]
+ * with all sums in float32; x and a enter the products as 16-bit floats of 11
+ * bits over a power of two for each row (values more than 2^28 below the row's
+ * largest lose bits, which changes the sum by less than 2^-38 of it), out is
+ * rounded once to bf16 and is the same for the same inputs whatever else the
+ * call computes.
+ * x: device bf16 [T][H]; ids: device int32 [T][k] (an expert may occur twice in
+ * a row; one outside [0, E) adds nothing and is reported); weights: device
+ * float32 [T][k]; up: [E][2 I][H], gate rows then up rows, and down: [E][H][I]
+ * in format fmt: TOPO_FMT_EIGHT as topo_quantize_weight's (scale: float32,
+ * row scales NULL), else as topo_quantize_rows_micro's.  out: device bf16
+ * [T][H].  A token whose row holds a NaN or an infinity gets NaN.
+ * T <= TOPO_FEW_MAX_TOKENS, E <= TOPO_GATE_MAX_E, k <= 64; H and I multiples of
+ * 16, of 32 in 4 bits, up to 2^15.  ws: topo_few_workspace_bytes bytes, header
+ * included (0 for invalid sizes).  Weights are read once for every 8 to 32
+ * tokens that share an expert (as many as fit the shared memory); past a dozen
+ * tokens or so the path through topo_reroute_layout is the alternative.
+ * Device errors: TOPO_ERANGE. */
+size_t topo_few_workspace_bytes(int32_t T, int32_t E, int32_t k, int32_t H, int32_t I);
+int topo_expert_few(int32_t T, int32_t E, int32_t k, int32_t H, int32_t I, int32_t fmt, const uint16_t *x,
+                    const int32_t *ids, const float *weights, const uint8_t *up, const void *up_scale, const float *up_row,
+                    const uint8_t *down, const void *down_scale, const float *down_row, uint16_t *out, void *ws,
+                    size_t ws_bytes, cudaStream_t stream);
 
 /* topo_hist without a caller-supplied workspace.  No passage of the pages
  * has a counterpart: it computes exactly what topo_hist computes (Omega), for

@@ -34,6 +34,8 @@ TOPO_SCORE_SOFTMAX = 0
 TOPO_SCORE_SIGMOID = 1
 TOPO_ROUTE_MAX_GROUPS = 32
 TOPO_BLOCK = 128
+TOPO_FMT_EIGHT, TOPO_FMT_MX, TOPO_FMT_NV = 0, 1, 2
+TOPO_FEW_MAX_TOKENS = 32
 TOPO_SHUFFLE_STATS = 4
 TOPO_SHUFFLE_MAX_RANKS = 256
 TOPO_PLACE_STATS = 4
@@ -47,7 +49,9 @@ EXPORTS = ("topo_workspace_bytes", "topo_ws_reset", "topo_hist", "topo_cooccur",
            "topo_shuffle_targets", "topo_place_experts", "topo_cooccur_workspace_bytes", "topo_route",
            "topo_route_grad", "topo_permute_quantize", "topo_quantize_rows", "topo_quantize_weight",
            "topo_cols_capacity", "topo_quantize_cols", "topo_swiglu_quantize", "topo_swiglu_grad",
-           "topo_expert_workspace_bytes", "topo_expert_gemm", "topo_expert_wgrad")
+           "topo_expert_workspace_bytes", "topo_expert_gemm", "topo_expert_wgrad", "topo_micro_pitch",
+           "topo_quantize_rows_micro", "topo_permute_quantize_micro", "topo_swiglu_quantize_micro",
+           "topo_dequantize_micro", "topo_expert_gemm_micro", "topo_few_workspace_bytes", "topo_expert_few")
 TOPO_HIST_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -132,6 +136,16 @@ def lib():
             L.topo_expert_workspace_bytes.restype = sz
             L.topo_expert_gemm.argtypes = [i32, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
             L.topo_expert_wgrad.argtypes = [i32, i64, i32, i32, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+            L.topo_micro_pitch.argtypes = [i32, i32]
+            L.topo_micro_pitch.restype = i64
+            L.topo_quantize_rows_micro.argtypes = [i64, i32, i32, vp, vp, vp, vp, vp]
+            L.topo_permute_quantize_micro.argtypes = [cfgp, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+            L.topo_swiglu_quantize_micro.argtypes = [i64, i32, i32, vp, vp, vp, vp, vp]
+            L.topo_dequantize_micro.argtypes = [i64, i32, i32, vp, vp, vp, vp, vp]
+            L.topo_expert_gemm_micro.argtypes = [i32, i64, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+            L.topo_few_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+            L.topo_few_workspace_bytes.restype = sz
+            L.topo_expert_few.argtypes = [i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
             L.topo_read_error.argtypes = [vp]
             L.topo_strerror.argtypes = [ctypes.c_int]
             L.topo_strerror.restype = ctypes.c_char_p
@@ -140,7 +154,9 @@ def lib():
                       "topo_hist_noalloc", "topo_permute", "topo_combine", "topo_dedup_layout", "topo_gate_hist", "topo_shuffle_targets", "topo_place_experts",
                       "topo_route", "topo_route_grad", "topo_permute_quantize", "topo_quantize_rows",
                       "topo_quantize_weight", "topo_quantize_cols", "topo_swiglu_quantize", "topo_swiglu_grad",
-                      "topo_expert_gemm", "topo_expert_wgrad"):
+                      "topo_expert_gemm", "topo_expert_wgrad", "topo_quantize_rows_micro",
+                      "topo_permute_quantize_micro", "topo_swiglu_quantize_micro", "topo_dequantize_micro",
+                      "topo_expert_gemm_micro", "topo_expert_few"):
                 getattr(L, f).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -384,6 +400,59 @@ def topo_expert_wgrad(n_seg: int, rows: int, N: int, K: int, cap: int, dy, dy_sc
     return _chk("topo_expert_wgrad", lib().topo_expert_wgrad(n_seg, rows, N, K, cap, _p(dy), _p(dy_scale), _p(x),
                                                              _p(x_scale), _p(seg_off), _p(dw), _p(ws), ws_bytes,
                                                              _s(stream)))
+
+
+def topo_micro_pitch(C: int, fmt: int) -> int:
+    """Bytes of the scales of a row of C values in 4 bits."""
+    return int(lib().topo_micro_pitch(C, fmt))
+
+
+def topo_quantize_rows_micro(rows: int, C: int, fmt: int, x, q, scale, row_scale=None, stream=None) -> int:
+    """bf16 rows (or weights) in microscaled 4 bits."""
+    return _chk("topo_quantize_rows_micro", lib().topo_quantize_rows_micro(rows, C, fmt, _p(x), _p(q), _p(scale),
+                                                                           _p(row_scale), _s(stream)))
+
+
+def topo_permute_quantize_micro(cfg: TopoCfg, n_layers: int, H: int, fmt: int, x, sorted_pairs, q, scale, row_scale, ws,
+                                ws_bytes: int, stream=None) -> int:
+    """Dispatch pack in microscaled 4 bits."""
+    return _chk("topo_permute_quantize_micro",
+                lib().topo_permute_quantize_micro(ctypes.byref(cfg), n_layers, H, fmt, _p(x), _p(sorted_pairs), _p(q),
+                                                  _p(scale), _p(row_scale), _p(ws), ws_bytes, _s(stream)))
+
+
+def topo_swiglu_quantize_micro(rows: int, I: int, fmt: int, h, q, scale, row_scale=None, stream=None) -> int:
+    """silu(g) * u of rows [g | u] in microscaled 4 bits."""
+    return _chk("topo_swiglu_quantize_micro", lib().topo_swiglu_quantize_micro(rows, I, fmt, _p(h), _p(q), _p(scale),
+                                                                               _p(row_scale), _s(stream)))
+
+
+def topo_dequantize_micro(rows: int, C: int, fmt: int, q, scale, row_scale, out, stream=None) -> int:
+    """The bf16 values of rows in microscaled 4 bits."""
+    return _chk("topo_dequantize_micro", lib().topo_dequantize_micro(rows, C, fmt, _p(q), _p(scale), _p(row_scale),
+                                                                     _p(out), _s(stream)))
+
+
+def topo_expert_gemm_micro(n_seg: int, rows: int, n_w: int, N: int, K: int, fmt: int, a, a_scale, a_row, seg_off, seg_w,
+                           w, w_scale, w_row, out, out_dtype: int, ws, ws_bytes: int, stream=None) -> int:
+    """The experts' products of rows and weights in microscaled 4 bits."""
+    return _chk("topo_expert_gemm_micro",
+                lib().topo_expert_gemm_micro(n_seg, rows, n_w, N, K, fmt, _p(a), _p(a_scale), _p(a_row), _p(seg_off),
+                                             _p(seg_w), _p(w), _p(w_scale), _p(w_row), _p(out), out_dtype, _p(ws),
+                                             ws_bytes, _s(stream)))
+
+
+def topo_few_workspace_bytes(T: int, E: int, k: int, H: int, I: int) -> int:
+    """Workspace bytes of topo_expert_few."""
+    return int(lib().topo_few_workspace_bytes(T, E, k, H, I))
+
+
+def topo_expert_few(T: int, E: int, k: int, H: int, I: int, fmt: int, x, ids, weights, up, up_scale, up_row, down,
+                    down_scale, down_row, out, ws, ws_bytes: int, stream=None) -> int:
+    """The experts applied to a few tokens: out = sum_j weights_j * W_down (silu(g) * u), [g | u] = W_up x."""
+    return _chk("topo_expert_few",
+                lib().topo_expert_few(T, E, k, H, I, fmt, _p(x), _p(ids), _p(weights), _p(up), _p(up_scale), _p(up_row),
+                                      _p(down), _p(down_scale), _p(down_row), _p(out), _p(ws), ws_bytes, _s(stream)))
 
 
 def topo_read_error(ws) -> int:

@@ -343,6 +343,15 @@ cudaError_t launch_quantize_cols(int nseg, int64_t rows, int C, const uint16_t *
 cudaError_t launch_quantize_weight(int n_w, int N, int K, const uint16_t *w, uint8_t *q, float *scale, uint8_t *qt,
                                    float *scale_t, cudaStream_t st);
 cudaError_t launch_swiglu_grad(int64_t rows, int I, const uint16_t *h, const uint16_t *dy, uint16_t *dh, cudaStream_t st);
+// Rows in microscaled 4 bits (k_micro.cu).  Bytes of a row's scales: one a block, filled
+// up to a multiple of 16.
+__host__ __device__ constexpr int64_t micro_pitch(int64_t C, int fmt) { return (C / (fmt == TOPO_FMT_NV ? 16 : 32) + 15) & ~(int64_t)15; }
+cudaError_t launch_quantize_rows_micro(int64_t rows, int C, int fmt, const uint16_t *x, uint8_t *q, uint8_t *scale,
+                                       float *row_scale, bool swiglu, cudaStream_t st);
+cudaError_t launch_permute_quantize_micro(const Geo &g, int H, int fmt, const uint16_t *x, const int32_t *sorted, uint8_t *q,
+                                          uint8_t *scale, float *row_scale, void *ws, cudaStream_t st);
+cudaError_t launch_dequantize_micro(int64_t rows, int C, int fmt, const uint8_t *q, const uint8_t *scale, const float *row_scale,
+                                    uint16_t *out, cudaStream_t st);
 // The experts' products (k_experts.cu).
 cudaError_t launch_expert_gemm(int nseg, int64_t rows, int n_w, int N, int K, const uint8_t *a, const float *a_scale,
                                const int32_t *seg_off, const int32_t *seg_w, const uint8_t *w, const float *w_scale,
@@ -350,5 +359,15 @@ cudaError_t launch_expert_gemm(int nseg, int64_t rows, int n_w, int N, int K, co
 cudaError_t launch_expert_wgrad(int nseg, int64_t rows, int N, int K, int64_t cap, const uint8_t *dy, const float *dy_scale,
                                 const uint8_t *x, const float *x_scale, const int32_t *seg_off, float *dw, void *ws,
                                 cudaStream_t st);
+cudaError_t launch_expert_gemm_micro(int nseg, int64_t rows, int n_w, int N, int K, int fmt, const uint8_t *a,
+                                     const uint8_t *a_scale, const float *a_row, const int32_t *seg_off, const int32_t *seg_w,
+                                     const uint8_t *w, const uint8_t *w_scale, const float *w_row, void *out, bool bf16, void *ws,
+                                     cudaStream_t st);
+// The experts applied to a few tokens (k_few.cu).
+size_t few_workspace(int T, int k, int H, int I);
+cudaError_t launch_expert_few(int T, int E, int k, int H, int I, int fmt, const uint16_t *x, const int32_t *ids,
+                              const float *weights, const uint8_t *up, const void *up_scale, const float *up_row,
+                              const uint8_t *down, const void *down_scale, const float *down_row, uint16_t *out, void *ws,
+                              cudaStream_t st);
 
 }  // namespace topo

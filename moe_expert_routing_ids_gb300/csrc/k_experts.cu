@@ -56,9 +56,13 @@
 namespace topo {
 namespace {
 
-enum { kProduct = 0, kGrad = 1 };
+// kMx, kNv: the product of rows and weights in 4 bits
+enum { kProduct = 0, kGrad = 1, kMx = TOPO_FMT_MX + 1, kNv = TOPO_FMT_NV + 1 };
 
-constexpr int kKB = 128;                          // contraction values of a block: one 128-byte swizzle row
+template <int MODE>
+constexpr bool kMicro = MODE == kMx || MODE == kNv;
+
+constexpr int kKB = 128;                          // bytes of a row's block, one 128-byte swizzle row: 128 values, 256 in 4 bits
 constexpr int kTileM = 128;
 constexpr int kTileN = 256;
 constexpr int kSumWarps = 8;                      // warps that scale, add and store
@@ -78,11 +82,23 @@ static_assert(kStages % 2 == 0, "the two scale warps take the stages in turn, an
 // difference where every SM streams weights anyway (24 rows an expert).
 constexpr int kFew = 32;
 constexpr int kScaleKB = 4;                       // blocks whose scales are brought together
-constexpr int kFlush = 16;                        // gradient: blocks summed in tensor memory before the sum
-                                                  // moves to registers
+// gradient and 4 bits: blocks summed in tensor memory before the sum moves to registers
 template <int MODE>
-constexpr int kSegCap = MODE == kProduct ? 1024 : 512;   // segments of one launch (the table in shared memory)
-constexpr uint32_t kStageOut = 2048;              // bytes a warp stores through shared memory at a time
+constexpr int kFlush = kMicro<MODE> ? 32 : 16;
+template <int MODE>
+constexpr int kSegCap = kMicro<MODE> ? 320 : MODE == kProduct ? 1024 : 512;   // segments of one launch (the table in shared memory)
+// bytes a warp stores through shared memory at a time, rows of 64 bytes (4 bits: the
+// stages with their scales leave half as much)
+template <int MODE>
+constexpr uint32_t kStageOut = kMicro<MODE> ? 1024 : 2048;
+// 4 bits: the 16 scale bytes of each of 128 rows, columns or (kNv) a block's of 16
+// values; tensor-memory columns of a stage's scales
+constexpr uint32_t kSfBytes = 16 * 128;
+template <int MODE>
+constexpr int kSfSteps = MODE == kNv ? 4 : 2;     // scale words of a row and block
+template <int MODE>
+constexpr int kSfCols = kMicro<MODE> ? 12 * kSfSteps<MODE> : 16;
+static_assert(kTileN + kStages * kSfCols<kNv> <= kTmemCols, "an accumulator and the stages' scales share tensor memory");
 constexpr int kSms = 152;
 constexpr int kMostTiles = 1 << 30;               // of one launch; segments in order have fewer than 2^26
 
@@ -92,6 +108,7 @@ struct GemmArgs {
     const int32_t *seg_w;       // [nseg] weights of each segment, or null: the segment's index + seg0
     const float *w_scale;       // product: [n_w][NB][KB] weights; gradient: [cap / 128][N] of dy
     const float *x_scale;       // product: [rows][KB] layout rows; gradient: [cap / 128][K] of x
+                                // (4 bits, by 16: w_scale [n_w][N] and x_scale [rows], one a row)
     void *out;
     WsHeader *hdr;
     int64_t rows;               // rows of the layout
@@ -114,7 +131,7 @@ struct Tile {
 
 template <int MODE>
 __device__ __forceinline__ int tiles_of(const GemmArgs &g, int len) {
-    const int m = MODE == kProduct ? len : g.N, n = MODE == kProduct ? g.N : g.K;
+    const int m = MODE != kGrad ? len : g.N, n = MODE != kGrad ? g.N : g.K;
     return ((m + kTileM - 1) / kTileM) * ((n + kTileN - 1) / kTileN);
 }
 
@@ -132,14 +149,14 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs &g, const int *tp, cons
     Tile r;
     r.seg = lo;
     const int loc = t - tp[lo], len = so[lo + 1] - so[lo];
-    const int me = MODE == kProduct ? len : g.N, ne = MODE == kProduct ? g.N : g.K;
+    const int me = MODE != kGrad ? len : g.N, ne = MODE != kGrad ? g.N : g.K;
     const int nm = (me + kTileM - 1) / kTileM, n = loc / nm, m = loc - n * nm;
     r.w = MODE == kGrad ? 0 : g.seg_w ? __ldg(g.seg_w + lo) : g.seg0 + lo;
     r.m0 = m * kTileM;
     r.mlim = min(kTileM, me - r.m0);
     r.n0 = n * kTileN;
     r.nlim = min(kTileN, ne - r.n0);
-    if (MODE == kProduct) r.m0 += so[lo];
+    if (MODE != kGrad) r.m0 += so[lo];
     r.ncols = (r.nlim + 15) & ~15;
     r.kb0 = MODE == kGrad ? pad[lo] : 0;
     // a segment whose blocks the operands do not hold is empty
@@ -177,7 +194,8 @@ __device__ __forceinline__ void add_rows(Acc &acc, uint32_t ta, float s) {
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUtensorMap map_few,
-          const __grid_constant__ CUtensorMap map_n, GemmArgs g) {
+          const __grid_constant__ CUtensorMap map_n, const __grid_constant__ CUtensorMap map_sm,
+          const __grid_constant__ CUtensorMap map_sn, GemmArgs g) {
     extern __shared__ __align__(1024) unsigned char ring[];
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], scaled[kStages], drained;
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], sc_full[2], sc_empty[2];
@@ -186,7 +204,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     __shared__ int so[kSegCap<MODE> + 1], tp[kSegCap<MODE> + 1], pad[MODE == kGrad ? kSegCap<MODE> + 1 : 1];
     // product: scales of the rows times the weight scale of each half of the columns
     __shared__ float cs[MODE == kProduct ? 2 : 1][kScaleKB][MODE == kProduct ? kTileN : 1];
-    __shared__ __align__(1024) unsigned char outs[kSumWarps * kStageOut];
+    __shared__ __align__(1024) unsigned char outs[kSumWarps * kStageOut<MODE>];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int first = blockIdx.x, step = gridDim.x;
 
@@ -194,7 +212,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             tc::mbar_init(&full[s], 1);
-            tc::mbar_init(&scaled[s], 1);
+            tc::mbar_init(&scaled[s], kMicro<MODE> ? 2 : 1);
             tc::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -210,6 +228,10 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     if (tid == kSumWarps * 32) {
         tc::tma_prefetch(&map_m);
         tc::tma_prefetch(&map_n);
+        if (kMicro<MODE>) {
+            tc::tma_prefetch(&map_sm);
+            tc::tma_prefetch(&map_sn);
+        }
     }
     pdl_trigger();
     pdl_wait();                                    // everything read or written from here on
@@ -245,7 +267,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     }
                 }
                 if (MODE == kGrad && ok) pb = (b - a + kKB - 1) / kKB;
-                if (MODE == kProduct && ok && b > a && run > kMostTiles) {
+                if (MODE != kGrad && ok && b > a && run > kMostTiles) {
                     set_error(g.hdr, TOPO_ESTATE);
                     ok = false;
                 }
@@ -288,15 +310,16 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             for (int t = first; t < ntiles && ok; t += step) {
                 const Tile q = find_tile<MODE>(g, tp, so, pad, t);
                 const int ym = q.m0;
-                const int yn = (MODE == kProduct ? q.w * g.N : 0) + q.n0;
+                const int yn = (MODE != kGrad ? q.w * g.N : 0) + q.n0;
                 const int boxes = (q.ncols + kTileM - 1) / kTileM;          // 128 columns to a load
                 // few rows: only they are loaded, 16 at a time (what the other rows of the
                 // stage hold goes into sums that are not stored)
-                const int few = MODE == kProduct && q.mlim <= kFew ? (q.mlim + 15) / 16 : 0;
+                const int few = MODE != kGrad && q.mlim <= kFew ? (q.mlim + 15) / 16 : 0;
                 uint32_t bytes = (few ? (uint32_t)few * 16 * kKB : kABytes) + (uint32_t)(boxes * kTileM) * kKB;
                 // gradient: the scales of the tile's rows and columns, whole pieces of 16
                 const uint32_t ms = MODE == kGrad ? 4u * (uint32_t)q.mlim : 0u, ns = MODE == kGrad ? 4u * (uint32_t)q.nlim : 0u;
                 bytes += ms + ns;
+                if (kMicro<MODE>) bytes += (uint32_t)(1 + boxes) * kSfBytes;
                 for (int kb = 0; kb < q.nkb; ++kb) {
                     if (fill > 0 && !tc::mbar_wait(&empty[s], (uint32_t)(fill - 1) & 1u)) {
                         ok = false;
@@ -318,6 +341,13 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                             tc::bulk_load(sf, g.w_scale + (int64_t)(q.kb0 + kb) * g.N + q.m0, ms, bar);
                             tc::bulk_load(sf + 512, g.x_scale + (int64_t)(q.kb0 + kb) * g.K + q.n0, ns, bar);
                         }
+                        if (kMicro<MODE>) {            // by 32: 16 bytes are the scales of two blocks
+                            const uint32_t sf = b + kTileN * kKB;
+                            const int xs = 16 * (MODE == kNv ? kb : kb >> 1);
+                            tc::tma_load(sf, &map_sm, xs, ym, bar);
+                            for (int c = 0; c < boxes; ++c)
+                                tc::tma_load(sf + (uint32_t)(c + 1) * kSfBytes, &map_sn, xs, yn + c * kTileM, bar);
+                        }
                     }
                     __syncwarp();
                     if (++s == kStages) {
@@ -338,15 +368,16 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             bool ok = true;
             for (int t = first; t < ntiles && ok; t += step) {
                 const Tile q = find_tile<MODE>(g, tp, so, pad, t);
-                const uint32_t idesc = MODE == kGrad ? tc::idesc_scaled(kTileM, q.ncols) : tc::idesc_e4m3(kTileM, q.ncols);
+                const uint32_t idesc = kMicro<MODE> ? tc::idesc_micro(kTileM, q.ncols, MODE == kMx)
+                                       : MODE == kGrad ? tc::idesc_scaled(kTileM, q.ncols) : tc::idesc_e4m3(kTileM, q.ncols);
                 for (int kb = 0; kb < q.nkb; ++kb) {
-                    // the product hands a block on in turn in two accumulators, the gradient
-                    // kFlush blocks in one
-                    const int b = MODE == kGrad ? 0 : it & 1, round = MODE == kGrad ? it : it >> 1;
-                    const bool begin = MODE != kGrad || kb % kFlush == 0;
-                    const bool end = MODE != kGrad || kb % kFlush == kFlush - 1 || kb + 1 == q.nkb;
+                    // the product in 8 bits hands a block on in turn in two accumulators, the
+                    // others kFlush blocks in one
+                    const int b = MODE != kProduct ? 0 : it & 1, round = MODE != kProduct ? it : it >> 1;
+                    const bool begin = MODE == kProduct || kb % kFlush<MODE> == 0;
+                    const bool end = MODE == kProduct || kb % kFlush<MODE> == kFlush<MODE> - 1 || kb + 1 == q.nkb;
                     if ((begin && round > 0 && !tc::mbar_wait(&acc_empty[b], (uint32_t)(round - 1) & 1u)) ||
-                        !tc::mbar_wait(MODE == kGrad ? &scaled[s] : &full[s], (uint32_t)fill & 1u)) {
+                        !tc::mbar_wait(MODE != kProduct ? &scaled[s] : &full[s], (uint32_t)fill & 1u)) {
                         ok = false;
                         break;
                     }
@@ -354,8 +385,17 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     const uint32_t a = tc::smem_u32(ring) + (uint32_t)s * g.stage_bytes;
                     if (tc::elect()) {
                         const uint64_t dm = tc::smem_desc(a), dn = tc::smem_desc(a + kABytes);
-                        if (MODE == kGrad) {
-                            const uint32_t ts = tmem + kTileN + 16u * (uint32_t)s;
+                        if (kMicro<MODE>) {
+                            // a step is 64 values, 32 bytes on within the swizzled row
+                            const uint32_t ta = tmem + kTileN + (uint32_t)(kSfCols<MODE> * s), tb = ta + 4 * kSfSteps<MODE>;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int u = MODE == kNv ? j : j >> 1;
+                                const uint32_t id = MODE == kNv ? idesc : idesc | tc::idesc_half(j & 1);
+                                tc::mma_micro<MODE == kNv>(tmem, dm + 2 * j, dn + 2 * j, id, ta + 4 * u, tb + 8 * u, !begin || j > 0);
+                            }
+                        } else if (MODE == kGrad) {
+                            const uint32_t ts = tmem + kTileN + (uint32_t)(kSfCols<MODE> * s);
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 tc::mma_scaled(tmem, dm + 2 * j, dn + 2 * j, idesc, ts, ts + 4, !begin || j > 0);
@@ -387,7 +427,56 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             for (int t = first; t < ntiles && ok; t += step) {
                 const Tile q = find_tile<MODE>(g, tp, so, pad, t);
                 const int m1 = q.m0;
-                if constexpr (MODE == kGrad) {
+                if constexpr (kMicro<MODE>) {
+                    // a block's scales came as 16 bytes a row; the tensor cores take the words of
+                    // 128 rows (4 of kNv's scales, 2 of kMx's for each of two steps) in the order
+                    // of tc::copy_scales: a lane turns its four rows' words and puts them back.
+                    // One warp does the rows and the first 128 columns, the other the last 128
+                    const int boxes = (q.ncols + kTileM - 1) / kTileM;
+                    const int u0 = warp == kSumWarps + 2 ? 0 : 2, u1 = warp == kSumWarps + 2 ? 2 : 1 + boxes;
+                    for (int kb = 0; kb < q.nkb; ++kb) {
+                        ok = tc::mbar_wait(&full[s], (uint32_t)fill & 1u);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        const uint32_t at = (uint32_t)s * g.stage_bytes + kABytes + kTileN * kKB;
+                        const uint32_t ts = tmem + kTileN + (uint32_t)(kSfCols<MODE> * s);
+                        for (int u = u0; u < u1; ++u) {
+                            uint4 *sf = reinterpret_cast<uint4 *>(ring + at + (uint32_t)u * kSfBytes);
+                            uint4 v[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[i] = sf[32 * i + lane];
+                            __syncwarp();
+                            if (MODE == kNv) {
+                                sf[lane] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+                                sf[32 + lane] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+                                sf[64 + lane] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
+                                sf[96 + lane] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+                            } else if (kb & 1) {
+                                sf[lane] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
+                                sf[32 + lane] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+                            } else {
+                                sf[lane] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+                                sf[32 + lane] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+                            }
+                        }
+                        tc::fence_async();
+                        __syncwarp();
+                        if (tc::elect()) {
+                            const uint32_t from = tc::smem_u32(ring) + at;
+                            for (int u = u0; u < u1; ++u)
+#pragma unroll
+                                for (int j = 0; j < kSfSteps<MODE>; ++j)
+                                    tc::copy_scales(u == 0 ? ts + 4 * j : ts + 4 * kSfSteps<MODE> + 8 * j + 4 * (u - 1),
+                                                    from + (uint32_t)u * kSfBytes + 512 * j);
+                            tc::mma_commit(tc::smem_u32(&scaled[s]));
+                        }
+                        __syncwarp();
+                        if (++s == kStages) {
+                            s = 0;
+                            ++fill;
+                        }
+                    }
+                } else if constexpr (MODE == kGrad) {
                     // the warps take the stages in turn: the loaded scales, powers of two, become
                     // their exponents, four times over (a step of 32 takes one), in the order
                     // of tc::copy_scales, and go to the stage's own tensor-memory columns
@@ -408,7 +497,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                             tc::fence_async();
                             __syncwarp();
                             if (tc::elect()) {
-                                const uint32_t ts = tmem + kTileN + 16u * (uint32_t)s, from = tc::smem_u32(ring) + at;
+                                const uint32_t ts = tmem + kTileN + (uint32_t)(kSfCols<MODE> * s), from = tc::smem_u32(ring) + at;
 #pragma unroll
                                 for (int i = 0; i < 3; ++i) tc::copy_scales(ts + 4 * i, from + 512 * i);
                                 tc::mma_commit(tc::smem_u32(&scaled[s]));
@@ -489,9 +578,9 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             Acc acc;
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-            constexpr int kStep = MODE == kGrad ? kFlush : 1;
+            constexpr int kStep = MODE != kProduct ? kFlush<MODE> : 1;
             for (int kb = 0; kb < nkb; kb += kStep, ++it) {
-                const int b = MODE == kGrad ? 0 : it & 1, round = MODE == kGrad ? it : it >> 1;
+                const int b = MODE != kProduct ? 0 : it & 1, round = MODE != kProduct ? it : it >> 1;
                 const int u = kb & (kScaleKB - 1), slot = gi & 1;
                 float scale = 1.f;
                 if (MODE == kProduct) {
@@ -518,7 +607,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             const int m1 = wq * 32;         // this warp's first row, from m0
             // 32 rows x 64 bytes at a time, turned through shared memory so that four lanes
             // store 64 neighbouring bytes: 16-byte pieces, piece index XOR (row / 2)
-            unsigned char *w = outs + warp * kStageOut;
+            unsigned char *w = outs + warp * kStageOut<MODE>;
             const int swz = (lane >> 1) & 3;
             const int64_t ld = g.N, at = (int64_t)(q.m0 + m1 + r8) * ld + q.n0 + c0;
             if constexpr (MODE == kGrad) {
@@ -539,41 +628,71 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                         __syncwarp();
                     }
                 }
-            } else if (g.out_bf16) {
-                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(g.out) + at + 8 * quad;
+            } else {
+                if (MODE == kNv && m1 < q.mlim) {           // the scales of whole rows, of a and of the weights
+                    const float ra = m1 + lane < q.mlim ? __ldg(g.x_scale + q.m0 + m1 + lane) : 0.f;
+                    const float4 *rw = reinterpret_cast<const float4 *>(g.w_scale + (int64_t)q.w * g.N + q.n0 + c0);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c0 + 32 * c < q.nlim) {
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<uint4 *>(w + lane * 64 + (i ^ swz) * 16) =
-                                make_uint4(pack_bf16(acc[16 * c + 4 * i]), pack_bf16(acc[16 * c + 4 * i + 1]),
-                                           pack_bf16(acc[16 * c + 4 * i + 2]), pack_bf16(acc[16 * c + 4 * i + 3]));
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(w + (8 * i + r8) * 64 + ((quad ^ ((r8 >> 1) & 3)) * 16));
-                            if (m1 + 8 * i + r8 < q.mlim && c0 + 32 * c + 8 * quad < q.nlim)
-                                *reinterpret_cast<uint4 *>(o + (int64_t)(8 * i) * ld + 32 * c) = v;
+                    for (int i = 0; i < 32; ++i) {
+                        if (c0 + 4 * i < q.nlim) {
+                            const float4 f = __ldg(rw + i);
+                            acc[2 * i].x *= ra * f.x;
+                            acc[2 * i].y *= ra * f.y;
+                            acc[2 * i + 1].x *= ra * f.z;
+                            acc[2 * i + 1].y *= ra * f.w;
                         }
                     }
                 }
-            } else {
-                float *o = static_cast<float *>(g.out) + at + 4 * quad;
+                // the rows that pass at a time, and whether this lane's row is among pass p's
+                constexpr int kRows = (int)kStageOut<MODE> / 64;
+                unsigned char *mine = w + (lane & (kRows - 1)) * 64;
+                const unsigned char *from = w + r8 * 64 + ((quad ^ ((r8 >> 1) & 3)) * 16);
+                if (g.out_bf16) {
+                    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(g.out) + at + 8 * quad;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    if (c0 + 16 * c < q.nlim) {
-                        __syncwarp();
+                    for (int c = 0; c < 4; ++c) {
+                        if (c0 + 32 * c >= q.nlim) continue;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<float4 *>(w + lane * 64 + (i ^ swz) * 16) =
-                                make_float4(acc[8 * c + 2 * i].x, acc[8 * c + 2 * i].y, acc[8 * c + 2 * i + 1].x, acc[8 * c + 2 * i + 1].y);
-                        __syncwarp();
+                        for (int p = 0; p < 32 / kRows; ++p) {
+                            __syncwarp();
+                            if (lane / kRows == p) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 v = *reinterpret_cast<const float4 *>(w + (8 * i + r8) * 64 + ((quad ^ ((r8 >> 1) & 3)) * 16));
-                            if (m1 + 8 * i + r8 < q.mlim) *reinterpret_cast<float4 *>(o + (int64_t)(8 * i) * ld + 16 * c) = v;
+                                for (int i = 0; i < 4; ++i)
+                                    *reinterpret_cast<uint4 *>(mine + (i ^ swz) * 16) =
+                                        make_uint4(pack_bf16(acc[16 * c + 4 * i]), pack_bf16(acc[16 * c + 4 * i + 1]),
+                                                   pack_bf16(acc[16 * c + 4 * i + 2]), pack_bf16(acc[16 * c + 4 * i + 3]));
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < kRows / 8; ++i) {
+                                const int r = kRows * p + 8 * i;
+                                const uint4 v = *reinterpret_cast<const uint4 *>(from + 8 * i * 64);
+                                if (m1 + r + r8 < q.mlim && c0 + 32 * c + 8 * quad < q.nlim)
+                                    *reinterpret_cast<uint4 *>(o + (int64_t)r * ld + 32 * c) = v;
+                            }
+                        }
+                    }
+                } else {
+                    float *o = static_cast<float *>(g.out) + at + 4 * quad;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        if (c0 + 16 * c >= q.nlim) continue;
+#pragma unroll
+                        for (int p = 0; p < 32 / kRows; ++p) {
+                            __syncwarp();
+                            if (lane / kRows == p) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    *reinterpret_cast<float4 *>(mine + (i ^ swz) * 16) = make_float4(
+                                        acc[8 * c + 2 * i].x, acc[8 * c + 2 * i].y, acc[8 * c + 2 * i + 1].x, acc[8 * c + 2 * i + 1].y);
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < kRows / 8; ++i) {
+                                const int r = kRows * p + 8 * i;
+                                const float4 v = *reinterpret_cast<const float4 *>(from + 8 * i * 64);
+                                if (m1 + r + r8 < q.mlim) *reinterpret_cast<float4 *>(o + (int64_t)r * ld + 16 * c) = v;
+                            }
                         }
                     }
                 }
@@ -621,6 +740,18 @@ cudaError_t make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t col
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Map of rows of scales, read in boxes of 128 rows x 16 bytes without a swizzle.
+cudaError_t make_scale_map(CUtensorMap *m, const void *base, int64_t rows, int64_t pitch) {
+    const EncodeFn f = encode_fn();
+    if (!f) return cudaErrorNotSupported;
+    const cuuint64_t dim[2] = {(cuuint64_t)pitch, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)pitch};
+    const cuuint32_t box[2] = {16, 128}, es[2] = {1, 1};
+    const CUresult r = f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dim, stride, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // Map of out[nseg][N][K] in float32, stored in boxes of 32 rows x 16 columns from
 // 64-byte rows in the 64-byte swizzle.
 cudaError_t make_out_map(CUtensorMap *m, float *out, int nseg, int N, int K) {
@@ -636,9 +767,11 @@ cudaError_t make_out_map(CUtensorMap *m, float *out, int nseg, int N, int K) {
 
 template <int MODE>
 cudaError_t run_experts(GemmArgs g, int nseg, const int32_t *seg_off, const int32_t *seg_w, const CUtensorMap &mm,
-                        const CUtensorMap &mf, const CUtensorMap &mn, cudaStream_t st) {
-    // the gradient's stages also hold their scales, and stay on 1024-byte boundaries
-    g.stage_bytes = kABytes + (uint32_t)kTileN * kKB + (MODE == kGrad ? 2048 : 0);
+                        const CUtensorMap &mf, const CUtensorMap &mn, const CUtensorMap &msm, const CUtensorMap &msn,
+                        cudaStream_t st) {
+    // the gradient's and the 4-bit product's stages also hold their scales, and stay on
+    // 1024-byte boundaries
+    g.stage_bytes = kABytes + (uint32_t)kTileN * kKB + (MODE == kGrad ? 2048 : kMicro<MODE> ? 3 * kSfBytes : 0);
     const size_t smem = (size_t)kStages * g.stage_bytes;
     cudaError_t e = ensure_smem((const void *)k_experts<MODE>, smem);
     if (e != cudaSuccess) return e;
@@ -647,7 +780,7 @@ cudaError_t run_experts(GemmArgs g, int nseg, const int32_t *seg_off, const int3
         g.seg0 = s0;
         g.seg_off = seg_off + s0;
         g.seg_w = seg_w ? seg_w + s0 : nullptr;
-        if ((e = launch_pdl(k_experts<MODE>, dim3(kSms), dim3(kThreads), smem, st, mm, mf, mn, g)) != cudaSuccess) return e;
+        if ((e = launch_pdl(k_experts<MODE>, dim3(kSms), dim3(kThreads), smem, st, mm, mf, mn, msm, msn, g)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
@@ -675,7 +808,34 @@ cudaError_t launch_expert_gemm(int nseg, int64_t rows, int n_w, int N, int K, co
     if ((e = make_map(&mx, a, rows, K, kTileM)) != cudaSuccess) return e;
     if ((e = make_map(&mf, a, rows, K, 16)) != cudaSuccess) return e;
     if ((e = make_map(&mw, w, (int64_t)n_w * N, K, kTileM)) != cudaSuccess) return e;
-    return run_experts<kProduct>(g, nseg, seg_off, seg_w, mx, mf, mw, st);
+    return run_experts<kProduct>(g, nseg, seg_off, seg_w, mx, mf, mw, mx, mw, st);
+}
+
+cudaError_t launch_expert_gemm_micro(int nseg, int64_t rows, int n_w, int N, int K, int fmt, const uint8_t *a,
+                                     const uint8_t *a_scale, const float *a_row, const int32_t *seg_off, const int32_t *seg_w,
+                                     const uint8_t *w, const uint8_t *w_scale, const float *w_row, void *out, bool bf16, void *ws,
+                                     cudaStream_t st) {
+    GemmArgs g = {};
+    g.w_scale = w_row;
+    g.x_scale = a_row;
+    g.out = out;
+    g.hdr = ws_at<WsHeader>(ws, 0);
+    g.rows = rows;
+    g.n_w = n_w;
+    g.N = N;
+    g.K = K;
+    g.KB = (K / 2 + kKB - 1) / kKB;
+    g.out_bf16 = bf16;
+    const int64_t pitch = micro_pitch(K, fmt);
+    CUtensorMap mx, mf, mw, sx, sw;
+    cudaError_t e;
+    if ((e = make_map(&mx, a, rows, K / 2, kTileM)) != cudaSuccess) return e;
+    if ((e = make_map(&mf, a, rows, K / 2, 16)) != cudaSuccess) return e;
+    if ((e = make_map(&mw, w, (int64_t)n_w * N, K / 2, kTileM)) != cudaSuccess) return e;
+    if ((e = make_scale_map(&sx, a_scale, rows, pitch)) != cudaSuccess) return e;
+    if ((e = make_scale_map(&sw, w_scale, (int64_t)n_w * N, pitch)) != cudaSuccess) return e;
+    return fmt == TOPO_FMT_NV ? run_experts<kNv>(g, nseg, seg_off, seg_w, mx, mf, mw, sx, sw, st)
+                              : run_experts<kMx>(g, nseg, seg_off, seg_w, mx, mf, mw, sx, sw, st);
 }
 
 cudaError_t launch_expert_wgrad(int nseg, int64_t rows, int N, int K, int64_t cap, const uint8_t *dy, const float *dy_scale,
@@ -696,7 +856,7 @@ cudaError_t launch_expert_wgrad(int nseg, int64_t rows, int N, int K, int64_t ca
     if ((e = make_map(&my, dy, N, cap, kTileM)) != cudaSuccess) return e;
     if ((e = make_map(&mx, x, K, cap, kTileM)) != cudaSuccess) return e;
     if ((e = make_out_map(&mo, dw, nseg, N, K)) != cudaSuccess) return e;
-    return run_experts<kGrad>(g, nseg, seg_off, nullptr, my, mo, mx, st);
+    return run_experts<kGrad>(g, nseg, seg_off, nullptr, my, mo, mx, my, mx, st);
 }
 
 }  // namespace topo

@@ -29,6 +29,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "rows.cuh"
 
 namespace topo {
 namespace {
@@ -54,15 +55,6 @@ __device__ __forceinline__ uint32_t cvt2(float lo, float hi) {
     return r;
 }
 
-__device__ __forceinline__ void unpack16(const uint4 &a, const uint4 &b, float (&v)[16]) {
-    const uint32_t q[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[2 * i] = __uint_as_float(q[i] << 16);
-        v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
-    }
-}
-
 // Largest finite magnitude of 16 values; NaN and infinities are made NaN.
 __device__ __forceinline__ float amax16(float (&v)[16]) {
     float m = 0.f;
@@ -86,14 +78,6 @@ __device__ __forceinline__ uint4 quant16(const float (&v)[16], float inv) {
         q[i] = cvt2(v[4 * i] * inv, v[4 * i + 1] * inv) | (cvt2(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16);
     return make_uint4(q[0], q[1], q[2], q[3]);
 }
-
-// Up to this size the token rows of a dispatch are read k times, position by
-// position (one launch), and not token by token through the inverse permutation
-// (three).  k = 8, H = 4096, the call's launches included, by position / by token:
-// 333 tokens 18.9 / 24.1 us, 1024 29.6 / 26.4, 4096 62.9 / 51.4, 16384 239 / 132.
-// Both sides were measured at k = 8 only.  By token at k = 1, 2, 4 and 8, 16384 tokens:
-// 52, 64, 83 and 124 us, against 30, 41, 61 and 103 for the bytes alone.
-constexpr int64_t kGatherBytes = 4 << 20;
 
 struct QuantArgs {
     const uint4 *x;          // bf16 rows, two uint4 per 16 values

@@ -158,6 +158,32 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t da, uint64_t db,
         : "memory");
 }
 
+// Products of packed 4-bit values (e2m1, two to a byte, the lower half the earlier
+// one; 1 in bits 7-9 and 10-11), K-major, 64 of them a step.  NV: kind::mxf4nvf4, four
+// UE4M3 scales a step, a word of 4 bytes; else kind::mxf4, two UE8M0 scales (bit 23),
+// the word's first two bytes or (idesc_half) its last two: ids 2 at bits 4-5 and 29-30.
+__host__ __device__ constexpr uint32_t idesc_micro(int m, int n, bool ue8m0) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((ue8m0 ? 1u : 0u) << 23) | ((uint32_t)(m >> 7) << 27);
+}
+__host__ __device__ constexpr uint32_t idesc_half(int h) { return h ? (2u << 4) | (2u << 29) : 0u; }
+
+template <bool NV>
+__device__ __forceinline__ void mma_micro(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                          uint32_t acc) {
+    if (NV)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+            "l"(da), "l"(db), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+            "l"(da), "l"(db), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+            : "memory");
+}
+
 // 32 rows of 16 bytes (rows 16 bytes apart, 128 bytes between groups of 8) from
 // shared memory to 4 tensor-memory columns of each of the four 32-lane quarters:
 // the scales of 128 rows, row r in word r / 32 of line r % 32.

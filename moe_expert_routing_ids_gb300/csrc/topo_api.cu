@@ -219,6 +219,20 @@ bool product_dims_ok(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, int32_
     return (int64_t)n_w * N <= INT32_MAX && (int64_t)n_w * K <= INT32_MAX;
 }
 
+bool micro_ok(int32_t C, int32_t fmt) { return (fmt == TOPO_FMT_MX || fmt == TOPO_FMT_NV) && C >= 32 && C % 32 == 0 && C <= (1 << 24); }
+
+// Buffers of rows in 4 bits.
+bool micro_rows_ok(int32_t fmt, const void *q, const void *scale, const float *row) {
+    if (!q || !scale || !aligned16(q, scale)) return false;
+    return fmt == TOPO_FMT_NV ? row && !((uintptr_t)row & 3) : !row;
+}
+
+// Sizes of topo_expert_few; rows of the weights must stay on 16 bytes.
+bool few_dims_ok(int32_t T, int32_t E, int32_t k, int32_t H, int32_t I, int32_t unit) {
+    if (T < 0 || T > TOPO_FEW_MAX_TOKENS || E < 1 || E > TOPO_GATE_MAX_E || k < 1 || k > kMaxK) return false;
+    return H >= unit && H % unit == 0 && H <= (1 << 15) && I >= unit && I % unit == 0 && I <= (1 << 15);
+}
+
 }  // namespace
 
 extern "C" {
@@ -540,6 +554,79 @@ int topo_expert_wgrad(int32_t n_seg, int64_t rows, int32_t N, int32_t K, int64_t
         !aligned16(dy_scale, x_scale) || ((uintptr_t)seg_off & 3))
         return TOPO_EINVAL;
     return cuda_rc(launch_expert_wgrad(n_seg, rows, N, K, cap, dy, dy_scale, x, x_scale, seg_off, dw, ws, stream));
+}
+
+int64_t topo_micro_pitch(int32_t C, int32_t fmt) { return micro_ok(C, fmt) ? micro_pitch(C, fmt) : 0; }
+
+int topo_quantize_rows_micro(int64_t rows, int32_t C, int32_t fmt, const uint16_t *x, uint8_t *q, uint8_t *scale,
+                             float *row_scale, cudaStream_t stream) {
+    if (!micro_ok(C, fmt) || !rows_ok(rows, C)) return TOPO_EINVAL;
+    if (rows == 0) return TOPO_OK;
+    if (!x || !aligned16(x, x) || !micro_rows_ok(fmt, q, scale, row_scale)) return TOPO_EINVAL;
+    return cuda_rc(launch_quantize_rows_micro(rows, C, fmt, x, q, scale, row_scale, false, stream));
+}
+
+int topo_permute_quantize_micro(const topo_cfg *cfg, int32_t n_layers, int32_t H, int32_t fmt, const uint16_t *x,
+                                const int32_t *sorted_pairs, uint8_t *q, uint8_t *scale, float *row_scale, void *ws,
+                                size_t ws_bytes, cudaStream_t stream) {
+    Geo g;
+    if (!micro_ok(H, fmt)) return TOPO_EINVAL;
+    const int rc = pack_args(cfg, n_layers, H, x, sorted_pairs, q, ws, ws_bytes, &g);
+    if (rc || n_layers == 0 || g.npairs == 0) return rc;
+    if (!micro_rows_ok(fmt, q, scale, row_scale)) return TOPO_EINVAL;
+    return cuda_rc(launch_permute_quantize_micro(g, H, fmt, x, sorted_pairs, q, scale, row_scale, ws, stream));
+}
+
+int topo_swiglu_quantize_micro(int64_t rows, int32_t I, int32_t fmt, const uint16_t *h, uint8_t *q, uint8_t *scale,
+                               float *row_scale, cudaStream_t stream) {
+    if (!micro_ok(I, fmt) || !rows_ok(rows, I)) return TOPO_EINVAL;
+    if (rows == 0) return TOPO_OK;
+    if (!h || !aligned16(h, h) || !micro_rows_ok(fmt, q, scale, row_scale)) return TOPO_EINVAL;
+    return cuda_rc(launch_quantize_rows_micro(rows, I, fmt, h, q, scale, row_scale, true, stream));
+}
+
+int topo_dequantize_micro(int64_t rows, int32_t C, int32_t fmt, const uint8_t *q, const uint8_t *scale,
+                          const float *row_scale, uint16_t *out, cudaStream_t stream) {
+    if (!micro_ok(C, fmt) || !rows_ok(rows, C)) return TOPO_EINVAL;
+    if (rows == 0) return TOPO_OK;
+    if (!out || !aligned16(out, out) || !micro_rows_ok(fmt, q, scale, row_scale)) return TOPO_EINVAL;
+    return cuda_rc(launch_dequantize_micro(rows, C, fmt, q, scale, row_scale, out, stream));
+}
+
+int topo_expert_gemm_micro(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, int32_t K, int32_t fmt, const uint8_t *a,
+                           const uint8_t *a_scale, const float *a_row, const int32_t *seg_off, const int32_t *seg_w,
+                           const uint8_t *w, const uint8_t *w_scale, const float *w_row, void *out, int32_t out_dtype,
+                           void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (!micro_ok(K, fmt) || !product_dims_ok(n_seg, rows, n_w, N, K) || !ws) return TOPO_EINVAL;
+    if (out_dtype != TOPO_DTYPE_F32 && out_dtype != TOPO_DTYPE_BF16) return TOPO_EINVAL;
+    if (!seg_w && n_seg > n_w) return TOPO_EINVAL;
+    if (ws_bytes < topo_expert_workspace_bytes(n_seg, rows, N, K)) return TOPO_ENOSPC;
+    if (n_seg == 0 || rows == 0) return TOPO_OK;
+    if (n_w == 0 || !seg_off || !out || !aligned16(out, w_row) || !micro_rows_ok(fmt, a, a_scale, a_row) ||
+        !micro_rows_ok(fmt, w, w_scale, w_row) || (((uintptr_t)seg_off | (uintptr_t)seg_w) & 3))
+        return TOPO_EINVAL;
+    return cuda_rc(launch_expert_gemm_micro(n_seg, rows, n_w, N, K, fmt, a, a_scale, a_row, seg_off, seg_w, w, w_scale, w_row,
+                                            out, out_dtype == TOPO_DTYPE_BF16, ws, stream));
+}
+
+size_t topo_few_workspace_bytes(int32_t T, int32_t E, int32_t k, int32_t H, int32_t I) {
+    return few_dims_ok(T, E, k, H, I, 16) ? few_workspace(T, k, H, I) : 0;
+}
+
+int topo_expert_few(int32_t T, int32_t E, int32_t k, int32_t H, int32_t I, int32_t fmt, const uint16_t *x,
+                    const int32_t *ids, const float *weights, const uint8_t *up, const void *up_scale, const float *up_row,
+                    const uint8_t *down, const void *down_scale, const float *down_row, uint16_t *out, void *ws,
+                    size_t ws_bytes, cudaStream_t stream) {
+    if (fmt != TOPO_FMT_EIGHT && fmt != TOPO_FMT_MX && fmt != TOPO_FMT_NV) return TOPO_EINVAL;
+    if (!few_dims_ok(T, E, k, H, I, fmt == TOPO_FMT_EIGHT ? 16 : 32) || !ws) return TOPO_EINVAL;
+    if (ws_bytes < few_workspace(T, k, H, I)) return TOPO_ENOSPC;
+    if (T == 0) return TOPO_OK;
+    if (!x || !ids || !weights || !out || !aligned16(x, out) || !aligned16(ws, ws) ||
+        (((uintptr_t)ids | (uintptr_t)weights) & 3))
+        return TOPO_EINVAL;
+    if (!micro_rows_ok(fmt, up, up_scale, up_row) || !micro_rows_ok(fmt, down, down_scale, down_row)) return TOPO_EINVAL;
+    return cuda_rc(launch_expert_few(T, E, k, H, I, fmt, x, ids, weights, up, up_scale, up_row, down, down_scale, down_row,
+                                     out, ws, stream));
 }
 
 int topo_read_error(const void *ws) {
