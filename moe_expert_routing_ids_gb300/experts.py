@@ -7,6 +7,11 @@ activation back in 8 bits, the down product and the weighted combine.  Every
 step is a call into libtopoep; torch holds the buffers, and in the backward
 pass forms the gradient of the combine (a gather and a dot product).
 
+A layer may hold its weights in 4 bits (fmt: TOPO_FMT_MX or TOPO_FMT_NV); its rows
+are then packed in 4 bits as well, and it has no backward pass.  few() is the same
+layer for a few tokens, without plan, layout or packed rows: it reads the weights of
+the experts in use once and keeps the activations in 16 bits.
+
 Ranks are logical partitions of one GPU's rows, as for the planner: replicas of
 an expert read the same weights, and their weight gradients are summed.
 """
@@ -14,10 +19,13 @@ from __future__ import annotations
 
 import torch
 
-from . import (TOPO_BLOCK, TOPO_CALL_PACK, TOPO_DTYPE_BF16, TopoRouteOpts, topo_cols_capacity, topo_combine,
-               topo_expert_gemm, topo_expert_wgrad, topo_expert_workspace_bytes, topo_permute_quantize,
-               topo_quantize_cols, topo_quantize_rows, topo_quantize_weight, topo_read_error, topo_swiglu_grad,
-               topo_swiglu_quantize, topo_workspace_bytes, topo_ws_reset)
+from . import (TOPO_BLOCK, TOPO_CALL_COOCCUR, TOPO_CALL_PACK, TOPO_DTYPE_BF16, TOPO_DTYPE_F32, TOPO_FEW_MAX_TOKENS,
+               TOPO_FMT_EIGHT, TOPO_FMT_MX, TOPO_FMT_NV, TopoRouteOpts, make_cfg, topo_cols_capacity, topo_combine,
+               topo_expert_few, topo_expert_gemm, topo_expert_gemm_micro, topo_expert_wgrad, topo_expert_workspace_bytes,
+               topo_few_workspace_bytes, topo_micro_pitch, topo_permute_quantize, topo_permute_quantize_micro,
+               topo_quantize_cols, topo_quantize_rows, topo_quantize_rows_micro, topo_quantize_weight, topo_read_error,
+               topo_route, topo_swiglu_grad, topo_swiglu_quantize, topo_swiglu_quantize_micro, topo_workspace_bytes,
+               topo_ws_reset)
 from .planner import Planner, need, ordered
 
 
@@ -25,17 +33,36 @@ def blocks(n: int) -> int:
     return (n + TOPO_BLOCK - 1) // TOPO_BLOCK
 
 
+def micro_rows(shape: tuple, C: int, fmt: int, device) -> tuple:
+    """Buffers of rows [*shape, C] in 4 bits: codes, scales, row scales (None for TOPO_FMT_MX)."""
+    pitch = topo_micro_pitch(C, fmt)
+    if pitch == 0:
+        raise ValueError(f"rows in 4 bits hold a multiple of 32 values, not {C}")
+    return (torch.empty((*shape, C // 2), dtype=torch.uint8, device=device),
+            torch.empty((*shape, pitch), dtype=torch.uint8, device=device),
+            torch.empty(shape, dtype=torch.float32, device=device) if fmt == TOPO_FMT_NV else None)
+
+
 class ExpertWeights:
     """bf16 weights [E, N, K] in 8 bits with a scale per 128 x 128 block, and
-    their transposes (the operand of the input gradient) when train is set."""
+    their transposes (the operand of the input gradient) when train is set; or
+    (fmt) in 4 bits, row by row."""
 
-    def __init__(self, w: torch.Tensor, train: bool = False, stream=None):
+    def __init__(self, w: torch.Tensor, train: bool = False, stream=None, fmt: int = TOPO_FMT_EIGHT):
         if not isinstance(w, torch.Tensor) or w.dim() != 3 or not w.is_cuda:
             raise ValueError("weights are a tensor [E, N, K] on a GPU")
+        if fmt not in (TOPO_FMT_EIGHT, TOPO_FMT_MX, TOPO_FMT_NV):
+            raise ValueError("fmt is TOPO_FMT_EIGHT, TOPO_FMT_MX or TOPO_FMT_NV")
+        if train and fmt != TOPO_FMT_EIGHT:
+            raise ValueError("weights in 4 bits have no backward pass")
         E, self.N, self.K = w.shape
-        self.E = E
+        self.E, self.fmt, self.row = E, fmt, None
         dev, u8, f32 = w.device, torch.uint8, torch.float32
         with ordered(stream, dev, w):
+            if fmt != TOPO_FMT_EIGHT:
+                self.q, self.scale, self.row = micro_rows((E, self.N), self.K, fmt, dev)
+                self.load(w)
+                return
             self.q = torch.empty((E, self.N, self.K), dtype=u8, device=dev)
             self.scale = torch.empty((E, blocks(self.N), blocks(self.K)), dtype=f32, device=dev)
             self.qt = torch.empty((E, self.K, self.N), dtype=u8, device=dev) if train else None
@@ -46,27 +73,32 @@ class ExpertWeights:
         """Takes the values of w (bf16 [E, N, K]) in place of those held."""
         need("weights", w, (torch.bfloat16,), self.E * self.N, self.K, self.q.device)
         with ordered(stream, self.q.device, w):
-            topo_quantize_weight(self.E, self.N, self.K, w, self.q, self.scale, self.qt, self.scale_t,
-                                 torch.cuda.current_stream(self.q.device))
+            s = torch.cuda.current_stream(self.q.device)
+            if self.fmt != TOPO_FMT_EIGHT:
+                topo_quantize_rows_micro(self.E * self.N, self.K, self.fmt, w, self.q, self.scale, self.row, s)
+            else:
+                topo_quantize_weight(self.E, self.N, self.K, w, self.q, self.scale, self.qt, self.scale_t, s)
 
 
 class ExpertLayer:
     """cfg: as for Planner (one layer per call); w_up: bf16 [E, 2 I, H], gate
-    rows then up rows; w_down: bf16 [E, H, I]; route: topo_route_opts.
+    rows then up rows; w_down: bf16 [E, H, I]; route: topo_route_opts; fmt: how
+    weights and packed rows are held, TOPO_FMT_EIGHT, or TOPO_FMT_MX or
+    TOPO_FMT_NV (4 bits, H and I multiples of 32, without train).
 
     stream: every step of every call runs on it (None: torch's current stream).
     The calls take their place in the caller's current stream all the same: what
     it holds so far comes before them, what it gets next comes after."""
 
     def __init__(self, cfg: dict, w_up: torch.Tensor, w_down: torch.Tensor, route: TopoRouteOpts, train: bool = False,
-                 stream=None):
+                 stream=None, fmt: int = TOPO_FMT_EIGHT):
         for name, w in (("w_up", w_up), ("w_down", w_down)):
             if not isinstance(w, torch.Tensor) or w.dim() != 3 or not w.is_cuda:
                 raise ValueError(f"{name} must be a tensor of three dimensions on a GPU")
         self.E, self.H, self.I, self.device = cfg["E"], w_down.shape[1], w_down.shape[2], w_up.device
         self._need_weights(w_up, w_down)
         with ordered(stream, w_up.device, w_up, w_down):
-            self._build(cfg, w_up, w_down, route, train, stream)
+            self._build(cfg, w_up, w_down, route, train, stream, fmt)
 
     def _need_weights(self, w_up, w_down):
         E, H, I = self.E, self.H, self.I
@@ -82,12 +114,12 @@ class ExpertLayer:
         self.up.load(w_up, self.planner.stream)
         self.down.load(w_down, self.planner.stream)
 
-    def _build(self, cfg, w_up, w_down, route, train, stream):
+    def _build(self, cfg, w_up, w_down, route, train, stream, fmt):
         self.planner = P = Planner(cfg, 1, w_up.device, stream)
         self.T, self.k, self.R = cfg["T"], cfg["k"], cfg["R"]
-        self.route, self.train = route, train
-        self.up = ExpertWeights(w_up, train, stream)
-        self.down = ExpertWeights(w_down, train, stream)
+        self.route, self.train, self.fmt = route, train, fmt
+        self.up = ExpertWeights(w_up, train, stream, fmt)
+        self.down = ExpertWeights(w_down, train, stream, fmt)
         dev, rows = self.device, self.T * self.k
         self.rows, self.n_seg = rows, self.R * P.n_local
         u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
@@ -97,9 +129,13 @@ class ExpertLayer:
 
         self.ids = buf(1, self.T, self.k, dtype=torch.int32)
         self.weights = buf(1, self.T, self.k, dtype=f32)
-        self.xq, self.xs = buf(rows, self.H, dtype=u8), buf(rows, blocks(self.H), dtype=f32)
+        if fmt == TOPO_FMT_EIGHT:
+            self.xq, self.xs = buf(rows, self.H, dtype=u8), buf(rows, blocks(self.H), dtype=f32)
+            self.aq, self.as_ = buf(rows, self.I, dtype=u8), buf(rows, blocks(self.I), dtype=f32)
+        else:
+            self.xq, self.xs, self.xr = micro_rows((rows,), self.H, fmt, dev)
+            self.aq, self.as_, self.ar = micro_rows((rows,), self.I, fmt, dev)
         self.h = buf(rows, 2 * self.I, dtype=bf16)
-        self.aq, self.as_ = buf(rows, self.I, dtype=u8), buf(rows, blocks(self.I), dtype=f32)
         self.y = buf(rows, self.H, dtype=bf16)
         self.pack_bytes = topo_workspace_bytes(P.cfg, 1, TOPO_CALL_PACK)
         self.pack_ws = buf(self.pack_bytes, dtype=u8)
@@ -108,10 +144,20 @@ class ExpertLayer:
         topo_ws_reset(self.pack_ws, self.pack_bytes, P._stream())
         topo_ws_reset(self.ws, self.ws_bytes, P._stream())
         self.seg_w = None
+        # few(): its own workspaces, for any number of tokens
+        self.few_ids = buf(TOPO_FEW_MAX_TOKENS, self.k, dtype=torch.int32)
+        self.few_weights = buf(TOPO_FEW_MAX_TOKENS, self.k, dtype=f32)
+        self.few_bytes = topo_few_workspace_bytes(TOPO_FEW_MAX_TOKENS, self.E, self.k, self.H, self.I)
+        self.few_ws = buf(max(self.few_bytes, topo_workspace_bytes(None, 0, TOPO_CALL_COOCCUR)), dtype=u8)
+        topo_ws_reset(self.few_ws, self.few_ws.numel(), P._stream())
 
     def _product(self, a, a_scale, N, K, w, w_scale, out):
         topo_expert_gemm(self.n_seg, self.rows, self.E, N, K, a, a_scale, self.planner.buf.seg_off, self.seg_w, w,
                          w_scale, out, TOPO_DTYPE_BF16, self.ws, self.ws_bytes, self.planner._stream())
+
+    def _product_micro(self, rows, w, out):
+        topo_expert_gemm_micro(self.n_seg, self.rows, self.E, w.N, w.K, self.fmt, *rows, self.planner.buf.seg_off, self.seg_w,
+                               w.q, w.scale, w.row, out, TOPO_DTYPE_BF16, self.ws, self.ws_bytes, self.planner._stream())
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor, bias: torch.Tensor | None = None) -> torch.Tensor:
         """x: bf16 [T, H]; logits: float32 or bf16 [T, E]; bias: float32 [E] or
@@ -127,14 +173,47 @@ class ExpertLayer:
         P.make_plan()
         P.reroute_layout(self.ids)
         self.seg_w = P.instance_experts()
-        topo_permute_quantize(P.cfg, 1, self.H, x, P.buf.sorted_pairs, self.xq, self.xs, self.pack_ws,
-                              self.pack_bytes, s)
-        self._product(self.xq, self.xs, 2 * self.I, self.H, self.up.q, self.up.scale, self.h)
-        topo_swiglu_quantize(self.rows, self.I, self.h, self.aq, self.as_, s)
-        self._product(self.aq, self.as_, self.H, self.I, self.down.q, self.down.scale, self.y)
+        if self.fmt == TOPO_FMT_EIGHT:
+            topo_permute_quantize(P.cfg, 1, self.H, x, P.buf.sorted_pairs, self.xq, self.xs, self.pack_ws,
+                                  self.pack_bytes, s)
+            self._product(self.xq, self.xs, 2 * self.I, self.H, self.up.q, self.up.scale, self.h)
+            topo_swiglu_quantize(self.rows, self.I, self.h, self.aq, self.as_, s)
+            self._product(self.aq, self.as_, self.H, self.I, self.down.q, self.down.scale, self.y)
+        else:
+            topo_permute_quantize_micro(P.cfg, 1, self.H, self.fmt, x, P.buf.sorted_pairs, self.xq, self.xs, self.xr,
+                                        self.pack_ws, self.pack_bytes, s)
+            self._product_micro((self.xq, self.xs, self.xr), self.up, self.h)
+            topo_swiglu_quantize_micro(self.rows, self.I, self.fmt, self.h, self.aq, self.as_, self.ar, s)
+            self._product_micro((self.aq, self.as_, self.ar), self.down, self.y)
         out = torch.empty((self.T, self.H), dtype=torch.bfloat16, device=self.device)
         topo_combine(P.cfg, 1, self.H, self.y, P.buf.sorted_pairs, self.weights, out, self.pack_ws, self.pack_bytes, s)
         return out
+
+    def few(self, x: torch.Tensor, logits: torch.Tensor, bias: torch.Tensor | None = None) -> torch.Tensor:
+        """The layer applied to n tokens, 0 to TOPO_FEW_MAX_TOKENS of them whatever
+        cfg's T: x bf16 [n, H]; logits float32 or bf16 [n, E]; bias float32 [E] or
+        None; returns bf16 [n, H].  The activations keep 16 bits, so the result is
+        nearer to the weights' own than forward()'s."""
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            raise ValueError("x must be a tensor [n, H]")
+        n = x.shape[0]
+        if n > TOPO_FEW_MAX_TOKENS or self.few_bytes == 0:
+            raise ValueError(f"few() takes up to {TOPO_FEW_MAX_TOKENS} tokens, H and I up to 32768")
+        need("x", x, (torch.bfloat16,), n, self.H, self.device)
+        need("logits", logits, (torch.float32, torch.bfloat16), n, self.E, self.device)
+        if bias is not None:
+            need("bias", bias, (torch.float32,), 1, self.E, self.device)
+        with ordered(self.planner.stream, self.device, x, logits, bias) as outs:
+            s, out = self.planner._stream(), torch.empty_like(x)
+            outs.append(out)
+            if n:
+                topo_route(make_cfg(n, self.E, self.k, 1, 1, 0), 1, self.route, logits,
+                           TOPO_DTYPE_F32 if logits.dtype == torch.float32 else TOPO_DTYPE_BF16, bias, self.few_ids,
+                           self.few_weights, None, self.few_ws, self.few_ws.numel(), s)
+                topo_expert_few(n, self.E, self.k, self.H, self.I, self.fmt, x, self.few_ids, self.few_weights, self.up.q,
+                                self.up.scale, self.up.row, self.down.q, self.down.scale, self.down.row, out, self.few_ws,
+                                self.few_ws.numel(), s)
+        return outs[0]
 
     def _rows8(self, x):
         q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
@@ -214,4 +293,5 @@ class ExpertLayer:
 
     def error(self) -> int:
         """First device error word of the layer's workspaces (synchronises the device)."""
-        return self.planner.error() or topo_read_error(self.pack_ws) or topo_read_error(self.ws)
+        return (self.planner.error() or topo_read_error(self.pack_ws) or topo_read_error(self.ws)
+                or topo_read_error(self.few_ws))
