@@ -9,9 +9,11 @@
 //
 // (n >= -126; 1 for zeros) and q = e2m1(v / s) or e2m1(v / (s g)), to nearest, ties
 // to even: no value is clipped.  A block that holds a NaN or an infinity gets the
-// scale NaN.  Division by a power of two is exact; the quotient by an e4m3 scale is
-// corrected by its residual (Markstein), so that a quotient on the border between
-// two values of e2m1, the only place where a last bit counts, comes out exactly.
+// scale NaN.  Division by a power of two is exact.  With an e4m3 scale of 4 bits, a bf16
+// value's quotient is a border between two values of e2m1 (at most 3 bits) or at least
+// 2^-8 of it away: the product with the scale's inverse, within 2^-23, rounded to f16 is
+// on the right side, or on the border.  The activation's quotients, of float32 values,
+// are corrected by their residuals (Markstein).
 //
 //   k_micro_rows     rows as they are, dispatch rows (by position, or token row t to the
 //                    k layout positions of its pairs), or the gated activation
@@ -50,13 +52,28 @@ __device__ __forceinline__ float e4m3_value(uint32_t b) {
     return __half2float(__ushort_as_half((unsigned short)h));
 }
 
-// Eight values in 4 bits, the first in the lowest.
+// Eight values in 4 bits, the first in the lowest.  HALF: through f16, whose 11 bits hold
+// every border between two values of e2m1.
+template <bool HALF>
 __device__ __forceinline__ uint32_t e2m1x8(const float *v) {
     uint32_t r;
-    asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
-        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
-        : "=r"(r)
-        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    if (HALF) {
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 p = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            h[i] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+        asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f16x2 a, %1;\n cvt.rn.satfinite.e2m1x2.f16x2 b, %2;\n"
+            " cvt.rn.satfinite.e2m1x2.f16x2 c, %3;\n cvt.rn.satfinite.e2m1x2.f16x2 d, %4;\n mov.b32 %0, {a, b, c, d};\n}\n"
+            : "=r"(r)
+            : "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]));
+    } else {
+        asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+            " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
+            : "=r"(r)
+            : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    }
     return r;
 }
 
@@ -72,18 +89,10 @@ struct MicroArgs {
     int T, k;                // kScatter, kGather: tokens per layer, copies of a row
     int nv;                  // 16-value groups per (output) row
     int pitch;
-    int parts, per;          // a row is split over `parts` warps of `per` groups of 32 lanes
-    int keep;                // NV, kSwiglu: a row's values pass through shared memory
+    int log_w;               // a row is split over 2^log_w warps, at most 8
 };
 
-// Bits of the largest magnitude of 16 values (as NaN > infinity > finite values), and of
-// the largest finite one where that is neither.
-__device__ __forceinline__ uint32_t amax_bits(const float (&v)[16]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    return m;
-}
+// Bits of the largest finite magnitude of 16 values.
 __device__ __forceinline__ uint32_t finite_bits(const float (&v)[16]) {
     uint32_t m = 0;
 #pragma unroll
@@ -94,200 +103,278 @@ __device__ __forceinline__ uint32_t finite_bits(const float (&v)[16]) {
     return m;
 }
 
-// Group c of a source row, zeros past its end.
-template <int SRC>
-__device__ __forceinline__ void load16(const MicroArgs &g, int64_t from, int c, float (&v)[16]) {
-    const uint4 z = make_uint4(0, 0, 0, 0);
-    const bool in = c < g.nv;
-    if (SRC == kSwiglu) {
-        const uint4 *src = g.x + from * (4 * (int64_t)g.nv);
-        float u[16];
-        unpack16(in ? __ldcs(src + 2 * c) : z, in ? __ldcs(src + 2 * c + 1) : z, v);
-        src += 2 * g.nv;
-        unpack16(in ? __ldcs(src + 2 * c) : z, in ? __ldcs(src + 2 * c + 1) : z, u);
+// v = silu(v) * u in float32: the reciprocal of 1 + exp(-v) from the approximate one by a
+// step of Newton's iteration, within 2^-23 of itself, where the divisors are below 2^120;
+// past that (v below -83, or not finite) the division.  Against dividing everywhere, as
+// topo_swiglu_quantize does, bits may be the neighbours'.
+__device__ __forceinline__ void gated(float (&v)[16], const float (&u)[16]) {
+    float top = 0.f, w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(__fdiv_rn(v[i], __fadd_rn(1.f, expf(-v[i]))), u[i]);
-    } else {
-        const uint4 *src = g.x + from * (2 * (int64_t)g.nv);
-        unpack16(in ? __ldg(src + 2 * c) : z, in ? __ldg(src + 2 * c + 1) : z, v);
+    for (int i = 0; i < 16; ++i) {
+        const float d = 1.f + expf(-v[i]);
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+        r = __fmaf_rn(__fmaf_rn(-d, r, 1.f), r, r);
+        top = fmaxf(top, d);
+        w[i] = v[i] * r * u[i];
     }
+    if (!(top < 0x1p120f)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = __fdiv_rn(v[i], 1.f + expf(-v[i])) * u[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = w[i];
 }
 
+// A lane's groups of a row: kGroups of them, 32 apart, at a time, kept as they are stored
+// (the activation's as float32).
+template <int SRC>
+constexpr int kGroups = SRC == kSwiglu ? 2 : 4;
+
+template <int SRC>
+struct Groups {
+    uint4 a[kGroups<SRC>][2];
+
+    __device__ __forceinline__ void load(const MicroArgs &g, int64_t from, int c0) {
+        const uint4 *src = g.x + from * (2 * (int64_t)g.nv);
+#pragma unroll
+        for (int j = 0; j < kGroups<SRC>; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) a[j][i] = c0 + 32 * j < g.nv ? __ldg(src + 2 * (c0 + 32 * j) + i) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(int j, float (&v)[16]) const { unpack16(a[j][0], a[j][1], v); }
+    // Bits (float32) of the largest magnitude of group j, as NaN > infinity > finite values.
+    __device__ __forceinline__ uint32_t amax(int j) const {
+        const uint32_t w[8] = {a[j][0].x, a[j][0].y, a[j][0].z, a[j][0].w, a[j][1].x, a[j][1].y, a[j][1].z, a[j][1].w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        return max(m << 16, m & 0xffff0000u);
+    }
+};
+template <>
+struct Groups<kSwiglu> {
+    float f[kGroups<kSwiglu>][16];
+
+    __device__ __forceinline__ void load(const MicroArgs &g, int64_t from, int c0) {
+        const uint4 *src = g.x + from * (4 * (int64_t)g.nv);
+        uint4 a[kGroups<kSwiglu>][4];
+#pragma unroll
+        for (int j = 0; j < kGroups<kSwiglu>; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + 32 * j;
+                a[j][i] = c < g.nv ? __ldg(src + 2 * (i < 2 ? c : g.nv + c) + (i & 1)) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+        for (int j = 0; j < kGroups<kSwiglu>; ++j) {
+            float u[16];
+            unpack16(a[j][0], a[j][1], f[j]);
+            unpack16(a[j][2], a[j][3], u);
+            gated(f[j], u);
+        }
+    }
+    __device__ __forceinline__ void get(int j, float (&v)[16]) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = f[j][i];
+    }
+    __device__ __forceinline__ uint32_t amax(int j) const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(f[j][i]) & 0x7fffffffu);
+        return m;
+    }
+};
+
 template <int SRC, bool NV>
-__global__ void __launch_bounds__(256)
+constexpr int kCtas = SRC == kSwiglu ? 2 : NV ? 3 : 4;      // to an SM
+
+// 2^log_w warps take a row, each kGroups * 32 groups of 16 values side by side; a row that
+// is longer than eight warps' goes round (NV: and is read twice, once for its largest
+// magnitude).  All of a lane's loads are on their way before the first is used.
+template <int SRC, bool NV>
+__global__ void __launch_bounds__(256, kCtas<SRC, NV>)
 k_micro_rows(MicroArgs g) {
-    extern __shared__ float kept[];                              // keep: a row of each warp
-    const int64_t unit = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int64_t row = unit / g.parts;
-    if (row >= g.rows) return;                                   // whole warp
-    const int part = (int)(unit - row * g.parts);
-    const int lane = threadIdx.x & 31;
+    constexpr int kPer = kGroups<SRC> * 32;
+    __shared__ uint32_t wmax[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = warp & ((1 << g.log_w) - 1);
+    const int64_t row = ((int64_t)blockIdx.x * 8 + warp) >> g.log_w;
+    bool live = row < g.rows;                                    // the same for a row's warps
     int pa = 0, pb = 0;
     int64_t base = 0, from = row;
     pdl_trigger();
     pdl_wait();
-    if (SRC == kGather) {
+    if (SRC == kGather && live) {
         const int64_t l = row / g.npairs;
         const int p = __ldg(g.inv + row);
         if ((uint64_t)p >= (uint64_t)g.npairs) {
             if (lane == 0) set_error(g.hdr, TOPO_ESTATE);
-            return;
+            live = false;
         }
         from = l * g.T + p / g.k;
     }
-    if (SRC == kScatter) {
+    if (SRC == kScatter && live) {
         base = (row / g.T) * g.npairs;
         const int32_t *iv = g.inv + row * g.k;
         pa = lane < g.k ? __ldg(iv + lane) : 0;
         pb = lane + 32 < g.k ? __ldg(iv + lane + 32) : 0;
         if (!__all_sync(0xffffffffu, (uint64_t)pa < (uint64_t)g.npairs && (uint64_t)pb < (uint64_t)g.npairs)) {
             if (lane == 0) set_error(g.hdr, TOPO_ESTATE);
-            return;
+            live = false;
         }
     }
-    float *mine = kept + (threadIdx.x >> 5) * ((g.nv + 31) / 32 * 512);
-    float ginv = 1.f;
+    if (!live) from = 0;
+    const int first = part * kPer + lane, span = kPer << g.log_w;
+    const int nv = live ? (g.nv + 31) & ~31 : 0;                 // whole warps of groups
+    Groups<SRC> in_regs;
+    float v[16];
+    uint32_t am[kGroups<SRC>];                                   // the groups' largest magnitudes
+    int n = 0;                                                   // NV: exponent of the row's scale
     if (NV) {
         // the whole row's largest finite magnitude first
         uint32_t m = 0;
-        for (int c = lane; c < g.nv; c += 32) {
-            float v[16];
-            load16<SRC>(g, from, c, v);
-            const uint32_t a = amax_bits(v);
-            m = max(m, a < kInf ? a : finite_bits(v));
-            if (SRC == kSwiglu && g.keep)
+        for (int c0 = first; c0 - lane < nv; c0 += span) {
+            in_regs.load(g, from, c0);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)                      // piece i of each lane side by side
-                    *reinterpret_cast<float4 *>(mine + (c >> 5) * 512 + i * 128 + 4 * lane) =
-                        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int j = 0; j < kGroups<SRC>; ++j) {
+                am[j] = in_regs.amax(j);
+                uint32_t a = am[j];
+                if (a >= kInf) {
+                    in_regs.get(j, v);
+                    a = finite_bits(v);
+                }
+                m = max(m, a);
+            }
         }
         m = __reduce_max_sync(0xffffffffu, m);
-        const int n = least_power(m, 0x280000u, 11);             // 6 * 448 = 1.3125 * 2^11
-        ginv = pow2(-n);
-        if (SRC == kScatter && part == 0) {
+        if (g.log_w > 0) {
+            if (lane == 0) wmax[warp] = m;
+            __syncthreads();
+            m = 0;
+            for (int i = 0; i < 1 << g.log_w; ++i) m = max(m, wmax[(warp & ~((1 << g.log_w) - 1)) + i]);
+        }
+        n = least_power(m, 0x280000u, 11);                       // 6 * 448 = 1.3125 * 2^11
+        if (SRC == kScatter && live && part == 0) {
             if (lane < g.k) g.row_scale[base + pa] = pow2(n);
             if (lane + 32 < g.k) g.row_scale[base + pb] = pow2(n);
-        } else if (lane == 0 && part == 0) {
+        } else if (live && lane == 0 && part == 0) {
             g.row_scale[row] = pow2(n);
         }
     }
-    const int end = min((g.nv + 31) & ~31, (part + 1) * g.per * 32);
-    for (int c0 = part * g.per * 32; c0 < end; c0 += 32) {
-        const int c = c0 + lane;
-        const bool in = c < g.nv;
-        float v[16];
-        if (NV && SRC == kSwiglu && g.keep) {
+    for (int c0 = first; c0 - lane < nv; c0 += span) {
+        if (!NV || g.nv > span) {
+            in_regs.load(g, from, c0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 f = in ? *reinterpret_cast<const float4 *>(mine + (c >> 5) * 512 + i * 128 + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-                v[4 * i] = f.x;
-                v[4 * i + 1] = f.y;
-                v[4 * i + 2] = f.z;
-                v[4 * i + 3] = f.w;
-            }
-        } else {
-            load16<SRC>(g, from, c, v);
+            for (int j = 0; j < kGroups<SRC>; ++j) am[j] = in_regs.amax(j);
         }
-        uint32_t m = amax_bits(v), sb;
-        if (NV) {
-            const float t = __uint_as_float(m) * ginv;           // at most 2688
-            uint16_t b;
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(0.f), "f"(t * (1.f / 6.f)));
-            sb = b;
-            float s = e4m3_value(sb);
-            if (6.f * s < t) s = e4m3_value(++sb);               // rounded down: the next one
-            if (m == 0u) s = 1.f, sb = 0x38u;
-            const float si = __frcp_rn(s);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float y = v[i] * ginv, q0 = y * si;
-                v[i] = __fmaf_rn(__fmaf_rn(-q0, s, y), si, q0);
-            }
-            if (m >= kInf) sb = 0x7fu;
-        } else {
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            const int n = m < kInf ? least_power(m, 0x400000u, 2) : 0;   // 6 = 1.5 * 2^2
-            const float inv = pow2(-n);
+        for (int j = 0; j < kGroups<SRC>; ++j) {
+            const int c = c0 + 32 * j;
+            if (c - lane >= nv) break;                           // whole warp
+            const bool in = c < g.nv;
+            in_regs.get(j, v);
+            uint32_t m = am[j], sb;
+            if (NV) {
+                const float t = __uint_as_float(m) * pow2(-n);   // at most 2688
+                uint16_t b;
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(0.f), "f"(t * (1.f / 6.f)));
+                sb = b;
+                float s = e4m3_value(sb);
+                if (6.f * s < t) s = e4m3_value(++sb);           // rounded down: the next one
+                if (m == 0u) s = 1.f, sb = 0x38u;
+                if (n < -112) {                                  // 1 / (s g) might be past float32's range
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] *= inv;
-            sb = m < kInf ? (uint32_t)(127 + n) : 255u;
-        }
-        const uint2 q = make_uint2(e2m1x8(v), e2m1x8(v + 8));
-        // four blocks' scales to a word, on the first of their lanes; bytes past the last
-        // block hold 1
-        constexpr int kLanes = NV ? 4 : 8;                       // lanes of a word
-        sb |= __shfl_down_sync(0xffffffffu, sb, kLanes / 4) << 8;
-        sb |= __shfl_down_sync(0xffffffffu, sb, kLanes / 2) << 16;
-        const int at = (c0 + lane) / kLanes * 4;
-        const bool word = lane % kLanes == 0 && at < g.pitch;
-        if (SRC == kScatter) {
-            for (int j = 0; j < g.k; ++j) {
-                const int a = __shfl_sync(0xffffffffu, pa, j & 31), b = __shfl_sync(0xffffffffu, pb, j & 31);
-                const int64_t r = base + (j < 32 ? a : b);
-                if (in) g.q[r * g.nv + c] = q;
-                if (word) *reinterpret_cast<uint32_t *>(g.scale + r * g.pitch + at) = sb;
+                    for (int i = 0; i < 16; ++i) v[i] *= 0x1p16f;
+                }
+                const float sg = s * pow2(n < -112 ? n + 16 : n), si = __frcp_rn(sg);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float q0 = v[i] * si;
+                    v[i] = SRC == kSwiglu ? __fmaf_rn(__fmaf_rn(-q0, sg, v[i]), si, q0) : q0;
+                }
+                if (m >= kInf) sb = 0x7fu;
+            } else {
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                const int n = m < kInf ? least_power(m, 0x400000u, 2) : 0;   // 6 = 1.5 * 2^2
+                const float inv = pow2(-n);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] *= inv;
+                sb = m < kInf ? (uint32_t)(127 + n) : 255u;
             }
-        } else {
-            if (in) g.q[row * g.nv + c] = q;
-            if (word) *reinterpret_cast<uint32_t *>(g.scale + row * g.pitch + at) = sb;
+            constexpr bool kHalf = NV && SRC != kSwiglu;
+            const uint2 q = make_uint2(e2m1x8<kHalf>(v), e2m1x8<kHalf>(v + 8));
+            // four blocks' scales to a word, on the first of their lanes; bytes past the last
+            // block hold 1
+            constexpr int kLanes = NV ? 4 : 8;                   // lanes of a word
+            sb |= __shfl_down_sync(0xffffffffu, sb, kLanes / 4) << 8;
+            sb |= __shfl_down_sync(0xffffffffu, sb, kLanes / 2) << 16;
+            const int at = c / kLanes * 4;
+            const bool word = lane % kLanes == 0 && at < g.pitch;
+            if (SRC == kScatter) {
+                for (int i = 0; i < g.k; ++i) {
+                    const int a = __shfl_sync(0xffffffffu, pa, i & 31), b = __shfl_sync(0xffffffffu, pb, i & 31);
+                    const int64_t r = base + (i < 32 ? a : b);
+                    if (in) g.q[r * g.nv + c] = q;
+                    if (word) *reinterpret_cast<uint32_t *>(g.scale + r * g.pitch + at) = sb;
+                }
+            } else {
+                if (in) g.q[row * g.nv + c] = q;
+                if (word) *reinterpret_cast<uint32_t *>(g.scale + row * g.pitch + at) = sb;
+            }
         }
     }
 }
 
-// A warp takes 512 values of a row.
+// A lane takes 8 neighbouring values (16 bytes out) four times, 256 values apart, so that
+// a warp's stores are whole lines and four loads are on their way at once.
 template <bool NV>
 __global__ void __launch_bounds__(256)
-k_micro_values(const uint2 *__restrict__ q, const uint8_t *__restrict__ scale, const float *__restrict__ row_scale, uint4 *out,
-               int64_t units, int nv, int pitch) {
+k_micro_values(const uint32_t *__restrict__ q, const uint8_t *__restrict__ scale, const float *__restrict__ row_scale, uint4 *out,
+               int64_t units, int chunks, int n8, int pitch) {
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31, chunks = (nv + 31) / 32;
-    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * 8) {
-        const int64_t row = u / chunks;
-        const int c = (int)(u - row * chunks) * 32 + lane;
-        if (c >= nv) continue;
-        const uint2 w = __ldcs(q + row * nv + c);
-        const uint32_t sb = __ldg(scale + row * pitch + (NV ? c : c >> 1));
+    const int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (u >= units) return;
+    const int64_t row = u / chunks;
+    const int c0 = (int)(u - row * chunks) * 128 + (threadIdx.x & 31);
+    uint32_t w[4], sb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int c = c0 + 32 * j;
+        w[j] = c < n8 ? __ldcs(q + row * n8 + c) : 0u;
+        sb[j] = c < n8 ? __ldg(scale + row * pitch + (NV ? c >> 1 : c >> 2)) : 0u;
+    }
+    const float g = NV ? __ldg(row_scale + row) : 1.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int c = c0 + 32 * j;
+        if (c >= n8) break;
         float s;
-        if (NV) s = (sb & 0x7fu) == 0x7fu ? __uint_as_float(0x7fffffffu) : e4m3_value(sb) * __ldg(row_scale + row);
-        else s = sb == 255u ? __uint_as_float(0x7fffffffu) : sb == 0u ? __uint_as_float(0x400000u) : pow2((int)sb - 127);
-        uint32_t o[8];
+        if (NV) s = (sb[j] & 0x7fu) == 0x7fu ? __uint_as_float(0x7fffffffu) : e4m3_value(sb[j]) * g;
+        else s = sb[j] == 255u ? __uint_as_float(0x7fffffffu) : sb[j] == 0u ? __uint_as_float(0x400000u) : pow2((int)sb[j] - 127);
+        uint32_t f[4], o[4];
+        asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+            " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+            : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+            : "r"(w[j]));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t f[4];
-            asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
-                " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
-                : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
-                : "r"(h ? w.y : w.x));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&f[i]));
-                const __nv_bfloat162 b = __floats2bfloat162_rn(p.x * s, p.y * s);
-                o[4 * h + i] = *reinterpret_cast<const uint32_t *>(&b);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&f[i]));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(p.x * s, p.y * s);
+            o[i] = *reinterpret_cast<const uint32_t *>(&b);
         }
-        uint4 *dst = out + (row * nv + c) * 2;
-        __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
-        __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
+        __stcs(out + row * n8 + c, make_uint4(o[0], o[1], o[2], o[3]));
     }
 }
 
 template <int SRC, bool NV>
 cudaError_t run_rows(MicroArgs a, cudaStream_t st) {
     if (a.rows == 0) return cudaSuccess;
-    const int chunks = (a.nv + 31) / 32;
-    // few rows: a row's 512-value chunks go to warps of their own
-    a.per = a.rows * chunks <= 152 * 64 ? 1 : chunks;
-    a.parts = (chunks + a.per - 1) / a.per;
-    const int64_t units = a.rows * a.parts;
-    size_t smem = 0;
-    if (NV && SRC == kSwiglu && a.parts == 1 && chunks <= 13) {  // 8 warps' rows of 512 float32 a chunk
-        a.keep = 1;
-        smem = (size_t)8 * chunks * 2048;
-        const cudaError_t e = ensure_smem((const void *)k_micro_rows<SRC, NV>, smem);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(k_micro_rows<SRC, NV>, dim3((unsigned)((units + 7) / 8)), dim3(256), smem, st, a);
+    a.log_w = 0;
+    while (a.log_w < 3 && (kGroups<SRC> * 32) << a.log_w < a.nv) ++a.log_w;
+    const int64_t warps = a.rows << a.log_w;
+    return launch_pdl(k_micro_rows<SRC, NV>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, a);
 }
 
 template <int SRC>
@@ -336,16 +423,15 @@ cudaError_t launch_permute_quantize_micro(const Geo &g, int H, int fmt, const ui
 
 cudaError_t launch_dequantize_micro(int64_t rows, int C, int fmt, const uint8_t *q, const uint8_t *scale, const float *row_scale,
                                     uint16_t *out, cudaStream_t st) {
-    const int nv = C / 16, pitch = (int)micro_pitch(C, fmt);
-    const int64_t units = rows * ((nv + 31) / 32);
+    const int n8 = C / 8, pitch = (int)micro_pitch(C, fmt), chunks = (n8 + 127) / 128;
+    const int64_t units = rows * chunks;
     if (units == 0) return cudaSuccess;
-    const int64_t want = (units + 7) / 8;
-    const dim3 grid((unsigned)(want < 152 * 32 ? want : 152 * 32));
-    const uint2 *qv = reinterpret_cast<const uint2 *>(q);
+    const dim3 grid((unsigned)((units + 7) / 8));
+    const uint32_t *qv = reinterpret_cast<const uint32_t *>(q);
     uint4 *ov = reinterpret_cast<uint4 *>(out);
     if (fmt == TOPO_FMT_NV)
-        return launch_pdl(k_micro_values<true>, grid, dim3(256), 0, st, qv, scale, row_scale, ov, units, nv, pitch);
-    return launch_pdl(k_micro_values<false>, grid, dim3(256), 0, st, qv, scale, row_scale, ov, units, nv, pitch);
+        return launch_pdl(k_micro_values<true>, grid, dim3(256), 0, st, qv, scale, row_scale, ov, units, chunks, n8, pitch);
+    return launch_pdl(k_micro_values<false>, grid, dim3(256), 0, st, qv, scale, row_scale, ov, units, chunks, n8, pitch);
 }
 
 }  // namespace topo
