@@ -37,15 +37,16 @@ constexpr int kMaxWarps = 16;
 constexpr int kRowBytes = 128;                    // of a weight row in a stage
 constexpr int kSfRow = 16;                        // scale bytes of a row in a stage, at most
 constexpr int kStageBytes = 16 * (kRowBytes + kSfRow);
-constexpr int kMaxTokens = 8;                     // of one launch, the N of a product
-constexpr int kMaxPairs = kMaxTokens * kMaxK;
-constexpr int kMaxRows = 16;                      // token rows that a CTA holds
+constexpr int kCols = 8;                          // token columns of a product
+constexpr int kMaxPairs = 512;                    // of one launch
+constexpr int kMaxRows = TOPO_FEW_MAX_TOKENS;     // token rows that a CTA holds
 constexpr int kMaxParts = 64;                     // partial tiles that it holds
+constexpr int kMaxSplit = 8;                      // parts of the up contraction, a power of two that divides 152
 constexpr int kCounters = (1 << 15) / 16;         // column tiles of the widest H
 
 struct FewArgs {
     const uint16_t *x;          // up: bf16 [T][K]
-    const float *act;           // down: [T * k][K]
+    const float *act;           // down: the activations [T * k][K], or for split > 1 [split][T * k][2 K], parts of g and u
     const int32_t *ids;         // [T][k]
     const float *weights;       // [T][k]
     const uint8_t *w;           // [E][rows][K]
@@ -60,8 +61,10 @@ struct FewArgs {
     int rows;                   // weight rows of an expert
     int units;                  // tiles of 16 rows of an expert
     int nc;                     // stages of a row
+    int split;                  // the up contraction's parts, each to its share of the CTAs
     int64_t pitch;              // 4 bits: scale bytes of a row
     int bpitch;                 // bytes of a token row in shared memory
+    int cols;                   // pairs of a group, at most kCols
     int warps, cap_rows, cap_parts;
 };
 
@@ -72,9 +75,9 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
     if (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
-// 16 bytes, or zeros
-__device__ __forceinline__ void copy_or_zero(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+// n = 16 bytes, or 16 zeros for n = 0
+__device__ __forceinline__ void copy_n(uint32_t dst, const void *src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -88,10 +91,23 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// d = the product.
+__device__ __forceinline__ void mma16_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Two e4m3 values as f16.
 __device__ __forceinline__ uint32_t e4m3x2(uint32_t v) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
+    return r;
+}
+// Two powers of two from their exponents' bytes (255: NaN), as bf16.
+__device__ __forceinline__ uint32_t ue8m0x2(uint32_t v) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
     return r;
 }
 // Eight e2m1 values as f16.
@@ -101,8 +117,10 @@ __device__ __forceinline__ void e2m1x8(uint32_t v, uint32_t (&r)[4]) {
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
         : "r"(v));
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+// Two f16 values times one half of s.
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t s, int high) {
+    const __half2 f = *reinterpret_cast<const __half2 *>(&s);
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), high ? __high2half2(f) : __low2half2(f));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
@@ -128,7 +146,7 @@ __device__ __forceinline__ void stage_product(float (&acc)[4], const unsigned ch
     const int r = lane >> 2, t = lane & 3;
     const unsigned char *sf = st + 16 * kRowBytes;
     if constexpr (FMT == TOPO_FMT_EIGHT) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        float d[4];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {                           // 64 values, 16 of them this lane's
             const uint4 v0 = *reinterpret_cast<const uint4 *>(st + r * kRowBytes + piece<FMT>(r, 4 * q + t));
@@ -144,7 +162,8 @@ __device__ __forceinline__ void stage_product(float (&acc)[4], const unsigned ch
             }
             const uint4 x0 = *reinterpret_cast<const uint4 *>(b + 128 * q + 32 * t);
             const uint4 x1 = *reinterpret_cast<const uint4 *>(b + 128 * q + 32 * t + 16);
-            mma16(d, f[0], x0.x, x0.y);
+            if (q == 0) mma16_new(d, f[0], x0.x, x0.y);
+            else mma16(d, f[0], x0.x, x0.y);
             mma16(d, f[1], x0.z, x0.w);
             mma16(d, f[2], x1.x, x1.y);
             mma16(d, f[3], x1.z, x1.w);
@@ -155,45 +174,42 @@ __device__ __forceinline__ void stage_product(float (&acc)[4], const unsigned ch
         acc[2] += d[2] * s.y;
         acc[3] += d[3] * s.y;
     } else {
-        uint32_t s0[4], s1[4];                                  // the scales of rows r and r + 8
+        // the scales of rows r and r + 8 for each 32 values (NV: of this lane's half of them), two to a word
+        uint32_t s0[4], s1[4];
         if (FMT == TOPO_FMT_NV) {
             const uint4 a = *reinterpret_cast<const uint4 *>(sf + r * 16), c = *reinterpret_cast<const uint4 *>(sf + (r + 8) * 16);
-            s0[0] = a.x, s0[1] = a.y, s0[2] = a.z, s0[3] = a.w;
-            s1[0] = c.x, s1[1] = c.y, s1[2] = c.z, s1[3] = c.w;
+            const uint32_t pick = t < 2 ? 0x6420u : 0x7531u;
+            const uint32_t a0 = __byte_perm(a.x, a.y, pick), a1 = __byte_perm(a.z, a.w, pick);
+            const uint32_t c0 = __byte_perm(c.x, c.y, pick), c1 = __byte_perm(c.z, c.w, pick);
+            s0[0] = e4m3x2(a0), s0[1] = e4m3x2(a0 >> 16), s0[2] = e4m3x2(a1), s0[3] = e4m3x2(a1 >> 16);
+            s1[0] = e4m3x2(c0), s1[1] = e4m3x2(c0 >> 16), s1[2] = e4m3x2(c1), s1[3] = e4m3x2(c1 >> 16);
         } else {
             const uint2 a = *reinterpret_cast<const uint2 *>(sf + r * 16), c = *reinterpret_cast<const uint2 *>(sf + (r + 8) * 16);
-            s0[0] = a.x, s0[1] = a.y;
-            s1[0] = c.x, s1[1] = c.y;
+            s0[0] = ue8m0x2(a.x), s0[1] = ue8m0x2(a.x >> 16), s0[2] = ue8m0x2(a.y), s0[3] = ue8m0x2(a.y >> 16);
+            s1[0] = ue8m0x2(c.x), s1[1] = ue8m0x2(c.x >> 16), s1[2] = ue8m0x2(c.y), s1[3] = ue8m0x2(c.y >> 16);
         }
-        const uint32_t pick = t < 2 ? 0x1010u : 0x3232u;        // NV: this lane's of a 32-value piece's two scales
 #pragma unroll
         for (int q = 0; q < 8; ++q) {                           // 32 values, 8 of them this lane's
             uint32_t f0[4], f1[4];
             e2m1x8(*reinterpret_cast<const uint32_t *>(st + r * kRowBytes + piece<FMT>(r, q) + 4 * t), f0);
             e2m1x8(*reinterpret_cast<const uint32_t *>(st + (r + 8) * kRowBytes + piece<FMT>(r, q) + 4 * t), f1);
             if (FMT == TOPO_FMT_NV) {
-                const uint32_t c0 = __byte_perm(e4m3x2(s0[q >> 1] >> (16 * (q & 1))), 0, pick);
-                const uint32_t c1 = __byte_perm(e4m3x2(s1[q >> 1] >> (16 * (q & 1))), 0, pick);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    f0[i] = mul2(f0[i], c0);
-                    f1[i] = mul2(f1[i], c1);
+                    f0[i] = mul2(f0[i], s0[q >> 1], q & 1);
+                    f1[i] = mul2(f1[i], s1[q >> 1], q & 1);
                 }
             }
             const uint32_t a0[4] = {f0[0], f1[0], f0[1], f1[1]}, a1[4] = {f0[2], f1[2], f0[3], f1[3]};
-            float m0 = 0.f, m1 = 0.f;
-            if (FMT == TOPO_FMT_MX) {                           // 2^(byte - 127), 2^-127 for a byte of 0
-                const uint32_t u0 = (s0[q >> 2] >> (8 * (q & 3))) << 23, u1 = (s1[q >> 2] >> (8 * (q & 3))) << 23;
-                m0 = __uint_as_float(max(u0 & 0x7f800000u, 0x400000u));
-                m1 = __uint_as_float(max(u1 & 0x7f800000u, 0x400000u));
-            }
             const uint4 x = *reinterpret_cast<const uint4 *>(b + 64 * q + 16 * t);
             if (FMT == TOPO_FMT_NV) {
                 mma16(acc, a0, x.x, x.y);
                 mma16(acc, a1, x.z, x.w);
             } else {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16(d, a0, x.x, x.y);
+                const float m0 = __uint_as_float(q & 1 ? s0[q >> 1] & 0xffff0000u : s0[q >> 1] << 16);
+                const float m1 = __uint_as_float(q & 1 ? s1[q >> 1] & 0xffff0000u : s1[q >> 1] << 16);
+                float d[4];
+                mma16_new(d, a0, x.x, x.y);
                 mma16(d, a1, x.z, x.w);
                 acc[0] += d[0] * m0;
                 acc[1] += d[1] * m0;
@@ -207,46 +223,52 @@ __device__ __forceinline__ void stage_product(float (&acc)[4], const unsigned ch
 // Issues one warp's stages of its items in order, ahead of their use.
 template <int FMT, bool DOWN>
 struct Feed {
-    const unsigned char *src[4];                                // this lane's piece of rows lane / 8 + 4 i
-    const unsigned char *sf;                                    // this lane's scales
-    int item, chunk, last;                                      // the next stage: its item, stages of it, its end
+    const unsigned char *src[4];                                // this lane's piece of rows lane / 8 + 4 i, in the next stage
+    const unsigned char *sf;                                    // this lane's scales there
+    int item, left;                                             // the next stage's item, its stages left
+    int bytes;                                                  // of the row from this lane's piece on
+    uint32_t dst[2];                                            // where the pieces go in a stage, i even and odd
 
     // First row of a tile in the expert's weights, from row h of the 16.
-    static __device__ __forceinline__ int64_t row_of(const FewArgs &g, int unit, int h) {
+    static __device__ __forceinline__ int row_of(const FewArgs &g, int unit, int h) {
         return DOWN ? 16 * unit + h : h < 8 ? 8 * unit + h : g.I + 8 * unit + h - 8;
     }
-    __device__ __forceinline__ void begin(const FewArgs &g, int e, int unit, int part, int log_s, int lane) {
-        chunk = (part * g.nc) >> log_s;
-        last = ((part + 1) * g.nc) >> log_s;
-        const int64_t kb = FMT == TOPO_FMT_EIGHT ? g.K : g.K / 2;
+    __device__ __forceinline__ void place(int lane) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            src[i] = g.w + ((int64_t)e * g.rows + row_of(g, unit, (lane >> 3) + 4 * i)) * kb + 16 * (lane & 7);
+        for (int i = 0; i < 2; ++i) dst[i] = ((lane >> 3) + 4 * i) * kRowBytes + piece<FMT>((lane >> 3) + 4 * i, lane & 7);
+    }
+    // Stages from .. to of a unit.
+    __device__ __forceinline__ void begin(const FewArgs &g, int e, int unit, int from, int to, int lane) {
+        left = to - from;
+        const int kb = FMT == TOPO_FMT_EIGHT ? g.K : g.K / 2, at = from * kRowBytes + 16 * (lane & 7);
+        bytes = kb - at;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) src[i] = g.w + ((int64_t)e * g.rows + row_of(g, unit, (lane >> 3) + 4 * i)) * kb + at;
         if (FMT == TOPO_FMT_EIGHT) {
             // the float32 of a 128 x 128 block: of the gate rows and of the up rows
-            const int64_t nb = (g.rows + 127) / 128, at = (int64_t)e * nb + row_of(g, unit, lane & 1 ? 8 : 0) / 128;
-            sf = g.scale + at * g.nc * 4;
+            const int nb = (g.rows + 127) / 128, at = e * nb + row_of(g, unit, lane & 1 ? 8 : 0) / 128;
+            sf = g.scale + ((int64_t)at * g.nc + from) * 4;
         } else {
-            sf = g.scale + ((int64_t)e * g.rows + row_of(g, unit, lane & 15)) * g.pitch;
+            sf = g.scale + ((int64_t)e * g.rows + row_of(g, unit, lane & 15)) * g.pitch + from * (FMT == TOPO_FMT_NV ? 16 : 8);
         }
     }
-    __device__ __forceinline__ void issue(const FewArgs &g, unsigned char *st, int lane) const {
-        const int kb = FMT == TOPO_FMT_EIGHT ? g.K : g.K / 2;
-        const int64_t at = (int64_t)chunk * kRowBytes;
-        const bool in = at + 16 * (lane & 7) < kb;
-        const uint32_t dst = smem_at(st);
+    __device__ __forceinline__ void issue(uint32_t st, int lane) {
+        const int n = bytes > 0 ? 16 : 0;                       // past the row's end: zeros, nothing is read
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int row = (lane >> 3) + 4 * i;
-            copy_or_zero(dst + row * kRowBytes + piece<FMT>(row, lane & 7), in ? src[i] + at : g.w, in);
+            copy_n(st + dst[i & 1] + (i >> 1) * 8 * kRowBytes, src[i], n);
+            src[i] += kRowBytes;
         }
-        const uint32_t ds = dst + 16 * kRowBytes;
+        bytes -= kRowBytes;
+        const uint32_t ds = st + 16 * kRowBytes;
         if (FMT == TOPO_FMT_EIGHT) {
-            if (lane < 2) copy_async<4>(ds + 4 * lane, sf + 4 * chunk);
+            if (lane < 2) copy_async<4>(ds + 4 * lane, sf);
         } else if (lane < 16) {
-            if (FMT == TOPO_FMT_NV) copy_async<16>(ds + 16 * lane, sf + 16 * chunk);
-            else copy_async<8>(ds + 16 * lane, sf + 8 * chunk);
+            if (FMT == TOPO_FMT_NV) copy_async<16>(ds + 16 * lane, sf);
+            else copy_async<8>(ds + 16 * lane, sf);
         }
+        sf += FMT == TOPO_FMT_EIGHT ? 4 : FMT == TOPO_FMT_NV ? 16 : 8;
+        --left;
     }
 };
 
@@ -289,13 +311,28 @@ __device__ __forceinline__ void convert_rows(unsigned char *tok, uint32_t *amax,
     }
 }
 
+__device__ __forceinline__ float gated(float g, float u) { return g / (1.f + expf(-g)) * u; }
+
+// Four of a pair's activations: as the up kernel left them, or from its parts of g and u.
+__device__ __forceinline__ float4 act4(const FewArgs &g, int pair, int c) {
+    if (g.split == 1) return __ldcg(reinterpret_cast<const float4 *>(g.act + (int64_t)pair * g.K) + c);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll
+    for (int p = 0; p < kMaxSplit; ++p) {
+        if (p >= g.split) break;
+        const float4 *src = reinterpret_cast<const float4 *>(g.act + ((int64_t)p * g.T * g.k + pair) * 2 * g.K);
+        const float4 v = __ldcg(src + c), w = __ldcg(src + g.K / 4 + c);
+        a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+        b.x += w.x, b.y += w.y, b.z += w.z, b.w += w.w;
+    }
+    return make_float4(gated(a.x, b.x), gated(a.y, b.y), gated(a.z, b.z), gated(a.w, b.w));
+}
+
 // An activation row as f16 in shared memory, in the same pieces; up to kKeep of them stay
 // in registers between the row's largest magnitude and the conversion, more are read twice.
-template <int FMT>
 __device__ __forceinline__ void load_act(const FewArgs &g, unsigned char *tok, uint32_t *amax, bool on, int row, int pair, int c0,
                                          int dc, int kpad) {
     constexpr int kKeep = 4;
-    const float4 *src = reinterpret_cast<const float4 *>(g.act + (int64_t)pair * g.K);
     const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
     float4 v[kKeep][2];
     const int n = on ? (kpad / 8 - c0 + dc - 1) / dc : 0;
@@ -305,8 +342,8 @@ __device__ __forceinline__ void load_act(const FewArgs &g, unsigned char *tok, u
         for (int i = 0; i < kKeep; ++i) {
             const int c = c0 + (i0 + i) * dc;
             const bool in = i0 + i < n && c < g.K / 8;
-            v[i][0] = in ? __ldcg(src + 2 * c) : z;
-            v[i][1] = in ? __ldcg(src + 2 * c + 1) : z;
+            v[i][0] = in ? act4(g, pair, 2 * c) : z;
+            v[i][1] = in ? act4(g, pair, 2 * c + 1) : z;
         }
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) {
@@ -329,8 +366,8 @@ __device__ __forceinline__ void load_act(const FewArgs &g, unsigned char *tok, u
             const int c = c0 + (i0 + i) * dc;
             if (i0 + i >= n) break;
             if (n > kKeep) {
-                v[i][0] = c < g.K / 8 ? __ldcg(src + 2 * c) : z;
-                v[i][1] = c < g.K / 8 ? __ldcg(src + 2 * c + 1) : z;
+                v[i][0] = c < g.K / 8 ? act4(g, pair, 2 * c) : z;
+                v[i][1] = c < g.K / 8 ? act4(g, pair, 2 * c + 1) : z;
             }
             const float4 a = v[i][0], d = v[i][1];
             *reinterpret_cast<uint4 *>(tok + row * g.bpitch + 16 * c) =
@@ -340,24 +377,87 @@ __device__ __forceinline__ void load_act(const FewArgs &g, unsigned char *tok, u
     }
 }
 
-// The tile's 16 columns of out[T][H], from the experts' outputs y, in slot order.
-__device__ __forceinline__ void combine(const FewArgs &g, const int16_t *pei, const uint8_t *slot, int unit, int lane) {
-    const int row = lane >> 2;
-    if (row >= g.T) return;
+// The pairs sorted by expert, and the groups of at most `cols` pairs of one expert: a group
+// is what the weights' tiles are read for.
+struct Groups {
+    int16_t key[kMaxPairs];                         // expert of each pair; E for one outside [0, E)
+    uint16_t pair[kMaxPairs];                       // sorted: the pair, its token, its expert's first place
+    uint8_t token[kMaxPairs];
+    uint16_t first[kMaxPairs];
+    uint16_t expert[kMaxPairs];                     // of each group
+    uint16_t start[kMaxPairs + 1];                  // its first place
+    int warp_sum[kMaxWarps];
+    int n;                                          // groups
+};
+
+// np <= kMaxPairs; id: this thread's, of pair tid.  Ends with a barrier.
+__device__ __forceinline__ void sort_pairs(const FewArgs &g, Groups &s, int np, int id, bool report) {
+    const int tid = threadIdx.x, lane = tid & 31, threads = g.warps * 32;
+    for (int i = tid; i < np; i += threads) {
+        if (i != tid) id = __ldg(g.ids + i);
+        const bool ok = (unsigned)id < (unsigned)g.E;
+        s.key[i] = (int16_t)(ok ? id : g.E);
+        if (!ok && report) set_error(g.hdr, TOPO_ERANGE);
+    }
+    __syncthreads();
+    for (int i = tid; i < np; i += threads) {
+        const int e = s.key[i];
+        int less = 0, same = 0;
+        for (int q = 0; q < np; ++q) {
+            const int f = s.key[q];
+            less += f < e;
+            same += f == e && q < i;
+        }
+        s.pair[less + same] = (uint16_t)i;
+        s.token[less + same] = (uint8_t)(i / g.k);
+        s.first[less + same] = (uint16_t)less;
+    }
+    __syncthreads();
+    // a group starts at every cols-th pair of an expert; their places by a running count
+    int base = 0, held = 0;
+    for (int i0 = 0; i0 < np; i0 += threads) {
+        const int i = i0 + tid;
+        const bool in = i < np && s.key[s.pair[i < np ? i : 0]] < g.E;
+        const bool opens = in && (i - s.first[i]) % g.cols == 0;
+        const unsigned m = __ballot_sync(0xffffffffu, opens), all = __ballot_sync(0xffffffffu, in);
+        if (lane == 0) s.warp_sum[tid >> 5] = __popc(m) | __popc(all) << 16;
+        __syncthreads();
+        int at = base, total = 0;
+        for (int w = 0; w < g.warps; ++w) {
+            if (w < tid >> 5) at += s.warp_sum[w] & 0xffff;
+            total += s.warp_sum[w];
+        }
+        if (opens) {
+            at += __popc(m & ((1u << lane) - 1));
+            s.expert[at] = (uint16_t)s.key[s.pair[i]];
+            s.start[at] = (uint16_t)i;
+        }
+        base += total & 0xffff;
+        held += total >> 16;
+        if (tid == 0) {
+            s.n = base;
+            s.start[base] = (uint16_t)held;
+        }
+        __syncthreads();
+    }
+}
+
+// Columns 4 q .. 4 q + 3 of out[t], from the pairs' outputs y, in slot order.
+__device__ __forceinline__ void combine(const FewArgs &g, const int16_t *key, int t, int q) {
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float *y = g.mid + (int64_t)row * g.k * g.H + 16 * unit + 4 * (lane & 3);
+    const float *y = g.mid + (int64_t)t * g.k * g.H + 4 * q;
 #pragma unroll 8
     for (int j = 0; j < g.k; ++j) {
-        const int ei = pei[row * g.k + j];
-        const float4 v = ei >= 0 ? __ldcg(reinterpret_cast<const float4 *>(y + (int64_t)slot[ei * kMaxTokens + row] * g.H)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float w = ei >= 0 ? __ldg(g.weights + row * g.k + j) : 0.f;
+        const bool in = key[t * g.k + j] < g.E;
+        const float4 v = in ? __ldcg(reinterpret_cast<const float4 *>(y + (int64_t)j * g.H)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float w = in ? __ldg(g.weights + t * g.k + j) : 0.f;
         o.x += w * v.x;
         o.y += w * v.y;
         o.z += w * v.z;
         o.w += w * v.w;
     }
     const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
-    *reinterpret_cast<uint2 *>(g.out + (int64_t)row * g.H + 16 * unit + 4 * (lane & 3)) =
+    *reinterpret_cast<uint2 *>(g.out + (int64_t)t * g.H + 4 * q) =
         make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
@@ -365,21 +465,21 @@ template <int FMT, bool DOWN, int STAGES>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 k_few(FewArgs g) {
     extern __shared__ __align__(128) unsigned char dyn[];
-    __shared__ uint32_t used[TOPO_GATE_MAX_E / 32];             // experts in use, and how many before each word's
-    __shared__ int before[TOPO_GATE_MAX_E / 32];
-    __shared__ uint16_t experts[kMaxPairs];
-    __shared__ int16_t ids[kMaxPairs], pei[kMaxPairs];          // of each pair: its expert, its place in `experts`
-    __shared__ __align__(16) uint8_t slot[kMaxPairs * kMaxTokens];   // a token's lowest slot that names an expert, or 255
+    __shared__ Groups grp;
     __shared__ uint32_t amax[kMaxRows];                         // of the token rows
-    __shared__ int pair_of[kMaxRows];                           // down: the pair of each token row
-    __shared__ int16_t seg_row[kMaxRows], seg_n[kMaxRows];      // down: the rows of each expert of a batch
-    __shared__ int n_used, batch_end, n_rows, n_done;
+    __shared__ int n_done;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = g.warps * 32;
+    constexpr int kStep = FMT == TOPO_FMT_EIGHT ? 128 : 256;    // values of a stage
     unsigned char *ring = dyn + warp * STAGES * kStageBytes;
+    const uint32_t ring_at = smem_at(ring);
     unsigned char *tok = dyn + g.warps * STAGES * kStageBytes;
     float4 *parts = reinterpret_cast<float4 *>(tok + g.cap_rows * g.bpitch);   // [cap_parts][32]
     const int np = g.T * g.k;
-    const int kpad = FMT == TOPO_FMT_EIGHT ? (g.K + 127) & ~127 : (g.K + 255) & ~255;
+    // this CTA's part of the contraction, in stages, and its place among the CTAs of that part
+    const int sp = DOWN ? 0 : blockIdx.x % g.split, splits = DOWN ? 1 : g.split;
+    const int cs = sp * g.nc / splits, ce = (sp + 1) * g.nc / splits;
+    const int cta = blockIdx.x / splits, ctas = gridDim.x / splits;
+    const int kpad = (ce - cs) * kStep;
 
     // Up: everything before this call is done and seen from here on, and the down kernel,
     // which may start now, can rely on that for the ids and the weights.  The token rows are
@@ -388,91 +488,54 @@ k_few(FewArgs g) {
         pdl_wait();
         pdl_trigger();
     }
-    int id = tid < np ? __ldg(g.ids + tid) : -1;
+    const int id = tid < np ? __ldg(g.ids + tid) : -1;
     if (!DOWN) {
-        for (int row = 0; row < g.T; ++row)
-            for (int c = tid; c < kpad / 8; c += threads)
-                copy_or_zero(smem_at(tok + row * g.bpitch + 16 * c), c < g.K / 8 ? g.x + (int64_t)row * g.K + 8 * c : g.x, c < g.K / 8);
+        for (int row = warp; row < g.T; row += g.warps)
+            for (int c = lane; c < kpad / 8; c += 32) {
+                const bool in = cs * kStep + 8 * c < g.K;
+                copy_n(smem_at(tok + row * g.bpitch + 16 * c), in ? g.x + (int64_t)row * g.K + cs * kStep + 8 * c : g.x, in ? 16 : 0);
+            }
         copies_end();
         if (blockIdx.x == 0)
             for (int i = tid; i < g.H / 16; i += threads) g.count[i] = 0;
     }
-    for (int i = tid; i < TOPO_GATE_MAX_E / 32; i += threads) used[i] = 0;
-    for (int i = tid; i < np * kMaxTokens / 4; i += threads) reinterpret_cast<uint32_t *>(slot)[i] = 0xffffffffu;
-    __syncthreads();
-    for (int i = tid; i < np; i += threads) {
-        if (i != tid) id = __ldg(g.ids + i);
-        const bool ok = (unsigned)id < (unsigned)g.E;
-        ids[i] = ok ? (int16_t)id : (int16_t)-1;
-        if (ok) atomicOr(&used[id >> 5], 1u << (id & 31));
-        else if (!DOWN && blockIdx.x == 0) set_error(g.hdr, TOPO_ERANGE);
-    }
-    __syncthreads();
-    if (warp == 0) {                                            // the experts in use, in ascending order
-        uint32_t w = used[lane];
-        const int n = __popc(w);
-        int at = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, at, o);
-            if (lane >= o) at += u;
-        }
-        if (lane == 31) n_used = at;
-        at -= n;
-        before[lane] = at;
-        for (; w; w &= w - 1) experts[at++] = (uint16_t)(32 * lane + __ffs(w) - 1);
-    }
-    __syncthreads();
-    for (int i = tid; i < np; i += threads) {
-        const int e = ids[i], t = i / g.k, j = i - t * g.k;
-        const int ei = e < 0 ? -1 : before[e >> 5] + __popc(used[e >> 5] & ((1u << (e & 31)) - 1));
-        pei[i] = (int16_t)ei;
-        int f = 0;
-        while (ids[t * g.k + f] != e) ++f;
-        if (e >= 0 && f == j) slot[ei * kMaxTokens + t] = (uint8_t)j;
-    }
-    const int total = n_used * g.units;                         // at most 512 * 4096
+    sort_pairs(g, grp, np, id, !DOWN && blockIdx.x == 0);
+    const int ng = grp.n, total = ng * g.units;                 // at most 512 * 4096
     if (DOWN && total == 0) {                                   // no expert at all
         pdl_wait();
         for (int i = blockIdx.x * threads + tid; i < g.T * g.H / 2; i += gridDim.x * threads) reinterpret_cast<uint32_t *>(g.out)[i] = 0;
         return;
     }
-    const int begin = (int)((int64_t)total * blockIdx.x / gridDim.x), hi = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
-    // Batches of items: up: all of them; down: of as many experts as there is room for the
-    // activations of their tokens.
+    // Items: units of groups, group by group; where a CTA has room for all pairs' activations
+    // unit by unit, so that few CTAs meet in a unit's sums.
+    const bool by_unit = DOWN && grp.start[ng] <= g.cap_rows;
+    const int begin = (int)((int64_t)total * cta / ctas), hi = cta < ctas ? (int)((int64_t)total * (cta + 1) / ctas) : begin;
+    auto place = [&](int gi, int &group, int &unit) {
+        const int q = gi / (by_unit ? ng : g.units), r = gi - q * (by_unit ? ng : g.units);
+        group = by_unit ? r : q;
+        unit = by_unit ? q : r;
+    };
+    // Batches of items: up: all of them; down: of as many groups as there is room for the
+    // activations of their pairs.
     for (int lo = begin; lo < hi;) {
-        const int ei0 = lo / g.units;
-        int end = hi;
+        int end = hi, row0 = 0, rows = g.T;
         if (DOWN) {
-            __syncthreads();                                    // `slot`; the batch before is through with its rows
-            if (warp == 0) {
-                int at = lo, rows = 0;
-                for (int i = 0; i < kMaxRows && at < hi; ++i) {
-                    const unsigned m = __ballot_sync(0xffffffffu, lane < g.T && slot[(ei0 + i) * kMaxTokens + (lane & (kMaxTokens - 1))] != 255);
-                    const int n = __popc(m);
-                    if (rows + n > g.cap_rows) break;
-                    if (m >> lane & 1u) pair_of[rows + __popc(m & ((1u << lane) - 1))] = lane * g.k + slot[(ei0 + i) * kMaxTokens + lane];
-                    if (lane == 0) {
-                        seg_row[i] = (int16_t)rows;
-                        seg_n[i] = (int16_t)n;
-                    }
-                    rows += n;
-                    at = min(hi, (ei0 + i + 1) * g.units);
-                }
-                if (lane == 0) {
-                    batch_end = at;
-                    n_rows = rows;
-                }
+            const int g0 = by_unit ? 0 : lo / g.units;
+            int g1 = by_unit ? ng : g0 + 1;
+            row0 = grp.start[g0];
+            if (!by_unit) {
+                while (g1 * g.units < hi && grp.start[g1 + 1] - row0 <= g.cap_rows) ++g1;
+                end = min(hi, g1 * g.units);
             }
-            __syncthreads();
-            end = batch_end;
+            rows = grp.start[g1] - row0;
+            if (lo != begin) __syncthreads();                   // the batch before is through with its rows
         }
         // A unit's contraction may be split over 2^log_s warps, so that the warps end together
-        const int nu = end - lo;
+        const int nu = end - lo, nc = ce - cs;
         int log_s = 0;
         for (int s = 1, best = (nu + g.warps - 1) / g.warps * 16; s <= 4; ++s) {
             const int cost = ((nu << s) + g.warps - 1) / g.warps * (16 >> s);
-            if (nu << s <= g.cap_parts && 1 << s <= g.nc && cost < best) {
+            if (nu << s <= g.cap_parts && 1 << s <= nc && cost < best) {
                 best = cost;
                 log_s = s;
             }
@@ -480,15 +543,18 @@ k_few(FewArgs g) {
         const int nitem = nu << log_s;
         Feed<FMT, DOWN> feed;
         feed.item = warp;
+        feed.place(lane);
         int put = 0, get = 0;
         auto open = [&]() {
-            const int gi = lo + (feed.item >> log_s), ei = gi / g.units;
-            feed.begin(g, experts[ei], gi - ei * g.units, feed.item & ((1 << log_s) - 1), log_s, lane);
+            int group, unit;
+            place(lo + (feed.item >> log_s), group, unit);
+            const int part = feed.item & ((1 << log_s) - 1);
+            feed.begin(g, grp.expert[group], unit, cs + (part * nc >> log_s), cs + ((part + 1) * nc >> log_s), lane);
         };
         auto next = [&]() {
             if (feed.item < nitem) {
-                feed.issue(g, ring + put * kStageBytes, lane);
-                if (++feed.chunk == feed.last) {
+                feed.issue(ring_at + put * kStageBytes, lane);
+                if (feed.left == 0) {
                     feed.item += g.warps;
                     if (feed.item < nitem) open();
                 }
@@ -510,71 +576,75 @@ k_few(FewArgs g) {
         if (!DOWN) copies_wait<STAGES - 1>();                   // the token rows, all but the weights
         __syncthreads();
         {
-            const int rows = DOWN ? n_rows : g.T;
             const int wpr = max(1, g.warps / rows);             // warps to a row
             const int dc = 32 * wpr;
             for (int r0 = 0; r0 < rows; r0 += g.warps) {        // once, but for few warps
                 const int row = r0 + warp / wpr, c0 = warp % wpr * 32 + lane;
                 const bool on = row < rows && warp < wpr * rows;
-                if (DOWN) load_act<FMT>(g, tok, amax, on, row, on ? pair_of[row] : 0, c0, dc, kpad);
+                if (DOWN) load_act(g, tok, amax, on, row, on ? grp.pair[row0 + row] : 0, c0, dc, kpad);
                 else convert_rows(tok + row * g.bpitch, &amax[on ? row : 0], on, c0, dc, kpad);
             }
         }
         __syncthreads();
 
         // one unit's sums, whole: lane l holds rows l / 4 and l / 4 + 8 of columns 2 (l % 4) and the next
-        auto finish = [&](int ei, int unit, const float (&acc)[4], float r0, float r1) {
-            const int r = lane >> 2, t = lane & 3;
-            const int row0 = DOWN ? seg_row[ei - ei0] : 0, ncol = DOWN ? seg_n[ei - ei0] : g.T;
+        auto finish = [&](int group, int unit, const float (&acc)[4], float r0, float r1) {
+            const int r = lane >> 2, at = grp.start[group] + 2 * (lane & 3);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int c = 2 * t + h;
-                if (c >= ncol) continue;
-                const float s = pow2(row_exp(amax[row0 + c]));
+                if (at + h >= grp.start[group + 1]) continue;
+                const int pair = grp.pair[at + h];
+                const float s = pow2(row_exp(amax[DOWN ? at + h - row0 : grp.token[at + h]]));
                 const float v0 = acc[h] * r0 * s, v1 = acc[2 + h] * r1 * s;
                 if (DOWN) {
-                    float *y = g.mid + (int64_t)pair_of[row0 + c] * g.H + 16 * unit;
+                    float *y = g.mid + (int64_t)pair * g.H + 16 * unit;
                     __stcg(y + r, v0);
                     __stcg(y + r + 8, v1);
+                } else if (g.split == 1) {
+                    __stcg(g.mid + (int64_t)pair * g.I + 8 * unit + r, gated(v0, v1));
                 } else {
-                    const int j = slot[ei * kMaxTokens + c];
-                    if (j != 255) __stcg(g.mid + ((int64_t)c * g.k + j) * g.I + 8 * unit + r, v0 / (1.f + expf(-v0)) * v1);
+                    float *p = g.mid + ((int64_t)sp * np + pair) * 2 * g.I + 8 * unit + r;
+                    __stcg(p, v0);
+                    __stcg(p + g.I, v1);
                 }
             }
         };
-        auto row_scales = [&](int ei, int unit, float &r0, float &r1) {
+        auto row_scales = [&](int group, int unit, float &r0, float &r1) {
             r0 = r1 = 1.f;
             if (FMT == TOPO_FMT_NV) {
-                const float *rs = g.row_scale + (int64_t)experts[ei] * g.rows;
+                const float *rs = g.row_scale + (int64_t)grp.expert[group] * g.rows;
                 r0 = __ldg(rs + Feed<FMT, DOWN>::row_of(g, unit, lane >> 2));
                 r1 = __ldg(rs + Feed<FMT, DOWN>::row_of(g, unit, (lane >> 2) + 8));
             }
         };
 
         for (int item = warp; item < nitem; item += g.warps) {
-            const int gi = lo + (item >> log_s), ei = gi / g.units, unit = gi - ei * g.units, part = item & ((1 << log_s) - 1);
+            int group, unit;
+            place(lo + (item >> log_s), group, unit);
+            const int part = item & ((1 << log_s) - 1);
             // this lane's token column; past the last: any row
-            const int row = DOWN ? seg_row[ei - ei0] + min(lane >> 2, seg_n[ei - ei0] - 1) : min(lane >> 2, g.T - 1);
-            const unsigned char *col = tok + row * g.bpitch;
+            const int at = min(grp.start[group] + (lane >> 2), grp.start[group + 1] - 1);
+            const unsigned char *col = tok + (DOWN ? at - row0 : grp.token[at]) * g.bpitch;
             float r0, r1, acc[4] = {0.f, 0.f, 0.f, 0.f};
-            if (log_s == 0) row_scales(ei, unit, r0, r1);
-            const int c1 = ((part + 1) * g.nc) >> log_s;
-            for (int c = (part * g.nc) >> log_s; c < c1; ++c) {
+            if (log_s == 0) row_scales(group, unit, r0, r1);
+            const int c1 = (part + 1) * nc >> log_s;
+            for (int c = part * nc >> log_s; c < c1; ++c) {
                 copies_wait<STAGES - 2>();
                 __syncwarp();                                   // every lane's copies are in, its reads of the stage before done
                 next();
-                stage_product<FMT>(acc, ring + get * kStageBytes, col + c * (FMT == TOPO_FMT_EIGHT ? 256 : 512), lane);
+                stage_product<FMT>(acc, ring + get * kStageBytes, col + c * 2 * kStep, lane);
                 if (++get == STAGES) get = 0;
             }
-            if (log_s == 0) finish(ei, unit, acc, r0, r1);
+            if (log_s == 0) finish(group, unit, acc, r0, r1);
             else parts[item * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
         }
         if (log_s > 0) {
             __syncthreads();
             for (int u = warp; u < nu; u += g.warps) {
-                const int ei = (lo + u) / g.units, unit = lo + u - ei * g.units;
+                int group, unit;
+                place(lo + u, group, unit);
                 float r0, r1;
-                row_scales(ei, unit, r0, r1);
+                row_scales(group, unit, r0, r1);
                 float4 s = parts[(u << log_s) * 32 + lane];
                 for (int p = 1; p < 1 << log_s; ++p) {
                     const float4 v = parts[((u << log_s) + p) * 32 + lane];
@@ -584,7 +654,7 @@ k_few(FewArgs g) {
                     s.w += v.w;
                 }
                 const float acc[4] = {s.x, s.y, s.z, s.w};
-                finish(ei, unit, acc, r0, r1);
+                finish(group, unit, acc, r0, r1);
             }
         }
         lo = end;
@@ -592,25 +662,32 @@ k_few(FewArgs g) {
     copies_wait<0>();
     if (!DOWN) return;
     if (begin == hi) pdl_wait();                                // as the kernels that follow rely on it
-    // Whoever brings a tile's last expert adds the tile's columns over the slots.  The fence
-    // comes once, after all items: it waits for the warp's copies as well.
+    // Whoever brings a unit's last group adds its columns over the slots.  The fence comes
+    // once, after all items: it waits for the warp's copies as well.
     int *list = reinterpret_cast<int *>(dyn);
     if (tid == 0) n_done = 0;
     __syncthreads();
     __threadfence();
-    for (int i = begin + tid; i < hi; i += threads)
-        if (atomicAdd(g.count + i % g.units, 1) == n_used - 1) list[atomicAdd(&n_done, 1)] = i % g.units;
+    for (int i = begin + tid; i < hi; i += threads) {
+        int group, unit;
+        place(i, group, unit);
+        if (atomicAdd(g.count + unit, 1) == ng - 1) list[atomicAdd(&n_done, 1)] = unit;
+    }
     __syncthreads();
     __threadfence();
-    for (int i = warp; i < n_done; i += g.warps) combine(g, pei, slot, list[i], lane);
+    const int tasks = n_done * g.T * 4;
+    for (int i = tid; i < tasks; i += threads) {
+        const int u = i / (4 * g.T), t = (i >> 2) - u * g.T;
+        combine(g, grp.key, t, 4 * list[u] + (i & 3));
+    }
 }
 
 // ------------------------------------------------------------------------ host
-constexpr size_t kFewSmem = 218 * 1024;           // dynamic; the tables take 8 KB
+constexpr size_t kFewSmem = 218 * 1024;           // dynamic; the tables take 7 KB
+constexpr int kLeastParts = 16 * 512;
 
-int token_pitch(int K, int fmt) {                 // 16 or 64 bytes past a multiple of 128 (the lanes' bank pattern)
-    return fmt == TOPO_FMT_EIGHT ? 2 * ((K + 127) & ~127) + 16 : 2 * ((K + 255) & ~255) + 64;
-}
+// A token row's bytes: 16 or 64 past a multiple of 128 (the lanes' bank pattern).
+int token_pitch(int values, int fmt) { return 2 * values + (fmt == TOPO_FMT_EIGHT ? 16 : 64); }
 
 template <int FMT, bool DOWN>
 cudaError_t run_few(FewArgs g, cudaStream_t st) {
@@ -619,10 +696,14 @@ cudaError_t run_few(FewArgs g, cudaStream_t st) {
     };
     int stages = 4;
     g.warps = kMaxWarps;
-    if (room(g.warps, stages, g.T) < 16 * 512) stages = 3;
-    while (g.warps > 8 && room(g.warps, stages, g.T) < 16 * 512) g.warps -= 2;
-    g.cap_rows = g.T;
-    while (DOWN && g.cap_rows < kMaxRows && room(g.warps, stages, g.cap_rows + 1) >= 16 * 512) ++g.cap_rows;
+    g.cols = kCols;
+    if (DOWN)                                                    // rows of a very wide layer
+        while (g.cols > 1 && room(8, 3, g.cols) < kLeastParts) --g.cols;
+    const int least = DOWN ? g.cols : g.T;                       // rows: of a group, or all tokens
+    if (room(g.warps, stages, least) < kLeastParts) stages = 3;
+    while (g.warps > 8 && room(g.warps, stages, least) < kLeastParts) g.warps -= 2;
+    g.cap_rows = least;
+    while (DOWN && g.cap_rows < kMaxRows && room(g.warps, stages, g.cap_rows + 1) >= kLeastParts) ++g.cap_rows;
     if (room(g.warps, stages, g.cap_rows) < 0) return cudaErrorInvalidValue;
     g.cap_parts = (int)std::min<int64_t>(kMaxParts, room(g.warps, stages, g.cap_rows) / 512);
     const size_t smem = (size_t)g.warps * stages * kStageBytes + (size_t)g.cap_rows * g.bpitch + (size_t)g.cap_parts * 512;
@@ -640,17 +721,36 @@ cudaError_t run_both(FewArgs up, FewArgs down, cudaStream_t st) {
 
 }  // namespace
 
+// Tokens of a launch, and the parts of the up contraction: as few as leave 16 warps their
+// rings of 4 stages beside the token rows.  Wider rows take fewer tokens.
+static int few_tokens(int T, int k, int H, int fmt, int *split) {
+    const int step = fmt == TOPO_FMT_EIGHT ? 128 : 256;
+    const int64_t room = kFewSmem - (int64_t)kMaxWarps * 4 * kStageBytes - kLeastParts;
+    const int nc = (H + step - 1) / step;
+    for (int n = std::min(std::min(T, kMaxPairs / k), kMaxRows); n > 1; --n)
+        for (*split = 1; *split <= kMaxSplit && *split <= nc; *split *= 2)
+            if (n * (int64_t)token_pitch((nc + *split - 1) / *split * step, fmt) <= room) return n;
+    *split = 1;
+    return 1;
+}
+
 size_t few_workspace(int T, int k, int H, int I) {
-    return sizeof(WsHeader) + kCounters * sizeof(int32_t) + (size_t)std::min(T, kMaxTokens) * k * ((size_t)H + I) * sizeof(float);
+    size_t most = 0;
+    for (int fmt : {TOPO_FMT_EIGHT, TOPO_FMT_MX}) {
+        int split;
+        const size_t pairs = (size_t)few_tokens(T, k, H, fmt, &split) * k;
+        most = std::max(most, pairs * ((size_t)H + (split == 1 ? 1 : 2 * (size_t)split) * I));
+    }
+    return sizeof(WsHeader) + kCounters * sizeof(int32_t) + most * sizeof(float);
 }
 
 cudaError_t launch_expert_few(int T, int E, int k, int H, int I, int fmt, const uint16_t *x, const int32_t *ids,
                               const float *weights, const uint8_t *up, const void *up_scale, const float *up_row,
                               const uint8_t *down, const void *down_scale, const float *down_row, uint16_t *out, void *ws,
                               cudaStream_t st) {
-    // tokens of a launch: as many as leave room for the rings of 8 warps
-    const int wide = token_pitch(std::max(H, I), fmt);
-    const int per = std::min(kMaxTokens, (int)((kFewSmem - 8 * (3 * kStageBytes) - 16 * 512) / wide));
+    int split = 1;
+    const int per = few_tokens(T, k, H, fmt, &split);
+    const int step = fmt == TOPO_FMT_EIGHT ? 128 : 256;          // values of a stage
     for (int t0 = 0; t0 < T; t0 += per) {
         FewArgs a = {};
         a.T = std::min(per, T - t0);
@@ -658,13 +758,14 @@ cudaError_t launch_expert_few(int T, int E, int k, int H, int I, int fmt, const 
         a.k = k;
         a.H = H;
         a.I = I;
+        a.split = split;
         a.ids = ids + (int64_t)t0 * k;
         a.weights = weights + (int64_t)t0 * k;
         a.hdr = ws_at<WsHeader>(ws, 0);
         a.count = ws_at<int32_t>(ws, sizeof(WsHeader));
-        float *act = ws_at<float>(ws, sizeof(WsHeader) + kCounters * sizeof(int32_t));
+        float *y = ws_at<float>(ws, sizeof(WsHeader) + kCounters * sizeof(int32_t));
+        float *act = y + (int64_t)per * k * H;
         FewArgs d = a;
-        const int step = fmt == TOPO_FMT_EIGHT ? 128 : 256;      // values of a stage
         a.x = x + (int64_t)t0 * H;
         a.w = up;
         a.scale = static_cast<const uint8_t *>(up_scale);
@@ -677,7 +778,7 @@ cudaError_t launch_expert_few(int T, int E, int k, int H, int I, int fmt, const 
         d.w = down;
         d.scale = static_cast<const uint8_t *>(down_scale);
         d.row_scale = down_row;
-        d.mid = act + (int64_t)std::min(T, kMaxTokens) * k * I;
+        d.mid = y;
         d.out = out + (int64_t)t0 * H;
         d.K = I;
         d.rows = H;
@@ -685,8 +786,9 @@ cudaError_t launch_expert_few(int T, int E, int k, int H, int I, int fmt, const 
         for (FewArgs *p : {&a, &d}) {
             p->nc = (p->K + step - 1) / step;
             p->pitch = fmt == TOPO_FMT_EIGHT ? 0 : micro_pitch(p->K, fmt);
-            p->bpitch = token_pitch(p->K, fmt);
         }
+        a.bpitch = token_pitch((a.nc + split - 1) / split * step, fmt);
+        d.bpitch = token_pitch(d.nc * step, fmt);
         const cudaError_t e = fmt == TOPO_FMT_EIGHT ? run_both<TOPO_FMT_EIGHT>(a, d, st)
                               : fmt == TOPO_FMT_MX ? run_both<TOPO_FMT_MX>(a, d, st) : run_both<TOPO_FMT_NV>(a, d, st);
         if (e != cudaSuccess) return e;
