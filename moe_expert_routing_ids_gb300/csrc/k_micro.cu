@@ -11,9 +11,9 @@
 // to even: no value is clipped.  A block that holds a NaN or an infinity gets the
 // scale NaN.  Division by a power of two is exact.  With an e4m3 scale of 4 bits, a bf16
 // value's quotient is a border between two values of e2m1 (at most 3 bits) or at least
-// 2^-8 of it away: the product with the scale's inverse, within 2^-23, rounded to f16 is
-// on the right side, or on the border.  The activation's quotients, of float32 values,
-// are corrected by their residuals (Markstein).
+// 2^-8 of it away: the product with the scale's inverse, within 2^-22, rounded to f16 is
+// on the right side, or on the border.  The activation's quotients, of float32 values, are
+// left as they are, within 2^-22.
 //
 //   k_micro_rows     rows as they are, dispatch rows (by position, or token row t to the
 //                    k layout positions of its pairs), or the gated activation
@@ -103,42 +103,49 @@ __device__ __forceinline__ uint32_t finite_bits(const float (&v)[16]) {
     return m;
 }
 
-// v = silu(v) * u in float32: the reciprocal of 1 + exp(-v) from the approximate one by a
-// step of Newton's iteration, within 2^-23 of itself, where the divisors are below 2^120;
-// past that (v below -83, or not finite) the division.  Against dividing everywhere, as
-// topo_swiglu_quantize does, bits may be the neighbours'.
-__device__ __forceinline__ void gated(float (&v)[16], const float (&u)[16]) {
-    float top = 0.f, w[16];
+// v = silu(v) * u in float32.  exp(-v) as a power of two of the rounded product t =
+// -v log2(e), times 1 + what the rounding left out; the reciprocal of 1 + exp(-v) by one
+// step of Newton's iteration from the approximate one: within 7 * 2^-24 of the value, where
+// topo_swiglu_quantize calls expf and divides (25 instructions a value; this, 15).  low: some
+// v may be below -83, where 1 + exp(-v) nears the end of float32's range: expf and division.
+__device__ __forceinline__ void gated(float (&v)[16], const float (&u)[16], bool low) {
+    if (low) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __fdiv_rn(v[i], 1.f + expf(-v[i])) * u[i];
+        return;
+    }
+    constexpr float kLog2e = 1.44269504088896f, kLog2eLo = 1.925963033500e-8f, kLn2 = 0.69314718f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const float d = 1.f + expf(-v[i]);
-        float r;
+        const float t = -kLog2e * v[i], left = __fmaf_rn(-kLog2eLo, v[i], __fmaf_rn(-kLog2e, v[i], -t));
+        float e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+        const float d = 1.f + __fmaf_rn(e * kLn2, left, e);
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
         r = __fmaf_rn(__fmaf_rn(-d, r, 1.f), r, r);
-        top = fmaxf(top, d);
-        w[i] = v[i] * r * u[i];
+        v[i] = v[i] * r * u[i];
     }
-    if (!(top < 0x1p120f)) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = __fdiv_rn(v[i], 1.f + expf(-v[i])) * u[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = w[i];
 }
 
 // A lane's groups of a row: kGroups of them, 32 apart, at a time, kept as they are stored
 // (the activation's as float32).
-template <int SRC>
-constexpr int kGroups = SRC == kSwiglu ? 2 : 4;
+// Measured in groups, CTAs to an SM: activation of 131072 x 2048 to MX 2, 2: 257 us, 2, 3:
+// 236, 1, 4: 249, 1, 5: 217; to NV 2, 2: 302, 2, 3: 257, 1, 5: 295; rows of 131072 x 7168 to
+// NV 4, 3: 429, 4, 4: 399, 5, 3: 458, 2, 5 (of a build before): 501 for 434.
+template <int SRC, bool NV>
+constexpr int kGroups = SRC != kSwiglu ? 4 : NV ? 2 : 1;
+template <int SRC, bool NV>
+constexpr int kCtas = SRC != kSwiglu ? 4 : NV ? 3 : 5;
 
-template <int SRC>
+template <int SRC, bool NV>
 struct Groups {
-    uint4 a[kGroups<SRC>][2];
+    static constexpr int kN = kGroups<SRC, NV>;
+    uint4 a[kN][2];
 
     __device__ __forceinline__ void load(const MicroArgs &g, int64_t from, int c0) {
         const uint4 *src = g.x + from * (2 * (int64_t)g.nv);
 #pragma unroll
-        for (int j = 0; j < kGroups<SRC>; ++j)
+        for (int j = 0; j < kN; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) a[j][i] = c0 + 32 * j < g.nv ? __ldg(src + 2 * (c0 + 32 * j) + i) : make_uint4(0, 0, 0, 0);
     }
@@ -152,26 +159,31 @@ struct Groups {
         return max(m << 16, m & 0xffff0000u);
     }
 };
-template <>
-struct Groups<kSwiglu> {
-    float f[kGroups<kSwiglu>][16];
+template <bool NV>
+struct Groups<kSwiglu, NV> {
+    static constexpr int kN = kGroups<kSwiglu, NV>;
+    float f[kN][16];
 
     __device__ __forceinline__ void load(const MicroArgs &g, int64_t from, int c0) {
         const uint4 *src = g.x + from * (4 * (int64_t)g.nv);
-        uint4 a[kGroups<kSwiglu>][4];
+        uint4 a[kN][4];
 #pragma unroll
-        for (int j = 0; j < kGroups<kSwiglu>; ++j)
+        for (int j = 0; j < kN; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int c = c0 + 32 * j;
                 a[j][i] = c < g.nv ? __ldg(src + 2 * (i < 2 ? c : g.nv + c) + (i & 1)) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-        for (int j = 0; j < kGroups<kSwiglu>; ++j) {
+        for (int j = 0; j < kN; ++j) {
+            const uint32_t w[8] = {a[j][0].x, a[j][0].y, a[j][0].z, a[j][0].w, a[j][1].x, a[j][1].y, a[j][1].z, a[j][1].w};
+            uint32_t most = 0;                                  // as 16-bit words: the most negative value
+#pragma unroll
+            for (int i = 0; i < 8; ++i) most = __vmaxu2(most, w[i]);
             float u[16];
             unpack16(a[j][0], a[j][1], f[j]);
             unpack16(a[j][2], a[j][3], u);
-            gated(f[j], u);
+            gated(f[j], u, max(most & 0xffffu, most >> 16) > 0xc2a6u);   // -83
         }
     }
     __device__ __forceinline__ void get(int j, float (&v)[16]) const {
@@ -186,16 +198,13 @@ struct Groups<kSwiglu> {
     }
 };
 
-template <int SRC, bool NV>
-constexpr int kCtas = SRC == kSwiglu ? 2 : NV ? 3 : 4;      // to an SM
-
 // 2^log_w warps take a row, each kGroups * 32 groups of 16 values side by side; a row that
 // is longer than eight warps' goes round (NV: and is read twice, once for its largest
 // magnitude).  All of a lane's loads are on their way before the first is used.
 template <int SRC, bool NV>
 __global__ void __launch_bounds__(256, kCtas<SRC, NV>)
 k_micro_rows(MicroArgs g) {
-    constexpr int kPer = kGroups<SRC> * 32;
+    constexpr int kPer = kGroups<SRC, NV> * 32;
     __shared__ uint32_t wmax[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = warp & ((1 << g.log_w) - 1);
@@ -227,9 +236,9 @@ k_micro_rows(MicroArgs g) {
     if (!live) from = 0;
     const int first = part * kPer + lane, span = kPer << g.log_w;
     const int nv = live ? (g.nv + 31) & ~31 : 0;                 // whole warps of groups
-    Groups<SRC> in_regs;
+    Groups<SRC, NV> in_regs;
     float v[16];
-    uint32_t am[kGroups<SRC>];                                   // the groups' largest magnitudes
+    uint32_t am[kGroups<SRC, NV>];                                   // the groups' largest magnitudes
     int n = 0;                                                   // NV: exponent of the row's scale
     if (NV) {
         // the whole row's largest finite magnitude first
@@ -237,7 +246,7 @@ k_micro_rows(MicroArgs g) {
         for (int c0 = first; c0 - lane < nv; c0 += span) {
             in_regs.load(g, from, c0);
 #pragma unroll
-            for (int j = 0; j < kGroups<SRC>; ++j) {
+            for (int j = 0; j < kGroups<SRC, NV>; ++j) {
                 am[j] = in_regs.amax(j);
                 uint32_t a = am[j];
                 if (a >= kInf) {
@@ -266,33 +275,36 @@ k_micro_rows(MicroArgs g) {
         if (!NV || g.nv > span) {
             in_regs.load(g, from, c0);
 #pragma unroll
-            for (int j = 0; j < kGroups<SRC>; ++j) am[j] = in_regs.amax(j);
+            for (int j = 0; j < kGroups<SRC, NV>; ++j) am[j] = in_regs.amax(j);
         }
 #pragma unroll
-        for (int j = 0; j < kGroups<SRC>; ++j) {
+        for (int j = 0; j < kGroups<SRC, NV>; ++j) {
             const int c = c0 + 32 * j;
             if (c - lane >= nv) break;                           // whole warp
             const bool in = c < g.nv;
             in_regs.get(j, v);
             uint32_t m = am[j], sb;
             if (NV) {
-                const float t = __uint_as_float(m) * pow2(-n);   // at most 2688
-                uint16_t b;
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(0.f), "f"(t * (1.f / 6.f)));
-                sb = b;
-                float s = e4m3_value(sb);
-                if (6.f * s < t) s = e4m3_value(++sb);           // rounded down: the next one
+                // t / 6, at most 448, rounded up to e4m3 (the quotient's last bits are cut, so that
+                // 6 times a scale gives the scale): a mantissa of 3 bits, or a multiple of 2^-9
+                const float t = __fmul_rz(__uint_as_float(m) * pow2(-n), 1.f / 6.f);
+                const uint32_t up = __float_as_uint(t) + 0xfffffu, low = __float_as_uint(__fadd_ru(t, 0x1p14f));
+                float s = __uint_as_float(up & 0xfff00000u);
+                sb = (up >> 20) - 960;
+                if (t < 0x1p-6f) {
+                    s = fmaxf(__uint_as_float(low) - 0x1p14f, 0x1p-9f);   // t may underflow
+                    sb = max(low & 0xffu, 1u);
+                }
                 if (m == 0u) s = 1.f, sb = 0x38u;
                 if (n < -112) {                                  // 1 / (s g) might be past float32's range
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] *= 0x1p16f;
                 }
-                const float sg = s * pow2(n < -112 ? n + 16 : n), si = __frcp_rn(sg);
+                const float sg = s * pow2(n < -112 ? n + 16 : n);
+                float si;
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(si) : "f"(sg));
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float q0 = v[i] * si;
-                    v[i] = SRC == kSwiglu ? __fmaf_rn(__fmaf_rn(-q0, sg, v[i]), si, q0) : q0;
-                }
+                for (int i = 0; i < 16; ++i) v[i] *= si;
                 if (m >= kInf) sb = 0x7fu;
             } else {
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -372,7 +384,7 @@ template <int SRC, bool NV>
 cudaError_t run_rows(MicroArgs a, cudaStream_t st) {
     if (a.rows == 0) return cudaSuccess;
     a.log_w = 0;
-    while (a.log_w < 3 && (kGroups<SRC> * 32) << a.log_w < a.nv) ++a.log_w;
+    while (a.log_w < 3 && (kGroups<SRC, NV> * 32) << a.log_w < a.nv) ++a.log_w;
     const int64_t warps = a.rows << a.log_w;
     return launch_pdl(k_micro_rows<SRC, NV>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, a);
 }

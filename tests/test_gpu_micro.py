@@ -114,7 +114,12 @@ def hard_rows(rng, rows, C):
         v[8] = -2.0 ** -126
         v[9, :16] *= 2.0 ** -12                               # a block far below its row's largest
         v[10, 1:] = 0.0
-    return v
+    if rows > 16:
+        v[11, 0], v[11, 16:32] = 3e38, 2.0 ** -130            # a quotient that underflows
+        v[12, :16] = 2.0 ** -115 * 3                          # the quotients' own scaling
+        v[13] = np.ldexp(v[14] / np.abs(v[14]).max(), -118)
+    with np.errstate(over="ignore", invalid="ignore"):
+        return bf16(v).double().numpy()                       # the oracle's values are those that the call gets
 
 
 def buffers(rows, C, fmt, dev):
