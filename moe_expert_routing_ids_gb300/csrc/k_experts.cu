@@ -319,7 +319,6 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 // gradient: the scales of the tile's rows and columns, whole pieces of 16
                 const uint32_t ms = MODE == kGrad ? 4u * (uint32_t)q.mlim : 0u, ns = MODE == kGrad ? 4u * (uint32_t)q.nlim : 0u;
                 bytes += ms + ns;
-                if (kMicro<MODE>) bytes += (uint32_t)(1 + boxes) * kSfBytes;
                 for (int kb = 0; kb < q.nkb; ++kb) {
                     if (fill > 0 && !tc::mbar_wait(&empty[s], (uint32_t)(fill - 1) & 1u)) {
                         ok = false;
@@ -328,8 +327,10 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     const uint32_t bar = tc::smem_u32(&full[s]);
                     const uint32_t a = tc::smem_u32(ring) + (uint32_t)s * g.stage_bytes, b = a + kABytes;
                     const int x = (q.kb0 + kb) * kKB;
+                    // 4 bits: 16 bytes of scales a row; by 32 they serve two blocks
+                    const bool sf_here = kMicro<MODE> && (MODE == kNv || (kb & 1) == 0);
                     if (tc::elect()) {
-                        tc::mbar_expect_tx(bar, bytes);
+                        tc::mbar_expect_tx(bar, bytes + (sf_here ? (uint32_t)(1 + boxes) * kSfBytes : 0u));
                         if (few)
                             for (int c = 0; c < few; ++c) tc::tma_load(a + (uint32_t)(c * 16) * kKB, &map_few, x, ym + 16 * c, bar);
                         else
@@ -341,7 +342,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                             tc::bulk_load(sf, g.w_scale + (int64_t)(q.kb0 + kb) * g.N + q.m0, ms, bar);
                             tc::bulk_load(sf + 512, g.x_scale + (int64_t)(q.kb0 + kb) * g.K + q.n0, ns, bar);
                         }
-                        if (kMicro<MODE>) {            // by 32: 16 bytes are the scales of two blocks
+                        if (sf_here) {
                             const uint32_t sf = b + kTileN * kKB;
                             const int xs = 16 * (MODE == kNv ? kb : kb >> 1);
                             tc::tma_load(sf, &map_sm, xs, ym, bar);
@@ -434,29 +435,37 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     // One warp does the rows and the first 128 columns, the other the last 128
                     const int boxes = (q.ncols + kTileM - 1) / kTileM;
                     const int u0 = warp == kSumWarps + 2 ? 0 : 2, u1 = warp == kSumWarps + 2 ? 2 : 1 + boxes;
+                    uint2 odd[2][4];                             // by 32: the words of the block that follows
                     for (int kb = 0; kb < q.nkb; ++kb) {
                         ok = tc::mbar_wait(&full[s], (uint32_t)fill & 1u);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         const uint32_t at = (uint32_t)s * g.stage_bytes + kABytes + kTileN * kKB;
                         const uint32_t ts = tmem + kTileN + (uint32_t)(kSfCols<MODE> * s);
-                        for (int u = u0; u < u1; ++u) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int u = u0 + h;
+                            if (u >= u1) break;
                             uint4 *sf = reinterpret_cast<uint4 *>(ring + at + (uint32_t)u * kSfBytes);
                             uint4 v[4];
+                            if (MODE == kNv || (kb & 1) == 0) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) v[i] = sf[32 * i + lane];
-                            __syncwarp();
+                                for (int i = 0; i < 4; ++i) v[i] = sf[32 * i + lane];
+                                __syncwarp();
+                            }
                             if (MODE == kNv) {
                                 sf[lane] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
                                 sf[32 + lane] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
                                 sf[64 + lane] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
                                 sf[96 + lane] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
                             } else if (kb & 1) {
-                                sf[lane] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
-                                sf[32 + lane] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+                                sf[lane] = make_uint4(odd[h][0].x, odd[h][1].x, odd[h][2].x, odd[h][3].x);
+                                sf[32 + lane] = make_uint4(odd[h][0].y, odd[h][1].y, odd[h][2].y, odd[h][3].y);
                             } else {
                                 sf[lane] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
                                 sf[32 + lane] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) odd[h][i] = make_uint2(v[i].z, v[i].w);
                             }
                         }
                         tc::fence_async();
