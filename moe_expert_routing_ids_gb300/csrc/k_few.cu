@@ -42,7 +42,6 @@ constexpr int kMaxPairs = 512;                    // of one launch
 constexpr int kMaxRows = TOPO_FEW_MAX_TOKENS;     // token rows that a CTA holds
 constexpr int kMaxParts = 64;                     // partial tiles that it holds
 constexpr int kMaxSplit = 8;                      // parts of the up contraction, a power of two that divides 152
-constexpr int kCounters = (1 << 15) / 16;         // column tiles of the widest H
 
 struct FewArgs {
     const uint16_t *x;          // up: bf16 [T][K]
@@ -53,8 +52,7 @@ struct FewArgs {
     const uint8_t *scale;
     const float *row_scale;     // NV
     float *mid;                 // up: act; down: y [T * k][H]
-    uint16_t *out;              // down: [T][H]
-    int32_t *count;             // [H / 16] experts done
+    uint16_t *out;              // [T][H]
     WsHeader *hdr;
     int T, E, k;
     int K, I, H;                // values contracted; the layer's sizes
@@ -476,41 +474,13 @@ __device__ __forceinline__ void sort_pairs(const FewArgs &g, Groups &s, int np, 
     }
 }
 
-// Columns 4 q .. 4 q + 3 of out[t], from the pairs' outputs y, in slot order; eight slots'
-// loads on their way at once (one after the other they held the last CTA up for 10 us).
-__device__ __forceinline__ void combine(const FewArgs &g, const int16_t *key, int t, int q) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float *y = g.mid + (int64_t)t * g.k * g.H + 4 * q;
-    for (int j0 = 0; j0 < g.k; j0 += 8) {
-        float4 v[8];
-        float w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bool in = j0 + j < g.k && key[t * g.k + j0 + j] < g.E;
-            v[j] = in ? __ldcg(reinterpret_cast<const float4 *>(y + (int64_t)(j0 + j) * g.H)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            w[j] = in ? __ldg(g.weights + t * g.k + j0 + j) : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            o.x += w[j] * v[j].x;
-            o.y += w[j] * v[j].y;
-            o.z += w[j] * v[j].z;
-            o.w += w[j] * v[j].w;
-        }
-    }
-    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
-    *reinterpret_cast<uint2 *>(g.out + (int64_t)t * g.H + 4 * q) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-}
-
 template <int FMT, bool DOWN, int STAGES>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 k_few(FewArgs g) {
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ Groups grp;
     __shared__ uint32_t amax[kMaxRows];                         // of the token rows
-    __shared__ int n_done;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = g.warps * 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kStep = FMT == TOPO_FMT_EIGHT ? 128 : 256;    // values of a stage
     unsigned char *ring = dyn + warp * STAGES * kStageBytes;
     const uint32_t ring_at = smem_at(ring);
@@ -539,17 +509,10 @@ k_few(FewArgs g) {
                 copy_n(smem_at(tok + row * g.bpitch + 16 * c), in ? g.x + (int64_t)row * g.K + cs * kStep + 8 * c : g.x, in ? 16 : 0);
             }
         copies_end();
-        if (blockIdx.x == 0)
-            for (int i = tid; i < g.H / 16; i += threads) g.count[i] = 0;
     }
     if (np <= 32) sort_few_pairs(g, grp, np, id, !DOWN && blockIdx.x == 0);
     else sort_pairs(g, grp, np, id, !DOWN && blockIdx.x == 0);
     const int ng = grp.n, total = ng * g.units;                 // at most 512 * 4096
-    if (DOWN && total == 0) {                                   // no expert at all
-        pdl_wait();
-        for (int i = blockIdx.x * threads + tid; i < g.T * g.H / 2; i += gridDim.x * threads) reinterpret_cast<uint32_t *>(g.out)[i] = 0;
-        return;
-    }
     // Items: units of groups, group by group.  (Unit by unit, where a CTA has room for all
     // pairs' activations, fewer CTAs meet in a unit's sums, but each loads all activations:
     // 2.6 us more for one token's 8 x 2048, against 1 us less at the end.)
@@ -700,26 +663,43 @@ k_few(FewArgs g) {
         lo = end;
     }
     copies_wait<0>();
-    if (!DOWN) return;
-    if (begin == hi) pdl_wait();                                // as the kernels that follow rely on it
-    // Whoever brings a unit's last group adds its columns over the slots.  The fence comes
-    // once, after all items: it waits for the warp's copies as well.
-    int *list = reinterpret_cast<int *>(dyn);
-    if (tid == 0) n_done = 0;
-    __syncthreads();
-    __threadfence();
-    for (int i = begin + tid; i < hi; i += threads) {
-        int group, unit;
-        place(i, group, unit);
-        if (atomicAdd(g.count + unit, 1) == ng - 1) list[atomicAdd(&n_done, 1)] = unit;
+    if (DOWN && begin == hi) pdl_wait();                        // as the kernels that follow rely on it
+}
+
+// out[t] = the sum of the pairs' outputs y over the slots, four columns to a thread, eight
+// slots' loads on their way at once.  (Done by the CTA that brings a tile's last expert,
+// counted with atomics, it took as long at one token, and 200 us more at 32, where that is
+// one and the same CTA for nearly all tiles.)
+__global__ void __launch_bounds__(128)
+k_few_sum(FewArgs g) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x, n4 = g.H / 4;
+    pdl_trigger();
+    pdl_wait();
+    if (i >= g.T * n4) return;
+    const int t = i / n4, q = i - t * n4;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float *y = g.mid + (int64_t)t * g.k * g.H + 4 * q;
+    for (int j0 = 0; j0 < g.k; j0 += 8) {
+        float4 v[8];
+        float w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // an id outside [0, E) has no output
+            const bool in = j0 + j < g.k && (unsigned)__ldg(g.ids + t * g.k + j0 + j) < (unsigned)g.E;
+            v[j] = in ? __ldcg(reinterpret_cast<const float4 *>(y + (int64_t)(j0 + j) * g.H)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            w[j] = in ? __ldg(g.weights + t * g.k + j0 + j) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            o.x += w[j] * v[j].x;
+            o.y += w[j] * v[j].y;
+            o.z += w[j] * v[j].z;
+            o.w += w[j] * v[j].w;
+        }
     }
-    __syncthreads();
-    __threadfence();
-    const int tasks = n_done * g.T * 4;
-    for (int i = tid; i < tasks; i += threads) {
-        const int u = i / (4 * g.T), t = (i >> 2) - u * g.T;
-        combine(g, grp.key, t, 4 * list[u] + (i & 3));
-    }
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
+    *reinterpret_cast<uint2 *>(g.out + (int64_t)t * g.H + 4 * q) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
 // ------------------------------------------------------------------------ host
@@ -755,17 +735,21 @@ cudaError_t run_few(FewArgs g, cudaStream_t st) {
 
 template <int FMT>
 cudaError_t run_both(FewArgs up, FewArgs down, cudaStream_t st) {
-    const cudaError_t e = run_few<FMT, false>(up, st);
-    return e != cudaSuccess ? e : run_few<FMT, true>(down, st);
+    cudaError_t e;
+    if ((e = run_few<FMT, false>(up, st)) != cudaSuccess) return e;
+    if ((e = run_few<FMT, true>(down, st)) != cudaSuccess) return e;
+    return launch_pdl(k_few_sum, dim3((unsigned)((down.T * (down.H / 4) + 127) / 128)), dim3(128), 0, st, down);
 }
 
 }  // namespace
 
-// Tokens of a launch, and the parts of the up contraction: as few as leave 16 warps their
-// rings of 4 stages beside the token rows.  Wider rows take fewer tokens.
+// Tokens of a launch, and the parts of the up contraction: as few as leave 14 warps rings
+// of 3 stages beside the token rows (32 tokens of 7168 in 4 parts and 14 x 3: 1094 us, in 8
+// parts and 16 x 4: 1188; 8 tokens in one part and 14 x 3 or in two and 16 x 4: the same).
+// Wider rows take fewer tokens.
 static int few_tokens(int T, int k, int H, int fmt, int *split) {
     const int step = fmt == TOPO_FMT_EIGHT ? 128 : 256;
-    const int64_t room = kFewSmem - (int64_t)kMaxWarps * 4 * kStageBytes - kLeastParts;
+    const int64_t room = kFewSmem - (int64_t)14 * 3 * kStageBytes - kLeastParts;
     const int nc = (H + step - 1) / step;
     for (int n = std::min(std::min(T, kMaxPairs / k), kMaxRows); n > 1; --n)
         for (*split = 1; *split <= kMaxSplit && *split <= nc; *split *= 2)
@@ -781,7 +765,7 @@ size_t few_workspace(int T, int k, int H, int I) {
         const size_t pairs = (size_t)few_tokens(T, k, H, fmt, &split) * k;
         most = std::max(most, pairs * ((size_t)H + (split == 1 ? 1 : 2 * (size_t)split) * I));
     }
-    return sizeof(WsHeader) + kCounters * sizeof(int32_t) + most * sizeof(float);
+    return sizeof(WsHeader) + most * sizeof(float);
 }
 
 cudaError_t launch_expert_few(int T, int E, int k, int H, int I, int fmt, const uint16_t *x, const int32_t *ids,
@@ -802,8 +786,7 @@ cudaError_t launch_expert_few(int T, int E, int k, int H, int I, int fmt, const 
         a.ids = ids + (int64_t)t0 * k;
         a.weights = weights + (int64_t)t0 * k;
         a.hdr = ws_at<WsHeader>(ws, 0);
-        a.count = ws_at<int32_t>(ws, sizeof(WsHeader));
-        float *y = ws_at<float>(ws, sizeof(WsHeader) + kCounters * sizeof(int32_t));
+        float *y = ws_at<float>(ws, sizeof(WsHeader));
         float *act = y + (int64_t)per * k * H;
         FewArgs d = a;
         a.x = x + (int64_t)t0 * H;
