@@ -592,21 +592,25 @@ int topo_expert_gemm_micro(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, 
  *   out[t] = sum over j of weights[t][j] * (W_down[e] a), e = ids[t][j],
  *   a = silu(g) * u,  [g | u] = W_up[e] x[t]
  * with all sums in float32; x and a enter the products as 16-bit floats of 11
- * bits over a power of two for each row (values more than 2^28 below the row's
- * largest lose bits, which changes the sum by less than 2^-38 of it), out is
- * rounded once to bf16 and is the same for the same inputs whatever else the
- * call computes.
+ * bits over a power of two for each row, or each part of one (values more than
+ * 2^28 below the row's largest lose bits, which changes the sum by less than
+ * 2^-38 of the largest for each weight's magnitude); out is rounded once to
+ * bf16.
  * x: device bf16 [T][H]; ids: device int32 [T][k] (an expert may occur twice in
  * a row; one outside [0, E) adds nothing and is reported); weights: device
  * float32 [T][k]; up: [E][2 I][H], gate rows then up rows, and down: [E][H][I]
  * in format fmt: TOPO_FMT_EIGHT as topo_quantize_weight's (scale: float32,
  * row scales NULL), else as topo_quantize_rows_micro's.  out: device bf16
- * [T][H].  A token whose row holds a NaN or an infinity gets NaN.
+ * [T][H].  A token whose row holds a NaN or an infinity, or whose activations
+ * do, gets values that are not finite, and no other token does; so do tokens
+ * of experts whose weights or scales are NaN.
  * T <= TOPO_FEW_MAX_TOKENS, E <= TOPO_GATE_MAX_E, k <= 64; H and I multiples of
- * 16, of 32 in 4 bits, up to 2^15.  ws: topo_few_workspace_bytes bytes, header
- * included (0 for invalid sizes).  Weights are read once for every 8 to 32
- * tokens that share an expert (as many as fit the shared memory); past a dozen
- * tokens or so the path through topo_reroute_layout is the alternative.
+ * 16, of 32 in 4 bits, up to 2^15; scales and pointers to rows 16-byte aligned.
+ * ws: topo_few_workspace_bytes bytes, header included (0 for invalid sizes),
+ * 16-byte aligned.  An expert's weights are read once for every 8 of its
+ * tokens (fewer for I past 9000 or so), by launches of all T tokens (fewer
+ * where T * k > 512 or 32 rows of H do not fit); where most experts have more
+ * tokens than that, the path through topo_reroute_layout is the one to take.
  * Device errors: TOPO_ERANGE. */
 size_t topo_few_workspace_bytes(int32_t T, int32_t E, int32_t k, int32_t H, int32_t I);
 int topo_expert_few(int32_t T, int32_t E, int32_t k, int32_t H, int32_t I, int32_t fmt, const uint16_t *x,

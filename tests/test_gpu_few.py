@@ -103,7 +103,9 @@ class Case:
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 1, 1, 32, 32), (1, 8, 2, 1024, 768), (2, 5, 3, 160, 96), (8, 16, 4, 288, 1056),
                                        (7, 64, 6, 512, 64), (9, 12, 8, 256, 128), (32, 40, 2, 96, 320), (3, 4, 64, 64, 32),
                                        (5, 300, 2, 32, 64), (1, 9, 8, 7168, 256), (4, 3, 2, 64, 4096), (8, 6, 6, 8224, 64),
-                                       (8, 1024, 8, 64, 32)])
+                                       (8, 1024, 8, 64, 32), (32, 3, 2, 7168, 32), (20, 2, 1, 5152, 64), (32, 20, 16, 7168, 32),
+                                       (3, 2, 2, 32768, 32), (32, 2, 1, 8224, 32), (5, 2, 2, 64, 16416), (1, 1, 1, 32, 32768),
+                                       (32, 1, 1, 64, 9248)])
 def test_few(T, E, k, H, I, fmt):
     c = Case(T, E, k, H, I, fmt)
     got, ws = c.run()

@@ -139,7 +139,7 @@ def check_rows(v, q, s, g, fmt):
 
 @gpu
 @pytest.mark.parametrize("fmt", [MX, NV])
-@pytest.mark.parametrize("rows,C", [(1, 32), (3, 128), (17, 160), (40, 1408), (11, 7168), (700, 288), (20000, 64), (5000, 1056)])
+@pytest.mark.parametrize("rows,C", [(1, 32), (3, 128), (17, 160), (40, 1408), (11, 7168), (700, 288), (20000, 64), (5000, 1056), (19, 20512)])
 def test_quantize_rows(rows, C, fmt):
     dev = _dev()
     v = hard_rows(np.random.default_rng([rows, C]), rows, C)
