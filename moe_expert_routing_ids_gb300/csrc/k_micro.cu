@@ -21,7 +21,12 @@
 //   k_micro_values   the bf16 values that such rows stand for
 //
 // A lane takes 16 consecutive values (32 bytes in, 8 bytes out): a block of NV, half
-// a block of MX.
+// a block of MX.  Measured, bytes moved over time: rows of 131072 x 7168 to MX 332 us,
+// 7.2 TB/s, to NV 397 us, 6.1 TB/s (the row's largest value first, its words in registers
+// meanwhile: issue 70 percent); weights of 64 x 2816 x 4096 to MX 256 us, 7.3 TB/s, and back
+// to bf16 266 us; activation of 131072 x 2048 to MX 192 us, 6.3 TB/s, to NV 235 us, 5.2 TB/s
+// (issue 74 percent); dispatch of 16384 tokens, k = 8, H = 7168 to NV 145 us and 5 us for the
+// inverse permutation.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -103,10 +108,31 @@ __device__ __forceinline__ uint32_t finite_bits(const float (&v)[16]) {
     return m;
 }
 
+// Two float32 values in a register pair, for the packed instructions.
+using f2 = uint64_t;
+__device__ __forceinline__ f2 pair(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f2 both(float a) { return pair(a, a); }
+__device__ __forceinline__ void halves(f2 p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // v = silu(v) * u in float32.  exp(-v) as a power of two of the rounded product t =
 // -v log2(e), times 1 + what the rounding left out; the reciprocal of 1 + exp(-v) by one
-// step of Newton's iteration from the approximate one: within 7 * 2^-24 of the value, where
-// topo_swiglu_quantize calls expf and divides (25 instructions a value; this, 15).  low: some
+// step of Newton's iteration from the approximate one: within 8 * 2^-24 of the value, where
+// topo_swiglu_quantize calls expf and divides (25 instructions a value; this, in packed
+// pairs, 9).  low: some
 // v may be below -83, where 1 + exp(-v) nears the end of float32's range: expf and division.
 __device__ __forceinline__ void gated(float (&v)[16], const float (&u)[16], bool low) {
     if (low) {
@@ -114,32 +140,36 @@ __device__ __forceinline__ void gated(float (&v)[16], const float (&u)[16], bool
         for (int i = 0; i < 16; ++i) v[i] = __fdiv_rn(v[i], 1.f + expf(-v[i])) * u[i];
         return;
     }
-    constexpr float kLog2e = 1.44269504088896f, kLog2eLo = 1.925963033500e-8f, kLn2 = 0.69314718f;
+    const f2 to = both(-1.44269504088896f), back = both(1.44269504088896f), lo = both(-1.925963033500e-8f);
+    const f2 ln2 = both(0.69314718f), one = both(1.f), less = both(-1.f);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float t = -kLog2e * v[i], left = __fmaf_rn(-kLog2eLo, v[i], __fmaf_rn(-kLog2e, v[i], -t));
-        float e, r;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-        const float d = 1.f + __fmaf_rn(e * kLn2, left, e);
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-        r = __fmaf_rn(__fmaf_rn(-d, r, 1.f), r, r);
-        v[i] = v[i] * r * u[i];
+    for (int i = 0; i < 16; i += 2) {
+        const f2 x = pair(v[i], v[i + 1]), t = mul2(x, to), left = fma2(lo, x, fma2(to, x, mul2(x, back)));   // x back = -t
+        float t0, t1, e0, e1, r0, r1;
+        halves(t, t0, t1);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
+        const f2 e = pair(e0, e1), c = fma2(mul2(e, ln2), left, e), nd = fma2(c, less, less);   // -(1 + exp(-v))
+        halves(nd, r0, r1);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(-r0));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(-r1));
+        const f2 r = pair(r0, r1);
+        halves(mul2(mul2(x, fma2(fma2(nd, r, one), r, r)), pair(u[i], u[i + 1])), v[i], v[i + 1]);
     }
 }
 
 // A lane's groups of a row: kGroups of them, 32 apart, at a time, kept as they are stored
 // (the activation's as float32).
-// Measured in groups, CTAs to an SM: activation of 131072 x 2048 to MX 2, 2: 257 us, 2, 3:
-// 236, 1, 4: 249, 1, 5: 217; to NV 2, 2: 302, 2, 3: 257, 1, 5: 295; rows of 131072 x 7168 to
-// NV 4, 3: 429, 4, 4: 399, 5, 3: 458, 2, 5 (of a build before): 501 for 434.
-template <int SRC, bool NV>
-constexpr int kGroups = SRC != kSwiglu ? 4 : NV ? 2 : 1;
-template <int SRC, bool NV>
-constexpr int kCtas = SRC != kSwiglu ? 4 : NV ? 3 : 5;
+// Measured in groups, CTAs to an SM: activation of 131072 x 2048 to MX 1, 4: 221 us, 1, 5: 231,
+// 2, 3: 204, 2, 4: 193, 3, 2: 310; to NV 1, 5: 296, 2, 3: 246, 2, 4: 236; rows of 131072 x 7168 to
+// NV 4, 3: 429, 4, 4: 399, 5, 3: 458.
+template <int SRC>
+constexpr int kGroups = SRC == kSwiglu ? 2 : 4;
+constexpr int kCtas = 4;                                        // to an SM
 
-template <int SRC, bool NV>
+template <int SRC>
 struct Groups {
-    static constexpr int kN = kGroups<SRC, NV>;
+    static constexpr int kN = kGroups<SRC>;
     uint4 a[kN][2];
 
     __device__ __forceinline__ void load(const MicroArgs &g, int64_t from, int c0) {
@@ -159,9 +189,9 @@ struct Groups {
         return max(m << 16, m & 0xffff0000u);
     }
 };
-template <bool NV>
-struct Groups<kSwiglu, NV> {
-    static constexpr int kN = kGroups<kSwiglu, NV>;
+template <>
+struct Groups<kSwiglu> {
+    static constexpr int kN = kGroups<kSwiglu>;
     float f[kN][16];
 
     __device__ __forceinline__ void load(const MicroArgs &g, int64_t from, int c0) {
@@ -191,10 +221,16 @@ struct Groups<kSwiglu, NV> {
         for (int i = 0; i < 16; ++i) v[i] = f[j][i];
     }
     __device__ __forceinline__ uint32_t amax(int j) const {
-        uint32_t m = 0;
+        float m = 0.f;                                          // drops a NaN: 0 * v tells of those
+        f2 z = both(0.f);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(f[j][i]) & 0x7fffffffu);
-        return m;
+        for (int i = 0; i < 16; i += 2) {
+            m = fmaxf(fmaxf(m, fabsf(f[j][i])), fabsf(f[j][i + 1]));
+            z = fma2(pair(f[j][i], f[j][i + 1]), both(0.f), z);
+        }
+        float a, b;
+        halves(z, a, b);
+        return a + b == 0.f ? __float_as_uint(m) : 0x7fffffffu;
     }
 };
 
@@ -202,9 +238,9 @@ struct Groups<kSwiglu, NV> {
 // is longer than eight warps' goes round (NV: and is read twice, once for its largest
 // magnitude).  All of a lane's loads are on their way before the first is used.
 template <int SRC, bool NV>
-__global__ void __launch_bounds__(256, kCtas<SRC, NV>)
+__global__ void __launch_bounds__(256, kCtas)
 k_micro_rows(MicroArgs g) {
-    constexpr int kPer = kGroups<SRC, NV> * 32;
+    constexpr int kPer = kGroups<SRC> * 32;
     __shared__ uint32_t wmax[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = warp & ((1 << g.log_w) - 1);
@@ -236,9 +272,9 @@ k_micro_rows(MicroArgs g) {
     if (!live) from = 0;
     const int first = part * kPer + lane, span = kPer << g.log_w;
     const int nv = live ? (g.nv + 31) & ~31 : 0;                 // whole warps of groups
-    Groups<SRC, NV> in_regs;
+    Groups<SRC> in_regs;
     float v[16];
-    uint32_t am[kGroups<SRC, NV>];                                   // the groups' largest magnitudes
+    uint32_t am[kGroups<SRC>];                                   // the groups' largest magnitudes
     int n = 0;                                                   // NV: exponent of the row's scale
     if (NV) {
         // the whole row's largest finite magnitude first
@@ -246,7 +282,7 @@ k_micro_rows(MicroArgs g) {
         for (int c0 = first; c0 - lane < nv; c0 += span) {
             in_regs.load(g, from, c0);
 #pragma unroll
-            for (int j = 0; j < kGroups<SRC, NV>; ++j) {
+            for (int j = 0; j < kGroups<SRC>; ++j) {
                 am[j] = in_regs.amax(j);
                 uint32_t a = am[j];
                 if (a >= kInf) {
@@ -275,10 +311,10 @@ k_micro_rows(MicroArgs g) {
         if (!NV || g.nv > span) {
             in_regs.load(g, from, c0);
 #pragma unroll
-            for (int j = 0; j < kGroups<SRC, NV>; ++j) am[j] = in_regs.amax(j);
+            for (int j = 0; j < kGroups<SRC>; ++j) am[j] = in_regs.amax(j);
         }
 #pragma unroll
-        for (int j = 0; j < kGroups<SRC, NV>; ++j) {
+        for (int j = 0; j < kGroups<SRC>; ++j) {
             const int c = c0 + 32 * j;
             if (c - lane >= nv) break;                           // whole warp
             const bool in = c < g.nv;
@@ -304,14 +340,14 @@ k_micro_rows(MicroArgs g) {
                 float si;
                 asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(si) : "f"(sg));
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] *= si;
+                for (int i = 0; i < 16; i += 2) halves(mul2(pair(v[i], v[i + 1]), both(si)), v[i], v[i + 1]);
                 if (m >= kInf) sb = 0x7fu;
             } else {
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 const int n = m < kInf ? least_power(m, 0x400000u, 2) : 0;   // 6 = 1.5 * 2^2
                 const float inv = pow2(-n);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] *= inv;
+                for (int i = 0; i < 16; i += 2) halves(mul2(pair(v[i], v[i + 1]), both(inv)), v[i], v[i + 1]);
                 sb = m < kInf ? (uint32_t)(127 + n) : 255u;
             }
             constexpr bool kHalf = NV && SRC != kSwiglu;
@@ -384,7 +420,7 @@ template <int SRC, bool NV>
 cudaError_t run_rows(MicroArgs a, cudaStream_t st) {
     if (a.rows == 0) return cudaSuccess;
     a.log_w = 0;
-    while (a.log_w < 3 && (kGroups<SRC, NV> * 32) << a.log_w < a.nv) ++a.log_w;
+    while (a.log_w < 3 && (kGroups<SRC> * 32) << a.log_w < a.nv) ++a.log_w;
     const int64_t warps = a.rows << a.log_w;
     return launch_pdl(k_micro_rows<SRC, NV>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, a);
 }

@@ -194,9 +194,12 @@ def test_permute_quantize_reports_bad_pairs(T, H, fmt):
 @pytest.mark.parametrize("fmt", [MX, NV])
 @pytest.mark.parametrize("rows,I", [(1, 32), (37, 160), (333, 1408), (5000, 288), (3, 8192), (2000, 6688)])
 def test_swiglu_quantize(rows, I, fmt):
-    """a is formed in float32, with an exp of at most 2 units in the last place and four
-    more roundings: within 8 * 2^-24 of itself (d); a scale then is that of an amax within d,
-    and a code's value within half of e2m1's step (0.25 below 2, 0.5 below 4, 1 above) and d."""
+    """a is formed in float32: 2^x within 2^-22.5 (2.9 * 2^-24) and four more roundings of 2^-24,
+    the reciprocal's step another: within 8 * 2^-24 of itself (d); expf within 2 units in the last
+    place (4 * 2^-24), a sum, a quotient and a product stay below that too.  A scale then is that of
+    an amax within d.  The quotient by a scale is a product with its approximate inverse, one unit
+    in the last place and a rounding: 3 * 2^-24 more, so a code's value is within half of e2m1's
+    step (0.25 below 2, 0.5 below 4, 1 above) and 11 * 2^-24 of the value (dq)."""
     dev = _dev()
     rng = np.random.default_rng([rows, I, 7])
     h = bf16(rng.standard_normal((rows, 2 * I)) * 3)
@@ -210,7 +213,7 @@ def test_swiglu_quantize(rows, I, fmt):
     x = h.double().numpy()
     with np.errstate(over="ignore", invalid="ignore"):
         a = x[:, :I] / (1 + np.exp(-x[:, :I])) * x[:, I:]
-    blk, d = BLOCK[fmt], 8 * 2.0 ** -24
+    blk, d, dq = BLOCK[fmt], 8 * 2.0 ** -24, 11 * 2.0 ** -24
     p = a.reshape(rows, -1, blk)
     bad = ~np.isfinite(p).all(-1)
     mag = np.where(np.isfinite(p), np.abs(p), 0.0)
@@ -235,7 +238,7 @@ def test_swiglu_quantize(rows, I, fmt):
     step = np.where(mag < 2 * sc[..., None], 0.25, np.where(mag < 4 * sc[..., None], 0.5, 1.0)) * sc[..., None]
     with np.errstate(invalid="ignore"):
         err = np.abs(v - p)
-    assert np.all((err <= step * (1 + d) + d * mag) | bad[..., None])
+    assert np.all((err <= step * (1 + d) + dq * mag) | bad[..., None])
 
 
 @gpu
