@@ -45,6 +45,23 @@
 // same).  Tiles of 256 x 192, which the two accumulators fill, kept in tensor memory and
 // taken while the next tile is multiplied: 1.20 ms, since each product of 128 rows reads
 // its columns again (1088 cycles of shared memory for one and a half times the work).
+//
+//   4 bits    y[r][n] = ra[r] * rw[n] * sum over blocks of sa[r][b] * sw[n][b] * (sum over k in b of a[r][k] * w[n][k])
+//             blocks of 32 (kMx: powers of two, no ra and rw) or 16 (kNv: e4m3)
+//
+// The same tiles and roles: a stage's 128 bytes of a row are 256 values, four steps of 64
+// (kind::mxf4, two scales a step; kind::mxf4nvf4, four).  The tensor cores apply the blocks'
+// scales; sums stay in tensor memory over 8192 values, and the rows' scales multiply them
+// in the registers.  A row's 16 scale bytes come with the stage as a box of their own, and
+// the scale warps turn the words of 128 rows into the order that tensor memory wants.
+// Measured: 131072 rows, N = 4096, K = 7168, 128 experts: by 32 1.56 ms, 4.9 PFLOP/s, by 16
+// 1.89 ms, 4.1 PFLOP/s (tensor pipe 50 and 40 percent of cycles); 1536 rows, 2816 x 4096,
+// 64 experts 67 and 75 us, 6.2 and 5.9 TB/s; 6 rows, 4096 x 1408: 11 and 15 us.  What bounds it:
+// the bytes of a stage are those of the 8-bit product, 768 cycles of shared memory; by 16, a
+// build that loads no scales and copies half of them to tensor memory still takes 1.78 ms.
+// Tried: scales by the scale warps' own 16-byte copies (a ring behind the stages, three
+// blocks ahead): 3.2 ms.  A row's 16 bytes loaded once for two blocks of kMx, the second's
+// words kept in registers: 1.76 -> 1.56 ms.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -1,26 +1,42 @@
 // The experts applied to a few tokens:
 //   out[t] = sum_j w[t][j] * W_down[e] (silu(g) * u),  [g | u] = W_up[e] x[t],  e = ids[t][j]
 //
-// The weights of the experts in use are read once and are all the traffic; a token's
-// products are next to nothing.  Two kernels, up and down, one CTA to an SM:
+// The weights of the experts in use are the traffic; a token's products are next to
+// nothing.  Three kernels: up and down, one CTA to an SM, and the sum over the slots.
 //
-//   items   a tile of 16 weight rows (8 gate rows and their 8 up rows; 16 rows of
-//           W_down) of one expert in use, in the experts' order; a CTA takes an equal
-//           share of neighbouring items, its warps one after the other (or, where a CTA
-//           has fewer items of an expert than warps, a part of the contraction each)
-//   weights each warp streams its rows through its own ring of shared memory, 128 bytes
-//           of each row a stage, by cp.async: no warp waits for another
-//   product mma.sync m16n8k16 in f16 with float32 sums: weight rows on M, tokens on N.
+//   groups  the pairs (t, j) sorted by expert, up to 8 pairs of one expert a group: the
+//           columns of a product, for which its weights are read once
+//   items   a tile of 16 weight rows (8 gate rows and their 8 up rows; 16 rows of W_down)
+//           of one group; a CTA takes an equal share of neighbouring items, its warps one
+//           after the other, or parts of an item's contraction where that ends sooner
+//   weights each warp streams its rows through its own ring of shared memory, 128 bytes of
+//           each row a stage, by cp.async: no warp waits for another
+//   product mma.sync m16n8k16 in f16 with float32 sums: weight rows on M, pairs on N.
 //           e4m3 and e2m1 are f16 values; scales by 128 and by 32 multiply a block's
 //           sum, scales by 16 the f16 weights (6 bits: exact)
 //   tokens  as f16 over a power of two for each row (its largest magnitude in
-//           [2^14, 2^15)): 11 bits, where bf16 has 8
-//   sums    float32 throughout: an expert's outputs for a token go to the workspace, and
-//           the warp that brings the last expert's of 16 columns adds them in slot order
-//           with their weights, so the result does not depend on who comes last
+//           [2^14, 2^15)): 11 bits, where bf16 has 8.  The up kernel holds all tokens'
+//           rows; where they do not fit, each CTA holds and contracts a part of H, and the
+//           down kernel adds the parts of g and u
+//   sums    float32 throughout; each pair's outputs go to the workspace and are added in
+//           slot order, so no result depends on the order of the CTAs
 //
-// The down kernel starts while the up kernel runs (its first weights do not depend on
-// it) and waits for it before it reads the activations.
+// The down kernel starts as the up kernel's CTAs end (its first weights do not depend on
+// it) and waits for all of it before it reads the activations.
+//
+// Measured (host call after call, E = 256 of 7168 x 2048, k = 8): one token in 8 bits 63 to
+// 66 us, 5.4 TB/s of weights, the up kernel's steady part at 7 TB/s; 32 tokens in MX 736 to
+// 768 us, 5.0 to 5.2 TB/s.  One token of 2048 x 768 in MX 17.6 us; 8 tokens of 64 experts,
+// 4096 x 1408, k = 6, NV 74 to 77 us, 4.4 to 4.6 TB/s.  What bounds it: in 8 bits memory,
+// and about 4 us to the first product of either kernel (the ids' round trip, the sort, the
+// first items' addresses, the rows' conversion: instructions, not waits); in 4 bits the
+// issue of 275 instructions (NV; MX 243) for a stage of 4096 weights at 58 to 63 percent of
+// the slots with 16 warps of 128 registers.  Tried: 20 or 24 warps (fewer registers, spills):
+// 7 to 50 percent slower; 8 warps, so that both kernels are resident: 9 percent faster for
+// the smallest layer, 5 to 25 slower elsewhere; rows of 144 bytes with their scales instead
+// of the exclusive or: 5 percent slower; weights first to leave the L2: equal; the last sum
+// in the down kernel, by the CTA that brings a tile's last expert: equal at one token,
+// 1186 us against 736 at 32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
