@@ -105,7 +105,7 @@ class Case:
                                        (5, 300, 2, 32, 64), (1, 9, 8, 7168, 256), (4, 3, 2, 64, 4096), (8, 6, 6, 8224, 64),
                                        (8, 1024, 8, 64, 32), (32, 3, 2, 7168, 32), (20, 2, 1, 5152, 64), (32, 20, 16, 7168, 32),
                                        (3, 2, 2, 32768, 32), (32, 2, 1, 8224, 32), (5, 2, 2, 64, 16416), (1, 1, 1, 32, 32768),
-                                       (32, 1, 1, 64, 9248)])
+                                       (32, 1, 1, 64, 9248), (20, 6, 64, 64, 32), (17, 1, 1, 32768, 32)])
 def test_few(T, E, k, H, I, fmt):
     c = Case(T, E, k, H, I, fmt)
     got, ws = c.run()
@@ -174,6 +174,27 @@ def test_rows_of_zeros_small_large_and_not_finite(fmt):
     assert fin.tolist() == [True] * 5 + [False, False, True]
     keep = [0, 1, 2, 3, 4, 7]
     assert torch.equal(got[keep], plain[keep]) and not bool(torch.isfinite(got[5:7]).any())
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [EIGHT, MX, NV])
+def test_weights_that_are_nan_reach_their_tokens_only(fmt):
+    """A NaN weight (8 bits) or scale (4 bits) of expert 2 in W_up's gate rows, then in W_down."""
+    c = Case(8, 6, 2, 256, 96, fmt, seed=9)
+    plain, _ = c.run()
+    for part, row in (("up", 17), ("down", 40)):
+        t = list(getattr(c, part))
+        i = 0 if fmt == EIGHT else 1
+        kept = t[i].clone()
+        t[i][2, row, 0] = {EIGHT: 0x7f, MX: 0xff, NV: 0x7f}[fmt]
+        got, ws = c.run()
+        t[i].copy_(kept)
+        hit = (c.ids == 2).any(1)
+        assert hit.any() and not hit.all()
+        fin = torch.isfinite(got).cpu()
+        assert bool(fin[~hit].all()) and torch.equal(got[~hit], plain[~hit])
+        # through W_up a NaN activation reaches all of a token, through W_down the row's column
+        assert not bool(fin[hit].any()) if part == "up" else fin[hit].sum(1).eq(255).all() and not bool(fin[hit][:, 40].any())
 
 
 @gpu
@@ -267,5 +288,8 @@ def test_refusals():
         refused(**change)
     refused(code=topo.TOPO_ENOSPC, nb=nb - 1)
     assert topo.topo_expert_few(*{**ok, "T": 0}.values()) == 0
+    for H, I, k in ((7168, 2048, 8), (32768, 32768, 64), (64, 32, 2), (4112, 48, 6), (5152, 9248, 3)):
+        sizes = [topo.topo_few_workspace_bytes(T, 64, k, H, I) for T in range(33)]
+        assert sizes == sorted(sizes) and sizes[1] > 256          # one made for more tokens serves fewer
     for dims in ((-1, 8, 2, 64, 32), (33, 8, 2, 64, 32), (4, 0, 2, 64, 32), (4, 8, 65, 64, 32), (4, 8, 2, 8, 32), (4, 8, 2, 64, 1 << 16)):
         assert topo.topo_few_workspace_bytes(*dims) == 0
