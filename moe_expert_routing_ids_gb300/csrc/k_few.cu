@@ -74,6 +74,7 @@ struct FewArgs {
     int K, I, H;                // values contracted; the layer's sizes
     int rows;                   // weight rows of an expert
     int units;                  // tiles of 16 rows of an expert
+    uint32_t inv_units;         // 2^32 / units, rounded up (units > 1)
     int nc;                     // stages of a row
     int split;                  // the up contraction's parts, each to its share of the CTAs
     int64_t pitch;              // 4 bits: scale bytes of a row
@@ -534,8 +535,13 @@ k_few(FewArgs g) {
     // 2.6 us more for one token's 8 x 2048, against 1 us less at the end.)
     const int begin = (int)((int64_t)total * cta / ctas), hi = cta < ctas ? (int)((int64_t)total * (cta + 1) / ctas) : begin;
     auto place = [&](int gi, int &group, int &unit) {
-        group = gi / g.units;
+        // gi / units, one too many at most (gi < 2^21, units <= 2^12)
+        group = g.units == 1 ? gi : (int)__umulhi((uint32_t)gi, g.inv_units);
         unit = gi - group * g.units;
+        if (unit < 0) {
+            --group;
+            unit += g.units;
+        }
     };
     // Batches of items: up: all of them; down: of as many groups as there is room for the
     // activations of their pairs.
@@ -824,6 +830,7 @@ cudaError_t launch_expert_few(int T, int E, int k, int H, int I, int fmt, const 
         d.units = H / 16;
         for (FewArgs *p : {&a, &d}) {
             p->nc = (p->K + step - 1) / step;
+            p->inv_units = (uint32_t)((((uint64_t)1 << 32) + p->units - 1) / p->units);
             p->pitch = fmt == TOPO_FMT_EIGHT ? 0 : micro_pitch(p->K, fmt);
         }
         a.bpitch = token_pitch((a.nc + split - 1) / split * step, fmt);
