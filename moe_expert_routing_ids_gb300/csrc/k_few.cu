@@ -392,16 +392,15 @@ __device__ __forceinline__ void load_act(const FewArgs &g, unsigned char *tok, u
     }
 }
 
-// The pairs sorted by expert, and the groups of at most `cols` pairs of one expert: a group
-// is what the weights' tiles are read for.
+// The pairs of experts in [0, E) sorted by expert, and the groups of at most `cols` pairs of
+// one expert: a group is what the weights' tiles are read for.  Each CTA sorts for itself:
+// which pairs a group holds is the same for all of them.
 struct Groups {
-    int16_t key[kMaxPairs];                         // expert of each pair; E for one outside [0, E)
-    uint16_t pair[kMaxPairs];                       // sorted: the pair, its token, its expert's first place
+    uint16_t pair[kMaxPairs];                       // sorted: the pair, its token
     uint8_t token[kMaxPairs];
-    uint16_t first[kMaxPairs];
     uint16_t expert[kMaxPairs];                     // of each group
     uint16_t start[kMaxPairs + 1];                  // its first place
-    int warp_sum[kMaxWarps];
+    int warp_sum[8];
     int n;                                          // groups
 };
 
@@ -422,8 +421,7 @@ __device__ __forceinline__ void sort_few_pairs(const FewArgs &g, Groups &s, int 
     const int at = less + same, mine = opens ? at : 64;
     int group = 0;
     for (int q = 0; q < np; ++q) group += __shfl_sync(0xffffffffu, mine, q) < at;
-    if (in) {
-        s.key[lane] = (int16_t)e;
+    if (ok) {
         s.pair[at] = (uint16_t)lane;
         s.token[at] = (uint8_t)(lane / g.k);
         if (opens) {
@@ -439,56 +437,82 @@ __device__ __forceinline__ void sort_few_pairs(const FewArgs &g, Groups &s, int 
     __syncwarp();
 }
 
-// np <= kMaxPairs; id: this thread's, of pair tid.  Ends with a barrier.
-__device__ __forceinline__ void sort_pairs(const FewArgs &g, Groups &s, int np, int id, bool report) {
+// np <= kMaxPairs; id: this thread's, of pair tid; count: scratch of TOPO_GATE_MAX_E words and
+// kMaxPairs half words.  The experts' first places and groups by a sum over shared counters, 4
+// to a thread of the first 8 warps.  A pair's place among its expert's by the counter, in any
+// order, where one group holds them all, else by the pairs before it.  Ends with a barrier.
+__device__ __forceinline__ void sort_pairs(const FewArgs &g, Groups &s, uint32_t *count, int np, int id, bool report) {
     const int tid = threadIdx.x, lane = tid & 31, threads = g.warps * 32;
-    for (int i = tid; i < np; i += threads) {
-        if (i != tid) id = __ldg(g.ids + i);
-        const bool ok = (unsigned)id < (unsigned)g.E;
-        s.key[i] = (int16_t)(ok ? id : g.E);
-        if (!ok && report) set_error(g.hdr, TOPO_ERANGE);
+    int16_t *const key = reinterpret_cast<int16_t *>(count + TOPO_GATE_MAX_E);
+    for (int i = tid; i < TOPO_GATE_MAX_E / 4; i += threads) reinterpret_cast<uint4 *>(count)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    int e[kMaxPairs / 256], rank[kMaxPairs / 256];               // 256 threads at least
+#pragma unroll
+    for (int j = 0; j < kMaxPairs / 256; ++j) {
+        const int i = tid + j * threads;
+        e[j] = g.E;
+        if (i >= np) continue;
+        e[j] = j == 0 ? id : __ldg(g.ids + i);
+        if ((unsigned)e[j] >= (unsigned)g.E) {
+            if (report) set_error(g.hdr, TOPO_ERANGE);
+            key[i] = (int16_t)(e[j] = g.E);
+        } else {
+            key[i] = (int16_t)e[j];
+            rank[j] = (int)atomicAdd(count + e[j], 1u);
+        }
     }
     __syncthreads();
-    for (int i = tid; i < np; i += threads) {
-        const int e = s.key[i];
-        int less = 0, same = 0;
-        for (int q = 0; q < np; ++q) {
-            const int f = s.key[q];
-            less += f < e;
-            same += f == e && q < i;
+    uint32_t c[4], sum = 0;                                      // pairs, and groups in the upper half
+    if (tid < 256) {
+        const uint4 v = reinterpret_cast<const uint4 *>(count)[tid];
+        c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[i] |= (c[i] + g.cols - 1) / g.cols << 16;
+            sum += c[i];
         }
-        s.pair[less + same] = (uint16_t)i;
-        s.token[less + same] = (uint8_t)(i / g.k);
-        s.first[less + same] = (uint16_t)less;
+    }
+    uint32_t at = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += u;
+    }
+    if (tid < 256 && lane == 31) s.warp_sum[tid >> 5] = (int)at;
+    __syncthreads();
+    at -= sum;
+    if (tid < 256) {
+        for (int w = 0; w < tid >> 5; ++w) at += (uint32_t)s.warp_sum[w];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int first = (int)(at & 0xffffu), group = (int)(at >> 16);
+            count[4 * tid + i] = (uint32_t)first | (c[i] >> 17 ? 1u << 31 : 0u);   // several groups
+            for (int k = 0; k < (int)(c[i] >> 16); ++k) {
+                s.expert[group + k] = (uint16_t)(4 * tid + i);
+                s.start[group + k] = (uint16_t)(first + k * g.cols);
+            }
+            at += c[i];
+        }
+        if (tid == 255) {
+            s.n = (int)(at >> 16);
+            s.start[at >> 16] = (uint16_t)(at & 0xffffu);
+        }
     }
     __syncthreads();
-    // a group starts at every cols-th pair of an expert; their places by a running count
-    int base = 0, held = 0;
-    for (int i0 = 0; i0 < np; i0 += threads) {
-        const int i = i0 + tid;
-        const bool in = i < np && s.key[s.pair[i < np ? i : 0]] < g.E;
-        const bool opens = in && (i - s.first[i]) % g.cols == 0;
-        const unsigned m = __ballot_sync(0xffffffffu, opens), all = __ballot_sync(0xffffffffu, in);
-        if (lane == 0) s.warp_sum[tid >> 5] = __popc(m) | __popc(all) << 16;
-        __syncthreads();
-        int at = base, total = 0;
-        for (int w = 0; w < g.warps; ++w) {
-            if (w < tid >> 5) at += s.warp_sum[w] & 0xffff;
-            total += s.warp_sum[w];
-        }
-        if (opens) {
-            at += __popc(m & ((1u << lane) - 1));
-            s.expert[at] = (uint16_t)s.key[s.pair[i]];
-            s.start[at] = (uint16_t)i;
-        }
-        base += total & 0xffff;
-        held += total >> 16;
-        if (tid == 0) {
-            s.n = base;
-            s.start[base] = (uint16_t)held;
-        }
-        __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMaxPairs / 256; ++j) {
+        const int i = tid + j * threads;
+        if (e[j] >= g.E) continue;
+        const uint32_t at_e = count[e[j]];
+        int to = (int)(at_e & 0xffffu);
+        if (at_e >> 31)
+            for (int q = 0; q < i; ++q) to += key[q] == e[j];
+        else
+            to += rank[j];
+        s.pair[to] = (uint16_t)i;
+        s.token[to] = (uint8_t)(i / g.k);
     }
+    __syncthreads();
 }
 
 template <int FMT, bool DOWN, int STAGES>
@@ -528,7 +552,7 @@ k_few(FewArgs g) {
         copies_end();
     }
     if (np <= 32) sort_few_pairs(g, grp, np, id, !DOWN && blockIdx.x == 0);
-    else sort_pairs(g, grp, np, id, !DOWN && blockIdx.x == 0);
+    else sort_pairs(g, grp, reinterpret_cast<uint32_t *>(dyn), np, id, !DOWN && blockIdx.x == 0);   // the rings are empty yet
     const int ng = grp.n, total = ng * g.units;                 // at most 512 * 4096
     // Items: units of groups, group by group.  (Unit by unit, where a CTA has room for all
     // pairs' activations, fewer CTAs meet in a unit's sums, but each loads all activations:
@@ -555,26 +579,34 @@ k_few(FewArgs g) {
             rows = grp.start[g1] - row0;
             if (lo != begin) __syncthreads();                   // the batch before is through with its rows
         }
-        // A unit's contraction may be split over 2^log_s warps, so that the warps end together
-        const int nu = end - lo, nc = ce - cs;
+        // Whole units as long as there is one for each warp; the rest in parts of their
+        // contraction, 2^log_s each, so that the warps end together
+        const int nu = end - lo, nc = ce - cs, whole = nu / g.warps * g.warps, rest = nu - whole;
         int log_s = 0;
-        for (int s = 1, best = (nu + g.warps - 1) / g.warps * 16; s <= 4; ++s) {
-            const int cost = ((nu << s) + g.warps - 1) / g.warps * (16 >> s);
-            if (nu << s <= g.cap_parts && 1 << s <= nc && cost < best) {
+        for (int s = 1, best = (rest + g.warps - 1) / g.warps * 16; s <= 4; ++s) {
+            const int cost = ((rest << s) + g.warps - 1) / g.warps * (16 >> s);
+            if (rest << s <= g.cap_parts && 1 << s <= nc && cost < best) {
                 best = cost;
                 log_s = s;
             }
         }
-        const int nitem = nu << log_s;
+        const int nitem = whole + (rest << log_s);
+        // item -> its unit, and the part's first and last stage
+        auto item_of = [&](int item, int &group, int &unit, int &from, int &to) {
+            const int r = item - whole;
+            place(lo + (r < 0 ? item : whole + (r >> log_s)), group, unit);
+            const int part = r & ((1 << log_s) - 1);
+            from = r < 0 ? cs : cs + (part * nc >> log_s);
+            to = r < 0 ? ce : cs + ((part + 1) * nc >> log_s);
+        };
         Feed<FMT, DOWN> feed;
         feed.item = warp;
         feed.place(lane);
         int put = 0, get = 0;
         auto open = [&]() {
-            int group, unit;
-            place(lo + (feed.item >> log_s), group, unit);
-            const int part = feed.item & ((1 << log_s) - 1);
-            feed.begin(g, grp.expert[group], unit, cs + (part * nc >> log_s), cs + ((part + 1) * nc >> log_s), lane);
+            int group, unit, from, to;
+            item_of(feed.item, group, unit, from, to);
+            feed.begin(g, grp.expert[group], unit, from, to, lane);
         };
         auto next = [&]() {
             if (feed.item < nitem) {
@@ -644,30 +676,29 @@ k_few(FewArgs g) {
         };
 
         for (int item = warp; item < nitem; item += g.warps) {
-            int group, unit;
-            place(lo + (item >> log_s), group, unit);
-            const int part = item & ((1 << log_s) - 1);
+            int group, unit, from, to;
+            item_of(item, group, unit, from, to);
+            const bool one = item < whole || log_s == 0;
             // this lane's token column; past the last: any row
             const int at = min(grp.start[group] + (lane >> 2), grp.start[group + 1] - 1);
             const unsigned char *col = tok + (DOWN ? at - row0 : grp.token[at]) * g.bpitch;
             float r0, r1, acc[4] = {0.f, 0.f, 0.f, 0.f};
-            if (log_s == 0) row_scales(group, unit, r0, r1);
-            const int c1 = (part + 1) * nc >> log_s;
-            for (int c = part * nc >> log_s; c < c1; ++c) {
+            if (one) row_scales(group, unit, r0, r1);
+            for (int c = from; c < to; ++c) {
                 copies_wait<STAGES - 2>();
                 __syncwarp();                                   // every lane's copies are in, its reads of the stage before done
                 next();
-                stage_product<FMT>(acc, ring + get * kStageBytes, col + c * 2 * kStep, lane);
+                stage_product<FMT>(acc, ring + get * kStageBytes, col + (c - cs) * 2 * kStep, lane);
                 if (++get == STAGES) get = 0;
             }
-            if (log_s == 0) finish(group, unit, acc, r0, r1);
-            else parts[item * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (one) finish(group, unit, acc, r0, r1);
+            else parts[(item - whole) * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
         }
         if (log_s > 0) {
             __syncthreads();
-            for (int u = warp; u < nu; u += g.warps) {
+            for (int u = warp; u < rest; u += g.warps) {
                 int group, unit;
-                place(lo + u, group, unit);
+                place(lo + whole + u, group, unit);
                 float r0, r1;
                 row_scales(group, unit, r0, r1);
                 float4 s = parts[(u << log_s) * 32 + lane];
