@@ -592,10 +592,9 @@ int topo_expert_gemm_micro(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, 
  *   out[t] = sum over j of weights[t][j] * (W_down[e] a), e = ids[t][j],
  *   a = silu(g) * u,  [g | u] = W_up[e] x[t]
  * with all sums in float32; x and a enter the products as 16-bit floats of 11
- * bits over a power of two for each row, or each part of one (values more than
- * 2^28 below the row's largest lose bits, which changes the sum by less than
- * 2^-38 of the largest for each weight's magnitude); out is rounded once to
- * bf16.
+ * bits over a power of two for each row (values more than 2^28 below the row's
+ * largest lose bits, which changes the sum by less than 2^-38 of the largest for
+ * each weight's magnitude); out is rounded once to bf16.
  * x: device bf16 [T][H]; ids: device int32 [T][k] (an expert may occur twice in
  * a row; one outside [0, E) adds nothing and is reported); weights: device
  * float32 [T][k]; up: [E][2 I][H], gate rows then up rows, and down: [E][H][I]
@@ -608,9 +607,9 @@ int topo_expert_gemm_micro(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, 
  * 16, of 32 in 4 bits, up to 2^15; scales and pointers to rows 16-byte aligned.
  * ws: topo_few_workspace_bytes bytes, header included (0 for invalid sizes),
  * 16-byte aligned.  An expert's weights are read once for every 8 of its
- * tokens (fewer for I past 9000 or so), by launches of all T tokens (fewer
- * where T * k > 512 or 32 rows of H do not fit); where most experts have more
- * tokens than that, the path through topo_reroute_layout is the one to take.
+ * tokens (fewer for H or I past 9000 or so), by launches of all T tokens (fewer
+ * where T * k > 512); where most experts have more tokens than that, the path
+ * through topo_reroute_layout is the one to take.
  * Device errors: TOPO_ERANGE. */
 size_t topo_few_workspace_bytes(int32_t T, int32_t E, int32_t k, int32_t H, int32_t I);
 int topo_expert_few(int32_t T, int32_t E, int32_t k, int32_t H, int32_t I, int32_t fmt, const uint16_t *x,

@@ -15,9 +15,9 @@
 //           e4m3 and e2m1 are f16 values; scales by 128 and by 32 multiply a block's
 //           sum, scales by 16 the f16 weights (6 bits: exact)
 //   tokens  as f16 over a power of two for each row (its largest magnitude in
-//           [2^14, 2^15)): 11 bits, where bf16 has 8.  The up kernel holds all tokens'
-//           rows; where they do not fit, each CTA holds and contracts a part of H, and the
-//           down kernel adds the parts of g and u
+//           [2^14, 2^15)): 11 bits, where bf16 has 8.  The up kernel's CTAs hold all tokens'
+//           rows or, where they do not fit, those of their items' pairs; the down kernel's
+//           hold their items' activations
 //   sums    float32 throughout; each pair's outputs go to the workspace and are added in
 //           slot order, so no result depends on the order of the CTAs
 //
@@ -57,11 +57,10 @@ constexpr int kCols = 8;                          // token columns of a product
 constexpr int kMaxPairs = 512;                    // of one launch
 constexpr int kMaxRows = TOPO_FEW_MAX_TOKENS;     // token rows that a CTA holds
 constexpr int kMaxParts = 64;                     // partial tiles that it holds
-constexpr int kMaxSplit = 8;                      // parts of the up contraction, a power of two that divides 152
 
 struct FewArgs {
     const uint16_t *x;          // up: bf16 [T][K]
-    const float *act;           // down: the activations [T * k][K], or for split > 1 [split][T * k][2 K], parts of g and u
+    const float *act;           // down: the activations [T * k][K]
     const int32_t *ids;         // [T][k]
     const float *weights;       // [T][k]
     const uint8_t *w;           // [E][rows][K]
@@ -76,7 +75,7 @@ struct FewArgs {
     int units;                  // tiles of 16 rows of an expert
     uint32_t inv_units;         // 2^32 / units, rounded up (units > 1)
     int nc;                     // stages of a row
-    int split;                  // the up contraction's parts, each to its share of the CTAs
+    int resident;               // up: a CTA holds all tokens' rows; else those of a batch's pairs
     int64_t pitch;              // 4 bits: scale bytes of a row
     int bpitch;                 // bytes of a token row in shared memory
     int cols;                   // pairs of a group, at most kCols
@@ -328,26 +327,12 @@ __device__ __forceinline__ void convert_rows(unsigned char *tok, uint32_t *amax,
 
 __device__ __forceinline__ float gated(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
-// Four of a pair's activations: as the up kernel left them, or from its parts of g and u.
-__device__ __forceinline__ float4 act4(const FewArgs &g, int pair, int c) {
-    if (g.split == 1) return __ldcg(reinterpret_cast<const float4 *>(g.act + (int64_t)pair * g.K) + c);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-#pragma unroll
-    for (int p = 0; p < kMaxSplit; ++p) {
-        if (p >= g.split) break;
-        const float4 *src = reinterpret_cast<const float4 *>(g.act + ((int64_t)p * g.T * g.k + pair) * 2 * g.K);
-        const float4 v = __ldcg(src + c), w = __ldcg(src + g.K / 4 + c);
-        a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-        b.x += w.x, b.y += w.y, b.z += w.z, b.w += w.w;
-    }
-    return make_float4(gated(a.x, b.x), gated(a.y, b.y), gated(a.z, b.z), gated(a.w, b.w));
-}
-
 // An activation row as f16 in shared memory, in the same pieces; up to kKeep of them stay
 // in registers between the row's largest magnitude and the conversion, more are read twice.
 __device__ __forceinline__ void load_act(const FewArgs &g, unsigned char *tok, uint32_t *amax, bool on, int row, int pair, int c0,
                                          int dc, int kpad) {
     constexpr int kKeep = 4;
+    const float4 *src = reinterpret_cast<const float4 *>(g.act + (int64_t)pair * g.K);
     const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
     float4 v[kKeep][2];
     const int n = on ? (kpad / 8 - c0 + dc - 1) / dc : 0;
@@ -357,8 +342,8 @@ __device__ __forceinline__ void load_act(const FewArgs &g, unsigned char *tok, u
         for (int i = 0; i < kKeep; ++i) {
             const int c = c0 + (i0 + i) * dc;
             const bool in = i0 + i < n && c < g.K / 8;
-            v[i][0] = in ? act4(g, pair, 2 * c) : z;
-            v[i][1] = in ? act4(g, pair, 2 * c + 1) : z;
+            v[i][0] = in ? __ldcg(src + 2 * c) : z;
+            v[i][1] = in ? __ldcg(src + 2 * c + 1) : z;
         }
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) {
@@ -381,8 +366,8 @@ __device__ __forceinline__ void load_act(const FewArgs &g, unsigned char *tok, u
             const int c = c0 + (i0 + i) * dc;
             if (i0 + i >= n) break;
             if (n > kKeep) {
-                v[i][0] = c < g.K / 8 ? act4(g, pair, 2 * c) : z;
-                v[i][1] = c < g.K / 8 ? act4(g, pair, 2 * c + 1) : z;
+                v[i][0] = c < g.K / 8 ? __ldcg(src + 2 * c) : z;
+                v[i][1] = c < g.K / 8 ? __ldcg(src + 2 * c + 1) : z;
             }
             const float4 a = v[i][0], d = v[i][1];
             *reinterpret_cast<uint4 *>(tok + row * g.bpitch + 16 * c) =
@@ -528,11 +513,13 @@ k_few(FewArgs g) {
     unsigned char *tok = dyn + g.warps * STAGES * kStageBytes;
     float4 *parts = reinterpret_cast<float4 *>(tok + g.cap_rows * g.bpitch);   // [cap_parts][32]
     const int np = g.T * g.k;
-    // this CTA's part of the contraction, in stages, and its place among the CTAs of that part
-    const int sp = DOWN ? 0 : blockIdx.x % g.split, splits = DOWN ? 1 : g.split;
-    const int cs = sp * g.nc / splits, ce = (sp + 1) * g.nc / splits;
-    const int cta = blockIdx.x / splits, ctas = gridDim.x / splits;
-    const int kpad = (ce - cs) * kStep;
+    const int kpad = g.nc * kStep;
+    // token row t to row `to` of the CTA's, as bf16
+    auto bring = [&](int t, int to) {
+        const uint16_t *src = g.x + (int64_t)t * g.K;
+        for (int c = lane; c < kpad / 8; c += 32)
+            copy_n(smem_at(tok + to * g.bpitch + 16 * c), 8 * c < g.K ? src + 8 * c : src, 8 * c < g.K ? 16 : 0);
+    };
 
     // Up: everything before this call is done and seen from here on, and the down kernel,
     // which may start now, can rely on that for the ids and the weights.  The token rows are
@@ -543,12 +530,8 @@ k_few(FewArgs g) {
     }
     const int mine = np <= 32 ? lane : tid;
     const int id = mine < np ? __ldg(g.ids + mine) : -1;
-    if (!DOWN) {
-        for (int row = warp; row < g.T; row += g.warps)
-            for (int c = lane; c < kpad / 8; c += 32) {
-                const bool in = cs * kStep + 8 * c < g.K;
-                copy_n(smem_at(tok + row * g.bpitch + 16 * c), in ? g.x + (int64_t)row * g.K + cs * kStep + 8 * c : g.x, in ? 16 : 0);
-            }
+    if (!DOWN && g.resident) {
+        for (int row = warp; row < g.T; row += g.warps) bring(row, row);
         copies_end();
     }
     if (np <= 32) sort_few_pairs(g, grp, np, id, !DOWN && blockIdx.x == 0);
@@ -557,7 +540,7 @@ k_few(FewArgs g) {
     // Items: units of groups, group by group.  (Unit by unit, where a CTA has room for all
     // pairs' activations, fewer CTAs meet in a unit's sums, but each loads all activations:
     // 2.6 us more for one token's 8 x 2048, against 1 us less at the end.)
-    const int begin = (int)((int64_t)total * cta / ctas), hi = cta < ctas ? (int)((int64_t)total * (cta + 1) / ctas) : begin;
+    const int begin = (int)((int64_t)total * blockIdx.x / gridDim.x), hi = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
     auto place = [&](int gi, int &group, int &unit) {
         // gi / units, one too many at most (gi < 2^21, units <= 2^12)
         group = g.units == 1 ? gi : (int)__umulhi((uint32_t)gi, g.inv_units);
@@ -567,25 +550,30 @@ k_few(FewArgs g) {
             unit += g.units;
         }
     };
-    // Batches of items: up: all of them; down: of as many groups as there is room for the
-    // activations of their pairs.
+    // Batches of items: of as many groups as there is room for the rows of their pairs; all of
+    // them where the CTA holds all tokens' rows.
+    const bool by_pair = DOWN || !g.resident;
     for (int lo = begin; lo < hi;) {
         int end = hi, row0 = 0, rows = g.T;
-        if (DOWN) {
+        if (by_pair) {
             int g1 = lo / g.units + 1;
             row0 = grp.start[g1 - 1];
             while (g1 * g.units < hi && grp.start[g1 + 1] - row0 <= g.cap_rows) ++g1;
             end = min(hi, g1 * g.units);
             rows = grp.start[g1] - row0;
             if (lo != begin) __syncthreads();                   // the batch before is through with its rows
+            if (!DOWN) {
+                for (int row = warp; row < rows; row += g.warps) bring(grp.token[row0 + row], row);
+                copies_end();
+            }
         }
         // Whole units as long as there is one for each warp; the rest in parts of their
         // contraction, 2^log_s each, so that the warps end together
-        const int nu = end - lo, nc = ce - cs, whole = nu / g.warps * g.warps, rest = nu - whole;
+        const int nu = end - lo, whole = nu / g.warps * g.warps, rest = nu - whole;
         int log_s = 0;
         for (int s = 1, best = (rest + g.warps - 1) / g.warps * 16; s <= 4; ++s) {
             const int cost = ((rest << s) + g.warps - 1) / g.warps * (16 >> s);
-            if (rest << s <= g.cap_parts && 1 << s <= nc && cost < best) {
+            if (rest << s <= g.cap_parts && 1 << s <= g.nc && cost < best) {
                 best = cost;
                 log_s = s;
             }
@@ -596,8 +584,8 @@ k_few(FewArgs g) {
             const int r = item - whole;
             place(lo + (r < 0 ? item : whole + (r >> log_s)), group, unit);
             const int part = r & ((1 << log_s) - 1);
-            from = r < 0 ? cs : cs + (part * nc >> log_s);
-            to = r < 0 ? ce : cs + ((part + 1) * nc >> log_s);
+            from = r < 0 ? 0 : part * g.nc >> log_s;
+            to = r < 0 ? g.nc : (part + 1) * g.nc >> log_s;
         };
         Feed<FMT, DOWN> feed;
         feed.item = warp;
@@ -624,7 +612,7 @@ k_few(FewArgs g) {
 #pragma unroll
         for (int i = 0; i < STAGES - 1; ++i) next();
 
-        // token rows: up: all tokens; down: the activations of the batch's pairs
+        // token rows: up: as they came, made f16; down: the activations of the batch's pairs
         if (DOWN && lo == begin) {
             pdl_wait();
             pdl_trigger();
@@ -651,18 +639,14 @@ k_few(FewArgs g) {
             for (int h = 0; h < 2; ++h) {
                 if (at + h >= grp.start[group + 1]) continue;
                 const int pair = grp.pair[at + h];
-                const float s = pow2(row_exp(amax[DOWN ? at + h - row0 : grp.token[at + h]]));
+                const float s = pow2(row_exp(amax[by_pair ? at + h - row0 : grp.token[at + h]]));
                 const float v0 = acc[h] * r0 * s, v1 = acc[2 + h] * r1 * s;
                 if (DOWN) {
                     float *y = g.mid + (int64_t)pair * g.H + 16 * unit;
                     __stcg(y + r, v0);
                     __stcg(y + r + 8, v1);
-                } else if (g.split == 1) {
-                    __stcg(g.mid + (int64_t)pair * g.I + 8 * unit + r, gated(v0, v1));
                 } else {
-                    float *p = g.mid + ((int64_t)sp * np + pair) * 2 * g.I + 8 * unit + r;
-                    __stcg(p, v0);
-                    __stcg(p + g.I, v1);
+                    __stcg(g.mid + (int64_t)pair * g.I + 8 * unit + r, gated(v0, v1));
                 }
             }
         };
@@ -681,14 +665,14 @@ k_few(FewArgs g) {
             const bool one = item < whole || log_s == 0;
             // this lane's token column; past the last: any row
             const int at = min(grp.start[group] + (lane >> 2), grp.start[group + 1] - 1);
-            const unsigned char *col = tok + (DOWN ? at - row0 : grp.token[at]) * g.bpitch;
+            const unsigned char *col = tok + (by_pair ? at - row0 : grp.token[at]) * g.bpitch;
             float r0, r1, acc[4] = {0.f, 0.f, 0.f, 0.f};
             if (one) row_scales(group, unit, r0, r1);
             for (int c = from; c < to; ++c) {
                 copies_wait<STAGES - 2>();
                 __syncwarp();                                   // every lane's copies are in, its reads of the stage before done
                 next();
-                stage_product<FMT>(acc, ring + get * kStageBytes, col + (c - cs) * 2 * kStep, lane);
+                stage_product<FMT>(acc, ring + get * kStageBytes, col + c * 2 * kStep, lane);
                 if (++get == STAGES) get = 0;
             }
             if (one) finish(group, unit, acc, r0, r1);
@@ -770,13 +754,16 @@ cudaError_t run_few(FewArgs g, cudaStream_t st) {
     int stages = 4;
     g.warps = kMaxWarps;
     g.cols = kCols;
-    if (DOWN)                                                    // rows of a very wide layer
+    // all tokens' rows, where they leave 14 warps rings of 3 stages (32 tokens of 7168: 1094 us
+    // with rings of 14 x 3, 1188 of 16 x 4 beside rows of half the bytes)
+    g.resident = !DOWN && room(14, 3, g.T) >= kLeastParts;
+    if (!g.resident)                                             // rows of a very wide layer
         while (g.cols > 1 && room(8, 3, g.cols) < kLeastParts) --g.cols;
-    const int least = DOWN ? g.cols : g.T;                       // rows: of a group, or all tokens
+    const int least = g.resident ? g.T : g.cols;
     if (room(g.warps, stages, least) < kLeastParts) stages = 3;
     while (g.warps > 8 && room(g.warps, stages, least) < kLeastParts) g.warps -= 2;
     g.cap_rows = least;
-    while (DOWN && g.cap_rows < kMaxRows && room(g.warps, stages, g.cap_rows + 1) >= kLeastParts) ++g.cap_rows;
+    while (!g.resident && g.cap_rows < kMaxRows && room(g.warps, stages, g.cap_rows + 1) >= kLeastParts) ++g.cap_rows;
     if (room(g.warps, stages, g.cap_rows) < 0) return cudaErrorInvalidValue;
     g.cap_parts = (int)std::min<int64_t>(kMaxParts, room(g.warps, stages, g.cap_rows) / 512);
     const size_t smem = (size_t)g.warps * stages * kStageBytes + (size_t)g.cap_rows * g.bpitch + (size_t)g.cap_parts * 512;
@@ -796,37 +783,17 @@ cudaError_t run_both(FewArgs up, FewArgs down, cudaStream_t st) {
 
 }  // namespace
 
-// Tokens of a launch, and the parts of the up contraction: as few as leave 14 warps rings
-// of 3 stages beside the token rows (32 tokens of 7168 in 4 parts and 14 x 3: 1094 us, in 8
-// parts and 16 x 4: 1188; 8 tokens in one part and 14 x 3 or in two and 16 x 4: the same).
-// Wider rows take fewer tokens.
-static int few_tokens(int T, int k, int H, int fmt, int *split) {
-    const int step = fmt == TOPO_FMT_EIGHT ? 128 : 256;
-    const int64_t room = kFewSmem - (int64_t)14 * 3 * kStageBytes - kLeastParts;
-    const int nc = (H + step - 1) / step;
-    for (int n = std::min(std::min(T, kMaxPairs / k), kMaxRows); n > 1; --n)
-        for (*split = 1; *split <= kMaxSplit && *split <= nc; *split *= 2)
-            if (n * (int64_t)token_pitch((nc + *split - 1) / *split * step, fmt) <= room) return n;
-    *split = 1;
-    return 1;
-}
+static int few_tokens(int T, int k) { return std::min(T, kMaxPairs / k); }      // of a launch
 
 size_t few_workspace(int T, int k, int H, int I) {
-    size_t most = 0;
-    for (int fmt : {TOPO_FMT_EIGHT, TOPO_FMT_MX}) {
-        int split;
-        const size_t pairs = (size_t)few_tokens(T, k, H, fmt, &split) * k;
-        most = std::max(most, pairs * ((size_t)H + (split == 1 ? 1 : 2 * (size_t)split) * I));
-    }
-    return sizeof(WsHeader) + most * sizeof(float);
+    return sizeof(WsHeader) + (size_t)few_tokens(T, k) * k * ((size_t)H + I) * sizeof(float);
 }
 
 cudaError_t launch_expert_few(int T, int E, int k, int H, int I, int fmt, const uint16_t *x, const int32_t *ids,
                               const float *weights, const uint8_t *up, const void *up_scale, const float *up_row,
                               const uint8_t *down, const void *down_scale, const float *down_row, uint16_t *out, void *ws,
                               cudaStream_t st) {
-    int split = 1;
-    const int per = few_tokens(T, k, H, fmt, &split);
+    const int per = few_tokens(T, k);
     const int step = fmt == TOPO_FMT_EIGHT ? 128 : 256;          // values of a stage
     for (int t0 = 0; t0 < T; t0 += per) {
         FewArgs a = {};
@@ -835,7 +802,6 @@ cudaError_t launch_expert_few(int T, int E, int k, int H, int I, int fmt, const 
         a.k = k;
         a.H = H;
         a.I = I;
-        a.split = split;
         a.ids = ids + (int64_t)t0 * k;
         a.weights = weights + (int64_t)t0 * k;
         a.hdr = ws_at<WsHeader>(ws, 0);
@@ -864,7 +830,7 @@ cudaError_t launch_expert_few(int T, int E, int k, int H, int I, int fmt, const 
             p->inv_units = (uint32_t)((((uint64_t)1 << 32) + p->units - 1) / p->units);
             p->pitch = fmt == TOPO_FMT_EIGHT ? 0 : micro_pitch(p->K, fmt);
         }
-        a.bpitch = token_pitch((a.nc + split - 1) / split * step, fmt);
+        a.bpitch = token_pitch(a.nc * step, fmt);
         d.bpitch = token_pitch(d.nc * step, fmt);
         const cudaError_t e = fmt == TOPO_FMT_EIGHT ? run_both<TOPO_FMT_EIGHT>(a, d, st)
                               : fmt == TOPO_FMT_MX ? run_both<TOPO_FMT_MX>(a, d, st) : run_both<TOPO_FMT_NV>(a, d, st);

@@ -105,7 +105,8 @@ class Case:
                                        (5, 300, 2, 32, 64), (1, 9, 8, 7168, 256), (4, 3, 2, 64, 4096), (8, 6, 6, 8224, 64),
                                        (8, 1024, 8, 64, 32), (32, 3, 2, 7168, 32), (20, 2, 1, 5152, 64), (32, 20, 16, 7168, 32),
                                        (3, 2, 2, 32768, 32), (32, 2, 1, 8224, 32), (5, 2, 2, 64, 16416), (1, 1, 1, 32, 32768),
-                                       (32, 1, 1, 64, 9248), (20, 6, 64, 64, 32), (17, 1, 1, 32768, 32)])
+                                       (32, 1, 1, 64, 9248), (20, 6, 64, 64, 32), (17, 1, 1, 32768, 32),
+                                       (32, 2, 16, 7168, 32), (32, 2, 16, 64, 9248), (32, 200, 16, 4128, 32)])
 def test_few(T, E, k, H, I, fmt):
     c = Case(T, E, k, H, I, fmt)
     got, ws = c.run()
