@@ -24,11 +24,11 @@
 // The down kernel starts as the up kernel's CTAs end (its first weights do not depend on
 // it) and waits for all of it before it reads the activations.
 //
-// Measured (host call after call, E = 256 of 7168 x 2048, k = 8): one token in 8 bits 63 to
-// 66 us, 5.4 TB/s of weights, the up kernel's steady part at 7 TB/s; 32 tokens in MX 736 to
-// 768 us, 5.0 to 5.2 TB/s.  One token of 2048 x 768 in MX 17.6 us; 8 tokens of 64 experts,
+// Measured (host call after call, E = 256 of 7168 x 2048, k = 8): one token in 8 bits 62 to
+// 66 us, 5.4 to 5.7 TB/s of weights, the up kernel's steady part at 7 TB/s; 32 tokens in MX
+// 661 to 709 us, 5.4 to 5.8 TB/s.  One token of 2048 x 768 in MX 16 us; 8 tokens of 64 experts,
 // 4096 x 1408, k = 6, NV 74 to 77 us, 4.4 to 4.6 TB/s.  What bounds it: in 8 bits memory,
-// and about 4 us to the first product of either kernel (the ids' round trip, the sort, the
+// and 3 to 4 us to the first product of either kernel (the ids' round trip, the sort, the
 // first items' addresses, the rows' conversion: instructions, not waits); in 4 bits the
 // issue of 275 instructions (NV; MX 243) for a stage of 4096 weights at 58 to 63 percent of
 // the slots with 16 warps of 128 registers.  Tried: 20 or 24 warps (fewer registers, spills):
@@ -36,7 +36,9 @@
 // the smallest layer, 5 to 25 slower elsewhere; rows of 144 bytes with their scales instead
 // of the exclusive or: 5 percent slower; weights first to leave the L2: equal; the last sum
 // in the down kernel, by the CTA that brings a tile's last expert: equal at one token,
-// 1186 us against 736 at 32.
+// 1186 us against 736 at 32; the up contraction split over CTAs, so that each holds a part
+// of all tokens' rows: 756 us against 709 at 32 tokens, 173 against 125 with 64 experts of
+// 4096 x 1408 (items of four stages).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
