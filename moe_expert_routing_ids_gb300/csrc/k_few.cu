@@ -75,7 +75,7 @@ struct FewArgs {
     int K, I, H;                // values contracted; the layer's sizes
     int rows;                   // weight rows of an expert
     int units;                  // tiles of 16 rows of an expert
-    uint32_t inv_units;         // 2^32 / units, rounded up (units > 1)
+    uint32_t inv_units, inv_warps, inv_k;   // 2^32 over units, warps, k, rounded up (where that is above 1)
     int nc;                     // stages of a row
     int resident;               // up: a CTA holds all tokens' rows; else those of a batch's pairs
     int64_t pitch;              // 4 bits: scale bytes of a row
@@ -391,6 +391,8 @@ struct Groups {
     int n;                                          // groups
 };
 
+__device__ __forceinline__ int token_of(const FewArgs &g, int pair) { return g.k == 1 ? pair : (int)__umulhi((uint32_t)pair, g.inv_k); }
+
 // np <= 32: each warp does it for itself, all of them writing the same; id: the lane's.
 // No barrier: 0.7 us sooner than below at 8 pairs, where the weights' first bytes wait for it.
 __device__ __forceinline__ void sort_few_pairs(const FewArgs &g, Groups &s, int np, int id, bool report) {
@@ -410,7 +412,7 @@ __device__ __forceinline__ void sort_few_pairs(const FewArgs &g, Groups &s, int 
     for (int q = 0; q < np; ++q) group += __shfl_sync(0xffffffffu, mine, q) < at;
     if (ok) {
         s.pair[at] = (uint16_t)lane;
-        s.token[at] = (uint8_t)(lane / g.k);
+        s.token[at] = (uint8_t)token_of(g, lane);
         if (opens) {
             s.expert[group] = (uint16_t)e;
             s.start[group] = (uint16_t)at;
@@ -497,7 +499,7 @@ __device__ __forceinline__ void sort_pairs(const FewArgs &g, Groups &s, uint32_t
         else
             to += rank[j];
         s.pair[to] = (uint16_t)i;
-        s.token[to] = (uint8_t)(i / g.k);
+        s.token[to] = (uint8_t)token_of(g, i);
     }
     __syncthreads();
 }
@@ -544,7 +546,8 @@ k_few(FewArgs g) {
     // 2.6 us more for one token's 8 x 2048, against 1 us less at the end.)
     const int begin = (int)((int64_t)total * blockIdx.x / gridDim.x), hi = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
     auto place = [&](int gi, int &group, int &unit) {
-        // gi / units, one too many at most (gi < 2^21, units <= 2^12)
+        // gi / units, one too many at most (gi < 2^21, units <= 2^12).  Every warp works the
+        // items out for itself: with the compiler's divisions that took 1 us
         group = g.units == 1 ? gi : (int)__umulhi((uint32_t)gi, g.inv_units);
         unit = gi - group * g.units;
         if (unit < 0) {
@@ -558,8 +561,9 @@ k_few(FewArgs g) {
     for (int lo = begin; lo < hi;) {
         int end = hi, row0 = 0, rows = g.T;
         if (by_pair) {
-            int g1 = lo / g.units + 1;
-            row0 = grp.start[g1 - 1];
+            int g1, unit0;
+            place(lo, g1, unit0);
+            row0 = grp.start[g1++];
             while (g1 * g.units < hi && grp.start[g1 + 1] - row0 <= g.cap_rows) ++g1;
             end = min(hi, g1 * g.units);
             rows = grp.start[g1] - row0;
@@ -571,10 +575,11 @@ k_few(FewArgs g) {
         }
         // Whole units as long as there is one for each warp; the rest in parts of their
         // contraction, 2^log_s each, so that the warps end together
-        const int nu = end - lo, whole = nu / g.warps * g.warps, rest = nu - whole;
+        const int nu = end - lo, whole = (int)__umulhi((uint32_t)nu, g.inv_warps) * g.warps, rest = nu - whole;
         int log_s = 0;
-        for (int s = 1, best = (rest + g.warps - 1) / g.warps * 16; s <= 4; ++s) {
-            const int cost = ((rest << s) + g.warps - 1) / g.warps * (16 >> s);
+#pragma unroll
+        for (int s = 1, best = rest > 0 ? 16 : 0; s <= 4; ++s) {
+            const int cost = (int)__umulhi((uint32_t)((rest << s) + g.warps - 1), g.inv_warps) * (16 >> s);
             if (rest << s <= g.cap_parts && 1 << s <= g.nc && cost < best) {
                 best = cost;
                 log_s = s;
@@ -745,6 +750,8 @@ k_few_sum(FewArgs g) {
 constexpr size_t kFewSmem = 218 * 1024;           // dynamic; the tables take 7 KB
 constexpr int kLeastParts = 16 * 512;
 
+uint32_t over(int n) { return (uint32_t)((((uint64_t)1 << 32) + n - 1) / n); }     // 2^32 / n, for n > 1
+
 // A token row's bytes: 16 or 64 past a multiple of 128 (the lanes' bank pattern).
 int token_pitch(int values, int fmt) { return 2 * values + (fmt == TOPO_FMT_EIGHT ? 16 : 64); }
 
@@ -767,6 +774,7 @@ cudaError_t run_few(FewArgs g, cudaStream_t st) {
     g.cap_rows = least;
     while (!g.resident && g.cap_rows < kMaxRows && room(g.warps, stages, g.cap_rows + 1) >= kLeastParts) ++g.cap_rows;
     if (room(g.warps, stages, g.cap_rows) < 0) return cudaErrorInvalidValue;
+    g.inv_warps = over(g.warps);
     g.cap_parts = (int)std::min<int64_t>(kMaxParts, room(g.warps, stages, g.cap_rows) / 512);
     const size_t smem = (size_t)g.warps * stages * kStageBytes + (size_t)g.cap_rows * g.bpitch + (size_t)g.cap_parts * 512;
     const auto fn = stages == 4 ? k_few<FMT, DOWN, 4> : k_few<FMT, DOWN, 3>;
@@ -829,7 +837,8 @@ cudaError_t launch_expert_few(int T, int E, int k, int H, int I, int fmt, const 
         d.units = H / 16;
         for (FewArgs *p : {&a, &d}) {
             p->nc = (p->K + step - 1) / step;
-            p->inv_units = (uint32_t)((((uint64_t)1 << 32) + p->units - 1) / p->units);
+            p->inv_units = over(p->units);
+            p->inv_k = over(k);
             p->pitch = fmt == TOPO_FMT_EIGHT ? 0 : micro_pitch(p->K, fmt);
         }
         a.bpitch = token_pitch(a.nc * step, fmt);
