@@ -401,15 +401,22 @@ __device__ __forceinline__ void sort_few_pairs(const FewArgs &g, Groups &s, int 
     if (in && !ok && report) set_error(g.hdr, TOPO_ERANGE);
     const int e = ok ? id : g.E;
     int less = 0, same = 0;
-    for (int q = 0; q < np; ++q) {
-        const int f = __shfl_sync(0xffffffffu, e, q);
-        less += f < e;
-        same += f == e && q < lane;
+    // eight lanes at once: those from np on hold E, which is below none
+    for (int q0 = 0; q0 < np; q0 += 8) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int f = __shfl_sync(0xffffffffu, e, q0 + q);
+            less += f < e;
+            same += f == e && q0 + q < lane;
+        }
     }
     const bool opens = ok && same % g.cols == 0;
     const int at = less + same, mine = opens ? at : 64;
     int group = 0;
-    for (int q = 0; q < np; ++q) group += __shfl_sync(0xffffffffu, mine, q) < at;
+    for (int q0 = 0; q0 < np; q0 += 8) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) group += __shfl_sync(0xffffffffu, mine, q0 + q) < at;
+    }
     if (ok) {
         s.pair[at] = (uint16_t)lane;
         s.token[at] = (uint8_t)token_of(g, lane);
@@ -717,29 +724,38 @@ k_few(FewArgs g) {
 __global__ void __launch_bounds__(128)
 k_few_sum(FewArgs g) {
     const int i = blockIdx.x * blockDim.x + threadIdx.x, n4 = g.H / 4;
+    const int t = min(i / n4, g.T - 1), q = i - t * n4;
+    // the ids and weights are older than the up kernel, for which the down kernel waited
+    // before it let this one start
+    int id[8];
+    float w[8];
+    auto slots = [&](int j0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            id[j] = j0 + j < g.k ? __ldg(g.ids + t * g.k + j0 + j) : -1;
+            w[j] = j0 + j < g.k ? __ldg(g.weights + t * g.k + j0 + j) : 0.f;
+        }
+    };
+    slots(0);
     pdl_trigger();
     pdl_wait();
     if (i >= g.T * n4) return;
-    const int t = i / n4, q = i - t * n4;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     const float *y = g.mid + (int64_t)t * g.k * g.H + 4 * q;
     for (int j0 = 0; j0 < g.k; j0 += 8) {
         float4 v[8];
-        float w[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            // an id outside [0, E) has no output
-            const bool in = j0 + j < g.k && (unsigned)__ldg(g.ids + t * g.k + j0 + j) < (unsigned)g.E;
-            v[j] = in ? __ldcg(reinterpret_cast<const float4 *>(y + (int64_t)(j0 + j) * g.H)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            w[j] = in ? __ldg(g.weights + t * g.k + j0 + j) : 0.f;
-        }
+        for (int j = 0; j < 8; ++j)
+            if (j0 + j < g.k) v[j] = __ldcg(reinterpret_cast<const float4 *>(y + (int64_t)(j0 + j) * g.H));
+        if (j0 > 0) slots(j0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            o.x += w[j] * v[j].x;
-            o.y += w[j] * v[j].y;
-            o.z += w[j] * v[j].z;
-            o.w += w[j] * v[j].w;
-        }
+        for (int j = 0; j < 8; ++j)
+            if ((unsigned)id[j] < (unsigned)g.E) {               // an id outside has no output
+                o.x += w[j] * v[j].x;
+                o.y += w[j] * v[j].y;
+                o.z += w[j] * v[j].z;
+                o.w += w[j] * v[j].w;
+            }
     }
     const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
     *reinterpret_cast<uint2 *>(g.out + (int64_t)t * g.H + 4 * q) =
