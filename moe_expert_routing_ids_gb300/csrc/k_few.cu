@@ -24,10 +24,10 @@
 // The down kernel starts as the up kernel's CTAs end (its first weights do not depend on
 // it) and waits for all of it before it reads the activations.
 //
-// Measured (host call after call, E = 256 of 7168 x 2048, k = 8): one token in 8 bits 62 to
-// 66 us, 5.4 to 5.7 TB/s of weights, the up kernel's steady part at 7 TB/s; 32 tokens in MX
-// 661 to 709 us, 5.4 to 5.8 TB/s.  One token of 2048 x 768 in MX 16 us; 8 tokens of 64 experts,
-// 4096 x 1408, k = 6, NV 74 to 77 us, 4.4 to 4.6 TB/s.  What bounds it: in 8 bits memory,
+// Measured (host call after call, E = 256 of 7168 x 2048, k = 8): one token in 8 bits 61 to
+// 64 us, 5.5 to 5.8 TB/s of weights, the up kernel's steady part at 7 TB/s; 32 tokens in MX
+// 661 to 711 us, 5.4 to 5.8 TB/s.  One token of 2048 x 768 in MX 15 us; 8 tokens of 64 experts,
+// 4096 x 1408, k = 6, NV 73 to 75 us, 4.6 to 4.7 TB/s.  What bounds it: in 8 bits memory,
 // and 3 to 4 us to the first product of either kernel (the ids' round trip, the sort, the
 // first items' addresses, the rows' conversion: instructions, not waits); in 4 bits the
 // issue of 275 instructions (NV; MX 243) for a stage of 4096 weights at 58 to 63 percent of
