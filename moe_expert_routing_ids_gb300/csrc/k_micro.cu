@@ -18,6 +18,7 @@
 //   k_micro_rows     rows as they are, dispatch rows (by position, or token row t to the
 //                    k layout positions of its pairs), or the gated activation
 //                    silu(g) * u of rows [g | u]
+//   k_micro_narrow   the same for rows of up to 512 values, several to a warp
 //   k_micro_values   the bf16 values that such rows stand for
 //
 // A lane takes 16 consecutive values (32 bytes in, 8 bytes out): a block of NV, half
@@ -95,6 +96,7 @@ struct MicroArgs {
     int nv;                  // 16-value groups per (output) row
     int pitch;
     int log_w;               // a row is split over 2^log_w warps, at most 8
+    int log_l;               // k_micro_narrow: a row takes 2^log_l lanes
 };
 
 // Bits of the largest finite magnitude of 16 values.
@@ -162,22 +164,24 @@ __device__ __forceinline__ void gated(float (&v)[16], const float (&u)[16], bool
 // (the activation's as float32).
 // Measured in groups, CTAs to an SM: activation of 131072 x 2048 to MX 1, 4: 221 us, 1, 5: 231,
 // 2, 3: 204, 2, 4: 193, 3, 2: 310; to NV 1, 5: 296, 2, 3: 246, 2, 4: 236; rows of 131072 x 7168 to
-// NV 4, 3: 429, 4, 4: 399, 5, 3: 458.
+// NV 4, 3: 429, 4, 4: 399, 5, 3: 458.  run_rows takes the activation's three, 3 CTAs, where
+// they need half as many warps.
 template <int SRC>
 constexpr int kGroups = SRC == kSwiglu ? 2 : 4;
-constexpr int kCtas = 4;                                        // to an SM
+constexpr int ctas(int src, int n) { return src == kSwiglu && n == 3 ? 3 : 4; }   // to an SM
 
-template <int SRC>
+template <int SRC, int N>
 struct Groups {
-    static constexpr int kN = kGroups<SRC>;
+    static constexpr int kN = N;
     uint4 a[kN][2];
 
-    __device__ __forceinline__ void load(const MicroArgs &g, int64_t from, int c0) {
-        const uint4 *src = g.x + from * (2 * (int64_t)g.nv);
+    // Group j at src(j), zeros where in(j) is false.
+    template <class Src, class In, class Any>
+    __device__ __forceinline__ void load(int, Src src, In in, Any) {
 #pragma unroll
         for (int j = 0; j < kN; ++j)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) a[j][i] = c0 + 32 * j < g.nv ? __ldg(src + 2 * (c0 + 32 * j) + i) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 2; ++i) a[j][i] = in(j) ? __ldg(src(j) + i) : make_uint4(0, 0, 0, 0);
     }
     __device__ __forceinline__ void get(int j, float (&v)[16]) const { unpack16(a[j][0], a[j][1], v); }
     // Bits (float32) of the largest magnitude of group j, as NaN > infinity > finite values.
@@ -189,23 +193,26 @@ struct Groups {
         return max(m << 16, m & 0xffff0000u);
     }
 };
-template <>
-struct Groups<kSwiglu> {
-    static constexpr int kN = kGroups<kSwiglu>;
+template <int N>
+struct Groups<kSwiglu, N> {
+    static constexpr int kN = N;
     float f[kN][16];
 
-    __device__ __forceinline__ void load(const MicroArgs &g, int64_t from, int c0) {
-        const uint4 *src = g.x + from * (4 * (int64_t)g.nv);
+    // any(j), the same for the whole warp: a lane has a group j.
+    template <class Src, class In, class Any>
+    __device__ __forceinline__ void load(int nv, Src src, In in, Any any) {
         uint4 a[kN][4];
 #pragma unroll
         for (int j = 0; j < kN; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c = c0 + 32 * j;
-                a[j][i] = c < g.nv ? __ldg(src + 2 * (i < 2 ? c : g.nv + c) + (i & 1)) : make_uint4(0, 0, 0, 0);
-            }
+            for (int i = 0; i < 4; ++i) a[j][i] = in(j) ? __ldg(src(j) + (i < 2 ? 0 : 2 * nv) + (i & 1)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
+            if (!any(j)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[j][i] = 0.f;
+                continue;
+            }
             const uint32_t w[8] = {a[j][0].x, a[j][0].y, a[j][0].z, a[j][0].w, a[j][1].x, a[j][1].y, a[j][1].z, a[j][1].w};
             uint32_t most = 0;                                  // as 16-bit words: the most negative value
 #pragma unroll
@@ -234,13 +241,51 @@ struct Groups<kSwiglu> {
     }
 };
 
+// A block's scale byte, v divided by the scale.  m: bits of the 16 values' largest magnitude,
+// n: NV: exponent of the row's scale.
+template <bool NV>
+__device__ __forceinline__ uint32_t to_block(float (&v)[16], uint32_t m, int n) {
+    uint32_t sb;
+    if (NV) {
+        // t / 6, at most 448, rounded up to e4m3 (the quotient's last bits are cut, so that
+        // 6 times a scale gives the scale): a mantissa of 3 bits, or a multiple of 2^-9
+        const float t = __fmul_rz(__uint_as_float(m) * pow2(-n), 1.f / 6.f);
+        const uint32_t up = __float_as_uint(t) + 0xfffffu, low = __float_as_uint(__fadd_ru(t, 0x1p14f));
+        float s = __uint_as_float(up & 0xfff00000u);
+        sb = (up >> 20) - 960;
+        if (t < 0x1p-6f) {
+            s = fmaxf(__uint_as_float(low) - 0x1p14f, 0x1p-9f);   // t may underflow
+            sb = max(low & 0xffu, 1u);
+        }
+        if (m == 0u) s = 1.f, sb = 0x38u;
+        if (n < -112) {                                  // 1 / (s g) might be past float32's range
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] *= 0x1p16f;
+        }
+        const float sg = s * pow2(n < -112 ? n + 16 : n);
+        float si;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(si) : "f"(sg));
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) halves(mul2(pair(v[i], v[i + 1]), both(si)), v[i], v[i + 1]);
+        if (m >= kInf) sb = 0x7fu;
+    } else {
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        n = m < kInf ? least_power(m, 0x400000u, 2) : 0;   // 6 = 1.5 * 2^2
+        const float inv = pow2(-n);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) halves(mul2(pair(v[i], v[i + 1]), both(inv)), v[i], v[i + 1]);
+        sb = m < kInf ? (uint32_t)(127 + n) : 255u;
+    }
+    return sb;
+}
+
 // 2^log_w warps take a row, each kGroups * 32 groups of 16 values side by side; a row that
 // is longer than eight warps' goes round (NV: and is read twice, once for its largest
 // magnitude).  All of a lane's loads are on their way before the first is used.
-template <int SRC, bool NV>
-__global__ void __launch_bounds__(256, kCtas)
+template <int SRC, bool NV, int N>
+__global__ void __launch_bounds__(256, ctas(SRC, N))
 k_micro_rows(MicroArgs g) {
-    constexpr int kPer = kGroups<SRC> * 32;
+    constexpr int kPer = N * 32;
     __shared__ uint32_t wmax[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = warp & ((1 << g.log_w) - 1);
@@ -272,17 +317,22 @@ k_micro_rows(MicroArgs g) {
     if (!live) from = 0;
     const int first = part * kPer + lane, span = kPer << g.log_w;
     const int nv = live ? (g.nv + 31) & ~31 : 0;                 // whole warps of groups
-    Groups<SRC> in_regs;
+    Groups<SRC, N> in_regs;
+    const uint4 *const src = g.x + from * ((SRC == kSwiglu ? 4 : 2) * (int64_t)g.nv);
+    const auto load = [&](int c0) {
+        in_regs.load(g.nv, [&](int j) { return src + 2 * (c0 + 32 * j); }, [&](int j) { return c0 + 32 * j < g.nv; },
+                     [](int) { return true; });
+    };
     float v[16];
-    uint32_t am[kGroups<SRC>];                                   // the groups' largest magnitudes
+    uint32_t am[N];                                   // the groups' largest magnitudes
     int n = 0;                                                   // NV: exponent of the row's scale
     if (NV) {
         // the whole row's largest finite magnitude first
         uint32_t m = 0;
         for (int c0 = first; c0 - lane < nv; c0 += span) {
-            in_regs.load(g, from, c0);
+            load(c0);
 #pragma unroll
-            for (int j = 0; j < kGroups<SRC>; ++j) {
+            for (int j = 0; j < N; ++j) {
                 am[j] = in_regs.amax(j);
                 uint32_t a = am[j];
                 if (a >= kInf) {
@@ -309,47 +359,17 @@ k_micro_rows(MicroArgs g) {
     }
     for (int c0 = first; c0 - lane < nv; c0 += span) {
         if (!NV || g.nv > span) {
-            in_regs.load(g, from, c0);
+            load(c0);
 #pragma unroll
-            for (int j = 0; j < kGroups<SRC>; ++j) am[j] = in_regs.amax(j);
+            for (int j = 0; j < N; ++j) am[j] = in_regs.amax(j);
         }
 #pragma unroll
-        for (int j = 0; j < kGroups<SRC>; ++j) {
+        for (int j = 0; j < N; ++j) {
             const int c = c0 + 32 * j;
             if (c - lane >= nv) break;                           // whole warp
             const bool in = c < g.nv;
             in_regs.get(j, v);
-            uint32_t m = am[j], sb;
-            if (NV) {
-                // t / 6, at most 448, rounded up to e4m3 (the quotient's last bits are cut, so that
-                // 6 times a scale gives the scale): a mantissa of 3 bits, or a multiple of 2^-9
-                const float t = __fmul_rz(__uint_as_float(m) * pow2(-n), 1.f / 6.f);
-                const uint32_t up = __float_as_uint(t) + 0xfffffu, low = __float_as_uint(__fadd_ru(t, 0x1p14f));
-                float s = __uint_as_float(up & 0xfff00000u);
-                sb = (up >> 20) - 960;
-                if (t < 0x1p-6f) {
-                    s = fmaxf(__uint_as_float(low) - 0x1p14f, 0x1p-9f);   // t may underflow
-                    sb = max(low & 0xffu, 1u);
-                }
-                if (m == 0u) s = 1.f, sb = 0x38u;
-                if (n < -112) {                                  // 1 / (s g) might be past float32's range
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] *= 0x1p16f;
-                }
-                const float sg = s * pow2(n < -112 ? n + 16 : n);
-                float si;
-                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(si) : "f"(sg));
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) halves(mul2(pair(v[i], v[i + 1]), both(si)), v[i], v[i + 1]);
-                if (m >= kInf) sb = 0x7fu;
-            } else {
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                const int n = m < kInf ? least_power(m, 0x400000u, 2) : 0;   // 6 = 1.5 * 2^2
-                const float inv = pow2(-n);
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) halves(mul2(pair(v[i], v[i + 1]), both(inv)), v[i], v[i + 1]);
-                sb = m < kInf ? (uint32_t)(127 + n) : 255u;
-            }
+            uint32_t sb = to_block<NV>(v, am[j], n);
             constexpr bool kHalf = NV && SRC != kSwiglu;
             const uint2 q = make_uint2(e2m1x8<kHalf>(v), e2m1x8<kHalf>(v + 8));
             // four blocks' scales to a word, on the first of their lanes; bytes past the last
@@ -370,6 +390,103 @@ k_micro_rows(MicroArgs g) {
                 if (in) g.q[row * g.nv + c] = q;
                 if (word) *reinterpret_cast<uint32_t *>(g.scale + row * g.pitch + at) = sb;
             }
+        }
+    }
+}
+
+// Rows of at most 32 groups: 2^log_l lanes take one, the groups of a lane are of kGroups
+// rows, 32 / 2^log_l apart, so that all lanes have work and as many loads on their way as
+// with a longer row.  131072 rows to MX / NV, against a warp for each row: of 128 values 6.7 /
+// 9.2 us and 36.7 / 53.1 (6.6 / 4.8 TB/s), of 512 values 27.4 / 34.6 and 42.4 / 57.8; activation
+// of 512 values 54 / 61 and 85 / 100; dispatch of 16384 tokens by token, k = 8, of 128 values
+// 10.0 / 12.7 and 47.1 / 66.5.
+template <int SRC, bool NV>
+__global__ void __launch_bounds__(256, 4)
+k_micro_narrow(MicroArgs g) {
+    constexpr int kN = kGroups<SRC>;
+    constexpr int kLanes = NV ? 4 : 8;                           // lanes of a word of scales
+    constexpr uint32_t kOne = NV ? 0x38u : 127u;                 // the scale 1
+    const int lane = threadIdx.x & 31, lanes = 1 << g.log_l, sub = lane & (lanes - 1), apart = 32 >> g.log_l;
+    const int64_t row0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * (kN * apart) + (lane >> g.log_l);
+    const uint32_t mine = (0xffffffffu >> (32 - lanes)) << (lane - sub);   // the row's lanes
+    const uint4 *src[kN];
+    const int32_t *inv[kN];                                      // kScatter: the token's positions
+    int64_t base[kN];
+    bool live[kN];
+    pdl_trigger();
+    pdl_wait();
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        const int64_t row = row0 + j * apart;
+        int64_t from = row;
+        live[j] = row < g.rows;
+        if (SRC == kGather && live[j]) {
+            const int p = __ldg(g.inv + row);
+            if ((uint64_t)p >= (uint64_t)g.npairs) {
+                if (sub == 0) set_error(g.hdr, TOPO_ESTATE);
+                live[j] = false;
+            }
+            from = row / g.npairs * g.T + p / g.k;
+        }
+        if (SRC == kScatter) {
+            base[j] = row / g.T * g.npairs;
+            inv[j] = g.inv + row * g.k;
+            bool bad = false;
+            if (live[j])
+                for (int i = sub; i < g.k; i += lanes) bad |= (uint64_t)__ldg(inv[j] + i) >= (uint64_t)g.npairs;
+            if (__ballot_sync(0xffffffffu, bad) & mine) {
+                if (sub == 0) set_error(g.hdr, TOPO_ESTATE);
+                live[j] = false;
+            }
+        }
+        src[j] = g.x + ((live[j] ? from : 0) * (SRC == kSwiglu ? 2 : 1) * g.nv + sub) * 2;
+    }
+    Groups<SRC, kN> in_regs;
+    in_regs.load(g.nv, [&](int j) { return src[j]; }, [&](int j) { return live[j] && sub < g.nv; },
+                 [&](int j) { return __any_sync(0xffffffffu, live[j]) != 0; });
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        if (!__any_sync(0xffffffffu, live[j])) continue;
+        const int64_t row = row0 + j * apart;
+        float v[16];
+        in_regs.get(j, v);
+        const uint32_t am = in_regs.amax(j);
+        int n = 0;
+        if (NV) {
+            uint32_t m = am < kInf ? am : finite_bits(v);
+            for (int d = lanes >> 1; d; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+            n = least_power(m, 0x280000u, 11);
+        }
+        uint32_t sb = to_block<NV>(v, am, n);
+        constexpr bool kHalf = NV && SRC != kSwiglu;
+        const uint2 q = make_uint2(e2m1x8<kHalf>(v), e2m1x8<kHalf>(v + 8));
+        // sixteen blocks' scales on the first of their lanes; those past the row's lanes are 1
+        uint32_t w[4];
+        const uint32_t s1 = __shfl_down_sync(0xffffffffu, sb, kLanes / 4);
+        sb |= (kLanes / 4 < lanes ? s1 : kOne) << 8;
+        const uint32_t s2 = __shfl_down_sync(0xffffffffu, sb, kLanes / 2);
+        sb |= (kLanes / 2 < lanes ? s2 : kOne * 0x101u) << 16;
+        w[0] = sb;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+            const uint32_t si = __shfl_down_sync(0xffffffffu, sb, i * kLanes);
+            w[i] = i * kLanes < lanes ? si : kOne * 0x1010101u;
+        }
+        const uint4 word = make_uint4(w[0], w[1], w[2], w[3]);
+        const int at = sub / kLanes * 4;
+        const bool first = sub % (4 * kLanes) == 0 && at < g.pitch;
+        if (!live[j]) continue;
+        if (SRC == kScatter) {
+            for (int i = 0; i < g.k; ++i) {
+                const int64_t r = base[j] + __ldg(inv[j] + i);
+                if (sub < g.nv) g.q[r * g.nv + sub] = q;
+                if (first) *reinterpret_cast<uint4 *>(g.scale + r * g.pitch + at) = word;
+                if (NV && sub == 0) g.row_scale[r] = pow2(n);
+            }
+        } else {
+            if (sub < g.nv) g.q[row * g.nv + sub] = q;
+            if (first) *reinterpret_cast<uint4 *>(g.scale + row * g.pitch + at) = word;
+            if (NV && sub == 0) g.row_scale[row] = pow2(n);
         }
     }
 }
@@ -416,13 +533,34 @@ k_micro_values(const uint32_t *__restrict__ q, const uint8_t *__restrict__ scale
     }
 }
 
+template <int SRC, bool NV, int N>
+cudaError_t run_wide(MicroArgs a, cudaStream_t st) {
+    a.log_w = 0;
+    while (a.log_w < 3 && (N * 32) << a.log_w < a.nv) ++a.log_w;
+    const int64_t warps = a.rows << a.log_w;
+    return launch_pdl(k_micro_rows<SRC, NV, N>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, a);
+}
+
 template <int SRC, bool NV>
 cudaError_t run_rows(MicroArgs a, cudaStream_t st) {
     if (a.rows == 0) return cudaSuccess;
-    a.log_w = 0;
-    while (a.log_w < 3 && (kGroups<SRC> * 32) << a.log_w < a.nv) ++a.log_w;
-    const int64_t warps = a.rows << a.log_w;
-    return launch_pdl(k_micro_rows<SRC, NV>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, a);
+    // By token, four rows of 17 to 32 groups to a warp leave too few warps that write: 16384
+    // tokens, k = 8, H = 288 to NV 24.7 us so, 22.6 by k_micro_rows.
+    if (a.nv <= (SRC == kScatter ? 16 : 32)) {
+        a.log_l = 1;
+        while (1 << a.log_l < a.nv) ++a.log_l;
+        const int64_t per = 8 * (kGroups<SRC> * (32 >> a.log_l));   // a CTA's rows
+        return launch_pdl(k_micro_narrow<SRC, NV>, dim3((unsigned)((a.rows + per - 1) / per)), dim3(256), 0, st, a);
+    }
+    if constexpr (SRC == kSwiglu) {
+        // Three groups to a lane leave fewer lanes without work in rows of, say, 65 to 96
+        // groups: 131072 x 1408 to MX 142 us and to NV 166, against 178 and 225 of two; 2560 270
+        // and 333 of three.  With all lanes at work two are the faster (above).
+        int w = 64;                                              // groups that one, two, four or eight warps take two to a lane
+        while (w < 512 && w < a.nv) w *= 2;
+        if (w > 64 && a.nv <= w / 4 * 3) return run_wide<SRC, NV, 3>(a, st);
+    }
+    return run_wide<SRC, NV, kGroups<SRC>>(a, st);
 }
 
 template <int SRC>

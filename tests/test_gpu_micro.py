@@ -242,6 +242,73 @@ def test_swiglu_quantize(rows, I, fmt):
 
 
 @gpu
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("rows,C", [(513, 32), (2, 64), (257, 96), (65, 128), (130, 256), (33, 480), (4099, 512), (18, 544)])
+def test_quantize_narrow_rows(rows, C, fmt):
+    """Several rows to a warp, the last warp's not all there."""
+    test_quantize_rows(rows, C, fmt)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("L,T,k,H", [(1, 3, 2, 64), (2, 35, 5, 96), (1, 70001, 2, 32), (2, 9000, 40, 224), (1, 16385, 3, 128)])
+def test_permute_quantize_narrow_rows(L, T, k, H, fmt):
+    test_permute_quantize(L, T, k, H, fmt)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("T,H", [(65, 32), (16400, 128)])
+def test_permute_quantize_narrow_rows_leaves_bad_pairs(T, H, fmt):
+    """A pair out of range: an error, and no row of it or its token; the others are there."""
+    dev = _dev()
+    rng = np.random.default_rng([T, H, 3])
+    k, by_token = 2, T * H * 2 > 4 << 20
+    cfg = topo.make_cfg(T=T, E=8, k=k, R=1, ranks_per_node=1, n_slot=0)
+    nb = topo.topo_workspace_bytes(cfg, 1, topo.TOPO_CALL_PACK)
+    ws = torch.zeros(nb, dtype=torch.uint8, device=dev)
+    x = bf16(hard_rows(rng, T, H)).to(dev)
+    sp = rng.permutation(T * k).astype(np.int32)
+    lost = sp[5] // k
+    sp[5] = T * k + 7
+    q, s, g = buffers(T * k, H, fmt, dev)
+    topo.topo_permute_quantize_micro(cfg, 1, H, fmt, x, torch.as_tensor(sp, device=dev), q, s, g, ws, nb)
+    torch.cuda.synchronize()
+    assert topo.topo_read_error(ws) == topo.TOPO_ESTATE
+    a, b, c = buffers(T, H, fmt, dev)
+    topo.topo_quantize_rows_micro(T, H, fmt, x, a, b, c)
+    keep = np.arange(T * k) != 5
+    if by_token:
+        keep &= sp // k != lost
+    at, rows = torch.as_tensor(sp[keep] // k, dtype=torch.int64, device=dev), torch.as_tensor(np.flatnonzero(keep), device=dev)
+    assert torch.equal(q[rows], a[at]) and torch.equal(s[rows], b[at])
+    assert fmt == MX or torch.equal(g[rows], c[at])
+    if not by_token:
+        assert bool((q[5] == 0x55).all()) and bool((s[5] == 0xEE).all())
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("rows,I", [(4, 32), (300, 64), (33, 96), (129, 256), (70, 480), (600, 512), (9, 544), (40, 768), (21, 1536),
+                                    (11, 2560), (7, 6144)])
+def test_swiglu_quantize_narrow_rows_and_three_groups_to_a_lane(rows, I, fmt):
+    test_swiglu_quantize(rows, I, fmt)
+    dev = _dev()
+    q, s, g = buffers(rows, I, fmt, dev)
+    topo.topo_swiglu_quantize_micro(rows, I, fmt, torch.ones(rows, 2 * I, dtype=torch.bfloat16, device=dev), q, s, g)
+    assert bool((s[:, I // BLOCK[fmt]:] == (127 if fmt == MX else 0x38)).all())
+    n = 1041                                                  # a row's values do not depend on its place
+    h = (torch.randn(n, 2 * I, generator=torch.Generator().manual_seed(I)) * 3).to(torch.bfloat16).to(dev)
+    whole = buffers(n, I, fmt, dev)
+    topo.topo_swiglu_quantize_micro(n, I, fmt, h, *whole)
+    for at in (0, 1, 515, n - 4):
+        four = buffers(4, I, fmt, dev)
+        topo.topo_swiglu_quantize_micro(4, I, fmt, h[at:at + 4], *four)
+        for x, y in zip(whole, four):
+            assert x is None or torch.equal(x[at:at + 4], y)
+
+
+@gpu
 def test_quantised_rows_in_the_order_of_any_launch():
     """Rows split over warps and whole rows give the same bytes."""
     dev = _dev()
