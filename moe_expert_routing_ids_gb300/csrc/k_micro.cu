@@ -492,31 +492,35 @@ k_micro_narrow(MicroArgs g) {
 }
 
 // A lane takes 8 neighbouring values (16 bytes out) four times, 256 values apart, so that
-// a warp's stores are whole lines and four loads are on their way at once.
+// a warp's stores are whole lines and four loads are on their way at once.  The values and
+// codes are one run without gaps, whatever the rows' length: 131072 x 128 7.1 us of MX and
+// 6.5 of NV (6.7 TB/s), against 18.2 by rows; 131072 x 7168 336 and 343 us, as by rows.
 template <bool NV>
 __global__ void __launch_bounds__(256)
 k_micro_values(const uint32_t *__restrict__ q, const uint8_t *__restrict__ scale, const float *__restrict__ row_scale, uint4 *out,
-               int64_t units, int chunks, int n8, int pitch) {
+               int64_t total, int n8, int pitch) {
     pdl_trigger();
     pdl_wait();
-    const int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (u >= units) return;
-    const int64_t row = u / chunks;
-    const int c0 = (int)(u - row * chunks) * 128 + (threadIdx.x & 31);
+    const int64_t e0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * 128, row0 = e0 / n8;
+    if (e0 >= total) return;
+    const uint32_t c0 = (uint32_t)(e0 - row0 * n8) + (threadIdx.x & 31);
+    const int64_t e = e0 + (threadIdx.x & 31);
     uint32_t w[4], sb[4];
+    float g[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int c = c0 + 32 * j;
-        w[j] = c < n8 ? __ldcs(q + row * n8 + c) : 0u;
-        sb[j] = c < n8 ? __ldg(scale + row * pitch + (NV ? c >> 1 : c >> 2)) : 0u;
+        const uint32_t down = (c0 + 32 * j) / (uint32_t)n8, c = c0 + 32 * j - down * n8;
+        const int64_t row = row0 + down;
+        const bool in = e + 32 * j < total;
+        w[j] = in ? __ldcs(q + e + 32 * j) : 0u;
+        sb[j] = in ? __ldg(scale + row * pitch + (NV ? c >> 1 : c >> 2)) : 0u;
+        g[j] = NV && in ? __ldg(row_scale + row) : 1.f;
     }
-    const float g = NV ? __ldg(row_scale + row) : 1.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int c = c0 + 32 * j;
-        if (c >= n8) break;
+        if (e + 32 * j >= total) break;
         float s;
-        if (NV) s = (sb[j] & 0x7fu) == 0x7fu ? __uint_as_float(0x7fffffffu) : e4m3_value(sb[j]) * g;
+        if (NV) s = (sb[j] & 0x7fu) == 0x7fu ? __uint_as_float(0x7fffffffu) : e4m3_value(sb[j]) * g[j];
         else s = sb[j] == 255u ? __uint_as_float(0x7fffffffu) : sb[j] == 0u ? __uint_as_float(0x400000u) : pow2((int)sb[j] - 127);
         uint32_t f[4], o[4];
         asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
@@ -529,7 +533,7 @@ k_micro_values(const uint32_t *__restrict__ q, const uint8_t *__restrict__ scale
             const __nv_bfloat162 b = __floats2bfloat162_rn(p.x * s, p.y * s);
             o[i] = *reinterpret_cast<const uint32_t *>(&b);
         }
-        __stcs(out + row * n8 + c, make_uint4(o[0], o[1], o[2], o[3]));
+        __stcs(out + e + 32 * j, make_uint4(o[0], o[1], o[2], o[3]));
     }
 }
 
@@ -609,15 +613,15 @@ cudaError_t launch_permute_quantize_micro(const Geo &g, int H, int fmt, const ui
 
 cudaError_t launch_dequantize_micro(int64_t rows, int C, int fmt, const uint8_t *q, const uint8_t *scale, const float *row_scale,
                                     uint16_t *out, cudaStream_t st) {
-    const int n8 = C / 8, pitch = (int)micro_pitch(C, fmt), chunks = (n8 + 127) / 128;
-    const int64_t units = rows * chunks;
-    if (units == 0) return cudaSuccess;
-    const dim3 grid((unsigned)((units + 7) / 8));
+    const int n8 = C / 8, pitch = (int)micro_pitch(C, fmt);
+    const int64_t total = rows * n8;
+    if (total == 0) return cudaSuccess;
+    const dim3 grid((unsigned)((total + 1023) / 1024));
     const uint32_t *qv = reinterpret_cast<const uint32_t *>(q);
     uint4 *ov = reinterpret_cast<uint4 *>(out);
     if (fmt == TOPO_FMT_NV)
-        return launch_pdl(k_micro_values<true>, grid, dim3(256), 0, st, qv, scale, row_scale, ov, units, chunks, n8, pitch);
-    return launch_pdl(k_micro_values<false>, grid, dim3(256), 0, st, qv, scale, row_scale, ov, units, chunks, n8, pitch);
+        return launch_pdl(k_micro_values<true>, grid, dim3(256), 0, st, qv, scale, row_scale, ov, total, n8, pitch);
+    return launch_pdl(k_micro_values<false>, grid, dim3(256), 0, st, qv, scale, row_scale, ov, total, n8, pitch);
 }
 
 }  // namespace topo

@@ -340,6 +340,22 @@ def test_dequantize_every_code_and_scale(fmt):
     assert np.array_equal(got, want, equal_nan=True)
 
 
+@gpu
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("rows,C", [(1, 32), (35, 32), (4097, 96), (700, 160), (33, 1408), (9, 20512), (3, 65568)])
+def test_dequantize_rows_of_any_length(rows, C, fmt):
+    """A product of a code (2 bits), a scale (4 bits) and a power of two is a bf16 value: equal."""
+    dev = _dev()
+    q, sb, g = random_rows(np.random.default_rng([rows, C, 5]), rows, C, fmt)
+    sb[:, C // BLOCK[fmt]:] = 0xEE                            # the padding is not a value's scale
+    out = torch.full((rows + 1, C), 7.0, dtype=torch.bfloat16, device=dev)
+    topo.topo_dequantize_micro(rows, C, fmt, torch.as_tensor(q, device=dev), torch.as_tensor(sb, device=dev),
+                               None if g is None else torch.as_tensor(g, device=dev), out)
+    want = values(q, sb, None if g is None else g.astype(np.float64), fmt)
+    assert np.array_equal(out[:rows].cpu().double().numpy(), want)
+    assert bool((out[rows] == 7).all())
+
+
 def segments(rng, n_seg, rows, empty=True):
     cuts = np.sort(rng.integers(0, rows + 1, n_seg - 1)) if n_seg > 1 else np.empty(0, np.int64)
     off = np.concatenate([[0], cuts, [rows]]).astype(np.int32)
