@@ -595,11 +595,18 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
         // storing), so that they reach the end with the rest of the CTA
         for (int t = first; t < ntiles; t += step) {
             int nkb, ncol;
+            float ra = 0.f;                         // kNv: the scale of this lane's row, four of the columns
+            float4 rw = make_float4(0.f, 0.f, 0.f, 0.f);
             {
                 const Tile q = find_tile<MODE>(g, tp, so, pad, t);
                 nkb = q.nkb;
                 // columns of this half; none for a warp whose rows all lie past the tile's
                 ncol = wq * 32 < q.mlim ? max(0, min(128, q.ncols - c0)) : 0;
+                if (MODE == kNv) {
+                    if (wq * 32 + lane < q.mlim) ra = __ldg(g.x_scale + q.m0 + wq * 32 + lane);
+                    if (c0 + 4 * lane < q.nlim)
+                        rw = __ldg(reinterpret_cast<const float4 *>(g.w_scale + (int64_t)q.w * g.N + q.n0 + c0) + lane);
+                }
             }
             Acc acc;
 #pragma unroll
@@ -655,18 +662,17 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     }
                 }
             } else {
-                if (MODE == kNv && m1 < q.mlim) {           // the scales of whole rows, of a and of the weights
-                    const float ra = m1 + lane < q.mlim ? __ldg(g.x_scale + q.m0 + m1 + lane) : 0.f;
-                    const float4 *rw = reinterpret_cast<const float4 *>(g.w_scale + (int64_t)q.w * g.N + q.n0 + c0);
+                if (MODE == kNv) {                          // the scales of whole rows, of a and of the weights
+                    __syncwarp();
+                    reinterpret_cast<float4 *>(w)[lane] = rw;
+                    __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        if (c0 + 4 * i < q.nlim) {
-                            const float4 f = __ldg(rw + i);
-                            acc[2 * i].x *= ra * f.x;
-                            acc[2 * i].y *= ra * f.y;
-                            acc[2 * i + 1].x *= ra * f.z;
-                            acc[2 * i + 1].y *= ra * f.w;
-                        }
+                        const float4 f = reinterpret_cast<const float4 *>(w)[i];
+                        acc[2 * i].x *= ra * f.x;
+                        acc[2 * i].y *= ra * f.y;
+                        acc[2 * i + 1].x *= ra * f.z;
+                        acc[2 * i + 1].y *= ra * f.w;
                     }
                 }
                 // the rows that pass at a time, and whether this lane's row is among pass p's
