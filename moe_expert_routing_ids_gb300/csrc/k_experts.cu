@@ -56,7 +56,8 @@
 // the scale warps turn the words of 128 rows into the order that tensor memory wants.
 // Measured: 131072 rows, N = 4096, K = 7168, 128 experts: by 32 1.56 ms, 4.9 PFLOP/s, by 16
 // 1.89 ms, 4.1 PFLOP/s (tensor pipe 50 and 40 percent of cycles); 1536 rows, 2816 x 4096,
-// 64 experts 67 and 75 us, 6.2 and 5.9 TB/s; 6 rows, 4096 x 1408: 11 and 15 us.  What bounds it:
+// 64 experts 66 and 72 us, 6.3 and 6.2 TB/s; 6 rows, 4096 x 1408: 12 and 14 us; 16384 rows of
+// 64 experts, 4096 x 1408: 84 and 100 us, without the stores 66 and 75.  What bounds it:
 // the bytes of a stage are those of the 8-bit product, 768 cycles of shared memory; by 16, a
 // build that loads no scales and copies half of them to tensor memory still takes 1.78 ms.
 // Tried: scales by the scale warps' own 16-byte copies (a ring behind the stages, three
@@ -602,7 +603,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 nkb = q.nkb;
                 // columns of this half; none for a warp whose rows all lie past the tile's
                 ncol = wq * 32 < q.mlim ? max(0, min(128, q.ncols - c0)) : 0;
-                if (MODE == kNv) {
+                if (MODE == kNv) {                  // before the wait: read behind it, 110 us for 100 of the above
                     if (wq * 32 + lane < q.mlim) ra = __ldg(g.x_scale + q.m0 + wq * 32 + lane);
                     if (c0 + 4 * lane < q.nlim)
                         rw = __ldg(reinterpret_cast<const float4 *>(g.w_scale + (int64_t)q.w * g.N + q.n0 + c0) + lane);
