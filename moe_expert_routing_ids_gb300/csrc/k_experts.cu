@@ -83,6 +83,7 @@ constexpr bool kMicro = MODE == kMx || MODE == kNv;
 constexpr int kKB = 128;                          // bytes of a row's block, one 128-byte swizzle row: 128 values, 256 in 4 bits
 constexpr int kTileM = 128;
 constexpr int kTileN = 256;
+constexpr int kNarrowN = 128;                     // 4 bits: columns of a tile where there are few tiles
 constexpr int kSumWarps = 8;                      // warps that scale, add and store
 constexpr int kThreads = (kSumWarps + 4) * 32;    // two summing warpgroups, one of producer, issuer and two scale warps
 // registers of a thread of the summing and of the other warpgroup; 2 * 128 times
@@ -147,16 +148,16 @@ struct Tile {
     int kb0, nkb;      // blocks contracted
 };
 
-template <int MODE>
+template <int MODE, int TN>
 __device__ __forceinline__ int tiles_of(const GemmArgs &g, int len) {
     const int m = MODE != kGrad ? len : g.N, n = MODE != kGrad ? g.N : g.K;
-    return ((m + kTileM - 1) / kTileM) * ((n + kTileN - 1) / kTileN);
+    return ((m + kTileM - 1) / kTileM) * ((n + TN - 1) / TN);
 }
 
 // Tile t: its segment by binary search over the exclusive prefix tp[0..nseg].
 // Within a segment the layout-row tiles of one weight tile are neighbours, so
 // that CTAs running together share the weights through L2.
-template <int MODE>
+template <int MODE, int TN>
 __device__ __forceinline__ Tile find_tile(const GemmArgs &g, const int *tp, const int *so, const int *pad, int t) {
     int lo = 0, hi = g.nseg - 1;
     while (lo < hi) {
@@ -172,8 +173,8 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs &g, const int *tp, cons
     r.w = MODE == kGrad ? 0 : g.seg_w ? __ldg(g.seg_w + lo) : g.seg0 + lo;
     r.m0 = m * kTileM;
     r.mlim = min(kTileM, me - r.m0);
-    r.n0 = n * kTileN;
-    r.nlim = min(kTileN, ne - r.n0);
+    r.n0 = n * TN;
+    r.nlim = min(TN, ne - r.n0);
     if (MODE != kGrad) r.m0 += so[lo];
     r.ncols = (r.nlim + 15) & ~15;
     r.kb0 = MODE == kGrad ? pad[lo] : 0;
@@ -209,7 +210,7 @@ __device__ __forceinline__ void add_rows(Acc &acc, uint32_t ta, float s) {
     }
 }
 
-template <int MODE>
+template <int MODE, int TN>
 __global__ void __launch_bounds__(kThreads, 1)
 k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUtensorMap map_few,
           const __grid_constant__ CUtensorMap map_n, const __grid_constant__ CUtensorMap map_sm,
@@ -221,7 +222,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
     __shared__ int expired;
     __shared__ int so[kSegCap<MODE> + 1], tp[kSegCap<MODE> + 1], pad[MODE == kGrad ? kSegCap<MODE> + 1 : 1];
     // product: scales of the rows times the weight scale of each half of the columns
-    __shared__ float cs[MODE == kProduct ? 2 : 1][kScaleKB][MODE == kProduct ? kTileN : 1];
+    __shared__ float cs[MODE == kProduct ? 2 : 1][kScaleKB][MODE == kProduct ? TN : 1];
     __shared__ __align__(1024) unsigned char outs[kSumWarps * kStageOut<MODE>];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int first = blockIdx.x, step = gridDim.x;
@@ -289,7 +290,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     set_error(g.hdr, TOPO_ESTATE);
                     ok = false;
                 }
-                if (MODE == kGrad || ok) n = tiles_of<MODE>(g, b - a);
+                if (MODE == kGrad || ok) n = tiles_of<MODE, TN>(g, b - a);
             }
             int x = n, y = pb;
 #pragma unroll
@@ -326,7 +327,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             int s = 0, fill = 0;                       // stage, and how often the ring went round
             bool ok = true;
             for (int t = first; t < ntiles && ok; t += step) {
-                const Tile q = find_tile<MODE>(g, tp, so, pad, t);
+                const Tile q = find_tile<MODE, TN>(g, tp, so, pad, t);
                 const int ym = q.m0;
                 const int yn = (MODE != kGrad ? q.w * g.N : 0) + q.n0;
                 const int boxes = (q.ncols + kTileM - 1) / kTileM;          // 128 columns to a load
@@ -356,12 +357,12 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                         for (int c = 0; c < boxes; ++c)
                             tc::tma_load(b + (uint32_t)(c * kTileM) * kKB, &map_n, x, yn + c * kTileM, bar);
                         if (MODE == kGrad) {
-                            const uint32_t sf = b + kTileN * kKB;
+                            const uint32_t sf = b + TN * kKB;
                             tc::bulk_load(sf, g.w_scale + (int64_t)(q.kb0 + kb) * g.N + q.m0, ms, bar);
                             tc::bulk_load(sf + 512, g.x_scale + (int64_t)(q.kb0 + kb) * g.K + q.n0, ns, bar);
                         }
                         if (sf_here) {
-                            const uint32_t sf = b + kTileN * kKB;
+                            const uint32_t sf = b + TN * kKB;
                             const int xs = 16 * (MODE == kNv ? kb : kb >> 1);
                             tc::tma_load(sf, &map_sm, xs, ym, bar);
                             for (int c = 0; c < boxes; ++c)
@@ -386,7 +387,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             int s = 0, fill = 0, it = 0;               // it: accumulators handed on
             bool ok = true;
             for (int t = first; t < ntiles && ok; t += step) {
-                const Tile q = find_tile<MODE>(g, tp, so, pad, t);
+                const Tile q = find_tile<MODE, TN>(g, tp, so, pad, t);
                 const uint32_t idesc = kMicro<MODE> ? tc::idesc_micro(kTileM, q.ncols, MODE == kMx)
                                        : MODE == kGrad ? tc::idesc_scaled(kTileM, q.ncols) : tc::idesc_e4m3(kTileM, q.ncols);
                 for (int kb = 0; kb < q.nkb; ++kb) {
@@ -406,7 +407,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                         const uint64_t dm = tc::smem_desc(a), dn = tc::smem_desc(a + kABytes);
                         if (kMicro<MODE>) {
                             // a step is 64 values, 32 bytes on within the swizzled row
-                            const uint32_t ta = tmem + kTileN + (uint32_t)(kSfCols<MODE> * s), tb = ta + 4 * kSfSteps<MODE>;
+                            const uint32_t ta = tmem + TN + (uint32_t)(kSfCols<MODE> * s), tb = ta + 4 * kSfSteps<MODE>;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const int u = MODE == kNv ? j : j >> 1;
@@ -414,14 +415,14 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                                 tc::mma_micro<MODE == kNv>(tmem, dm + 2 * j, dn + 2 * j, id, ta + 4 * u, tb + 8 * u, !begin || j > 0);
                             }
                         } else if (MODE == kGrad) {
-                            const uint32_t ts = tmem + kTileN + (uint32_t)(kSfCols<MODE> * s);
+                            const uint32_t ts = tmem + TN + (uint32_t)(kSfCols<MODE> * s);
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 tc::mma_scaled(tmem, dm + 2 * j, dn + 2 * j, idesc, ts, ts + 4, !begin || j > 0);
                         } else {
 #pragma unroll
                             for (int j = 0; j < 4; ++j)        // 32 bytes on within the swizzled row
-                                tc::mma_e4m3(tmem + (uint32_t)(b * kTileN), dm + 2 * j, dn + 2 * j, idesc, j > 0);
+                                tc::mma_e4m3(tmem + (uint32_t)(b * TN), dm + 2 * j, dn + 2 * j, idesc, j > 0);
                         }
                         tc::mma_commit(tc::smem_u32(&empty[s]));
                         if (end) tc::mma_commit(tc::smem_u32(&acc_full[b]));
@@ -444,22 +445,23 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             int gi = 0, s = 0, fill = 0, it = 0;
             bool ok = true;
             for (int t = first; t < ntiles && ok; t += step) {
-                const Tile q = find_tile<MODE>(g, tp, so, pad, t);
+                const Tile q = find_tile<MODE, TN>(g, tp, so, pad, t);
                 const int m1 = q.m0;
                 if constexpr (kMicro<MODE>) {
                     // a block's scales came as 16 bytes a row; the tensor cores take the words of
                     // 128 rows (4 of kNv's scales, 2 of kMx's for each of two steps) in the order
                     // of tc::copy_scales: a lane turns its four rows' words and puts them back.
                     // One warp does the rows and the first 128 columns, the other the last 128
+                    // (or the only ones)
                     const int boxes = (q.ncols + kTileM - 1) / kTileM;
-                    const int u0 = warp == kSumWarps + 2 ? 0 : 2, u1 = warp == kSumWarps + 2 ? 2 : 1 + boxes;
+                    const int u0 = warp == kSumWarps + 2 ? 0 : boxes, u1 = warp == kSumWarps + 2 ? boxes : 1 + boxes;
                     uint2 odd[2][4];                             // by 32: the words of the block that follows
                     for (int kb = 0; kb < q.nkb; ++kb) {
                         ok = tc::mbar_wait(&full[s], (uint32_t)fill & 1u);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
-                        const uint32_t at = (uint32_t)s * g.stage_bytes + kABytes + kTileN * kKB;
-                        const uint32_t ts = tmem + kTileN + (uint32_t)(kSfCols<MODE> * s);
+                        const uint32_t at = (uint32_t)s * g.stage_bytes + kABytes + TN * kKB;
+                        const uint32_t ts = tmem + TN + (uint32_t)(kSfCols<MODE> * s);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int u = u0 + h;
@@ -512,7 +514,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                             ok = tc::mbar_wait(&full[s], (uint32_t)fill & 1u);
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok) break;
-                            const uint32_t at = (uint32_t)s * g.stage_bytes + kABytes + kTileN * kKB;
+                            const uint32_t at = (uint32_t)s * g.stage_bytes + kABytes + TN * kKB;
                             uint32_t *sf = reinterpret_cast<uint32_t *>(ring + at);
                             uint32_t v[12];
 #pragma unroll
@@ -524,7 +526,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                             tc::fence_async();
                             __syncwarp();
                             if (tc::elect()) {
-                                const uint32_t ts = tmem + kTileN + (uint32_t)(kSfCols<MODE> * s), from = tc::smem_u32(ring) + at;
+                                const uint32_t ts = tmem + TN + (uint32_t)(kSfCols<MODE> * s), from = tc::smem_u32(ring) + at;
 #pragma unroll
                                 for (int i = 0; i < 3; ++i) tc::copy_scales(ts + 4 * i, from + 512 * i);
                                 tc::mma_commit(tc::smem_u32(&scaled[s]));
@@ -599,7 +601,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             float ra = 0.f;                         // kNv: the scale of this lane's row, four of the columns
             float4 rw = make_float4(0.f, 0.f, 0.f, 0.f);
             {
-                const Tile q = find_tile<MODE>(g, tp, so, pad, t);
+                const Tile q = find_tile<MODE, TN>(g, tp, so, pad, t);
                 nkb = q.nkb;
                 // columns of this half; none for a warp whose rows all lie past the tile's
                 ncol = wq * 32 < q.mlim ? max(0, min(128, q.ncols - c0)) : 0;
@@ -624,7 +626,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                 if (live) live = tc::mbar_wait_tries(&acc_full[b], (uint32_t)round & 1u);
                 __syncwarp();
                 tc::fence_after();
-                if (ncol > 0) add_rows<MODE == kProduct ? 32 : 16>(acc, tmem + lanes + (uint32_t)(b * kTileN + c0), scale);
+                if (ncol > 0) add_rows<MODE == kProduct ? 32 : 16>(acc, tmem + lanes + (uint32_t)(b * TN + c0), scale);
                 tc::fence_before();
                 __syncwarp();
                 const bool last = MODE == kProduct && (u == kScaleKB - 1 || kb + 1 == nkb);
@@ -637,7 +639,7 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
             live = __all_sync(0xffffffffu, live);
             if (!live) continue;
             // found again rather than kept in registers over the loop
-            const Tile q = find_tile<MODE>(g, tp, so, pad, t);
+            const Tile q = find_tile<MODE, TN>(g, tp, so, pad, t);
             const int m1 = wq * 32;         // this warp's first row, from m0
             // 32 rows x 64 bytes at a time, turned through shared memory so that four lanes
             // store 64 neighbouring bytes: 16-byte pieces, piece index XOR (row / 2)
@@ -798,22 +800,22 @@ cudaError_t make_out_map(CUtensorMap *m, float *out, int nseg, int N, int K) {
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int MODE>
+template <int MODE, int TN = kTileN>
 cudaError_t run_experts(GemmArgs g, int nseg, const int32_t *seg_off, const int32_t *seg_w, const CUtensorMap &mm,
                         const CUtensorMap &mf, const CUtensorMap &mn, const CUtensorMap &msm, const CUtensorMap &msn,
                         cudaStream_t st) {
     // the gradient's and the 4-bit product's stages also hold their scales, and stay on
     // 1024-byte boundaries
-    g.stage_bytes = kABytes + (uint32_t)kTileN * kKB + (MODE == kGrad ? 2048 : kMicro<MODE> ? 3 * kSfBytes : 0);
+    g.stage_bytes = kABytes + (uint32_t)TN * kKB + (MODE == kGrad ? 2048 : kMicro<MODE> ? 3 * kSfBytes : 0);
     const size_t smem = (size_t)kStages * g.stage_bytes;
-    cudaError_t e = ensure_smem((const void *)k_experts<MODE>, smem);
+    cudaError_t e = ensure_smem((const void *)k_experts<MODE, TN>, smem);
     if (e != cudaSuccess) return e;
     for (int s0 = 0; s0 < nseg; s0 += kSegCap<MODE>) {
         g.nseg = std::min(kSegCap<MODE>, nseg - s0);
         g.seg0 = s0;
         g.seg_off = seg_off + s0;
         g.seg_w = seg_w ? seg_w + s0 : nullptr;
-        if ((e = launch_pdl(k_experts<MODE>, dim3(kSms), dim3(kThreads), smem, st, mm, mf, mn, msm, msn, g)) != cudaSuccess) return e;
+        if ((e = launch_pdl(k_experts<MODE, TN>, dim3(kSms), dim3(kThreads), smem, st, mm, mf, mn, msm, msn, g)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
@@ -867,6 +869,16 @@ cudaError_t launch_expert_gemm_micro(int nseg, int64_t rows, int n_w, int N, int
     if ((e = make_map(&mw, w, (int64_t)n_w * N, K / 2, kTileM)) != cudaSuccess) return e;
     if ((e = make_scale_map(&sx, a_scale, rows, pitch)) != cudaSuccess) return e;
     if ((e = make_scale_map(&sw, w_scale, (int64_t)n_w * N, pitch)) != cudaSuccess) return e;
+    // Few tiles: each CTA's own loads take the longest, and tiles of half as many columns share
+    // them among twice the CTAs: 89 rows, 3 experts, 1536 x 4064 by 32 and 16 14.6 and 16.8 ->
+    // 11.1 and 12.6 us (x 1024 6.9 and 7.9 -> 6.6 and 7.3); 200 rows, 2048 x 4096 12.0 and 14.4 -> 10.9
+    // and 12.1; 1 row, 4096 x 7168 16.5 and 19.4 -> 15.0 and 17.0.  128 of them are too many: 20
+    // rows, 4 experts, 4096 x 3584 11.5 and 13.4 -> 11.9 and 16.0.  The lengths of the segments are on
+    // the device: decided by a bound
+    const int64_t most = (rows / kTileM + std::min<int64_t>(rows, nseg)) * ((N + kNarrowN - 1) / kNarrowN);
+    if (N > kNarrowN && most <= kSms / 2)
+        return fmt == TOPO_FMT_NV ? run_experts<kNv, kNarrowN>(g, nseg, seg_off, seg_w, mx, mf, mw, sx, sw, st)
+                                  : run_experts<kMx, kNarrowN>(g, nseg, seg_off, seg_w, mx, mf, mw, sx, sw, st);
     return fmt == TOPO_FMT_NV ? run_experts<kNv>(g, nseg, seg_off, seg_w, mx, mf, mw, sx, sw, st)
                               : run_experts<kMx>(g, nseg, seg_off, seg_w, mx, mf, mw, sx, sw, st);
 }

@@ -466,6 +466,33 @@ def test_products_repeat_and_do_not_depend_on_other_rows(fmt):
 
 @gpu
 @pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("rows,n_seg,n_w,N,K,bf", [(89, 3, 3, 1536, 4064, True), (400, 1, 1, 144, 288, False), (2, 1, 1, 512, 5024, True),
+                                                   (150, 2, 3, 1040, 544, False), (19, 19, 2, 1024, 96, True)])
+def test_products_of_few_tiles(rows, n_seg, n_w, N, K, bf, fmt):
+    """Tiles of half as many columns."""
+    test_products(rows, n_seg, n_w, N, K, bf, fmt)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("n_seg", [17, 18, 19, 20, 38, 39])
+def test_products_do_not_depend_on_the_tiles_width(n_seg, fmt):
+    """4 or 8 tiles a segment: narrow ones for a single segment, wide ones for many."""
+    dev = _dev()
+    rng = np.random.default_rng(19)
+    n, N, K = 39, 1008, 800
+    a, w = random_rows(rng, 2 * n, K, fmt), random_rows(rng, 3 * N, K, fmt)
+    seg_w = rng.integers(0, 3, n).astype(np.int32)
+    off = np.arange(0, 2 * n + 1, 2).astype(np.int32)
+    got, err = product(a, w, off[:n_seg + 1], seg_w[:n_seg], 3, N, K, fmt, False, dev)
+    assert err == 0 and bool((got[2 * n_seg:] == 7).all())
+    for i in (0, 5, n_seg - 1):
+        one, _ = product(a, w, off[i:i + 2], seg_w[i:i + 1], 3, N, K, fmt, False, dev)
+        assert torch.equal(one[2 * i:2 * i + 2], got[2 * i:2 * i + 2])
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [MX, NV])
 def test_calls_captured_in_a_graph(fmt):
     dev = _dev()
     rng = np.random.default_rng(14)
