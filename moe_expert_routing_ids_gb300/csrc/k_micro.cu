@@ -134,15 +134,18 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
 // -v log2(e), times 1 + what the rounding left out; the reciprocal of 1 + exp(-v) by one
 // step of Newton's iteration from the approximate one: within 8 * 2^-24 of the value, where
 // topo_swiglu_quantize calls expf and divides (25 instructions a value; this, in packed
-// pairs, 9).  low: some
-// v may be below -83, where 1 + exp(-v) nears the end of float32's range: expf and division.
-__device__ __forceinline__ void gated(float (&v)[16], const float (&u)[16], bool low) {
-    if (low) {
+// pairs, 9).  far: some |v| may be above 83: expf and division.  (Below -83 1 + exp(-v)
+// nears the end of float32's range, above 2.35e38 v log2(e) is past it.  A bound of its own for
+// either sign costs a second maximum: 131072 x 2048 to MX and NV 189 and 234 us with the one for
+// -83 alone, 194 and 240 with both, 191 and 235 with this one.)
+__device__ __forceinline__ void gated(float (&v)[16], const float (&u)[16], bool far) {
+    if (far) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = __fdiv_rn(v[i], 1.f + expf(-v[i])) * u[i];
         return;
     }
-    const f2 to = both(-1.44269504088896f), back = both(1.44269504088896f), lo = both(-1.925963033500e-8f);
+    constexpr double kLog2e = 1.44269504088896341;               // in two parts
+    const f2 to = both(-(float)kLog2e), back = both((float)kLog2e), lo = both((float)((float)kLog2e - kLog2e));
     const f2 ln2 = both(0.69314718f), one = both(1.f), less = both(-1.f);
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
@@ -214,13 +217,15 @@ struct Groups<kSwiglu, N> {
                 continue;
             }
             const uint32_t w[8] = {a[j][0].x, a[j][0].y, a[j][0].z, a[j][0].w, a[j][1].x, a[j][1].y, a[j][1].z, a[j][1].w};
-            uint32_t most = 0;                                  // as 16-bit words: the most negative value
+            const __nv_bfloat162 *const p = reinterpret_cast<const __nv_bfloat162 *>(w);
+            __nv_bfloat162 most = __habs2(p[0]);                // the largest magnitudes; drops a NaN
 #pragma unroll
-            for (int i = 0; i < 8; ++i) most = __vmaxu2(most, w[i]);
+            for (int i = 1; i < 8; ++i) most = __hmax2(most, __habs2(p[i]));
+            const uint32_t bits = *reinterpret_cast<const uint32_t *>(&most);
             float u[16];
             unpack16(a[j][0], a[j][1], f[j]);
             unpack16(a[j][2], a[j][3], u);
-            gated(f[j], u, max(most & 0xffffu, most >> 16) > 0xc2a6u);   // -83
+            gated(f[j], u, max(bits & 0xffffu, bits >> 16) > 0x42a6u);   // 83
         }
     }
     __device__ __forceinline__ void get(int j, float (&v)[16]) const {
