@@ -69,6 +69,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "rows.cuh"
 #include "tcgen.cuh"
 
 namespace topo {
@@ -669,13 +670,19 @@ k_experts(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUt
                     __syncwarp();
                     reinterpret_cast<float4 *>(w)[lane] = rw;
                     __syncwarp();
+                    const float r = first_factor(ra);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const float4 f = reinterpret_cast<const float4 *>(w)[i];
-                        acc[2 * i].x *= ra * f.x;
-                        acc[2 * i].y *= ra * f.y;
-                        acc[2 * i + 1].x *= ra * f.z;
-                        acc[2 * i + 1].y *= ra * f.w;
+                        acc[2 * i].x = acc[2 * i].x * r * f.x;
+                        acc[2 * i].y = acc[2 * i].y * r * f.y;
+                        acc[2 * i + 1].x = acc[2 * i + 1].x * r * f.z;
+                        acc[2 * i + 1].y = acc[2 * i + 1].y * r * f.w;
+                    }
+                    if (__any_sync(0xffffffffu, far_scale(ra))) {
+                        const float rest = rest_factor(ra);
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) acc[i] = make_float2(acc[i].x * rest, acc[i].y * rest);
                     }
                 }
                 // the rows that pass at a time, and whether this lane's row is among pass p's

@@ -1,4 +1,4 @@
-// What the kernels that quantise rows (8 bits, 4 bits) share.
+// What the kernels of quantised rows (8 bits, 4 bits) share.
 #pragma once
 
 #include <cstdint>
@@ -22,5 +22,16 @@ __device__ __forceinline__ void unpack16(const uint4 &a, const uint4 &b, float (
 // Both sides were measured at k = 8 only.  By token at k = 1, 2, 4 and 8, 16384 tokens:
 // 52, 64, 83 and 124 us, against 30, 41, 61 and 103 for the bytes alone.
 constexpr int64_t kGatherBytes = 4 << 20;
+
+// A sum of products times two float32 scales r and s, where r * s, or the sum times either, may be
+// past float32's range though the result is not: first_factor(r), then s, then rest_factor(r),
+// which is 1 unless r is beyond 2^-90 .. 2^77, and then about as far from 1 as the first, a
+// power of two.  Sums of e2m1 values and e4m3 scales, or of f16 ones in their place, are 0 or
+// within 2^-34 .. 2^45: neither step leaves float32's normal numbers where the result does not.
+__device__ __forceinline__ int scale_exp(float r) { return (int)(__float_as_uint(r) >> 23 & 0xffu) - 127; }
+__device__ __forceinline__ bool far_scale(float r) { return r != 0.f && (scale_exp(r) < -90 || scale_exp(r) >= 77); }
+__device__ __forceinline__ float half_power(float r, int sign) { return __uint_as_float((uint32_t)(127 + sign * (scale_exp(r) / 2)) << 23); }
+__device__ __forceinline__ float first_factor(float r) { return far_scale(r) ? half_power(r, 1) : r; }
+__device__ __forceinline__ float rest_factor(float r) { return far_scale(r) ? r * half_power(r, -1) : 1.f; }
 
 }  // namespace topo

@@ -1,9 +1,10 @@
-"""Rows and products in 4 bits at the ends of their ranges."""
+"""Rows and products in 4 bits at the ends of their ranges: gates near bf16's largest, row
+scales whose product float32 does not hold."""
 import numpy as np
 import pytest
 
 import moe_expert_routing_ids_gb300 as topo
-from test_gpu_micro import BLOCK, E4M3, MX, NV, _dev, bf16, buffers, least_power, values
+from test_gpu_micro import BLOCK, E4M3, MX, NV, _dev, bf16, buffers, least_power, product, random_rows, segments, values
 
 torch = pytest.importorskip("torch")
 gpu = pytest.mark.gpu
@@ -58,3 +59,44 @@ def test_activation_of_gates_near_the_largest(rows, I, fmt):
     assert np.all(ok | bad)
     step = np.where(mag < 2 * sc[..., None], 0.25, np.where(mag < 4 * sc[..., None], 0.5, 1.0)) * sc[..., None]
     assert np.all((np.abs(v - p) <= step * (1 + d) + dq * mag) | bad[..., None])
+
+
+@gpu
+@pytest.mark.parametrize("bf", [False, True])
+@pytest.mark.parametrize("rows,n_seg,N,K", [(70, 1, 144, 288), (200, 3, 272, 96), (300, 20, 1040, 64)])
+@pytest.mark.parametrize("ea,ew", [(-118, -40), (-126, -30), (120, -120), (-120, 118), (100, 20), (127, -126), (-140, 100), (-60, -70), (0, 0)])
+def test_row_scales_whose_product_float32_does_not_hold(ea, ew, rows, n_seg, N, K, bf):
+    """Any float32 row scales: out = ra rw sum.  The sum's bound is that of the products' own
+    test; each scale is one multiplication (2^-24; a power of two taken out of it none), and
+    what ends below float32's normal numbers is off by 2^-149 at most.  Sums past float32's
+    range are infinite; rows and columns of a scale 0 stay 0."""
+    dev = _dev()
+    rng = np.random.default_rng([rows, N, abs(ea), abs(ew)])
+    off = segments(rng, n_seg, rows)
+
+    def scales(n, e):
+        m = np.exp2(np.clip(e + rng.integers(-3, 4, n), -149, 127)) * np.where(rng.random(n) < 0.5, 1.0, rng.uniform(1, 1.9, n))
+        return np.where(rng.random(n) < 0.05, 0.0, np.minimum(m, 3.4e38)).astype(np.float32)
+
+    a, w = list(random_rows(rng, rows, K, NV)), list(random_rows(rng, n_seg * N, K, NV))
+    a[2], w[2] = scales(rows, ea), scales(n_seg * N, ew)
+    if rows > 100:
+        a[2][40:100] = scales(60, 0)                          # rows of a warp with different ranges
+    got, err = product(a, w, off, None, n_seg, N, K, NV, bf, dev)
+    assert err == 0
+    got = got.double().cpu()
+    ones = (np.ones(rows, np.float32), np.ones(n_seg * N, np.float32))
+    va = torch.as_tensor(values(a[0], a[1], ones[0], NV))
+    vw = torch.as_tensor(values(w[0], w[1], ones[1], NV)).reshape(n_seg, N, K)
+    ra, rw = torch.as_tensor(a[2]).double(), torch.as_tensor(w[2]).double().reshape(n_seg, N)
+    for i in range(n_seg):
+        r0, r1 = int(off[i]), int(off[i + 1])
+        f = ra[r0:r1, None] * rw[i]
+        want, A = (va[r0:r1] @ vw[i].T) * f, (va[r0:r1].abs() @ vw[i].abs().T) * f
+        tol = (K / 64 + K / 8192 + 4) * 2.0 ** -23 * A + (2.0 ** -8 * want.abs() if bf else 0) + (2.0 ** -133 if bf else 2.0 ** -149)
+        inside = (want.abs() + tol) < 3.38e38
+        far = (want.abs() - tol) > 3.41e38
+        g = got[r0:r1]
+        assert not bool(torch.isnan(g).any())
+        assert bool(((g - want).abs() <= tol)[inside].all())
+        assert bool((g.abs() == float("inf"))[far].all()) and bool((torch.sign(g) == torch.sign(want))[far].all())
