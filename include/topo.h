@@ -594,7 +594,9 @@ int topo_expert_gemm_micro(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, 
  * with all sums in float32; x and a enter the products as 16-bit floats of 11
  * bits over a power of two for each row (values more than 2^28 below the row's
  * largest lose bits, which changes the sum by less than 2^-38 of the largest for
- * each weight's magnitude); out is rounded once to bf16.
+ * each weight's magnitude); out is rounded once to bf16.  The magnitudes of a
+ * row of weights in 8 bits or TOPO_FMT_MX add up to less than 2^113 (of
+ * TOPO_FMT_NV any row scales): the sums over a row's power of two stay finite.
  * x: device bf16 [T][H]; ids: device int32 [T][k] (an expert may occur twice in
  * a row; one outside [0, E) adds nothing and is reported); weights: device
  * float32 [T][k]; up: [E][2 I][H], gate rows then up rows, and down: [E][H][I]

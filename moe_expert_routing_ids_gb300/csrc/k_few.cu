@@ -46,6 +46,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "rows.cuh"
 
 namespace topo {
 namespace {
@@ -654,7 +655,7 @@ k_few(FewArgs g) {
                 if (at + h >= grp.start[group + 1]) continue;
                 const int pair = grp.pair[at + h];
                 const float s = pow2(row_exp(amax[by_pair ? at + h - row0 : grp.token[at + h]]));
-                const float v0 = acc[h] * r0 * s, v1 = acc[2 + h] * r1 * s;
+                const float v0 = two_scales(acc[h], r0, s), v1 = two_scales(acc[2 + h], r1, s);
                 if (DOWN) {
                     float *y = g.mid + (int64_t)pair * g.H + 16 * unit;
                     __stcg(y + r, v0);

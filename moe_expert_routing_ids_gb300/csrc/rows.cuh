@@ -33,5 +33,6 @@ __device__ __forceinline__ bool far_scale(float r) { return r != 0.f && (scale_e
 __device__ __forceinline__ float half_power(float r, int sign) { return __uint_as_float((uint32_t)(127 + sign * (scale_exp(r) / 2)) << 23); }
 __device__ __forceinline__ float first_factor(float r) { return far_scale(r) ? half_power(r, 1) : r; }
 __device__ __forceinline__ float rest_factor(float r) { return far_scale(r) ? r * half_power(r, -1) : 1.f; }
+__device__ __forceinline__ float two_scales(float sum, float r, float s) { return sum * first_factor(r) * s * rest_factor(r); }
 
 }  // namespace topo
