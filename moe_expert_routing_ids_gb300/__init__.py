@@ -165,6 +165,8 @@ def lib():
 def _p(x):
     if x is None:
         return None
+    if type(x) is int:
+        return x or None
     try:
         return x.data_ptr() or None
     except AttributeError:

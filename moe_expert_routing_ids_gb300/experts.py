@@ -19,7 +19,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (TOPO_BLOCK, TOPO_CALL_COOCCUR, TOPO_CALL_PACK, TOPO_DTYPE_BF16, TOPO_DTYPE_F32, TOPO_FEW_MAX_TOKENS,
+from . import (TOPO_BLOCK, TOPO_CALL_PACK, TOPO_DTYPE_BF16, TOPO_DTYPE_F32, TOPO_FEW_MAX_TOKENS,
                TOPO_FMT_EIGHT, TOPO_FMT_MX, TOPO_FMT_NV, TopoRouteOpts, make_cfg, topo_cols_capacity, topo_combine,
                topo_expert_few, topo_expert_gemm, topo_expert_gemm_micro, topo_expert_wgrad, topo_expert_workspace_bytes,
                topo_few_workspace_bytes, topo_micro_pitch, topo_permute_quantize, topo_permute_quantize_micro,
@@ -88,7 +88,11 @@ class ExpertLayer:
 
     stream: every step of every call runs on it (None: torch's current stream).
     The calls take their place in the caller's current stream all the same: what
-    it holds so far comes before them, what it gets next comes after."""
+    it holds so far comes before them, what it gets next comes after.
+
+    forward(), backward() and set_weights() work in the layer's own buffers: on one
+    layer they must not overlap, on two streams or as replays of graphs that hold
+    them.  few() works in buffers of its own call."""
 
     def __init__(self, cfg: dict, w_up: torch.Tensor, w_down: torch.Tensor, route: TopoRouteOpts, train: bool = False,
                  stream=None, fmt: int = TOPO_FMT_EIGHT):
@@ -144,12 +148,9 @@ class ExpertLayer:
         topo_ws_reset(self.pack_ws, self.pack_bytes, P._stream())
         topo_ws_reset(self.ws, self.ws_bytes, P._stream())
         self.seg_w = None
-        # few(): its own workspaces, for any number of tokens
-        self.few_ids = buf(TOPO_FEW_MAX_TOKENS, self.k, dtype=torch.int32)
-        self.few_weights = buf(TOPO_FEW_MAX_TOKENS, self.k, dtype=f32)
+        # few(): its workspace is each call's own; 0: sizes that it does not take
         self.few_bytes = topo_few_workspace_bytes(TOPO_FEW_MAX_TOKENS, self.E, self.k, self.H, self.I)
-        self.few_ws = buf(max(self.few_bytes, topo_workspace_bytes(None, 0, TOPO_CALL_COOCCUR)), dtype=u8)
-        topo_ws_reset(self.few_ws, self.few_ws.numel(), P._stream())
+        self.few_ids, self.few_sizes = None, {}
 
     def _product(self, a, a_scale, N, K, w, w_scale, out):
         topo_expert_gemm(self.n_seg, self.rows, self.E, N, K, a, a_scale, self.planner.buf.seg_off, self.seg_w, w,
@@ -193,7 +194,8 @@ class ExpertLayer:
         """The layer applied to n tokens, 0 to TOPO_FEW_MAX_TOKENS of them whatever
         cfg's T: x bf16 [n, H]; logits float32 or bf16 [n, E]; bias float32 [E] or
         None; returns bf16 [n, H].  The activations keep 16 bits, so the result is
-        nearer to the weights' own than forward()'s."""
+        nearer to the weights' own than forward()'s.  Calls of few() may overlap one
+        another and a forward(), on several streams or in graphs."""
         if not isinstance(x, torch.Tensor) or x.dim() != 2:
             raise ValueError("x must be a tensor [n, H]")
         n = x.shape[0]
@@ -203,17 +205,34 @@ class ExpertLayer:
         need("logits", logits, (torch.float32, torch.bfloat16), n, self.E, self.device)
         if bias is not None:
             need("bias", bias, (torch.float32,), 1, self.E, self.device)
+        if self.planner.stream is None:                         # the caller's own: nothing to order
+            return self._few(n, x, logits, bias)
         with ordered(self.planner.stream, self.device, x, logits, bias) as outs:
-            s, out = self.planner._stream(), torch.empty_like(x)
-            outs.append(out)
-            if n:
-                topo_route(make_cfg(n, self.E, self.k, 1, 1, 0), 1, self.route, logits,
-                           TOPO_DTYPE_F32 if logits.dtype == torch.float32 else TOPO_DTYPE_BF16, bias, self.few_ids,
-                           self.few_weights, None, self.few_ws, self.few_ws.numel(), s)
-                topo_expert_few(n, self.E, self.k, self.H, self.I, self.fmt, x, self.few_ids, self.few_weights, self.up.q,
-                                self.up.scale, self.up.row, self.down.q, self.down.scale, self.down.row, out, self.few_ws,
-                                self.few_ws.numel(), s)
+            outs.append(self._few(n, x, logits, bias))
         return outs[0]
+
+    def _few(self, n, x, logits, bias):
+        s, out = self.planner._stream(), torch.empty_like(x)
+        if n:
+            # this call's alone (a captured call's in its graph's memory): calls on several
+            # streams and graphs that hold one may run at once.  The workspace, the weights behind it
+            cfg, nb = self._few_sizes(n)
+            ids = torch.empty((n, self.k), dtype=torch.int32, device=self.device)
+            scratch = torch.empty(nb // 4 + n * self.k, dtype=torch.float32, device=self.device)
+            ws = scratch.data_ptr()
+            topo_route(cfg, 1, self.route, logits, TOPO_DTYPE_F32 if logits.dtype == torch.float32 else TOPO_DTYPE_BF16,
+                       bias, ids, ws + nb, None, ws, nb, s)
+            topo_expert_few(n, self.E, self.k, self.H, self.I, self.fmt, x, ids, ws + nb, self.up.q, self.up.scale,
+                            self.up.row, self.down.q, self.down.scale, self.down.row, out, ws, nb, s)
+            self.few_ids = ids                                  # the last call's
+        return out
+
+    def _few_sizes(self, n):
+        """The routing's configuration and the workspace's bytes for n tokens."""
+        if n not in self.few_sizes:
+            self.few_sizes[n] = (make_cfg(n, self.E, self.k, 1, 1, 0),
+                                 topo_few_workspace_bytes(n, self.E, self.k, self.H, self.I))
+        return self.few_sizes[n]
 
     def _rows8(self, x):
         q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
@@ -292,6 +311,6 @@ class ExpertLayer:
         return dx, dlogits, dw_up, dw_down
 
     def error(self) -> int:
-        """First device error word of the layer's workspaces (synchronises the device)."""
-        return (self.planner.error() or topo_read_error(self.pack_ws) or topo_read_error(self.ws)
-                or topo_read_error(self.few_ws))
+        """First device error word of the layer's workspaces (synchronises the device).
+        few() has none to report: its ids come from the routing, all in range."""
+        return self.planner.error() or topo_read_error(self.pack_ws) or topo_read_error(self.ws)
