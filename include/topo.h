@@ -539,8 +539,9 @@ int topo_expert_wgrad(int32_t n_seg, int64_t rows, int32_t N, int32_t K, int64_t
  *   TOPO_FMT_MX  blocks of 32; byte b is the scale 2^(b - 127), 255 a NaN.
  *                The quantising calls use the smallest power of two s with
  *                amax <= 6 s (exponent at least -126; 1 for a block of zeros).
- *   TOPO_FMT_NV  blocks of 16; a byte is the scale in e4m3, times the row's
- *                float32 row_scale.  The quantising calls use for the row the
+ *   TOPO_FMT_NV  blocks of 16; a byte is the scale in e4m3, 0 to 0x7e and 0x7f for a
+ *                NaN (never negative: the products take a scale without a sign),
+ *                times the row's float32 row_scale.  The quantising calls use for the row the
  *                smallest power of two g with amax <= 6 * 448 g, amax over the
  *                row's finite values (exponent at least -126; 1 for a row of
  *                zeros), and for a block the smallest e4m3 value s with
@@ -582,7 +583,7 @@ int topo_dequantize_micro(int64_t rows, int32_t C, int32_t fmt, const uint8_t *q
  * as float32.  a: device [rows][K / 2]; w: device [n_w][N][K / 2]; w_row: device
  * float32 [n_w][N].  Segments, out, ws, limits and device errors as
  * topo_expert_gemm; N a multiple of 16, K of 32; bytes past the last block of a
- * row's scales hold no NaN (0xff; 0x7f, 0xff). */
+ * row's scales hold no NaN (0xff; 0x7f). */
 int topo_expert_gemm_micro(int32_t n_seg, int64_t rows, int32_t n_w, int32_t N, int32_t K, int32_t fmt, const uint8_t *a,
                            const uint8_t *a_scale, const float *a_row, const int32_t *seg_off, const int32_t *seg_w,
                            const uint8_t *w, const uint8_t *w_scale, const float *w_row, void *out, int32_t out_dtype,
