@@ -3,7 +3,8 @@ every scale byte.  Bounds are those of the call's own test."""
 import pytest
 
 import moe_expert_routing_ids_gb300 as topo
-from test_gpu_few import EIGHT, MX, NV, Case
+from test_gpu_few import MX, NV, Case
+from test_gpu_micro import BLOCK, values
 
 torch = pytest.importorskip("torch")
 gpu = pytest.mark.gpu
@@ -31,4 +32,21 @@ def test_row_scales_far_from_one(up, x, down, T, k, H, I):
         assert bool(((t[2] > 0) & torch.isfinite(t[2])).all())
         setattr(c, v, getattr(c, v) * 2.0 ** e)
     c.x = (c.x.double() * 2.0 ** x).to(torch.bfloat16)
+    check(c)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("T,k,H,I", [(1, 2, 128, 64), (8, 2, 544, 96), (32, 3, 96, 288)])
+def test_every_scale_byte(fmt, T, k, H, I):
+    """Subnormal e4m3 scales and 0; powers of two down to 2^-127, and of W_down up to 2^99."""
+    c = Case(T, 6, k, H, I, fmt, seed=12)
+    gen = torch.Generator().manual_seed(13)
+    for part, v, K, top in (("up", "vu", H, 127), ("down", "vd", I, 227)):
+        q, s, r = getattr(c, part)
+        n = K // BLOCK[fmt]
+        s[..., :n] = torch.randint(0, 127 if fmt == NV else top, (*s.shape[:-1], n), generator=gen).to(torch.uint8).to(c.dev)
+        if fmt == MX and part == "up":                            # near 1 in every third block, far below elsewhere
+            s[..., :n:3] = torch.randint(118, 126, s[..., :n:3].shape, generator=gen).to(torch.uint8).to(c.dev)
+        setattr(c, v, torch.as_tensor(values(q.cpu().numpy(), s.cpu().numpy(), None if r is None else r.cpu().double().numpy(), fmt)))
     check(c)

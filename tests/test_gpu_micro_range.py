@@ -1,5 +1,5 @@
 """Rows and products in 4 bits at the ends of their ranges: gates near bf16's largest, row
-scales whose product float32 does not hold."""
+scales whose product float32 does not hold, every scale byte."""
 import numpy as np
 import pytest
 
@@ -100,3 +100,34 @@ def test_row_scales_whose_product_float32_does_not_hold(ea, ew, rows, n_seg, N, 
         assert not bool(torch.isnan(g).any())
         assert bool(((g - want).abs() <= tol)[inside].all())
         assert bool((g.abs() == float("inf"))[far].all()) and bool((torch.sign(g) == torch.sign(want))[far].all())
+
+
+@gpu
+@pytest.mark.parametrize("rows,n_seg,N,K", [(3, 1, 48, 32), (150, 2, 272, 288), (130, 1, 128, 1056), (70, 9, 1040, 544)])
+@pytest.mark.parametrize("fmt,a_bytes,w_bytes", [(NV, (0, 127), (0, 127)), (NV, (0, 8), (0, 127)), (NV, (0, 127), (0, 8)), (NV, (0, 8), (0, 8)),
+                                                 (MX, (0, 24), (231, 255)), (MX, (231, 255), (0, 24)), (MX, (87, 168), (87, 168)),
+                                                 (MX, (1, 255), (127, 128)), (MX, (127, 128), (1, 252))])
+def test_products_of_every_scale_byte(fmt, a_bytes, w_bytes, rows, n_seg, N, K):
+    """Subnormal e4m3 scales and 0 (bytes below 8), powers of two to the ends.  The bound of the
+    products' own test, of the terms' magnitudes: a product is 0 or far above 2^-149 but for the
+    last two sets, where what is lost below float32's numbers is 2^-149 a product and more."""
+    dev = _dev()
+    rng = np.random.default_rng([rows, N, K, *a_bytes, *w_bytes])
+    off = segments(rng, n_seg, rows)
+    a, w = list(random_rows(rng, rows, K, fmt)), list(random_rows(rng, n_seg * N, K, fmt))
+    for t, b in ((a, a_bytes), (w, w_bytes)):
+        t[1][:, :K // BLOCK[fmt]] = rng.integers(*b, (len(t[1]), K // BLOCK[fmt]))
+    got, err = product(a, w, off, None, n_seg, N, K, fmt, False, dev)
+    assert err == 0
+    got = got.double().cpu()
+    va, vw = torch.as_tensor(values(*a, fmt)), torch.as_tensor(values(*w, fmt)).reshape(n_seg, N, K)
+    for i in range(n_seg):
+        r0, r1 = int(off[i]), int(off[i + 1])
+        if r0 == r1:
+            continue
+        want, A = va[r0:r1] @ vw[i].T, va[r0:r1].abs() @ vw[i].abs().T
+        tol = (K / 64 + K / 8192 + 4) * 2.0 ** -23 * A + K * 2.0 ** -149
+        inside = A < 3.4e38                                       # a partial sum may pass float32's range
+        g = got[r0:r1]
+        assert bool(((g - want).abs() <= tol)[inside].all())
+        assert bool(inside.any())
