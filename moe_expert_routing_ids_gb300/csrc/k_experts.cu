@@ -54,9 +54,9 @@
 // scales; sums stay in tensor memory over 8192 values, and the rows' scales multiply them
 // in the registers.  A row's 16 scale bytes come with the stage as a box of their own, and
 // the scale warps turn the words of 128 rows into the order that tensor memory wants.
-// Measured: 131072 rows, N = 4096, K = 7168, 128 experts: by 32 1.56 ms, 4.9 PFLOP/s, by 16
-// 1.89 ms, 4.1 PFLOP/s (tensor pipe 50 and 40 percent of cycles); 1536 rows, 2816 x 4096,
-// 64 experts 66 and 72 us, 6.3 and 6.2 TB/s; 6 rows, 4096 x 1408: 12 and 14 us; 16384 rows of
+// Measured: 131072 rows, N = 4096, K = 7168, 128 experts: by 32 1.54 to 1.56 ms, 5.0 PFLOP/s, by
+// 16 1.81 to 1.89 ms, 4.1 to 4.2 PFLOP/s (tensor pipe 50 and 40 percent of cycles); 1536 rows,
+// 2816 x 4096, 64 experts 67 and 72 us, 6.2 TB/s; 6 rows, 4096 x 1408: 10 and 12 us; 16384 rows of
 // 64 experts, 4096 x 1408: 84 and 100 us, without the stores 66 and 75.  What bounds it:
 // the bytes of a stage are those of the 8-bit product, 768 cycles of shared memory; by 16, a
 // build that loads no scales and copies half of them to tensor memory still takes 1.78 ms.
@@ -105,8 +105,11 @@ constexpr int kScaleKB = 4;                       // blocks whose scales are bro
 // gradient and 4 bits: blocks summed in tensor memory before the sum moves to registers
 template <int MODE>
 constexpr int kFlush = kMicro<MODE> ? 32 : 16;
+// Segments of one launch (the table in shared memory, where the 4-bit stages with their scales
+// leave the least).  More take a launch each, one after the other: 322 segments of 4 rows, 1024 x
+// 2048 by 32 and 16 73 and 81 us, 320 64 and 70; 512 108 and 118 (8 bits, one launch, 170).
 template <int MODE>
-constexpr int kSegCap = kMicro<MODE> ? 320 : MODE == kProduct ? 1024 : 512;   // segments of one launch (the table in shared memory)
+constexpr int kSegCap = kMicro<MODE> ? 320 : MODE == kProduct ? 1024 : 512;
 // bytes a warp stores through shared memory at a time, rows of 64 bytes (4 bits: the
 // stages with their scales leave half as much)
 template <int MODE>

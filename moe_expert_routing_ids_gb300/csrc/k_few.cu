@@ -24,10 +24,10 @@
 // The down kernel starts as the up kernel's CTAs end (its first weights do not depend on
 // it) and waits for all of it before it reads the activations.
 //
-// Measured (host call after call, E = 256 of 7168 x 2048, k = 8): one token in 8 bits 61 to
-// 64 us, 5.5 to 5.8 TB/s of weights, the up kernel's steady part at 7 TB/s; 32 tokens in MX
-// 661 to 711 us, 5.4 to 5.8 TB/s.  One token of 2048 x 768 in MX 15 us; 8 tokens of 64 experts,
-// 4096 x 1408, k = 6, NV 73 to 75 us, 4.6 to 4.7 TB/s.  What bounds it: in 8 bits memory,
+// Measured (host call after call, E = 256 of 7168 x 2048, k = 8): one token in 8 bits 60 to
+// 63 us, 5.6 to 5.9 TB/s of weights, the up kernel's steady part at 7 TB/s; 32 tokens in MX
+// 668 to 725 us, 5.3 to 5.7 TB/s.  One token of 2048 x 768 in MX 15 us, in NV 16; 8 tokens of 64
+// experts, 4096 x 1408, k = 6, NV 72 to 75 us, 4.5 to 4.7 TB/s.  What bounds it: in 8 bits memory,
 // and 3 to 4 us to the first product of either kernel (the ids' round trip, the sort, the
 // first items' addresses, the rows' conversion: instructions, not waits); in 4 bits the
 // issue of 275 instructions (NV; MX 243) for a stage of 4096 weights at 58 to 63 percent of
@@ -36,9 +36,10 @@
 // the smallest layer, 5 to 25 slower elsewhere; rows of 144 bytes with their scales instead
 // of the exclusive or: 5 percent slower; weights first to leave the L2: equal; the last sum
 // in the down kernel, by the CTA that brings a tile's last expert: equal at one token,
-// 1186 us against 736 at 32; the up contraction split over CTAs, so that each holds a part
+// much slower at 32 (with it and rings of 16 x 4 the call took 1186 us, without it and with
+// rings of 14 x 3 736); the up contraction split over CTAs, so that each holds a part
 // of all tokens' rows: 756 us against 709 at 32 tokens, 173 against 125 with 64 experts of
-// 4096 x 1408 (items of four stages).
+// 4096 x 1408 (items of four stages).  W_down's kernel in MX keeps five words in local memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -720,7 +721,7 @@ k_few(FewArgs g) {
 
 // out[t] = the sum of the pairs' outputs y over the slots, four columns to a thread, eight
 // slots' loads on their way at once.  (Done by the CTA that brings a tile's last expert,
-// counted with atomics, it took as long at one token, and 200 us more at 32, where that is
+// counted with atomics, it took as long at one token and far longer at 32, where that is
 // one and the same CTA for nearly all tiles.)
 __global__ void __launch_bounds__(128)
 k_few_sum(FewArgs g) {
@@ -764,7 +765,7 @@ k_few_sum(FewArgs g) {
 }
 
 // ------------------------------------------------------------------------ host
-constexpr size_t kFewSmem = 218 * 1024;           // dynamic; the tables take 7 KB
+constexpr size_t kFewSmem = 218 * 1024;           // dynamic; the tables take 4 KB
 constexpr int kLeastParts = 16 * 512;
 
 uint32_t over(int n) { return (uint32_t)((((uint64_t)1 << 32) + n - 1) / n); }     // 2^32 / n, for n > 1
@@ -780,8 +781,10 @@ cudaError_t run_few(FewArgs g, cudaStream_t st) {
     int stages = 4;
     g.warps = kMaxWarps;
     g.cols = kCols;
-    // all tokens' rows, where they leave 14 warps rings of 3 stages (32 tokens of 7168: 1094 us
-    // with rings of 14 x 3, 1188 of 16 x 4 beside rows of half the bytes)
+    // all tokens' rows, where they leave 14 warps rings of 3 stages.  Against a batch's rows
+    // beside rings of 16 x 4, in 8 bits, MX and NV: 6 tokens of 256 experts, 7168 x 2048, k = 8
+    // 317, 217 and 201 us for 321, 212 and 202; 12 of 64, 4096 x 1408, k = 6 133, 91 and 89 for 133, 89
+    // and 89; 28 of 64, 2048 x 1024, k = 8 78, 51 and 56 for 75, 50 and 54: next to equal
     g.resident = !DOWN && room(14, 3, g.T) >= kLeastParts;
     if (!g.resident)                                             // rows of a very wide layer
         while (g.cols > 1 && room(8, 3, g.cols) < kLeastParts) --g.cols;

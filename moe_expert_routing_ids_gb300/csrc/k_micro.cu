@@ -168,7 +168,8 @@ __device__ __forceinline__ void gated(float (&v)[16], const float (&u)[16], bool
 // Measured in groups, CTAs to an SM: activation of 131072 x 2048 to MX 1, 4: 221 us, 1, 5: 231,
 // 2, 3: 204, 2, 4: 193, 3, 2: 310; to NV 1, 5: 296, 2, 3: 246, 2, 4: 236; rows of 131072 x 7168 to
 // NV 4, 3: 429, 4, 4: 399, 5, 3: 458.  run_rows takes the activation's three, 3 CTAs, where
-// they need half as many warps.
+// they need half as many warps.  At four CTAs' 64 registers rows to NV keep 13 or 14 words in
+// local memory, narrow ones by token 13 (to MX 2), the activation to NV 4, of three groups 8.
 template <int SRC>
 constexpr int kGroups = SRC == kSwiglu ? 2 : 4;
 constexpr int ctas(int src, int n) { return src == kSwiglu && n == 3 ? 3 : 4; }   // to an SM

@@ -21,6 +21,11 @@ __device__ __forceinline__ void unpack16(const uint4 &a, const uint4 &b, float (
 // 333 tokens 18.9 / 24.1 us, 1024 29.6 / 26.4, 4096 62.9 / 51.4, 16384 239 / 132.
 // Both sides were measured at k = 8 only.  By token at k = 1, 2, 4 and 8, 16384 tokens:
 // 52, 64, 83 and 124 us, against 30, 41, 61 and 103 for the bytes alone.
+// The 4-bit rows' border at k = 8 is the same or a little higher, to MX and NV, by position / by
+// token: H = 4096, 4 MB 6.5 and 9.1 / 13 and 13 us, 8 MB 11 and 16 / 13 and 15, 16 MB 21 and 29 /
+// 18 and 20; H = 1024, 4 MB 8.6 and 11 / 11 and 11, 8 MB 15 and 20 / 14 and 16; H = 128, 8 MB 18 and
+// 23 / 19 and 21.  At k = 1 and 2 by position is the faster up to 16 MB at least (H = 4096, k = 2:
+// 6.5 and 9.1 / 13 and 13): the rule does not ask for k.
 constexpr int64_t kGatherBytes = 4 << 20;
 
 // A sum of products times two float32 scales r and s, where r * s, or the sum times either, may be

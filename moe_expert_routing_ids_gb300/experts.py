@@ -92,7 +92,8 @@ class ExpertLayer:
 
     forward(), backward() and set_weights() work in the layer's own buffers: on one
     layer they must not overlap, on two streams or as replays of graphs that hold
-    them.  few() works in buffers of its own call."""
+    them.  few() works in buffers of its own call, and only set_weights() must not
+    overlap it."""
 
     def __init__(self, cfg: dict, w_up: torch.Tensor, w_down: torch.Tensor, route: TopoRouteOpts, train: bool = False,
                  stream=None, fmt: int = TOPO_FMT_EIGHT):
@@ -113,7 +114,7 @@ class ExpertLayer:
 
     def set_weights(self, w_up: torch.Tensor, w_down: torch.Tensor):
         """New values of the weights, as after an optimiser's step; the layer keeps
-        them in 8 bits only.  A backward() belongs to the weights of its forward()."""
+        them in its format only.  A backward() belongs to the weights of its forward()."""
         self._need_weights(w_up, w_down)
         self.up.load(w_up, self.planner.stream)
         self.down.load(w_down, self.planner.stream)
