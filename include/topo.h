@@ -566,8 +566,10 @@ int topo_permute_quantize_micro(const topo_cfg *cfg, int32_t n_layers, int32_t H
                                 const int32_t *sorted_pairs, uint8_t *q, uint8_t *scale, float *row_scale, void *ws,
                                 size_t ws_bytes, cudaStream_t stream);
 
-/* The gated activation of topo_swiglu_quantize into 4 bits.  h: device bf16
- * [rows][2 I]. */
+/* The gated activation of topo_swiglu_quantize into 4 bits, in float32 before it
+ * is rounded (gates below -88.7, whose exp(-g) is infinite there, give 0, as in
+ * that call and in topo_expert_few; a product past its range is an infinity).
+ * h: device bf16 [rows][2 I]. */
 int topo_swiglu_quantize_micro(int64_t rows, int32_t I, int32_t fmt, const uint16_t *h, uint8_t *q, uint8_t *scale,
                                float *row_scale, cudaStream_t stream);
 
